@@ -289,6 +289,215 @@ int moe_profile_phases(moe_handle* h, double* mean_us, double* max_us, int32_t n
 int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const uint16_t* x_bf16,
                              int32_t rows, float* out, unsigned* dev_status, void* stream);
 
+/* ======================================================================================
+ * The attention side of a verify round
+ *
+ * What a round runs around its expert layers: the page and slot map of the rows to come
+ * (moe_round_map), the norms and rotation of their queries and keys with the write into
+ * the paged cache (moe_qk_rope_cache), the attention of the drafted rows over that cache
+ * (moe_tree_attention), and the log probabilities of the drafted tokens under the logits
+ * (moe_token_logprobs).  The pages leave these steps to the surrounding engine; their
+ * definitions here are this library's own.
+ *
+ * Conventions, besides those at the top of this file:
+ *   - No handle.  A call runs on the current device and takes one descriptor struct that
+ *     a caller fills once and may reuse for every round; the struct itself is host
+ *     memory, read during the call, and its pointers are device memory.  Lengths, maps
+ *     and masks are read on the device, so a captured graph follows their contents.
+ *   - Device pointers are 16-byte aligned except where a field says otherwise.
+ *   - dev_status: a caller-owned device word, required, 4-byte aligned.  A kernel ORs
+ *     MOE_DEV_* bits into it and never clears it; the caller does.
+ *   - Nothing outside the described buffers is read or written whatever the device-side
+ *     maps hold: an entry that does not fit is skipped and raises its bit.
+ *   - The calls allocate nothing and synchronise with nothing; workspaces are passed in.
+ *     Calls that share a workspace must not overlap.
+ *   - Outputs do not depend on the order in which thread blocks finish (bitwise).
+ *   - Element types: MOE_BF16, MOE_F16, and MOE_F32 where a call says so.  Sums, softmax
+ *     statistics and norms are held in 32 bits; results are rounded once.
+ * ====================================================================================== */
+
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+
+enum {
+  MOE_DEV_TIMEOUT = 1, /* a bounded device wait gave up: outputs are incomplete */
+  MOE_DEV_SLOT = 2,    /* an expert table entry outside the bank (expert layer calls) */
+  MOE_DEV_PAGES = 4,   /* free pages or table columns ran out */
+  MOE_DEV_LENGTH = 8,  /* a length that is negative, too long or does not fit the rest */
+  MOE_DEV_INDEX = 16   /* a page, slot, parent or token index outside its range */
+};
+
+/* A paged cache of keys and values, DEVICE pointers.  The element (page, slot in page,
+ * head, e) of either is at page * page_stride + slot * slot_stride + head * head_stride
+ * + e, strides in elements (multiples of 8, not negative), so both [page][slot][head][D]
+ * and [page][head][slot][D] orders and slices of larger buffers can be described.  A
+ * position p of a request lives in page block_table[request][p / page_size] at slot
+ * p % page_size; its flat slot number is page * page_size + p % page_size, and
+ * n_pages * page_size must stay below 2^31.  page_size: 1..65536. */
+typedef struct moe_kv_cache {
+  void* k;
+  void* v;
+  int64_t page_stride, slot_stride, head_stride;
+  int32_t n_pages, page_size;
+} moe_kv_cache;
+
+/* Block tables, slots and tree masks of a round, from the requests' lengths alone.
+ * Request b has ctx_len[b] cached positions and brings new_len[b] rows (0 allowed),
+ * which take the positions after the context in the cache.  Rows are numbered request
+ * after request.  With P = page_size, held_b = pages_held[b] (ceil(ctx_len[b] / P) where
+ * pages_held is NULL) and need_b = ceil((ctx_len[b] + new_len[b]) / P), each request
+ * takes max(0, need_b - held_b) pages from free_pages, in request order, and they are
+ * written behind its held ones: block_table[b][held_b ..].  Other table entries stay.
+ *   row_start [n_req + 1]  first row of each request; row_start[n_req] = all rows
+ *   pages     [n_req]      pages the request holds now (the next call's pages_held)
+ *   n_taken   [1]          pages taken: free_pages[0 .. n_taken) are in use now
+ *   row_req   [n_rows]     request of the row
+ *   row_pos   [n_rows]     ctx_len + depth of the row in its tree (the rotation's position)
+ *   row_slot  [n_rows]     flat cache slot of the row's key and value
+ *   tree_mask [n_rows]     bit j: row j of the same request is the row itself or one of
+ *                          its ancestors (may be NULL)
+ * parents [n_rows]: index within the request of the row's parent, less than the row's
+ * own, or -1 for a row that follows the context directly (several may); requests then
+ * bring at most 64 rows.  NULL: each row follows the one before it (a chain, or a
+ * prompt); tree_mask is then the chain's, for at most 64 rows.
+ * n_rows is the capacity of the row arrays: rows that no request brings get row_req -1,
+ * row_pos 0, row_slot -1 and an empty mask, so a captured round can keep its width.
+ * Raised bits: MOE_DEV_PAGES (too few free pages, or more than table_width columns
+ * needed: rows without a page get slot -1, fresh table entries without one -1);
+ * MOE_DEV_LENGTH (a negative length or one past 2^31 - 1, taken as 0; pages_held below
+ * what the context needs or outside the table; more rows than n_rows, the rest is left
+ * out; a tree of more than 64 rows, its later rows get an empty mask); MOE_DEV_INDEX (a
+ * page outside [0, n_pages), treated as none; a parent outside [-1, row), treated as -1).
+ * Limits: 1 <= n_req <= 16384, 0 <= n_rows, 1 <= table_width, 0 <= n_free. */
+typedef struct moe_map_args {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  const int32_t* pages_held;
+  const int32_t* free_pages;
+  const int32_t* parents;
+  int32_t* block_table; /* [n_req][table_width] */
+  int32_t* row_start;
+  int32_t* pages;
+  int32_t* n_taken;
+  int32_t* row_req;
+  int32_t* row_pos;
+  int32_t* row_slot;
+  uint64_t* tree_mask;
+  unsigned* dev_status;
+  int32_t n_req, n_rows, n_free, page_size, n_pages, table_width;
+} moe_map_args;
+int moe_round_map(const moe_map_args* args, void* stream);
+
+/* Norm and rotation of queries and keys, and the cache write, in one pass.  Per row and
+ * head, in 32 bits: y = x * gain / sqrt(mean(x^2) + eps) (y = x where the gain is NULL);
+ * then the first rot_dim elements are rotated in pairs (a, b) by the angle
+ * row_pos * inv_freq[i]: (a cos - b sin, b cos + a sin) * rot_scale.  Pair i is elements
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved.  Angles are reduced exactly for
+ * any 32-bit position (inv_freq is in 64 bits; its value is taken modulo one turn a
+ * position).  Queries go to q_out; keys go to the cache at the row's slot, and so do the
+ * values, as they are.  A row with slot -1 has its queries written and nothing cached;
+ * other slots outside the cache raise MOE_DEV_INDEX and are skipped.  Two rows must not
+ * share a slot.
+ *   q [n_rows][q_heads][D], k and v [n_rows][kv_heads][D]: the strides are from row to
+ *   row, in elements (multiples of 8), so the three may lie in one projection's output.
+ *   q_out may be q itself (same stride); k and v must not lie in the cache.
+ * dtype: MOE_BF16 or MOE_F16, of every element array.  head_dim 64, 128 or 256; rot_dim a
+ * multiple of 16, 16..head_dim, or 0 (no rotation); q_heads and kv_heads 1..256;
+ * eps >= 0. */
+typedef struct moe_qk_rope_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  const void* q_gain;     /* [D] or NULL */
+  const void* k_gain;     /* [D] or NULL */
+  const double* inv_freq; /* [rot_dim / 2] */
+  const int32_t* row_pos;
+  const int32_t* row_slot;
+  unsigned* dev_status;
+  moe_kv_cache cache;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int32_t n_rows, q_heads, kv_heads, head_dim, rot_dim, interleaved, dtype;
+  float eps, rot_scale;
+} moe_qk_rope_args;
+int moe_qk_rope_cache(const moe_qk_rope_args* args, void* stream);
+
+/* Attention of drafted rows over the paged cache.  Request b brings the rows
+ * [row_start[b], row_start[b + 1]), n_b of them, at most max_tree; the keys and values of
+ * its ctx_len[b] context positions and then of its own rows lie in the cache.  Row i sees
+ * every context position, and row j of its request where bit j of tree_mask[row] is set
+ * (tree_mask NULL: where j <= i).  Query head h reads key/value head h / (q_heads /
+ * kv_heads).  In 32 bits: s = scale * (q . k), out = sum softmax(s) v over what is seen;
+ * lse = log(sum exp(s)).  A row that sees nothing gets out 0 and lse -infinity.  Positions
+ * that are not seen have no influence, whatever their cached bits hold (infinities and
+ * NaN included).  With n_b = 1 this is the decode step of a single token.
+ * The softmax weights are rounded to the element type for the product with v (their sum
+ * is not); everything else stays in 32 bits until out is rounded.
+ *   q, out [n_rows][q_heads][D], the strides from row to row in elements (multiples of
+ *   8); lse fp32 [n_rows][q_heads] or NULL; row_start [n_req + 1] and ctx_len [n_req] as
+ *   moe_round_map writes and reads them (4-byte aligned is enough).  Rows that belong to
+ *   no request are not written.
+ * dtype MOE_BF16 or MOE_F16; head_dim 64, 128 or 256; kv_heads a divisor of q_heads with
+ * a quotient of at most 64; max_tree 1..64; n_req 1..16384.
+ * MOE_DEV_LENGTH: a negative context, row_start not ascending within n_rows, more rows
+ * than max_tree, or a length beyond the table: that request's rows are not computed (out
+ * 0, lse -infinity where the rows themselves are valid).  MOE_DEV_INDEX: a needed page
+ * outside the cache; its positions count as not seen.  MOE_DEV_TIMEOUT: thread blocks
+ * that share a request's context waited for each other for more than 2 s.
+ * ws: moe_tree_attention_workspace_bytes (0 for arguments that the call would refuse),
+ * 16-byte aligned, set to zero once before its first use; a call that ends without
+ * MOE_DEV_TIMEOUT leaves it ready for the next. */
+typedef struct moe_tree_attention_args {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* row_start;
+  const int32_t* ctx_len;
+  const int32_t* block_table; /* [n_req][table_width] */
+  const uint64_t* tree_mask;  /* [n_rows] or NULL */
+  unsigned* dev_status;
+  moe_kv_cache cache;
+  int64_t q_stride, out_stride;
+  int32_t n_req, n_rows, max_tree, table_width, q_heads, kv_heads, head_dim, dtype;
+  float scale;
+} moe_tree_attention_args;
+size_t moe_tree_attention_workspace_bytes(const moe_tree_attention_args* args);
+int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* Log probabilities of given tokens under rows of logits.  With z = logit *
+ * inv_temperature and lse = log(sum exp(z)) over the row:
+ *   logp     [n_rows]         z[token] - lse
+ *   entropy  [n_rows]         -sum p log p, p = exp(z - lse), 0 log 0 = 0
+ *   rank     [n_rows] int32   entries before the token by (logit descending, id ascending)
+ *   top_ids  [n_rows][top_k] int32, top_logp [n_rows][top_k]: the first top_k entries in
+ *                             that order and their log probabilities
+ * Any output may be NULL, top_ids and top_logp only where top_k is 0.  A logit of
+ * -infinity is an entry that cannot occur: it has log probability -infinity and never is
+ * a top entry; where fewer than top_k entries can occur the rest is id -1 and -infinity.  A row without any entry that can occur: logp -infinity, entropy 0.  A token
+ * of -1 stands for no token: logp -infinity, rank -1; other tokens outside the vocabulary
+ * do the same and raise MOE_DEV_INDEX.  NaN or +infinity in a row makes its logp, entropy
+ * and top_logp NaN and its ids unspecified.
+ *   logits [n_rows][vocab] of MOE_F32, MOE_BF16 or MOE_F16, stride from row to row in
+ *   elements, any alignment of the element type; tokens [n_rows] (NULL if neither logp nor
+ *   rank is asked for).  vocab 1..2^24, top_k 0..32, inv_temperature > 0 and finite.
+ * ws: moe_token_logprobs_workspace_bytes (0 for arguments that the call would refuse),
+ * 16-byte aligned, set to zero once before its first use; every call leaves it ready for
+ * the next. */
+typedef struct moe_logprob_args {
+  const void* logits;
+  const int32_t* tokens;
+  float* logp;
+  float* entropy;
+  int32_t* rank;
+  int32_t* top_ids;
+  float* top_logp;
+  unsigned* dev_status;
+  int64_t stride;
+  int32_t n_rows, vocab, top_k, dtype;
+  float inv_temperature;
+} moe_logprob_args;
+size_t moe_token_logprobs_workspace_bytes(const moe_logprob_args* args);
+int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, void* stream);
+
 const char* moe_strerror(int code);
 
 #ifdef __cplusplus

@@ -26,7 +26,12 @@ ABI_SYMBOLS = (
     "moe_profile_read",
     "moe_profile_phases", "moe_decode_layer_noalloc", "moe_prefill_workspace_bytes",
     "moe_prefill_layer", "moe_strerror",
+    "moe_round_map", "moe_qk_rope_cache", "moe_tree_attention_workspace_bytes", "moe_tree_attention",
+    "moe_token_logprobs_workspace_bytes", "moe_token_logprobs",
 )
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2  # element types of the attention-side calls
+# bits of their device status word
+MOE_DEV_TIMEOUT, MOE_DEV_SLOT, MOE_DEV_PAGES, MOE_DEV_LENGTH, MOE_DEV_INDEX = 1, 2, 4, 8, 16
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 KIND_ROUND = 0
 MMA_ROWS = 13  # rounds of at least this many rows run on the tensor cores
@@ -48,6 +53,43 @@ class moe_layer_w(ctypes.Structure):
                 ("gateup_scale", ctypes.c_void_p), ("down_nib", ctypes.c_void_p),
                 ("down_scale", ctypes.c_void_p), ("slot_of_expert", ctypes.c_void_p),
                 ("n_slots", ctypes.c_int32)]
+
+
+def _fields(spec):
+    kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64, "f": ctypes.c_float}
+    return [(name, kinds[kind]) for kind, names in spec for name in names.split()]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = _fields([("p", "k v"), ("l", "page_stride slot_stride head_stride"), ("i", "n_pages page_size")])
+
+
+class moe_map_args(ctypes.Structure):
+    _fields_ = _fields([
+        ("p", "ctx_len new_len pages_held free_pages parents block_table row_start pages n_taken row_req row_pos "
+              "row_slot tree_mask dev_status"),
+        ("i", "n_req n_rows n_free page_size n_pages table_width")])
+
+
+class moe_qk_rope_args(ctypes.Structure):
+    _fields_ = (_fields([("p", "q k v q_out q_gain k_gain inv_freq row_pos row_slot dev_status")])
+                + [("cache", moe_kv_cache)]
+                + _fields([("l", "q_stride k_stride v_stride q_out_stride"),
+                           ("i", "n_rows q_heads kv_heads head_dim rot_dim interleaved dtype"),
+                           ("f", "eps rot_scale")]))
+
+
+class moe_tree_attention_args(ctypes.Structure):
+    _fields_ = (_fields([("p", "q out lse row_start ctx_len block_table tree_mask dev_status")])
+                + [("cache", moe_kv_cache)]
+                + _fields([("l", "q_stride out_stride"),
+                           ("i", "n_req n_rows max_tree table_width q_heads kv_heads head_dim dtype"),
+                           ("f", "scale")]))
+
+
+class moe_logprob_args(ctypes.Structure):
+    _fields_ = _fields([("p", "logits tokens logp entropy rank top_ids top_logp dev_status"), ("l", "stride"),
+                        ("i", "n_rows vocab top_k dtype"), ("f", "inv_temperature")])
 
 
 class MoeError(RuntimeError):
@@ -102,6 +144,18 @@ _lib.moe_prefill_workspace_bytes.argtypes = [ctypes.POINTER(moe_dims), _i32]
 _lib.moe_prefill_workspace_bytes.restype = _sz
 _lib.moe_prefill_layer.argtypes = [_vp, ctypes.POINTER(moe_layer_w), _vp, _i32, _vp, _vp, _vp, _sz, _vp]
 _lib.moe_prefill_layer.restype = ctypes.c_int
+_lib.moe_round_map.argtypes = [ctypes.POINTER(moe_map_args), _vp]
+_lib.moe_round_map.restype = ctypes.c_int
+_lib.moe_qk_rope_cache.argtypes = [ctypes.POINTER(moe_qk_rope_args), _vp]
+_lib.moe_qk_rope_cache.restype = ctypes.c_int
+_lib.moe_tree_attention_workspace_bytes.argtypes = [ctypes.POINTER(moe_tree_attention_args)]
+_lib.moe_tree_attention_workspace_bytes.restype = _sz
+_lib.moe_tree_attention.argtypes = [ctypes.POINTER(moe_tree_attention_args), _vp, _sz, _vp]
+_lib.moe_tree_attention.restype = ctypes.c_int
+_lib.moe_token_logprobs_workspace_bytes.argtypes = [ctypes.POINTER(moe_logprob_args)]
+_lib.moe_token_logprobs_workspace_bytes.restype = _sz
+_lib.moe_token_logprobs.argtypes = [ctypes.POINTER(moe_logprob_args), _vp, _sz, _vp]
+_lib.moe_token_logprobs.restype = ctypes.c_int
 _lib.moe_strerror.argtypes = [ctypes.c_int]
 _lib.moe_strerror.restype = ctypes.c_char_p
 
@@ -243,3 +297,76 @@ def moe_decode_layer_noalloc(dims: moe_dims, w: moe_layer_w, x_bf16: int, rows: 
     """Allocation-free moe_decode_layer on the current device (static device scratch)."""
     _check(_lib.moe_decode_layer_noalloc(ctypes.byref(dims), ctypes.byref(w), x_bf16, int(rows), out,
                                          dev_status, stream), "moe_decode_layer_noalloc")
+
+
+# ---- the attention side of a verify round: one descriptor per call, filled once and reused ----
+
+def make_kv_cache(k: int, v: int, *, n_pages: int, page_size: int, page_stride: int, slot_stride: int,
+                  head_stride: int) -> moe_kv_cache:
+    """A paged key/value cache by device addresses; strides in elements (tensor.stride())."""
+    return moe_kv_cache(k, v, page_stride, slot_stride, head_stride, n_pages, page_size)
+
+
+def make_map_args(*, n_req: int, n_rows: int, page_size: int, n_pages: int, table_width: int, n_free: int,
+                  ctx_len: int, new_len: int, free_pages: int, block_table: int, row_start: int, pages: int,
+                  n_taken: int, row_req: int, row_pos: int, row_slot: int, dev_status: int, pages_held: int = 0,
+                  parents: int = 0, tree_mask: int = 0) -> moe_map_args:
+    """Descriptor of moe_round_map; addresses are device memory, 0 where the header allows NULL."""
+    return moe_map_args(ctx_len, new_len, pages_held or None, free_pages or None, parents or None, block_table,
+                        row_start, pages, n_taken, row_req or None, row_pos or None, row_slot or None,
+                        tree_mask or None, dev_status, n_req, n_rows, n_free, page_size, n_pages, table_width)
+
+
+def make_qk_rope_args(*, n_rows: int, q_heads: int, kv_heads: int, head_dim: int, rot_dim: int, dtype: int, q: int,
+                      k: int, v: int, q_stride: int, k_stride: int, v_stride: int, q_out: int, q_out_stride: int,
+                      row_pos: int, row_slot: int, cache: moe_kv_cache, dev_status: int, inv_freq: int = 0,
+                      q_gain: int = 0, k_gain: int = 0, interleaved: bool = False, eps: float = 1e-6,
+                      rot_scale: float = 1.0) -> moe_qk_rope_args:
+    """Descriptor of moe_qk_rope_cache; strides in elements from row to row."""
+    return moe_qk_rope_args(q or None, k or None, v or None, q_out or None, q_gain or None, k_gain or None,
+                            inv_freq or None, row_pos or None, row_slot or None, dev_status, cache, q_stride,
+                            k_stride, v_stride, q_out_stride, n_rows, q_heads, kv_heads, head_dim, rot_dim,
+                            1 if interleaved else 0, dtype, eps, rot_scale)
+
+
+def make_tree_attention_args(*, n_req: int, n_rows: int, max_tree: int, q_heads: int, kv_heads: int, head_dim: int,
+                             dtype: int, q: int, q_stride: int, out: int, out_stride: int, row_start: int,
+                             ctx_len: int, block_table: int, table_width: int, cache: moe_kv_cache, scale: float,
+                             dev_status: int, tree_mask: int = 0, lse: int = 0) -> moe_tree_attention_args:
+    """Descriptor of moe_tree_attention; strides in elements from row to row."""
+    return moe_tree_attention_args(q or None, out or None, lse or None, row_start, ctx_len, block_table,
+                                   tree_mask or None, dev_status, cache, q_stride, out_stride, n_req, n_rows,
+                                   max_tree, table_width, q_heads, kv_heads, head_dim, dtype, scale)
+
+
+def make_logprob_args(*, n_rows: int, vocab: int, dtype: int, logits: int, stride: int, dev_status: int,
+                      tokens: int = 0, top_k: int = 0, inv_temperature: float = 1.0, logp: int = 0, entropy: int = 0,
+                      rank: int = 0, top_ids: int = 0, top_logp: int = 0) -> moe_logprob_args:
+    """Descriptor of moe_token_logprobs; 0 for an output that is not wanted."""
+    return moe_logprob_args(logits or None, tokens or None, logp or None, entropy or None, rank or None,
+                            top_ids or None, top_logp or None, dev_status, stride, n_rows, vocab, top_k, dtype,
+                            inv_temperature)
+
+
+def moe_round_map(args: moe_map_args, stream: int) -> None:
+    _check(_lib.moe_round_map(args, stream), "moe_round_map")
+
+
+def moe_qk_rope_cache(args: moe_qk_rope_args, stream: int) -> None:
+    _check(_lib.moe_qk_rope_cache(args, stream), "moe_qk_rope_cache")
+
+
+def moe_tree_attention_workspace_bytes(args: moe_tree_attention_args) -> int:
+    return int(_lib.moe_tree_attention_workspace_bytes(args))
+
+
+def moe_tree_attention(args: moe_tree_attention_args, ws: int, ws_bytes: int, stream: int) -> None:
+    _check(_lib.moe_tree_attention(args, ws, ws_bytes, stream), "moe_tree_attention")
+
+
+def moe_token_logprobs_workspace_bytes(args: moe_logprob_args) -> int:
+    return int(_lib.moe_token_logprobs_workspace_bytes(args))
+
+
+def moe_token_logprobs(args: moe_logprob_args, ws: int, ws_bytes: int, stream: int) -> None:
+    _check(_lib.moe_token_logprobs(args, ws, ws_bytes, stream), "moe_token_logprobs")

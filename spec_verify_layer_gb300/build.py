@@ -7,13 +7,14 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("moe_verify.cu", "moe_prefill.cu", "moe_host.cpp")]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("moe_internal.h", "moe_common.cuh")] + [
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("moe_verify.cu", "moe_prefill.cu", "moe_round_map.cu", "moe_qk_rope.cu",
+                                                  "moe_tree_attn.cu", "moe_logprob.cu", "moe_host.cpp")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("moe_internal.h", "moe_common.cuh", "moe_round_ops.cuh")] + [
     os.path.join(ROOT, "include", "moe_verify.h")]
 OUT = os.path.join(HERE, "libmoeverify.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC", "-shared", "--threads", "0"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,90 @@
+// Shared by the attention-side operators of a verify round (moe_round_map.cu,
+// moe_qk_rope.cu, moe_tree_attn.cu, moe_logprob.cu): argument checks and the element
+// types.  Internal; not part of the public ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_verify.h"
+
+namespace moe {
+
+inline bool ptr_ok(const void* p, unsigned align) { return p && (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
+// NULL, or aligned
+inline bool opt_ok(const void* p, unsigned align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
+
+// strides of a cache in elements: multiples of 8, not negative, and no offset past 2^62
+inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 40); }
+
+inline int check_cache(const moe_kv_cache& c) {
+  if (!ptr_ok(c.k, 16) || !ptr_ok(c.v, 16)) return MOE_EINVAL;
+  if (c.n_pages < 1 || c.page_size < 1) return MOE_EINVAL;
+  if (!stride_ok(c.page_stride) || !stride_ok(c.slot_stride) || !stride_ok(c.head_stride)) return MOE_EINVAL;
+  if (c.page_size > 65536 || (int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31)) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// The current device's SM count; 0 if there is no usable device.
+inline int current_sms() {
+  int dev = -1, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// What the launch itself reported; a failed launch leaves no error behind for the caller's next call.
+inline int launch_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return MOE_ECUDA;
+}
+
+#ifdef __CUDACC__
+
+// A 32-bit word of two elements <-> two floats.
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (DT == MOE_BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == MOE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+  const uint32_t s = a + b;
+  return s < a ? 0xffffffffu : s;
+}
+
+// Largest b in [0, n) with start[b] <= x, for start ascending with start[0] <= x.
+template <typename T>
+__device__ __forceinline__ int last_not_above(const T* start, int n, T x) {
+  int lo = 0, hi = n;  // start[lo] <= x, start[hi] > x or hi == n
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace moe
