@@ -11,7 +11,7 @@
 // same time, the second out of L2.
 //
 // In a block, four roles meet at mbarriers:
-//   - four producer warps copy key and value rows (cp.async, 16 bytes a lane, page table
+//   - two producer warps copy key and value rows (cp.async, 16 bytes a lane, page table
 //     looked up per row) into a ring of shared-memory slots in the 128-byte swizzle that
 //     the tensor cores read;
 //   - one thread issues the products: S = Q K^T into tensor memory, and O += P V with P
@@ -32,14 +32,16 @@
 // product: slots past the last position are zero-filled, and the values of drafted rows
 // are looked over on their way: what is not finite becomes 0 in the slot and is added at
 // the end to the rows that see it.
+#include <type_traits>
+
 #include "moe_round_ops.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kTree = 64;
-constexpr int kThreads = 512;           // 8 softmax warps, 4 producer warps, 1 issuing warp (3 idle: warpgroups)
-constexpr int kSoftmaxThreads = 256, kProducers = 128;
+constexpr int kThreads = 384;  // 8 softmax warps, 2 producer warps, 1 issuing warp, 1 idle: 168 registers a thread
+constexpr int kSoftmaxThreads = 256, kProducers = 64;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 constexpr float kRescale = 8.0f;        // log2 of how far a maximum may lag behind
@@ -47,15 +49,19 @@ constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 
 template <int D>
 struct Shape {
-  static constexpr int KT = D == 256 ? 64 : 128;       // keys of a tile
+  static constexpr int KT = D == 256 ? 64 : 128;       // keys of a tile in shared memory
   static constexpr int NS = D == 256 ? 1 : 2;          // streams (tensor memory holds 512 columns)
+  static constexpr int PARTS = KT / 64;                // the weights are handed over 64 keys at a time
   static constexpr int MG = 128 * NS;                  // query rows of a group
   static constexpr int kSlot = KT * D * 2;             // bytes of a key or value tile
   static constexpr int kQ = 128 * D * 2;               // bytes of a query tile
   static constexpr int CPR = D / 8;                    // 16-byte chunks of a row
-  static constexpr int RPP = kProducers / CPR;         // rows a pass of the producers copies
-  static constexpr int PASSES = KT / RPP;
-  __host__ __device__ static constexpr int s_col(int s) { return NS == 2 ? 256 * s : 64 * s; }
+  static constexpr int RW = KT / 2;                    // rows of a tile that a producer warp copies
+  static constexpr int RPI = 32 / CPR;                 // of them with one instruction
+  // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
+  // there is one stream); the weights, in 16 bits, go over the second half of their scores.
+  __host__ __device__ static constexpr int s_col(int buf) { return NS == 2 ? 256 * buf : 64 * buf; }
+  __host__ __device__ static constexpr int p_col(int buf) { return s_col(buf) + KT / 2; }
   __host__ __device__ static constexpr int o_col(int s) { return NS == 2 ? 256 * s + 128 : 256; }
 };
 
@@ -64,25 +70,26 @@ struct Plan {  // host-computed, the same for every block
   int nslot;
   int group;   // query heads of a key/value head
   int part_rows;
+  unsigned group_mul;  // n / group = umulhi(n, group_mul); 0: group is 1
   unsigned page_mul;
   int page_shift;
-  int flip;    // scale is negative: the queries are negated
+  int flip;    // of the queries: 1 negated (a negative scale), 2 taken as 0 (a scale of 0)
   float c;     // |scale| * log2(e)
-  float* part;       // [blocks][2][part_rows][D]
-  float2* part_ml;   // [blocks][2][part_rows]
+  float4* part;      // [blocks][2][D / 4][part_rows]: a warp's rows side by side
+  float4* part_ml;   // [blocks][2][part_rows]: maximum, sum
   unsigned* arrive;  // [blocks]
   unsigned* done;    // [blocks]
 };
 
 struct Control {  // the start of dynamic shared memory
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
-  unsigned long long s_full[2], p_full[2], o_done[2], q_ready, drain;
+  unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  __align__(16) unsigned short hole[8][16];  // per tile: rows without a page, by pass
-  long long total, red[16];
-  int redn[16];
-  int maxn, start_b;
-  long long start_off;
+  __align__(16) unsigned hole[8][4];  // per tile: keys without a page
+  int red[kThreads / 32], redn[kThreads / 32];
+  // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
+  int total, w0, w1, start_off;
+  int start_b, gangs, groups, gang, member;
   unsigned tmem;
   int abort;
 };
@@ -107,7 +114,7 @@ __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the phase of `parity` to end; false once any wait of the block gave up.
-__device__ __noinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, int* abort_flag, unsigned* status) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, int* abort_flag, unsigned* status) {
   const long long t0 = clock64();
   while (!bar_try(b, parity)) {
     if (*(volatile int*)abort_flag) return false;
@@ -168,13 +175,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(unsigned long long* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
 }
-// A load and its wait are one statement: the registers are not ready in between.
-__device__ __forceinline__ void tm_load(uint32_t (&r)[32], uint32_t addr) {
+// The registers of a load are ready after tm_wait; `ready` makes their users wait for it
+// (a volatile statement alone would not keep plain arithmetic behind it).
+__device__ __forceinline__ void tm_load(uint32_t* r, uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
@@ -182,14 +189,26 @@ __device__ __forceinline__ void tm_load(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tm_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ready(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+__device__ __forceinline__ void tm_read(uint32_t* r, uint32_t addr) {
+  tm_load(r, addr);
+  tm_wait();
+  ready(r);
+}
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -213,7 +232,37 @@ __device__ __forceinline__ float2 tm_load2(uint32_t addr) {
                : "memory");
   return make_float2(__uint_as_float(x), __uint_as_float(y));
 }
+__device__ __forceinline__ void tm_read8(float* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      : "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two floats in one register pair: one instruction for both.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float2 split(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -249,45 +298,43 @@ template <int D>
 struct Walk {  // a block's share, unit (stretch of one head's tiles) after unit
   Req q;
   int b, h, t0, t1;
-  long long w, end;  // place in the list, end of the share
-  int seq;           // units so far that have rows for this block
-  __device__ __forceinline__ void begin(const moe_tree_attention_args& a, int b_, long long off, long long w_,
-                                        long long end_) {
-    w = w_;
-    end = end_;
+  int left;  // tiles left in the share, this unit's among them
+  __device__ __forceinline__ void begin(const moe_tree_attention_args& a, int b_, int off, int left_) {
+    left = left_;
     b = b_;
-    seq = -1;
-    if (w >= end) return;
+    if (left <= 0) return;
     q = request<D>(a, b);
-    h = (int)(off / q.tiles);
-    t0 = (int)(off - (long long)h * q.tiles);
-    t1 = (int)min((long long)q.tiles, t0 + (end - w));
+    h = off / q.tiles;
+    t0 = off - h * q.tiles;
+    t1 = min(q.tiles, t0 + left);
   }
-  __device__ __forceinline__ bool more() const { return w < end; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(const moe_tree_attention_args& a) {
-    w += t1 - t0;
-    if (w >= end) return;
+    left -= t1 - t0;
+    if (left <= 0) return;
     t0 = 0;
     if (++h == a.kv_heads) {
       h = 0;
-      if (b + 1 >= a.n_req) {
-        w = end;
-        return;
-      }
-      do q = request<D>(a, ++b);
-      while (q.tiles == 0 && b + 1 < a.n_req);
-      if (q.tiles == 0) {  // not while the lengths stay as they were
-        w = end;
-        return;
-      }
+      do {
+        if (++b >= a.n_req) {  // not while the lengths stay as they were
+          left = 0;
+          return;
+        }
+        q = request<D>(a, b);
+      } while (q.tiles == 0);
     }
-    t1 = (int)min((long long)q.tiles, end - w);
+    t1 = min(q.tiles, left);
   }
 };
 
-__device__ __forceinline__ long long share(long long total, int gangs, int g) { return total * g / gangs; }
-__device__ __forceinline__ int gang_of(long long total, int gangs, long long x) {
-  return (int)(((x + 1) * gangs - 1) / total);
+// Shares of the list: floor(total * g / gangs) to floor(total * (g + 1) / gangs); where equal
+// heads divide the blocks no share crosses from one head to the next.
+__device__ __forceinline__ int share(int total, int gangs, int g) {
+  const int each = total / gangs;
+  return each * g + (total - each * gangs) * g / gangs;
+}
+__device__ __forceinline__ int gang_of(int total, int gangs, int x) {
+  return (int)((((unsigned long long)x + 1) * gangs - 1) / (unsigned)total);
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -296,7 +343,7 @@ template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tree_attn(const __grid_constant__ moe_tree_attention_args a, const __grid_constant__ Plan p) {
   using Sh = Shape<D>;
-  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, RPP = Sh::RPP, PASSES = Sh::PASSES;
+  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, RW = Sh::RW, RPI = Sh::RPI;
   constexpr uint32_t kBlk = KT * 128;  // bytes of a 64-element block of a key or value tile
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -306,104 +353,94 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.group;
 
-  if (tid == 0) {
-    for (int i = 0; i < p.nslot; ++i) {
-      bar_init(&ct.full[i], kProducers);
-      bar_init(&ct.empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&ct.s_full[i], 1);
-      bar_init(&ct.p_full[i], 4);
-      bar_init(&ct.o_done[i], 1);
-    }
-    bar_init(&ct.q_ready, kSoftmaxThreads / 32);
-    bar_init(&ct.drain, 1);
-    ct.abort = 0;
-    ct.start_b = 0;
-    ct.start_off = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (tid < 8) ct.bad[tid] = 0;
-  if (tid < 128) (&ct.hole[0][0])[tid] = 0;
-  if (warp == 12) {
+  // total work, the widest request, and the request that holds this block's first place
+  unsigned flags = 0;
+  int total = 0, maxn = 0, lo, mine;
+  Req first{0, 0, 0, 0};
+  if (tid < a.n_req) first = request<D>(a, tid);
+  if (tid == 0 && __ldg(a.row_start) != 0) flags |= MOE_DEV_LENGTH;
+  if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ct.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == 11) {
+    if (lane < p.nslot) {
+      bar_init(&ct.full[lane], kProducers);
+      bar_init(&ct.empty[lane], 1);
+    }
+    if (lane < 4) bar_init(&ct.p_full[lane], 4);
+    if (lane < 2) {
+      bar_init(&ct.s_full[lane], 1);
+      bar_init(&ct.o_done[lane], 1);
+    }
+    if (lane == 0) {
+      bar_init(&ct.q_ready, kSoftmaxThreads / 32);
+      bar_init(&ct.drain, 1);
+      ct.abort = 0;
+    }
+    if (lane < 8) ct.bad[lane] = 0;
+    (&ct.hole[0][0])[lane] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-
-  // total work and the widest request
-  unsigned flags = 0;
+  const auto scan = [&](int b0, const Req& q) {  // lo: places before request b0 + tid, mine: its own
+    mine = q.tiles * a.kv_heads;
+    int incl = mine;
+    const int widest = __reduce_max_sync(0xffffffffu, q.tiles ? q.n : 0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (b0) __syncthreads();  // red is read below
+    if (lane == 31) {
+      ct.red[warp] = incl;
+      ct.redn[warp] = widest;
+    }
+    __syncthreads();
+    lo = total + incl - mine;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      const int x = ct.red[i];
+      if (i < warp) lo += x;
+      total += x;
+      maxn = max(maxn, ct.redn[i]);
+    }
+  };
+  scan(0, first);
+  for (int b0 = kThreads; b0 < a.n_req; b0 += kThreads) {
+    Req q{0, 0, 0, 0};
+    if (b0 + tid < a.n_req) q = request<D>(a, b0 + tid);
+    scan(b0, q);
+  }
   {
-    long long sum = 0;
-    int maxn = 0;
-    for (int b = tid; b < a.n_req; b += kThreads) {
-      const Req q = request<D>(a, b);
-      sum += (long long)q.tiles * a.kv_heads;
-      if (q.tiles) maxn = max(maxn, q.n);
-      if (q.n != 0 && q.tiles == 0) {
-        flags |= MOE_DEV_LENGTH;
-        if (q.n > 0 && b % (int)gridDim.x == (int)blockIdx.x) {
-          for (int r = q.s; r < q.s + q.n; ++r) {
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (long long)r * a.out_stride);
-            for (int i = 0; i < a.q_heads * CPR; ++i) o[i] = make_uint4(0, 0, 0, 0);
-            if (a.lse)
-              for (int i = 0; i < a.q_heads; ++i) a.lse[(long long)r * a.q_heads + i] = -INFINITY;
-          }
+    const int groups = max(1, (maxn * G + Sh::MG - 1) / Sh::MG);
+    const int gangs = min(total, max(1, (int)gridDim.x / groups));
+    const int gang = (int)blockIdx.x / groups;
+    const bool works = gang < gangs && groups <= (int)gridDim.x;
+    const int w0 = works ? share(total, gangs, gang) : 0, w1 = works ? share(total, gangs, gang + 1) : 0;
+    if (tid == 0) {
+      ct.total = total;
+      ct.w0 = w0;
+      ct.w1 = w1;
+      ct.groups = groups;
+      ct.gangs = gangs;
+      ct.gang = gang;
+      ct.member = (int)blockIdx.x - gang * groups;
+    }
+    if (works && a.n_req > kThreads) {  // the sums again, up to that request
+      total = 0;
+      for (int b0 = 0; b0 < a.n_req && total <= w0; b0 += kThreads) {
+        __syncthreads();
+        Req q{0, 0, 0, 0};
+        if (b0 + tid < a.n_req) q = request<D>(a, b0 + tid);
+        scan(b0, q);
+        if (w0 >= lo && w0 < lo + mine) {
+          ct.start_b = b0 + tid;
+          ct.start_off = w0 - lo;
         }
       }
-    }
-    if (tid == 0 && __ldg(a.row_start) != 0) flags |= MOE_DEV_LENGTH;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    maxn = __reduce_max_sync(0xffffffffu, maxn);
-    if (lane == 0) {
-      ct.red[warp] = sum;
-      ct.redn[warp] = maxn;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      long long t = 0;
-      int m = 0;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        t += ct.red[i];
-        m = max(m, ct.redn[i]);
-      }
-      ct.total = t;
-      ct.maxn = m;
-    }
-    __syncthreads();
-  }
-  const long long total = ct.total;
-  const int groups = max(1, (ct.maxn * G + Sh::MG - 1) / Sh::MG);
-  const int gangs = (int)min(total, (long long)max(1, (int)gridDim.x / groups));
-  const int gang = (int)blockIdx.x / groups, member = (int)blockIdx.x - gang * groups;
-  const bool works = gang < gangs && groups <= (int)gridDim.x;
-  const long long w0 = works ? share(total, gangs, gang) : 0, w1 = works ? share(total, gangs, gang + 1) : 0;
-  // the request that holds place w0
-  if (works) {
-    long long before = 0;
-    for (int b0 = 0; b0 < a.n_req; b0 += kThreads) {
-      const int b = b0 + tid;
-      const long long mine = b < a.n_req ? (long long)request<D>(a, b).tiles * a.kv_heads : 0;
-      long long incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-      }
-      __syncthreads();
-      if (lane == 31) ct.red[warp] = incl;
-      __syncthreads();
-      long long lo = before;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) lo += ct.red[i];
-        before += ct.red[i];
-      }
-      lo += incl - mine;
-      if (w0 >= lo && w0 < lo + mine) {
-        ct.start_b = b;
-        ct.start_off = w0 - lo;
-      }
-      if (before > w0) break;  // the same for every thread
+    } else if (works && w0 >= lo && w0 < lo + mine) {
+      ct.start_b = tid;
+      ct.start_off = w0 - lo;
     }
   }
   fence_before();
@@ -411,52 +448,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = ct.tmem;
   Walk<D> wk;
-  wk.begin(a, ct.start_b, ct.start_off, w0, w1);
+  const int member = ct.member;
+  wk.begin(a, ct.start_b, ct.start_off, ct.w1 - ct.w0);
 
-  if (warp >= 8 && warp < 12) {
+  if (warp == 8 || warp == 9) {
     // ---------------- producers
-    const int pt = tid - kSoftmaxThreads, chunk = pt % CPR, rr = pt / CPR;
+    const int pw = warp - 8, chunk = lane % CPR, sub = lane / CPR;
     const uint32_t kv0 = smem_u32(sm_kv);
     int slot = 0, tile_seq = 0;
-    unsigned holes = 0;  // entries of ct.hole that this thread left set
+    unsigned holes = 0;  // entries of ct.hole that this warp left set
     uint32_t phase = 1;  // the slots start empty
     bool ok = true;
     for (int seq = 0; ok && wk.more(); wk.next(a)) {
       if (wk.q.n * G <= member * Sh::MG) continue;
       const int len = wk.q.ctx + wk.q.n;
       const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-      const long long head_at = wk.h * a.cache.head_stride + chunk * 8;
+      const long long head_at = wk.h * a.cache.head_stride;
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
-        long long at[PASSES];
-        unsigned hole = 0;
+        // a lane looks up one row in 32; -1: nothing there
+        long long at[RW / 32];
+        unsigned any = 0, hole[RW / 32];
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-          const int pos = t * KT + i * RPP + rr;
-          at[i] = -1;
+        for (int j = 0; j < RW / 32; ++j) {
+          const int pos = t * KT + pw * RW + 32 * j + lane;
+          at[j] = -1;
           if (pos < len) {
             const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
             const int page = __ldg(table + col);
             if (page >= 0 && page < a.cache.n_pages)
-              at[i] = page * a.cache.page_stride + (pos - col * a.cache.page_size) * a.cache.slot_stride + head_at;
-            else
-              hole |= 1u << i;
+              at[j] = page * a.cache.page_stride + (pos - col * a.cache.page_size) * a.cache.slot_stride + head_at;
           }
+          hole[j] = __ballot_sync(0xffffffffu, pos < len && at[j] < 0);
+          any |= hole[j];
         }
-        if (hole) flags |= MOE_DEV_INDEX;
-        const bool noted = chunk == 0 && (hole != 0 || (holes >> (tile_seq & 7) & 1));
+        if (any) flags |= MOE_DEV_INDEX;
+        const int entry = tile_seq & 7;
+        const bool noted = lane == 0 && (any != 0 || (holes >> entry & 1));
         if (noted) {
-          ct.hole[tile_seq & 7][rr] = (unsigned short)hole;
-          holes = (holes & ~(1u << (tile_seq & 7))) | (hole ? 1u << (tile_seq & 7) : 0u);
-        }
 #pragma unroll
+          for (int j = 0; j < RW / 32; ++j) ct.hole[entry][pw * (RW / 32) + j] = hole[j];
+        }
+        holes = (holes & ~(1u << entry)) | (any ? 1u << entry : 0u);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          if (!(ok = ok && bar_wait(&ct.empty[slot], phase, ct, a.dev_status))) break;
-          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.cache.v : a.cache.k);
+          ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
+          if (!ok) break;
+          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.cache.v : a.cache.k) + chunk * 8;
           const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 3) * kBlk;
 #pragma unroll
-          for (int i = 0; i < PASSES; ++i) {
-            const int r = i * RPP + rr;
-            copy16(dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src + max(at[i], 0ll), at[i] >= 0);
+          for (int i = 0; i < RW / RPI; ++i) {
+            const int rl = i * RPI + sub, r = pw * RW + rl;
+            const long long from = __shfl_sync(0xffffffffu, at[i * RPI / 32], rl & 31);
+            copy16(dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src + max(from, 0ll), from >= 0);
           }
           const bool drafted = kv == 1 && (t + 1) * KT > wk.q.ctx;
           if (drafted) {
@@ -464,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // looks over what it copied itself)
             asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-            for (int i = 0; i < PASSES; ++i) {
-              const int r = i * RPP + rr, node = t * KT + r - wk.q.ctx;
+            for (int i = 0; i < RW / RPI; ++i) {
+              const int r = pw * RW + i * RPI + sub, node = t * KT + r - wk.q.ctx;
               if (node < 0 || node >= wk.q.n) continue;
               uint4* v = reinterpret_cast<uint4*>(sm_kv + (size_t)slot * Sh::kSlot + (chunk >> 3) * kBlk + r * 128 +
                                                   (((chunk & 7) ^ (r & 7)) << 4));
@@ -489,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 atomicOr(&ct.bad[seq & 7], 1ull << node);
               }
             }
+            __syncwarp();
           }
           if (drafted || (kv == 0 && noted)) {
             // what this thread wrote itself goes ahead of its arrival
@@ -498,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&ct.full[slot])) : "memory");
           }
+          __syncwarp();
           if (++slot == p.nslot) {
             slot = 0;
             phase ^= 1;
@@ -507,15 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++seq;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 12) {
+  } else if (warp >= 10) {
     // ---------------- issue of the products
-    if (lane == 0) {
+    if (warp == 10 && lane == 0) {
       constexpr uint32_t id_s = instruction<DT>(KT, false), id_o = instruction<DT>(D, true);
-      const uint32_t kv0 = smem_u32(sm_kv), q0 = smem_u32(sm_q);
+      const uint64_t kv0 = operand(smem_u32(sm_kv), kBlk), q0 = operand(smem_u32(sm_q), 0);
       int k_slot = 0, v_slot = 1;       // slots of the next key and value tile
-      uint32_t k_ph = 0, v_ph = 0;
-      uint32_t p_par = 0;
-      uint32_t q_ph = 0;
+      uint32_t k_ph = 0, v_ph = 0, p_par = 0, q_ph = 0;
       bool ok = true;
       const auto take = [&](int& s, uint32_t& ph) {  // key and value tiles take turns in the ring
         s += 2;
@@ -524,34 +567,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       };
-      const auto scores = [&](int s, int qt, int slot) {  // S_s = Q_qt K^T
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t qa = operand(q0 + qt * Sh::kQ + (k >> 2) * (128 * 128) + (k & 3) * 32, 0);
-          const uint64_t kb = operand(kv0 + slot * Sh::kSlot + (k >> 2) * kBlk + (k & 3) * 32, 0);
-          mma_ss(tmem + Sh::s_col(s), qa, kb, id_s, k > 0);
-        }
-        mma_commit(&ct.s_full[s]);
-      };
-      const auto values = [&](int s, int slot, bool first) {  // O += P_s V
-        const int o = NS == 2 ? s : 0;
-#pragma unroll
-        for (int k = 0; k < KT / 16; ++k) {
-          const uint64_t vb = operand(kv0 + slot * Sh::kSlot + k * 2048, kBlk);
-          mma_ts(tmem + Sh::o_col(o), tmem + Sh::s_col(s) + k * 8, vb, id_o, !(first && k == 0));
-        }
-        mma_commit(&ct.o_done[o]);
-      };
-      const auto wait_p = [&](int s) {
-        if (!bar_wait(&ct.p_full[s], p_par >> s & 1, ct, a.dev_status)) return false;
-        p_par ^= 1u << s;
+      const auto wait_p = [&](int buf) {
+        if (!bar_wait(&ct.p_full[buf], p_par >> buf & 1, ct, a.dev_status)) return false;
+        p_par ^= 1u << buf;
         fence_after();
+        return true;
+      };
+      // (addresses in descriptors are in units of 16 bytes)
+      const auto scores = [&](int buf, int qt) {  // S_buf = Q_qt K^T
+        const uint64_t qa = q0 + qt * (Sh::kQ >> 4), kb = kv0 + k_slot * (Sh::kSlot >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + Sh::s_col(buf), qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2,
+                 kb + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, id_s, k > 0);
+        mma_commit(&ct.s_full[buf]);
+      };
+      const auto values = [&](int buf, int s, bool first) {  // O_s += P_buf V, as the parts come, the last keys first
+        const uint64_t vb = kv0 + v_slot * (Sh::kSlot >> 4);
+#pragma unroll
+        for (int part = Sh::PARTS - 1; part >= 0; --part) {
+          if (!wait_p(2 * buf + part)) return false;
+#pragma unroll
+          for (int k = 4 * part; k < 4 * part + 4; ++k)
+            mma_ts(tmem + Sh::o_col(s), tmem + Sh::p_col(buf) + k * 8, vb + k * (2048 >> 4), id_o,
+                   !(first && k == 4 * (Sh::PARTS - 1)));
+        }
+        mma_commit(&ct.o_done[s]);
         return true;
       };
       const auto wait_tile = [&](int slot, uint32_t ph) {
         if (!bar_wait(&ct.full[slot], ph, ct, a.dev_status)) return false;
         fence_async();  // the copies were ordinary writes: order them before the tensor cores' reads
         return true;
+      };
+      const auto free_tile = [&](int& slot, uint32_t& ph) {
+        mma_commit(&ct.empty[slot]);
+        take(slot, ph);
       };
       for (; ok && wk.more(); wk.next(a)) {
         const int rows = min(Sh::MG, wk.q.n * G - member * Sh::MG);
@@ -562,44 +613,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         const int nt = wk.t1 - wk.t0;
         if (two) {
+          // both streams, tile after tile
           for (int t = 0; ok && t <= nt; ++t) {
-            for (int s = 0; ok && s < 2; ++s) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
               if (t > 0) {
-                ok = wait_p(s) && (s == 1 || wait_tile(v_slot, v_ph));
+                ok = (s == 1 || wait_tile(v_slot, v_ph)) && values(s, s, t == 1);
                 if (!ok) break;
-                values(s, v_slot, t == 1);
-                if (s == 1) {
-                  mma_commit(&ct.empty[v_slot]);
-                  take(v_slot, v_ph);
-                }
+                if (s == 1) free_tile(v_slot, v_ph);
               }
               if (t < nt) {
-                ok = s == 1 || wait_tile(k_slot, k_ph);
-                if (!ok) break;
-                scores(s, s, k_slot);
-                if (s == 1) {
-                  mma_commit(&ct.empty[k_slot]);
-                  take(k_slot, k_ph);
-                }
+                if (s == 0 && !(ok = wait_tile(k_slot, k_ph))) break;
+                scores(s, s);
+                if (s == 1) free_tile(k_slot, k_ph);
               }
             }
           }
         } else {
+          // tiles take turns between the streams (or the score buffers of one)
           for (int t = 0; ok && t <= nt; ++t) {
             if (t < nt) {
-              ok = wait_tile(k_slot, k_ph);
-              if (!ok) break;
-              scores(t & 1, 0, k_slot);
-              mma_commit(&ct.empty[k_slot]);
-              take(k_slot, k_ph);
+              if (!(ok = wait_tile(k_slot, k_ph))) break;
+              scores(t & 1, 0);
+              free_tile(k_slot, k_ph);
             }
             if (t > 0) {
-              const int s = (t - 1) & 1;
-              ok = wait_p(s) && wait_tile(v_slot, v_ph);
+              ok = wait_tile(v_slot, v_ph) && values((t - 1) & 1, NS == 2 ? (t - 1) & 1 : 0, t <= NS);
               if (!ok) break;
-              values(s, v_slot, t <= NS);  // the stream's first
-              mma_commit(&ct.empty[v_slot]);
-              take(v_slot, v_ph);
+              free_tile(v_slot, v_ph);
             }
           }
         }
@@ -607,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(&ct.drain);  // nothing runs on when the block ends
       bar_wait(&ct.drain, 0, ct, a.dev_status);
     }
-  } else if (warp < 8) {
+  } else {
     // ---------------- softmax
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes of tensor memory
@@ -620,19 +661,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = member * Sh::MG, rows = min(Sh::MG, wk.q.n * G - m0);
       if (rows <= 0) continue;
       const bool two = NS == 2 && rows > 128;
-      // the group's queries into the swizzle
+      // the group's queries into the swizzle (a rolled loop: it runs once a unit, and its
+      // instructions have to come from memory the first time)
+      const auto q_at = [&](int i) {
+        const int r = i / CPR, ch = i % CPR;
+        return q0 + (r >> 7) * Sh::kQ + (ch >> 3) * (128 * 128) + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+      };
+#pragma unroll 1
       for (int i = tid; i < rows * CPR; i += kSoftmaxThreads) {
-        const int r = i / CPR, ch = i % CPR, mi = m0 + r, n = mi / G, g = mi - n * G;
-        uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (long long)(wk.q.s + n) * a.q_stride +
-                                                       (long long)(wk.h * G + g) * D) + ch);
-        if (p.flip) {
-          x.x ^= 0x80008000u;
-          x.y ^= 0x80008000u;
-          x.z ^= 0x80008000u;
-          x.w ^= 0x80008000u;
+        const int mi = m0 + i / CPR, n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, g = mi - n * G;
+        copy16(q_at(i), static_cast<const uint16_t*>(a.q) + (long long)(wk.q.s + n) * a.q_stride + (wk.h * G + g) * D + i % CPR * 8,
+               true);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (p.flip) {
+#pragma unroll 1
+        for (int i = tid; i < rows * CPR; i += kSoftmaxThreads) {
+          uint4* x = reinterpret_cast<uint4*>(smem + (q_at(i) - q0));
+          *x = p.flip == 2 ? make_uint4(0, 0, 0, 0)
+                           : make_uint4(x->x ^ 0x80008000u, x->y ^ 0x80008000u, x->z ^ 0x80008000u, x->w ^ 0x80008000u);
         }
-        const uint32_t dst = q0 + (r >> 7) * Sh::kQ + (ch >> 3) * (128 * 128) + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
       }
       fence_async();
       fence_before();
@@ -643,79 +691,91 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = (two ? wg * 128 : 0) + (warp & 3) * 32 < rows;  // any row of this warp
       uint64_t tree = 0;  // rows of the request that this one sees
       if (mr < rows) {
-        const int i = (m0 + mr) / G;
+        const int mi = m0 + mr, i = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi;
         tree = a.tree_mask ? __ldg(a.tree_mask + wk.q.s + i) : i >= 63 ? ~0ull : (2ull << i) - 1;
       }
       const int len = wk.q.ctx + wk.q.n, nt = wk.t1 - wk.t0;
       float m = -INFINITY, l = 0.f;
       const bool mine_all = two || NS == 1;
+      const int o = NS == 2 ? wg : 0;  // this warpgroup's stream
       if (NS == 2 || wg == 0) {
-        for (int ti = mine_all ? 0 : wg; ti < nt; ti += mine_all ? 1 : 2) {
-          const int buf = NS == 2 ? wg : ti & 1, o = NS == 2 ? wg : 0;
+        const int step = mine_all ? 1 : 2, ti0 = mine_all ? 0 : wg;
+        for (int ti = ti0; ok && ti < nt; ti += step) {
+          const int buf = NS == 2 ? wg : ti & 1;
           ok = __all_sync(0xffffffffu, bar_wait(&ct.s_full[buf], s_par >> buf & 1, ct, a.dev_status));
           if (!ok) break;
           s_par ^= 1u << buf;
           fence_after();
+          const auto hand_over = [&](int part) {
+            if (live) tm_wait_store();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ct.p_full[2 * buf + part]);
+          };
+          // The scores' barrier covers the stream's products up to this tile, except with one
+          // stream, where the last one may still run: waited for here it is never two behind.
+          const auto last_product = [&]() {
+            if (NS == 1 && o_cnt > 0) {
+              ok = __all_sync(0xffffffffu, bar_wait(&ct.o_done[0], (o_cnt - 1) & 1, ct, a.dev_status));
+              if (ok) fence_after();
+            }
+            return ok;
+          };
           if (live) {
-            const uint32_t s_at = lanes + Sh::s_col(buf);
             const int base = (wk.t0 + ti) * KT;
             // which of the tile's keys this row sees, unless it is all
-            unsigned seen[KT / 32];
-            bool all = base + KT <= wk.q.ctx;
-            const unsigned short* hole = ct.hole[(tile_seq + ti) & 7];
-            bool holes = false;
-#pragma unroll
-            for (int r = 0; r < RPP; r += 2) holes |= *reinterpret_cast<const volatile unsigned*>(hole + r) != 0;
-            all = all && !holes;
-            if (!all) {
-              const int d = wk.q.ctx - base;  // context keys of the tile
-#pragma unroll
-              for (int w = 0; w < KT / 32; ++w) {
-                const int k = d - 32 * w;  // context keys of the word
-                unsigned bits = k >= 32 ? 0xffffffffu : k > 0 ? (1u << k) - 1 : 0u;
-                if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
-                const int v = len - base - 32 * w;  // positions of the word
-                seen[w] = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
-              }
-              if (holes) {
-#pragma unroll
-                for (int w = 0; w < KT / 32; ++w)
-                  for (int j = 0; j < 32; ++j) {
-                    const int r = 32 * w + j;
-                    if (hole[r % RPP] >> (r / RPP) & 1) seen[w] &= ~(1u << j);
-                  }
-              }
-            }
-            // S lies in registers a quarter at a time: once for the maximum, once for the weights
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < KT / 32; ++w) {
-              uint32_t x[32];
-              tm_load(x, s_at + 32 * w);
+            const uint4 hole = *reinterpret_cast<const uint4*>(ct.hole[(tile_seq + ti) & 7]);
+            const bool holes = (hole.x | hole.y | hole.z | hole.w) != 0, all = base + KT <= wk.q.ctx && !holes;
+            const auto seen = [&](int w) {  // of keys 32 w .. 32 w + 31
+              const int k = wk.q.ctx - base - 32 * w;  // context keys of the word
+              unsigned bits = k >= 32 ? 0xffffffffu : k > 0 ? (1u << k) - 1 : 0u;
+              if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
+              const int v = len - base - 32 * w;  // positions of the word
+              bits = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
+              return bits & ~(w == 0 ? hole.x : w == 1 ? hole.y : w == 2 ? hole.z : hole.w);
+            };
+            // 64 scores of a row in registers at a time: a pass for the maximum, a pass for the
+            // weights, the last keys first (their place is the one that is read already).  The
+            // halves are rolled loops and the mask a branch inside: this code is fetched anew by
+            // every launch, and its length shows in the short ones.
+            uint32_t x[64];
+            const auto fetch = [&](int half) {
+              const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
+              tm_load(x, at);
+              tm_load(x + 32, at + 32);
+              tm_wait();
+              ready(x);
+              ready(x + 32);
               if (!all) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(seen[w] >> j & 1)) x[j] = 0xff800000u;
-              }
+                for (int w = 0; w < 2; ++w) {
+                  const unsigned bits = seen(2 * half + w);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(x[j]));
+                  for (int j = 0; j < 32; ++j)
+                    if (!(bits >> j & 1)) x[32 * w + j] = 0xff800000u;
+                }
+              }
+            };
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int half = 0; half < Sh::PARTS; ++half) {
+              fetch(half);
+#pragma unroll
+              for (int j = 0; j < 64; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
             }
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             const bool far = m == -INFINITY ? top > -INFINITY : (top - m) * c > kRescale;
             if (__any_sync(0xffffffffu, far)) {
               const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : exp2_fast((m - to) * c);
-              if (ti >= (mine_all ? 1 : 2)) {
-                if (NS == 1) {  // (two streams: the scores' barrier covers the product before)
-                  ok = __all_sync(0xffffffffu, bar_wait(&ct.o_done[0], (o_cnt - 1) & 1, ct, a.dev_status));
-                  if (!ok) break;
-                  fence_after();
-                }
+              if (ti > ti0) {  // O holds something
+                if (!last_product()) break;
 #pragma unroll 1
                 for (int w = 0; w < D / 32; ++w) {
-                  uint32_t x[32];
-                  tm_load(x, lanes + Sh::o_col(o) + 32 * w);
+                  uint32_t y[32];
+                  tm_read(y, lanes + Sh::o_col(o) + 32 * w);
 #pragma unroll
-                  for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                  tm_store32(lanes + Sh::o_col(o) + 32 * w, x);
+                  for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                  tm_store32(lanes + Sh::o_col(o) + 32 * w, y);
                 }
                 tm_wait_store();
               }
@@ -723,45 +783,44 @@ __global__ void __launch_bounds__(kThreads, 1)
               m = to;
             }
             const float shift = m == -INFINITY ? 0.f : m * c;
+            const Pair c2 = pair(c, c), shift2 = pair(-shift, -shift);
+            Pair sums[2] = {0, 0};
+#pragma unroll 1
+            for (int half = Sh::PARTS - 1; half >= 0; --half) {
+              if (Sh::PARTS > 1) fetch(half);  // (one part: still there)
 #pragma unroll
-            for (int w = 0; w < KT / 32; ++w) {
-              uint32_t x[32], y[16];
-              tm_load(x, s_at + 32 * w);
+              for (int w = 0; w < 2; ++w) {
+                uint32_t y[16];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), c, -shift));
-              if (!all) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(seen[w] >> j & 1)) x[j] = 0xff800000u;
+                for (int j = 0; j < 16; ++j) {
+                  const int k = 32 * w + 2 * j;
+                  const float2 z = split(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, shift2));
+                  const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                  sums[j & 1] = add2(sums[j & 1], pair(e0, e1));
+                  y[j] = pack2<DT>(e0, e1);
+                }
+                tm_store16(lanes + Sh::p_col(buf) + 32 * half + 16 * w, y);
               }
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float e0 = exp2_fast(__uint_as_float(x[2 * j])), e1 = exp2_fast(__uint_as_float(x[2 * j + 1]));
-                l += e0 + e1;
-                y[j] = pack2<DT>(e0, e1);
-              }
-              tm_store16(s_at + 16 * w, y);  // over the quarter's own and earlier columns
+              if (half == 1) hand_over(1);
             }
-            tm_wait_store();
+            const float2 sum = split(add2(sums[0], sums[1]));
+            l += sum.x + sum.y;
+          } else if (KT == 128) {
+            hand_over(1);
           }
-          if (NS == 1 && o_cnt > 0) {  // keeps this warp within a phase of the barrier
-            ok = __all_sync(0xffffffffu, bar_wait(&ct.o_done[0], (o_cnt - 1) & 1, ct, a.dev_status));
-            if (!ok) break;
-          }
+          if (!last_product()) break;
           ++o_cnt;
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&ct.p_full[buf]);
+          hand_over(0);
         }
       }
       tile_seq += nt;
       // every product of the unit is done when the last of each stream is
       const bool used = NS == 1 ? wg == 0 : two || nt > wg;
       if (ok && used)
-        ok = __all_sync(0xffffffffu, bar_wait(&ct.o_done[NS == 2 ? wg : 0], (o_cnt - 1) & 1, ct, a.dev_status));
+        ok = __all_sync(0xffffffffu, bar_wait(&ct.o_done[o], (o_cnt - 1) & 1, ct, a.dev_status));
       fence_after();
       if (!two && ok && (NS == 2 || wg == 0)) {  // maxima and sums change hands where the scores were
-        tm_store2(lanes + Sh::s_col(NS == 2 ? wg : 0), m, l);
+        tm_store2(lanes + Sh::o_col(o) - 128, m, l);
         tm_wait_store();
       }
       fence_before();
@@ -773,8 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float f0 = 1.f, f1 = 0.f;
       bool add = false;
       if (!two) {
-        const float2 x = tm_load2(lanes + Sh::s_col(0));
-        const float2 y = NS == 2 ? tm_load2(lanes + Sh::s_col(1)) : make_float2(-INFINITY, 0.f);
+        const float2 x = tm_load2(lanes + Sh::o_col(0) - 128);
+        const float2 y = NS == 2 ? tm_load2(lanes + Sh::o_col(1) - 128) : make_float2(-INFINITY, 0.f);
         add = NS == 2 && nt > 1;
         m = fmaxf(x.x, y.x);
         f0 = x.x == -INFINITY ? 1.f : exp2_fast((x.x - m) * c);  // nothing seen: sums of zeros, or NaN that has to stay
@@ -785,154 +844,186 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned long long bad = *(volatile unsigned long long*)&ct.bad[seq & 7];
       if (live) {
         const int c0 = two ? 0 : wg * (D / 2), c1 = two ? D : c0 + D / 2;
-        const int part = wk.w == w0 ? 0 : 1;
-        const long long slot = ((long long)blockIdx.x * 2 + part) * p.part_rows + mr;
-        const int mi = m0 + mr, i = mi / G, head = wk.h * G + mi - i * G;
+        const int part = wk.left == ct.w1 - ct.w0 ? 0 : 1;
+        const long long slot = (long long)blockIdx.x * 2 + part;
+        const int mi = m0 + mr, i = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = wk.h * G + mi - i * G;
         const long long orow = wk.q.s + i;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        for (int col = c0; col < c1; col += 32) {
+        uint16_t* out = static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D;
+        float4* to = p.part + slot * (D / 4) * p.part_rows + mr;
+        const unsigned long long own_bad = mr < rows ? bad & tree : 0;
+        if (whole && !two) f0 *= inv, f1 *= inv;  // (rows of two tiles: f0 is 1)
+        if (whole && two) f0 = inv;
+#pragma unroll 1
+        for (int col = c0; col < c1; col += 8) {
           __syncwarp();
-          uint32_t x[32];
-          tm_load(x, lanes + Sh::o_col(two ? wg : 0) + col);
-          if (!two) {
+          float x[8];
+          tm_read8(x, lanes + Sh::o_col(two ? wg : 0) + col);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f0);
-            if (add) {
-              uint32_t y[32];
-              tm_load(y, lanes + Sh::o_col(1 % NS) + col);
+          for (int j = 0; j < 8; ++j) x[j] *= f0;
+          if (add) {
+            float y[8];
+            tm_read8(y, lanes + Sh::o_col(1 % NS) + col);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), f1, __uint_as_float(x[j])));
-            }
+            for (int j = 0; j < 8; ++j) x[j] = fmaf(y[j], f1, x[j]);
           }
-          if (mr >= rows) continue;
-          if (bad & tree) {
+          if (own_bad) {
+#pragma unroll 1
             for (int nd = 0; nd < kTree; ++nd) {
-              if (!((bad & tree) >> nd & 1)) continue;
+              if (!(own_bad >> nd & 1)) continue;
               const int pos = wk.q.ctx + nd, pc = pos / a.cache.page_size;
               const int page = __ldg(a.block_table + (long long)wk.b * a.table_width + pc);
               const uint32_t* v = reinterpret_cast<const uint32_t*>(
                   static_cast<const uint16_t*>(a.cache.v) + page * a.cache.page_stride +
                   (pos - pc * a.cache.page_size) * a.cache.slot_stride + wk.h * a.cache.head_stride + col);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 4; ++j) {
                 const float2 e = unpack2<DT>(v[j]);
-                if (!(fabsf(e.x) < INFINITY)) x[2 * j] = __float_as_uint(__uint_as_float(x[2 * j]) + e.x);
-                if (!(fabsf(e.y) < INFINITY)) x[2 * j + 1] = __float_as_uint(__uint_as_float(x[2 * j + 1]) + e.y);
+                if (!(fabsf(e.x) < INFINITY)) x[2 * j] += e.x;
+                if (!(fabsf(e.y) < INFINITY)) x[2 * j + 1] += e.y;
               }
             }
           }
-          if (whole) {
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D + col);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                w[q] = pack2<DT>(__uint_as_float(x[8 * j + 2 * q]) * inv, __uint_as_float(x[8 * j + 2 * q + 1]) * inv);
-              o[j] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (mr < rows) {
+            if (whole) {
+              *reinterpret_cast<uint4*>(out + col) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
+                                                                pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+            } else {
+              __stcg(to + (col / 4) * p.part_rows, make_float4(x[0], x[1], x[2], x[3]));
+              __stcg(to + (col / 4 + 1) * p.part_rows, make_float4(x[4], x[5], x[6], x[7]));
             }
-          } else {
-            float4* o = reinterpret_cast<float4*>(p.part + slot * D + col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              __stcg(o + j, make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
-                                        __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])));
           }
         }
         if (mr < rows && c0 == 0) {
-          if (!whole) __stcg(p.part_ml + slot, make_float2(m, l));
+          if (!whole) __stcg(p.part_ml + slot * p.part_rows + mr, make_float4(m, l, 0.f, 0.f));
           else if (a.lse) a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
       }
       if (!whole) {
-        __threadfence();
-        named_sync(1, kSoftmaxThreads);
+        named_sync(1, kSoftmaxThreads);  // one fence covers what the block wrote before it
         if (tid == 0) {
-          const int first = gang_of(total, gangs, wk.w - wk.t0);
+          const int first = gang_of(ct.total, ct.gangs, ct.w1 - wk.left - wk.t0);
           __threadfence();
-          atomicAdd(p.arrive + first * groups + member, 1u);
+          atomicAdd(p.arrive + first * ct.groups + member, 1u);
         }
       }
       ++seq;
     }
+    // ---------------- heads that are split over blocks: each of these joins some rows
+    if (ok) {
+      const int total = ct.total;
+      const int gangs = ct.gangs, groups = ct.groups, gang = ct.gang;
+      // the share's first and last unit (the same one, maybe)
+      Walk<D> jk;
+      jk.begin(a, ct.start_b, ct.start_off, ct.w1 - ct.w0);
+      for (; jk.more(); jk.next(a)) {
+        if (jk.t0 == 0 && jk.t1 == jk.q.tiles) continue;
+        const int m0 = member * Sh::MG, rows = min(Sh::MG, jk.q.n * G - m0);
+        if (rows <= 0) continue;
+        const int u0 = ct.w1 - jk.left - jk.t0;
+        const int first = gang_of(total, gangs, u0), last = gang_of(total, gangs, u0 + jk.q.tiles - 1);
+        const int parts = last - first + 1;
+        unsigned* arrive = p.arrive + first * groups + member;
+        if (tid == 0) {
+          const long long t0 = clock64();
+          unsigned v;
+          do {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrive) : "memory");
+            if (clock64() - t0 > kWaitCycles) {
+              atomicOr(a.dev_status, MOE_DEV_TIMEOUT);
+              ct.abort = 1;
+              break;
+            }
+          } while (v < (unsigned)parts);
+        }
+        named_sync(1, kSoftmaxThreads);
+        if (*(volatile int*)&ct.abort) break;  // written before the barrier, if at all
+        // items: four columns of 32 rows (a lane per row); as many warps of a block to an item
+        // as there are to spare, each with every TW-th part
+        const int first_part = share(total, gangs, first) == u0 ? 0 : 1;
+        const int row_blocks = (rows + 31) >> 5, items = row_blocks * (D / 4);
+        int tw = 8;
+        while (tw > 1 && parts * (8 / tw) < items) tw >>= 1;
+        const int teams = 8 / tw, mine_k = warp % tw;
+        float4* sm_acc = reinterpret_cast<float4*>(smem);         // [8][32]
+        float2* sm_ml = reinterpret_cast<float2*>(smem + 8 * 32 * 16);
+        float4* sm_in = reinterpret_cast<float4*>(smem + 8 * 32 * 24);           // [8][12][32]
+        float4* sm_in_ml = reinterpret_cast<float4*>(smem + 8 * 32 * (24 + 12 * 16));  // [8][12][32]
+        for (int it0 = (gang - first) * teams; it0 < items; it0 += parts * teams) {
+          const int it = it0 + warp / tw, rb = it % row_blocks, c4 = it / row_blocks, r = rb * 32 + lane;
+          const bool here = it < items && r < rows;
+          float top = -INFINITY, l = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          const auto join = [&](float2 ml, float4 v) {
+            const float to = fmaxf(top, ml.x);
+            const float f = top == -INFINITY ? 1.f : exp2_fast((top - to) * p.c);  // (nothing so far: zeros, or NaN)
+            const float g = ml.x == -INFINITY ? 1.f : exp2_fast((ml.x - to) * p.c);
+            top = to;
+            l = fmaf(l, f, ml.y * g);
+            acc = make_float4(fmaf(acc.x, f, v.x * g), fmaf(acc.y, f, v.y * g), fmaf(acc.z, f, v.z * g),
+                              fmaf(acc.w, f, v.w * g));
+          };
+          // a lane's parts come through shared memory, all in flight: the loops stay short
+          constexpr int kAhead = 12;
+          float4* in = sm_in + (warp * kAhead) * 32 + lane;
+          float4* in_ml = sm_in_ml + (warp * kAhead) * 32 + lane;
+#pragma unroll 1
+          for (int k0 = mine_k; k0 < parts && here; k0 += tw * kAhead) {
+            int n = 0;
+#pragma unroll 1
+            for (int k = k0; k < parts && n < kAhead; k += tw, ++n) {
+              const long long slot = (long long)((first + k) * groups + member) * 2 + (k ? 0 : first_part);
+              copy16(smem_u32(in + n * 32), p.part + (slot * (D / 4) + c4) * p.part_rows + r, true);
+              copy16(smem_u32(in_ml + n * 32), p.part_ml + slot * p.part_rows + r, true);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) join(make_float2(in_ml[j * 32].x, in_ml[j * 32].y), in[j * 32]);
+          }
+          __syncwarp();
+          if (tw > 1) {
+            named_sync(1, kSoftmaxThreads);
+            sm_acc[warp * 32 + lane] = acc;
+            sm_ml[warp * 32 + lane] = make_float2(top, l);
+            named_sync(1, kSoftmaxThreads);
+            if (mine_k == 0)
+              for (int q = 1; q < tw; ++q) join(sm_ml[(warp + q) * 32 + lane], sm_acc[(warp + q) * 32 + lane]);
+          }
+          if (here && mine_k == 0) {
+            const int mi = m0 + r, i = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = jk.h * G + mi - i * G;
+            const long long orow = jk.q.s + i;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D + 4 * c4) =
+                make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
+            if (c4 == 0 && a.lse)
+              a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (top * p.c + log2f(l)) * 0.6931471805599453f;
+          }
+        }
+        named_sync(1, kSoftmaxThreads);
+        if (tid == 0) {
+          unsigned* done = p.done + first * groups + member;
+          if (atomicAdd(done, 1u) == (unsigned)parts - 1) {  // all have seen the count: ready for the next call
+            *arrive = 0;
+            *done = 0;
+            __threadfence();
+          }
+        }
+      }
+    }
   }
   __syncthreads();
   __syncwarp();
-  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-
-  // ---------------- heads that are split over blocks: each of these joins some rows
-  if (works && !ct.abort) {
-    // the share's first and last unit (the same one, maybe)
-    Walk<D> jk;
-    jk.begin(a, ct.start_b, ct.start_off, w0, w1);
-    for (; jk.more(); jk.next(a)) {
-      if (jk.t0 == 0 && jk.t1 == jk.q.tiles) continue;
-      const int m0 = member * Sh::MG, rows = min(Sh::MG, jk.q.n * G - m0);
-      if (rows <= 0) continue;
-      const long long u0 = jk.w - jk.t0;
-      const int first = gang_of(total, gangs, u0), last = gang_of(total, gangs, u0 + jk.q.tiles - 1);
-      const int parts = last - first + 1;
-      unsigned* arrive = p.arrive + first * groups + member;
-      if (tid == 0) {
-        const long long t0 = clock64();
-        unsigned v;
-        do {
-          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrive) : "memory");
-          if (clock64() - t0 > kWaitCycles) {
-            atomicOr(a.dev_status, MOE_DEV_TIMEOUT);
-            ct.abort = 1;
-            break;
-          }
-        } while (v < (unsigned)parts);
-      }
-      __syncthreads();
-      if (ct.abort) break;
-      const int first_part = share(total, gangs, first) == u0 ? 0 : 1;
-      for (int r = (gang - first) + parts * warp; r < rows; r += parts * (kThreads / 32)) {
-        // lane j: every 32nd part's maximum and sum
-        float top = -INFINITY;
-        for (int k = lane; k < parts; k += 32) {
-          const long long at = ((long long)((first + k) * groups + member) * 2 + (k ? 0 : first_part)) * p.part_rows + r;
-          top = fmaxf(top, __ldcg(p.part_ml + at).x);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int mi = m0 + r, i = mi / G, head = jk.h * G + mi - i * G;
-        const long long orow = jk.q.s + i;
-        constexpr int PER = D / 32;  // columns of a lane
-        float acc[PER], l = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) acc[j] = 0.f;
-#pragma unroll 4
-        for (int k = 0; k < parts; ++k) {
-          const long long at = ((long long)((first + k) * groups + member) * 2 + (k ? 0 : first_part)) * p.part_rows + r;
-          const float2 ml = __ldcg(p.part_ml + at);
-          const float f = ml.x == -INFINITY ? 1.f : exp2_fast((ml.x - top) * p.c);
-          l = fmaf(ml.y, f, l);
-          const float2* o = reinterpret_cast<const float2*>(p.part + at * D + lane * PER);
-#pragma unroll
-          for (int j = 0; j < PER / 2; ++j) {
-            const float2 v = __ldcg(o + j);
-            acc[2 * j] = fmaf(v.x, f, acc[2 * j]);
-            acc[2 * j + 1] = fmaf(v.y, f, acc[2 * j + 1]);
-          }
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D) +
-                        lane * (PER / 2);
-#pragma unroll
-        for (int j = 0; j < PER / 2; ++j) out[j] = pack2<DT>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
-        if (lane == 0 && a.lse) a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (top * p.c + log2f(l)) * 0.6931471805599453f;
-      }
-      __syncthreads();
-      if (tid == 0) {
-        unsigned* done = p.done + first * groups + member;
-        if (atomicAdd(done, 1u) == (unsigned)parts - 1) {  // all have seen the count: ready for the next call
-          *arrive = 0;
-          *done = 0;
-          __threadfence();
-        }
-      }
+  if (warp == 10) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  // requests that are left out: their rows, where they are rows at all, get nothing seen
+  for (int b = (int)blockIdx.x * kThreads + tid; b < a.n_req; b += (int)gridDim.x * kThreads) {
+    const Req q = request<D>(a, b);
+    if (q.n == 0 || q.tiles) continue;
+    flags |= MOE_DEV_LENGTH;
+    for (int r = q.s; r < q.s + q.n; ++r) {
+      uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (long long)r * a.out_stride);
+      for (int i = 0; i < a.q_heads * CPR; ++i) to[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int i = 0; i < a.q_heads; ++i) a.lse[(long long)r * a.q_heads + i] = -INFINITY;
     }
   }
   if (flags) atomicOr(a.dev_status, flags);
@@ -953,6 +1044,9 @@ int check(const moe_tree_attention_args* p) {
     return MOE_EUNSUPPORTED;
   const int rc = check_cache(a.cache);
   if (rc != MOE_OK) return rc;
+  // the list of (request, head, tile) is numbered in 32 bits
+  if (((int64_t)a.table_width * a.cache.page_size / 64 + 1) * a.n_req * a.kv_heads >= ((int64_t)1 << 31))
+    return MOE_EUNSUPPORTED;
   if (!stride_ok(a.q_stride) || !stride_ok(a.out_stride)) return MOE_EINVAL;
   if (!ptr_ok(a.dev_status, 4) || !ptr_ok(a.row_start, 4) || !ptr_ok(a.ctx_len, 4) || !ptr_ok(a.block_table, 4) ||
       !opt_ok(a.lse, 4) || !opt_ok(a.tree_mask, 8))
@@ -965,7 +1059,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int group_rows(const moe_tree_attention_args& a) {  // query rows of a group, as the workspace holds them
   const int rows = a.max_tree * (a.q_heads / a.kv_heads), most = a.head_dim == 256 ? 128 : 256;
-  return rows < most ? rows : most;
+  return ((rows < most ? rows : most) + 31) & ~31;
 }
 
 struct Workspace {
@@ -976,7 +1070,7 @@ Workspace layout(const moe_tree_attention_args& a) {
   const size_t rows = (size_t)kMaxBlocks * 2 * group_rows(a);
   w.counters = 0;
   w.ml = up256((size_t)2 * kMaxBlocks * 4);
-  w.part = w.ml + up256(rows * 8);
+  w.part = w.ml + up256(rows * 16);
   w.total = w.part + up256(rows * a.head_dim * 4);
   return w;
 }
@@ -1034,17 +1128,18 @@ extern "C" int moe_tree_attention(const moe_tree_attention_args* args, void* ws,
   Plan p{};
   p.group = a.q_heads / a.kv_heads;
   p.part_rows = group_rows(a);
+  p.group_mul = p.group == 1 ? 0u : (unsigned)((1ull << 32) / (unsigned)p.group + 1);
   // n / page_size = (n * mul) >> shift for every n below 2^31
   int bits = 0;
   while ((1 << bits) < a.cache.page_size) ++bits;
   p.page_shift = 31 + bits;
   p.page_mul = (unsigned)((1ull << p.page_shift) / (unsigned)a.cache.page_size + 1);
-  p.flip = a.scale < 0.f;
-  p.c = std::fabs(a.scale) * 1.4426950408889634f;
+  p.flip = a.scale < 0.f ? 1 : a.scale == 0.f ? 2 : 0;
+  p.c = (a.scale == 0.f ? 1.f : std::fabs(a.scale)) * 1.4426950408889634f;
   p.arrive = reinterpret_cast<unsigned*>(base);
   p.done = p.arrive + kMaxBlocks;
-  p.part_ml = reinterpret_cast<float2*>(base + w.ml);
-  p.part = reinterpret_cast<float*>(base + w.part);
+  p.part_ml = reinterpret_cast<float4*>(base + w.ml);
+  p.part = reinterpret_cast<float4*>(base + w.part);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = a.dtype == MOE_BF16;
   switch (a.head_dim) {
