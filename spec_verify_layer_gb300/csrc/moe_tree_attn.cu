@@ -11,7 +11,7 @@
 // same time, the second out of L2.
 //
 // In a block, four roles meet at mbarriers:
-//   - two producer warps copy key and value rows (cp.async, 16 bytes a lane, page table
+//   - three producer warps copy key and value rows (cp.async, 16 bytes a lane, page table
 //     looked up per row) into a ring of shared-memory slots in the 128-byte swizzle that
 //     the tensor cores read;
 //   - one thread issues the products: S = Q K^T into tensor memory, and O += P V with P
@@ -40,8 +40,8 @@ namespace moe {
 namespace {
 
 constexpr int kTree = 64;
-constexpr int kThreads = 384;  // 8 softmax warps, 2 producer warps, 1 issuing warp, 1 idle: 168 registers a thread
-constexpr int kSoftmaxThreads = 256, kProducers = 64;
+constexpr int kThreads = 384;  // 8 softmax warps, 3 producer warps, 1 issuing warp: 168 registers a thread
+constexpr int kSoftmaxThreads = 256, kProducers = 3;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 constexpr float kRescale = 8.0f;        // log2 of how far a maximum may lag behind
@@ -56,8 +56,8 @@ struct Shape {
   static constexpr int kSlot = KT * D * 2;             // bytes of a key or value tile
   static constexpr int kQ = 128 * D * 2;               // bytes of a query tile
   static constexpr int CPR = D / 8;                    // 16-byte chunks of a row
-  static constexpr int RW = KT / 2;                    // rows of a tile that a producer warp copies
-  static constexpr int RPI = 32 / CPR;                 // of them with one instruction
+  static constexpr int RPI = 32 / CPR;                 // rows that a warp copies with one instruction
+  static constexpr int STEPS = (KT / RPI + kProducers - 1) / kProducers;  // instructions of a producer for a tile
   // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
   // there is one stream); the weights, in 16 bits, go over the second half of their scores.
   __host__ __device__ static constexpr int s_col(int buf) { return NS == 2 ? 256 * buf : 64 * buf; }
@@ -75,21 +75,26 @@ struct Plan {  // host-computed, the same for every block
   int page_shift;
   int flip;    // of the queries: 1 negated (a negative scale), 2 taken as 0 (a scale of 0)
   float c;     // |scale| * log2(e)
-  float4* part;      // [blocks][2][D / 4][part_rows]: a warp's rows side by side
-  float4* part_ml;   // [blocks][2][part_rows]: maximum, sum
+  float4* part;      // [blocks][2: as Control::split][D / 4][part_rows]: a warp's rows side by side
+  float2* part_ml;   // [blocks][2][part_rows]: maximum, sum
   unsigned* arrive;  // [blocks]
   unsigned* done;    // [blocks]
 };
 
-struct Control {  // the start of dynamic shared memory
+struct Split {  // a head that is split over blocks: its request's rows, its first block, how many
+  int s, n, h, first, parts;
+};
+
+struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  __align__(16) unsigned hole[8][4];  // per tile: keys without a page
+  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows
   int red[kThreads / 32], redn[kThreads / 32];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;
   int start_b, gangs, groups, gang, member;
+  Split split[2];  // of the share's units: one that began in a share before, one that goes on in the next
   unsigned tmem;
   int abort;
 };
@@ -343,7 +348,7 @@ template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_tree_attn(const __grid_constant__ moe_tree_attention_args a, const __grid_constant__ Plan p) {
   using Sh = Shape<D>;
-  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, RW = Sh::RW, RPI = Sh::RPI;
+  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, RPI = Sh::RPI;
   constexpr uint32_t kBlk = KT * 128;  // bytes of a 64-element block of a key or value tile
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == 11) {
     if (lane < p.nslot) {
-      bar_init(&ct.full[lane], kProducers);
+      bar_init(&ct.full[lane], 33 * kProducers);  // a warp's copies, and what its first lane wrote
       bar_init(&ct.empty[lane], 1);
     }
     if (lane < 4) bar_init(&ct.p_full[lane], 4);
@@ -376,9 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&ct.q_ready, kSoftmaxThreads / 32);
       bar_init(&ct.drain, 1);
       ct.abort = 0;
+      ct.split[0].parts = ct.split[1].parts = 0;
     }
     if (lane < 8) ct.bad[lane] = 0;
-    (&ct.hole[0][0])[lane] = 0;
+    (&ct.hole[0][0])[lane] = (&ct.hole[0][0])[lane + 32] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const auto scan = [&](int b0, const Req& q) {  // lo: places before request b0 + tid, mine: its own
@@ -451,12 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int member = ct.member;
   wk.begin(a, ct.start_b, ct.start_off, ct.w1 - ct.w0);
 
-  if (warp == 8 || warp == 9) {
-    // ---------------- producers
-    const int pw = warp - 8, chunk = lane % CPR, sub = lane / CPR;
+  if (warp == 8 || warp == 9 || warp == 11) {
+    // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
+    // g = k * kProducers + its number
+    const int pw = warp == 11 ? 2 : warp - 8, chunk = lane % CPR, sub = lane / CPR;
+    constexpr int LOOKS = (Sh::STEPS * RPI + 31) / 32;  // rows of a warp that a lane looks up
+    constexpr uint32_t kNone = 0xffffffffu;
     const uint32_t kv0 = smem_u32(sm_kv);
     int slot = 0, tile_seq = 0;
-    unsigned holes = 0;  // entries of ct.hole that this warp left set
     uint32_t phase = 1;  // the slots start empty
     bool ok = true;
     for (int seq = 0; ok && wk.more(); wk.next(a)) {
@@ -464,52 +472,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int len = wk.q.ctx + wk.q.n;
       const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
       const long long head_at = wk.h * a.cache.head_stride;
+      if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
+        const int at = ct.w1 - wk.left - wk.t0;               // the head's place in the list
+        const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
+        if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
+      }
+      // the table entries of this lane's rows, a tile ahead of their use
+      int page[LOOKS];
+      const auto look = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          const int mine = 32 * j + lane, r = (mine / RPI * kProducers + pw) * RPI + mine % RPI, pos = t * KT + r;
+          page[j] = 0;
+          if (r < KT && pos < len) page[j] = __ldg(table + (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift));
+        }
+      };
+      look(wk.t0);
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
-        // a lane looks up one row in 32; -1: nothing there
-        long long at[RW / 32];
-        unsigned any = 0, hole[RW / 32];
+        uint32_t at[LOOKS];  // places in the cache in units of 16 bytes
+        unsigned hole[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < RW / 32; ++j) {
-          const int pos = t * KT + pw * RW + 32 * j + lane;
-          at[j] = -1;
-          if (pos < len) {
-            const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
-            const int page = __ldg(table + col);
-            if (page >= 0 && page < a.cache.n_pages)
-              at[j] = page * a.cache.page_stride + (pos - col * a.cache.page_size) * a.cache.slot_stride + head_at;
+        for (int j = 0; j < LOOKS; ++j) {
+          const int mine = 32 * j + lane, r = (mine / RPI * kProducers + pw) * RPI + mine % RPI, pos = t * KT + r;
+          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
+          const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
+          at[j] = good ? (uint32_t)((page[j] * a.cache.page_stride + (pos - col * a.cache.page_size) * a.cache.slot_stride +
+                                     head_at) >> 3)
+                       : kNone;
+          hole[j] = __ballot_sync(0xffffffffu, there && !good);
+        }
+        if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
+        if (t + 1 < wk.t1) look(t + 1);
+        const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
+        ok = bar_wait(&ct.empty[slot], phase, ct, a.dev_status) &&
+             bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        {
+          const uint4* k_src = static_cast<const uint4*>(a.cache.k) + chunk;
+          const uint4* v_src = static_cast<const uint4*>(a.cache.v) + chunk;
+          const uint32_t k_dst = kv0 + slot * Sh::kSlot + (chunk >> 3) * kBlk;
+          const uint32_t v_dst = kv0 + v_slot * Sh::kSlot + (chunk >> 3) * kBlk;
+#pragma unroll 11
+          for (int k = 0; k < Sh::STEPS; ++k) {
+            const int g = k * kProducers + pw, r = g * RPI + sub, mine = k * RPI + sub;
+            const uint32_t from = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], mine & 31);
+            const uint32_t to = r * 128 + (((chunk & 7) ^ (r & 7)) << 4), off = from == kNone ? 0 : from;
+            if (g < KT / RPI) {
+              copy16(k_dst + to, k_src + off, from != kNone);
+              copy16(v_dst + to, v_src + off, from != kNone);
+            }
           }
-          hole[j] = __ballot_sync(0xffffffffu, pos < len && at[j] < 0);
-          any |= hole[j];
         }
-        if (any) flags |= MOE_DEV_INDEX;
-        const int entry = tile_seq & 7;
-        const bool noted = lane == 0 && (any != 0 || (holes >> entry & 1));
-        if (noted) {
-#pragma unroll
-          for (int j = 0; j < RW / 32; ++j) ct.hole[entry][pw * (RW / 32) + j] = hole[j];
-        }
-        holes = (holes & ~(1u << entry)) | (any ? 1u << entry : 0u);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
-          if (!ok) break;
-          const uint16_t* src = static_cast<const uint16_t*>(kv ? a.cache.v : a.cache.k) + chunk * 8;
-          const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 3) * kBlk;
-#pragma unroll
-          for (int i = 0; i < RW / RPI; ++i) {
-            const int rl = i * RPI + sub, r = pw * RW + rl;
-            const long long from = __shfl_sync(0xffffffffu, at[i * RPI / 32], rl & 31);
-            copy16(dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4), src + max(from, 0ll), from >= 0);
-          }
-          const bool drafted = kv == 1 && (t + 1) * KT > wk.q.ctx;
-          if (drafted) {
+          const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+          if (kv == 1 && node0 < KT) {
             // drafted rows' values: what is not finite is noted and taken out (a thread
             // looks over what it copied itself)
             asm volatile("cp.async.wait_all;" ::: "memory");
+            const int from = max(node0, 0), to = min(KT, node0 + wk.q.n);
 #pragma unroll 1
-            for (int i = 0; i < RW / RPI; ++i) {
-              const int r = pw * RW + i * RPI + sub, node = t * KT + r - wk.q.ctx;
-              if (node < 0 || node >= wk.q.n) continue;
+            for (int k = max(0, (from / RPI - pw) / kProducers); k < Sh::STEPS; ++k) {
+              const int r = (k * kProducers + pw) * RPI + sub;
+              if (r - sub >= to) break;
+              if (r < from || r >= to) continue;
               uint4* v = reinterpret_cast<uint4*>(sm_kv + (size_t)slot * Sh::kSlot + (chunk >> 3) * kBlk + r * 128 +
                                                   (((chunk & 7) ^ (r & 7)) << 4));
               const uint4 x = *v;
@@ -529,18 +556,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (found) {
                 *v = make_uint4(w[0], w[1], w[2], w[3]);
-                atomicOr(&ct.bad[seq & 7], 1ull << node);
+                atomicOr(&ct.bad[seq & 7], 1ull << (r - node0));
               }
             }
             __syncwarp();
-          }
-          if (drafted || (kv == 0 && noted)) {
-            // what this thread wrote itself goes ahead of its arrival
-            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async();
             bar_arrive(&ct.full[slot]);
           } else {
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&ct.full[slot])) : "memory");
+          }
+          if (lane == 0) {
+            if (kv == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
+            bar_arrive(&ct.full[slot]);  // behind what this lane wrote
           }
           __syncwarp();
           if (++slot == p.nslot) {
@@ -552,9 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++seq;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp >= 10) {
+  } else if (warp == 10) {
     // ---------------- issue of the products
-    if (warp == 10 && lane == 0) {
+    if (lane == 0) {
       constexpr uint32_t id_s = instruction<DT>(KT, false), id_o = instruction<DT>(D, true);
       const uint64_t kv0 = operand(smem_u32(sm_kv), kBlk), q0 = operand(smem_u32(sm_q), 0);
       int k_slot = 0, v_slot = 1;       // slots of the next key and value tile
@@ -724,15 +751,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (live) {
             const int base = (wk.t0 + ti) * KT;
             // which of the tile's keys this row sees, unless it is all
-            const uint4 hole = *reinterpret_cast<const uint4*>(ct.hole[(tile_seq + ti) & 7]);
-            const bool holes = (hole.x | hole.y | hole.z | hole.w) != 0, all = base + KT <= wk.q.ctx && !holes;
+            const unsigned* hole = ct.hole[(tile_seq + ti) & 7];
+            const uint4 hole_a = *reinterpret_cast<const uint4*>(hole);
+            const uint2 hole_b = *reinterpret_cast<const uint2*>(hole + 4);
+            const bool holes = (hole_a.x | hole_a.y | hole_a.z | hole_a.w | hole_b.x | hole_b.y) != 0;
+            const bool all = base + KT <= wk.q.ctx && !holes;
             const auto seen = [&](int w) {  // of keys 32 w .. 32 w + 31
               const int k = wk.q.ctx - base - 32 * w;  // context keys of the word
               unsigned bits = k >= 32 ? 0xffffffffu : k > 0 ? (1u << k) - 1 : 0u;
               if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
               const int v = len - base - 32 * w;  // positions of the word
               bits = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
-              return bits & ~(w == 0 ? hole.x : w == 1 ? hole.y : w == 2 ? hole.z : hole.w);
+              if (holes) {
+#pragma unroll 1
+                for (int j = 0; j < 32; ++j) {
+                  const int r = 32 * w + j, g = r / RPI, q = g / kProducers * RPI + r % RPI;
+                  if (hole[2 * (g % kProducers) + (q >> 5)] >> (q & 31) & 1) bits &= ~(1u << j);
+                }
+              }
+              return bits;
             };
             // 64 scores of a row in registers at a time: a pass for the maximum, a pass for the
             // weights, the last keys first (their place is the one that is read already).  The
@@ -844,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned long long bad = *(volatile unsigned long long*)&ct.bad[seq & 7];
       if (live) {
         const int c0 = two ? 0 : wg * (D / 2), c1 = two ? D : c0 + D / 2;
-        const int part = wk.left == ct.w1 - ct.w0 ? 0 : 1;
+        const int part = wk.t0 == 0;
         const long long slot = (long long)blockIdx.x * 2 + part;
         const int mi = m0 + mr, i = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = wk.h * G + mi - i * G;
         const long long orow = wk.q.s + i;
@@ -895,118 +932,123 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (mr < rows && c0 == 0) {
-          if (!whole) __stcg(p.part_ml + slot * p.part_rows + mr, make_float4(m, l, 0.f, 0.f));
+          if (!whole) __stcg(p.part_ml + slot * p.part_rows + mr, make_float2(m, l));
           else if (a.lse) a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
         }
       }
       if (!whole) {
-        named_sync(1, kSoftmaxThreads);  // one fence covers what the block wrote before it
-        if (tid == 0) {
-          const int first = gang_of(ct.total, ct.gangs, ct.w1 - wk.left - wk.t0);
+        named_sync(1, kSoftmaxThreads);
+        if (tid == 0) {  // one fence covers what the block wrote before the barrier
           __threadfence();
-          atomicAdd(p.arrive + first * ct.groups + member, 1u);
+          atomicAdd(p.arrive + ct.split[wk.t0 == 0].first * ct.groups + member, 1u);
         }
       }
       ++seq;
     }
     // ---------------- heads that are split over blocks: each of these joins some rows
-    if (ok) {
-      const int total = ct.total;
-      const int gangs = ct.gangs, groups = ct.groups, gang = ct.gang;
-      // the share's first and last unit (the same one, maybe)
-      Walk<D> jk;
-      jk.begin(a, ct.start_b, ct.start_off, ct.w1 - ct.w0);
-      for (; jk.more(); jk.next(a)) {
-        if (jk.t0 == 0 && jk.t1 == jk.q.tiles) continue;
-        const int m0 = member * Sh::MG, rows = min(Sh::MG, jk.q.n * G - m0);
-        if (rows <= 0) continue;
-        const int u0 = ct.w1 - jk.left - jk.t0;
-        const int first = gang_of(total, gangs, u0), last = gang_of(total, gangs, u0 + jk.q.tiles - 1);
-        const int parts = last - first + 1;
-        unsigned* arrive = p.arrive + first * groups + member;
-        if (tid == 0) {
-          const long long t0 = clock64();
-          unsigned v;
-          do {
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrive) : "memory");
-            if (clock64() - t0 > kWaitCycles) {
-              atomicOr(a.dev_status, MOE_DEV_TIMEOUT);
-              ct.abort = 1;
-              break;
+#pragma unroll 1
+    for (int which = 0; ok && which < 2; ++which) {
+      const Split sp = ct.split[which];
+      const int m0 = member * Sh::MG, rows = min(Sh::MG, sp.n * G - m0);
+      if (sp.parts == 0 || rows <= 0) continue;
+      unsigned* arrive = p.arrive + sp.first * ct.groups + member;
+      if (tid == 0) {
+        const long long t0 = clock64();
+        unsigned v;
+        do {
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrive) : "memory");
+          if (clock64() - t0 > kWaitCycles) {
+            atomicOr(a.dev_status, MOE_DEV_TIMEOUT);
+            *(volatile int*)&ct.abort = 1;
+            break;
+          }
+        } while (v < (unsigned)sp.parts);
+      }
+      ok = named_all(1, kSoftmaxThreads, !*(volatile int*)&ct.abort || tid != 0);
+      if (!ok) break;
+      // items: four columns of 32 rows, a lane per row; as many warps of a block to an item as
+      // there are to spare, each with every tw-th part
+      const int row_blocks = (rows + 31) >> 5, items = row_blocks * (D / 4);
+      int tw_log = 3;
+      while (tw_log > 0 && sp.parts << (3 - tw_log) < items) --tw_log;
+      const int tw = 1 << tw_log, teams = 8 >> tw_log, mine_k = warp & (tw - 1);
+      const int stride = 2 * ct.groups * (D / 4) * p.part_rows;  // from a block's part to the next one's
+      float4* sm_acc = reinterpret_cast<float4*>(smem);          // [8][32]
+      float2* sm_ml = reinterpret_cast<float2*>(smem + 8 * 32 * 16);
+#pragma unroll 1
+      for (int it0 = (ct.gang - sp.first) * teams; it0 < items; it0 += sp.parts * teams) {
+        const int it = it0 + (warp >> tw_log), c4 = it & (D / 4 - 1), r = it / (D / 4) * 32 + lane;
+        const bool here = it < items && r < rows;
+        float top = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const auto join = [&](float2 ml, float4 v) {
+          const float to = fmaxf(top, ml.x);
+          const float f = top == -INFINITY ? 1.f : exp2_fast((top - to) * p.c);  // (nothing so far: zeros, or NaN)
+          const float g = ml.x == -INFINITY ? 1.f : exp2_fast((ml.x - to) * p.c);
+          top = to;
+          l = fmaf(l, f, ml.y * g);
+          acc = make_float4(fmaf(acc.x, f, v.x * g), fmaf(acc.y, f, v.y * g), fmaf(acc.z, f, v.z * g),
+                            fmaf(acc.w, f, v.w * g));
+        };
+        // the first block's part lies in its second place
+        const int block0 = (sp.first * ct.groups + member) * 2;
+        const float4* from = p.part + ((long long)block0 * (D / 4) + c4) * p.part_rows + r;
+        const float2* from_ml = p.part_ml + (long long)block0 * p.part_rows + r;
+        constexpr int kAhead = 10;
+#pragma unroll 1
+        for (int k0 = mine_k; k0 < sp.parts && here; k0 += tw * kAhead) {
+          float2 ml[kAhead];
+          float4 v[kAhead];
+          int k = k0;
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j, k += tw) {
+            ml[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < sp.parts) {
+              ml[j] = __ldcg(from_ml + (k ? k * (stride / (D / 4)) : p.part_rows));
+              v[j] = __ldcg(from + (k ? k * stride : (D / 4) * p.part_rows));
             }
-          } while (v < (unsigned)parts);
+          }
+          float2 all = ml[0];
+#pragma unroll
+          for (int j = 1; j < kAhead; ++j) all.x = fmaxf(all.x, ml[j].x);
+          all.y = 0.f;
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const float g = ml[j].x == -INFINITY ? 1.f : exp2_fast((ml[j].x - all.x) * p.c);
+            all.y = fmaf(ml[j].y, g, all.y);
+            sum = make_float4(fmaf(v[j].x, g, sum.x), fmaf(v[j].y, g, sum.y), fmaf(v[j].z, g, sum.z),
+                              fmaf(v[j].w, g, sum.w));
+          }
+          join(all, sum);
         }
-        named_sync(1, kSoftmaxThreads);
-        if (*(volatile int*)&ct.abort) break;  // written before the barrier, if at all
-        // items: four columns of 32 rows (a lane per row); as many warps of a block to an item
-        // as there are to spare, each with every TW-th part
-        const int first_part = share(total, gangs, first) == u0 ? 0 : 1;
-        const int row_blocks = (rows + 31) >> 5, items = row_blocks * (D / 4);
-        int tw = 8;
-        while (tw > 1 && parts * (8 / tw) < items) tw >>= 1;
-        const int teams = 8 / tw, mine_k = warp % tw;
-        float4* sm_acc = reinterpret_cast<float4*>(smem);         // [8][32]
-        float2* sm_ml = reinterpret_cast<float2*>(smem + 8 * 32 * 16);
-        float4* sm_in = reinterpret_cast<float4*>(smem + 8 * 32 * 24);           // [8][12][32]
-        float4* sm_in_ml = reinterpret_cast<float4*>(smem + 8 * 32 * (24 + 12 * 16));  // [8][12][32]
-        for (int it0 = (gang - first) * teams; it0 < items; it0 += parts * teams) {
-          const int it = it0 + warp / tw, rb = it % row_blocks, c4 = it / row_blocks, r = rb * 32 + lane;
-          const bool here = it < items && r < rows;
-          float top = -INFINITY, l = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          const auto join = [&](float2 ml, float4 v) {
-            const float to = fmaxf(top, ml.x);
-            const float f = top == -INFINITY ? 1.f : exp2_fast((top - to) * p.c);  // (nothing so far: zeros, or NaN)
-            const float g = ml.x == -INFINITY ? 1.f : exp2_fast((ml.x - to) * p.c);
-            top = to;
-            l = fmaf(l, f, ml.y * g);
-            acc = make_float4(fmaf(acc.x, f, v.x * g), fmaf(acc.y, f, v.y * g), fmaf(acc.z, f, v.z * g),
-                              fmaf(acc.w, f, v.w * g));
-          };
-          // a lane's parts come through shared memory, all in flight: the loops stay short
-          constexpr int kAhead = 12;
-          float4* in = sm_in + (warp * kAhead) * 32 + lane;
-          float4* in_ml = sm_in_ml + (warp * kAhead) * 32 + lane;
+        __syncwarp();
+        if (tw > 1) {
+          named_sync(1, kSoftmaxThreads);
+          sm_acc[warp * 32 + lane] = acc;
+          sm_ml[warp * 32 + lane] = make_float2(top, l);
+          named_sync(1, kSoftmaxThreads);
 #pragma unroll 1
-          for (int k0 = mine_k; k0 < parts && here; k0 += tw * kAhead) {
-            int n = 0;
-#pragma unroll 1
-            for (int k = k0; k < parts && n < kAhead; k += tw, ++n) {
-              const long long slot = (long long)((first + k) * groups + member) * 2 + (k ? 0 : first_part);
-              copy16(smem_u32(in + n * 32), p.part + (slot * (D / 4) + c4) * p.part_rows + r, true);
-              copy16(smem_u32(in_ml + n * 32), p.part_ml + slot * p.part_rows + r, true);
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-            for (int j = 0; j < n; ++j) join(make_float2(in_ml[j * 32].x, in_ml[j * 32].y), in[j * 32]);
-          }
-          __syncwarp();
-          if (tw > 1) {
-            named_sync(1, kSoftmaxThreads);
-            sm_acc[warp * 32 + lane] = acc;
-            sm_ml[warp * 32 + lane] = make_float2(top, l);
-            named_sync(1, kSoftmaxThreads);
-            if (mine_k == 0)
-              for (int q = 1; q < tw; ++q) join(sm_ml[(warp + q) * 32 + lane], sm_acc[(warp + q) * 32 + lane]);
-          }
-          if (here && mine_k == 0) {
-            const int mi = m0 + r, i = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = jk.h * G + mi - i * G;
-            const long long orow = jk.q.s + i;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D + 4 * c4) =
-                make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
-            if (c4 == 0 && a.lse)
-              a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (top * p.c + log2f(l)) * 0.6931471805599453f;
-          }
+          for (int q = 1; q < tw && mine_k == 0; ++q) join(sm_ml[(warp + q) * 32 + lane], sm_acc[(warp + q) * 32 + lane]);
         }
-        named_sync(1, kSoftmaxThreads);
-        if (tid == 0) {
-          unsigned* done = p.done + first * groups + member;
-          if (atomicAdd(done, 1u) == (unsigned)parts - 1) {  // all have seen the count: ready for the next call
-            *arrive = 0;
-            *done = 0;
-            __threadfence();
-          }
+        if (here && mine_k == 0) {
+          const int mi = m0 + r, i = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = sp.h * G + mi - i * G;
+          const long long orow = sp.s + i;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D + 4 * c4) =
+              make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
+          if (c4 == 0 && a.lse)
+            a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (top * p.c + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      named_sync(1, kSoftmaxThreads);
+      if (tid == 0) {
+        unsigned* done = p.done + sp.first * ct.groups + member;
+        if (atomicAdd(done, 1u) == (unsigned)sp.parts - 1) {  // all have seen the count: ready for the next call
+          *arrive = 0;
+          *done = 0;
+          __threadfence();
         }
       }
     }
@@ -1044,6 +1086,10 @@ int check(const moe_tree_attention_args* p) {
     return MOE_EUNSUPPORTED;
   const int rc = check_cache(a.cache);
   if (rc != MOE_OK) return rc;
+  // offsets in the cache travel in units of 16 bytes, in 32 bits
+  if ((a.cache.n_pages - 1) * a.cache.page_stride + (a.cache.page_size - 1) * a.cache.slot_stride +
+          (a.kv_heads - 1) * a.cache.head_stride >= ((int64_t)8 << 32) - 256)
+    return MOE_EUNSUPPORTED;
   // the list of (request, head, tile) is numbered in 32 bits
   if (((int64_t)a.table_width * a.cache.page_size / 64 + 1) * a.n_req * a.kv_heads >= ((int64_t)1 << 31))
     return MOE_EUNSUPPORTED;
@@ -1070,7 +1116,7 @@ Workspace layout(const moe_tree_attention_args& a) {
   const size_t rows = (size_t)kMaxBlocks * 2 * group_rows(a);
   w.counters = 0;
   w.ml = up256((size_t)2 * kMaxBlocks * 4);
-  w.part = w.ml + up256(rows * 16);
+  w.part = w.ml + up256(rows * 8);
   w.total = w.part + up256(rows * a.head_dim * 4);
   return w;
 }
@@ -1138,7 +1184,7 @@ extern "C" int moe_tree_attention(const moe_tree_attention_args* args, void* ws,
   p.c = (a.scale == 0.f ? 1.f : std::fabs(a.scale)) * 1.4426950408889634f;
   p.arrive = reinterpret_cast<unsigned*>(base);
   p.done = p.arrive + kMaxBlocks;
-  p.part_ml = reinterpret_cast<float4*>(base + w.ml);
+  p.part_ml = reinterpret_cast<float2*>(base + w.ml);
   p.part = reinterpret_cast<float4*>(base + w.part);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = a.dtype == MOE_BF16;
