@@ -3,26 +3,34 @@
 //
 // A block takes a slice of one row, a chunk at a time: a thread holds four 16-byte vectors
 // of the chunk in registers and updates its own running maximum m (of the logits), sum
-// s = sum 2^u and w = sum 2^u u with u = (x - m) / T * log2(e); no thread waits for another
-// until the slice ends.  Entropy is ln s - ln 2 * w / s, log probabilities (x - m) / T - ln s.
+// s = sum 2^u and w = sum 2^u u with u = (x - m) / T * log2(e), two elements an instruction;
+// nothing waits for another warp until the slice ends.  Entropy is ln s - ln 2 * w / s, log
+// probabilities (x - m) / T - ln s.
 //
-// Top entries: 64-bit keys (logit order, ~id) make the order total.  A chunk's entries that
-// may be among the first k are those at or above the k-th largest of 32 group maxima (each
-// of 16 threads), and above the k-th so far; they are few (about 30 of 16384 for k = 20),
-// go to shared memory, and each finds its place by counting the larger ones.
+// Top entries: 64-bit keys (logit order, ~id) make the order total; a block keeps its first k
+// in shared memory.  Of the first chunk it takes what is not below a bound that k entries
+// are known to reach (from the threads' maxima); from then on an entry only counts if it is
+// above the k-th, which few are (k of each doubling of what was seen), so threads append
+// such entries to a buffer and the block merges it in after 1, 2, 4, 8 ... chunks, each
+// entry counting the larger ones for its place.  A buffer that runs over (rising logits) has
+// its chunks gone through again, one maximum after the other.  The lists of slices are
+// joined alike: their first entries give the bound.
 //
 // With few rows a row is cut into 2^i slices, up to 32; the block that ends last joins the
 // slices' partials in their order, so the result does not depend on which one that is.
+#include <type_traits>
+
 #include "moe_common.cuh"
 #include "moe_round_ops.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpBlocks = 4;    // of an SM
 constexpr int kLpVecs = 4;      // 16-byte vectors a thread holds of a chunk
 constexpr int kLpMaxK = 32, kLpMaxSlices = 32;
-constexpr int kLpCand = 1024;   // entries at or above the threshold that are kept
+constexpr int kLpPend = 480;    // entries that wait to be merged
 using Key = unsigned long long;
 
 struct LpPartial {  // a slice's result in the workspace
@@ -33,7 +41,7 @@ struct LpPartial {  // a slice's result in the workspace
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -107,32 +115,85 @@ __device__ __forceinline__ Vec<DT> load_vec(const void* row, int first, int voca
   return v;
 }
 
+// Two floats in one register pair.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float2 split(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float one_if_ge(float x, float y) {
+  float r;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 struct LpShared {
-  Key list[2][kLpMaxK];
-  Key group[kLpWarps * 2];
-  Key cand[kLpCand + kLpMaxK];
+  Key list[kLpMaxSlices * kLpMaxK];  // what waits to be merged; candidates of the join of slices
+  Key top[kLpMaxK];                  // the block's first k so far, in order; 0 where there are fewer
   Key best[kLpWarps];
   float m[kLpWarps], s[kLpWarps], w[kLpWarps];
   int rank[kLpWarps];
-  int count;
-  int last;
+  unsigned kth[kLpWarps], part[kLpWarps];
+  int count, last;
 };
 
-// sm.cand[0 .. n) -> the first k of them in order, in `out` (0 where there are fewer).
-__device__ __forceinline__ void place(LpShared& sm, int n, int k, Key* out) {
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const Key mine = sm.cand[i];
+// sm.list[0 .. n) -> the first k of them in order in sm.top, 0 where there are fewer.  (All
+// threads call, behind a barrier; ends with one.)
+__device__ __forceinline__ void place(LpShared& sm, int n, int k) {
+  const int tid = threadIdx.x;
+  if (tid < k) sm.top[tid] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kLpThreads) {
+    const Key mine = sm.list[i];
     int before = 0;
-    for (int j = 0; j < n; ++j) before += sm.cand[j] > mine;
-    if (before < k) out[before] = mine;
+    for (int j = 0; j < n; ++j) before += sm.list[j] > mine;
+    if (before < k && mine) sm.top[before] = mine;
   }
-  if ((int)threadIdx.x < k && (int)threadIdx.x >= n) out[threadIdx.x] = 0;
+  __syncthreads();
+}
+
+// The first k entries of the slices' lists (descending, 2^i of them, 32 at most) into sm.top.
+// The 32 / n first entries of each are maxima of 32 groups, so nothing below the k-th largest
+// of them is among the first k.  (All threads call.)
+__device__ __forceinline__ void join_lists(LpShared& sm, int n, int k, const LpPartial* all) {
+  const int tid = threadIdx.x, lane = tid & 31, each = 32 / n;
+  if (tid == 0) sm.count = 0;
+  const Key head = sort_desc(lane % each < k ? __ldcg(&all[lane / each].top[lane % each]) : 0, lane);
+  const Key thr = max_key(__shfl_sync(0xffffffffu, head, k - 1), 1);
+  __syncthreads();
+  for (int i = tid; i < n * k; i += kLpThreads) {
+    const Key key = __ldcg(&all[i / k].top[i % k]);
+    if (key >= thr) sm.list[atomicAdd(&sm.count, 1)] = key;
+  }
+  __syncthreads();
+  place(sm, sm.count, k);
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_constant__ moe_logprob_args a, int slices,
-                                                                  int slice_vecs, unsigned* counters,
-                                                                  LpPartial* partials) {
+__global__ void __launch_bounds__(kLpThreads, kLpBlocks)
+    k_token_logprobs(const __grid_constant__ moe_logprob_args a, int slices, int slice_vecs, unsigned* counters,
+                     LpPartial* partials) {
   constexpr int N = Vec<DT>::N;
   __shared__ LpShared sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.top_k;
@@ -145,26 +206,31 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
   const int token = a.tokens ? a.tokens[row] : -1;
   const bool has_token = token >= 0 && token < a.vocab;
   const float xt = has_token ? logit_at<DT>(base, token) : INFINITY;
-  const float above = nextafterf(xt, INFINITY);  // entries behind the token have to exceed it
+  const float above = nextafterf(xt, INFINITY);  // what entries behind the token have to reach
   const float c2 = a.inv_temperature * 1.4426950408889634f;
   float m = -INFINITY, s = 0.f, w = 0.f;
-  int rank = 0, cur = 0;
-  if (tid < kLpMaxK) sm.list[0][tid] = 0;
+  int rank = 0;
+  float kth = -INFINITY;  // the k-th logit so far: later entries have to be above it
+  if (tid < kLpMaxK) sm.top[tid] = 0;
+  if (tid == 0) sm.count = 0;
   __syncthreads();
 
-  for (int c = v0; c < v1; c += kLpThreads * kLpVecs) {
+  const auto chunk = [&](int c, auto inner) {  // inner: every vector is there in full, the token in none
     Vec<DT> x[kLpVecs];
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j) {
       const int v = c + j * kLpThreads + tid;
-      if (v < v1) x[j] = load_vec<DT>(base, v * N - lead, a.vocab);
+      if constexpr (inner.value)
+        x[j].raw = __ldcs(reinterpret_cast<const uint4*>(base + (long long)(v * N - lead) * (16 / N)));
+      else if (v < v1) x[j] = load_vec<DT>(base, v * N - lead, a.vocab);
       else x[j].raw = make_uint4(Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone);
     }
-    float top = -INFINITY;
+    float tops[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j)
 #pragma unroll
-      for (int e = 0; e < N; ++e) top = fmaxf(top, x[j].at(e));
+      for (int e = 0; e < N; e += 2) tops[j & 1] = fmaxf(fmaxf(tops[j & 1], x[j].at(e)), x[j].at(e + 1));
+    const float top = fmaxf(tops[0], tops[1]);
     if (top > m) {
       if (m > -INFINITY) {
         const float d = (m - top) * c2, f = exp2_fast(d);
@@ -174,103 +240,132 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
       m = top;
     }
     const float shift = m == -INFINITY ? 0.f : m;
+    const Pair less = pair(-shift, -shift), scale = pair(c2, c2);
+    Pair s2 = 0, w2 = 0, r2 = 0;
+    const float ahead = token < c * N - lead ? above : xt;
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j) {
       const int v = c + j * kLpThreads + tid, first = v * N - lead;
-      const bool full = v < v1 && first >= 0 && first + N <= a.vocab;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float u = (x[j].at(e) - shift) * c2, p = exp2_fast(u);
-        s += p;
-        w = fmaf(p, fmaxf(u, -300.f), w);  // 0 * -infinity is 0 here; p carries a NaN
+      // entries before the token count from its logit on, those behind it above that
+      float thr = ahead;
+      bool apart = false;
+      if constexpr (!inner.value) {
+        thr = v >= v1 ? INFINITY : token < first ? above : xt;
+        apart = v < v1 && ((token >= first && token < first + N) ||
+                           (xt == -INFINITY && (first < 0 || first + N > a.vocab)));
       }
-      if (full && (token < first || token >= first + N)) {
-        const float thr = token < first ? above : xt;
 #pragma unroll
-        for (int e = 0; e < N; ++e) rank += x[j].at(e) >= thr;
-      } else if (v < v1) {
+      for (int e = 0; e < N; e += 2) {
+        const float x0 = x[j].at(e), x1 = x[j].at(e + 1);
+        const float2 u = split(mul2(add2(pair(x0, x1), less), scale));
+        const Pair p = pair(exp2_fast(u.x), exp2_fast(u.y));
+        s2 = add2(s2, p);
+        w2 = fma2(p, pair(fmaxf(u.x, -300.f), fmaxf(u.y, -300.f)), w2);  // 0 * -infinity is 0 here; p carries a NaN
+        r2 = add2(r2, pair(one_if_ge(x0, thr), one_if_ge(x1, thr)));
+      }
+      if (apart) {  // the token's own vector, or one with filled places under a token of -infinity
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const int i = first + e;
-          if (i >= 0 && i < a.vocab) rank += x[j].at(e) > xt || (x[j].at(e) == xt && i < token);
+          const float f = x[j].at(e);
+          rank -= f >= thr;
+          if (i >= 0 && i < a.vocab) rank += f > xt || (f == xt && i < token);
         }
       }
     }
-    if (k == 0) continue;
-
-    const Key floor_key = sm.list[cur][k - 1];
-    Key mine = 0;
-    if (top > -INFINITY && order_key(top) >= (unsigned)(floor_key >> 32)) {
-      int id = 0;
-#pragma unroll
-      for (int j = kLpVecs - 1; j >= 0; --j)
-#pragma unroll
-        for (int e = N - 1; e >= 0; --e)
-          if (x[j].at(e) == top) id = (c + j * kLpThreads + tid) * N - lead + e;
-      mine = key_of(top, id);
-      if (mine <= floor_key) mine = 0;
+    {
+      const float2 sv = split(s2), wv = split(w2), rv = split(r2);
+      s += sv.x + sv.y;
+      w += wv.x + wv.y;
+      rank += (int)(rv.x + rv.y);
     }
-    if (!__syncthreads_or(mine != 0)) continue;
-    Key g = mine;
+    if (k == 0) return;
+    float least = kth;  // entries above it are appended; for the first chunk, from it on
+    if (c == v0) {
+      // each warp's k-th of its lanes' maxima is a bound that k entries reach, and so is the
+      // least of what every warp has its part of the k of
+      unsigned sorted = order_key(top);
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) g = max_key(g, __shfl_xor_sync(0xffffffffu, g, o));
-    if ((lane & 15) == 0) sm.group[2 * warp + (lane >> 4)] = g;
-    if (tid == 0) sm.count = 0;
-    __syncthreads();
-    const Key sorted = sort_desc(sm.group[lane], lane);
-    const Key thr = max_key(__shfl_sync(0xffffffffu, sorted, k - 1), floor_key + 1);
-    if (mine >= thr) {
+      for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) {
+          const unsigned y = __shfl_xor_sync(0xffffffffu, sorted, o);
+          sorted = ((lane & o) == 0) == ((lane & size) == 0) ? max(sorted, y) : min(sorted, y);
+        }
+      if (lane == k - 1) sm.kth[warp] = sorted;
+      if (lane == (k + kLpWarps - 1) / kLpWarps - 1) sm.part[warp] = sorted;
+      __syncthreads();
+      unsigned bound = 0, all = 0xffffffffu;
+#pragma unroll
+      for (int q = 0; q < kLpWarps; ++q) {
+        bound = max(bound, sm.kth[q]);
+        all = min(all, sm.part[q]);
+      }
+      // the key below the bound's, so that "above" means from the bound on (-0 has no key of its own)
+      const unsigned below = max(max(bound, all), 0x00800000u) - 1u;
+      least = key_value(below == 0x7fffffffu ? below - 1u : below);
+    }
+    if (top > least) {
 #pragma unroll
       for (int j = 0; j < kLpVecs; ++j)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float f = x[j].at(e);
-          if (f > -INFINITY) {
-            const Key key = key_of(f, (c + j * kLpThreads + tid) * N - lead + e);
-            if (key >= thr) {
-              const int at = atomicAdd(&sm.count, 1);
-              if (at < kLpCand) sm.cand[at] = key;
-            }
+          if (f > least) {
+            const int at = atomicAdd(&sm.count, 1);
+            if (at < kLpPend) sm.list[at] = key_of(f, (c + j * kLpThreads + tid) * N - lead + e);
           }
         }
     }
+  };
+  // What waits is merged with the list so far; chunks [from, to) are where it came from.
+  const auto merge = [&](int from, int to) {
     __syncthreads();
     int n = sm.count;
-    if (n > kLpCand) {
-      // many equal or ordered logits: the k largest one after the other
-      __syncthreads();
+    if (n > kLpPend) {
+      // rising logits, or many equal ones: the chunks' first k, one maximum after the other
       Key prev = ~0ull;
-      for (int r = 0; r < k; ++r) {
+#pragma unroll 1
+      for (n = 0; n < k; ++n) {
         Key b = 0;
-#pragma unroll
-        for (int j = 0; j < kLpVecs; ++j)
+#pragma unroll 1
+        for (int v = from + tid; v < min(to, v1); v += kLpThreads) {
+          const Vec<DT> x = load_vec<DT>(base, v * N - lead, a.vocab);
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            const float f = x[j].at(e);
-            if (f > -INFINITY) {
-              const Key key = key_of(f, (c + j * kLpThreads + tid) * N - lead + e);
-              if (key < prev) b = max_key(b, key);
-            }
+            const Key key = x.at(e) > -INFINITY ? key_of(x.at(e), v * N - lead + e) : 0;
+            if (key < prev) b = max_key(b, key);
           }
+        }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) b = max_key(b, __shfl_xor_sync(0xffffffffu, b, o));
+        __syncthreads();
         if (lane == 0) sm.best[warp] = b;
         __syncthreads();
-        prev = sm.best[0];
-        for (int q = 1; q < kLpWarps; ++q) prev = max_key(prev, sm.best[q]);
-        if (tid == 0) sm.cand[r] = prev;
-        __syncthreads();
+        for (int q = 0; q < kLpWarps; ++q) b = max_key(b, sm.best[q]);
+        prev = b;
+        if (tid == 0) sm.list[n] = b;
       }
-      n = k;
     }
-    // the list so far joins the candidates: its entries are other ids than the chunk's
-    if (tid < k) sm.cand[n + tid] = sm.list[cur][tid];
+    if (tid < k) sm.list[n + tid] = sm.top[tid];
     __syncthreads();
-    int total = n;
-    for (int j = 0; j < k; ++j) total += sm.cand[n + j] != 0;
-    place(sm, total, k, sm.list[cur ^ 1]);
-    cur ^= 1;
+    place(sm, n + k, k);
+    if (tid == 0) sm.count = 0;
+    const Key last = sm.top[k - 1];
+    kth = last ? key_logit(last) : -INFINITY;
     __syncthreads();
+  };
+  constexpr int kStep = kLpThreads * kLpVecs;
+  int merged = v0, next = v0 + kStep;
+  for (int c = v0; c < v1; c += kStep) {
+    const int first = c * N - lead, last = first + kStep * N;
+    if (c + kStep <= v1 && first >= 0 && last <= a.vocab && (token < first || token >= last)) chunk(c, std::true_type{});
+    else chunk(c, std::false_type{});
+    if (k > 0 && (c + kStep == next || c + kStep >= v1)) {
+      merge(merged, c + kStep);
+      merged = c + kStep;
+      next = v0 + 2 * (merged - v0);
+    }
   }
 
   // the block's sums, in a fixed order
@@ -278,10 +373,6 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
     float top = m;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sm.m[warp] = top;
-    __syncthreads();
-    top = sm.m[0];
-    for (int q = 1; q < kLpWarps; ++q) top = fmaxf(top, sm.m[q]);
     const float d = m == -INFINITY ? 0.f : (m - top) * c2, f = exp2_fast(d);
     w = f * fmaf(d, s, w);
     s *= f;
@@ -292,21 +383,23 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
       rank += __shfl_xor_sync(0xffffffffu, rank, o);
     }
     if (lane == 0) {
+      sm.m[warp] = top;
       sm.s[warp] = s;
       sm.w[warp] = w;
       sm.rank[warp] = rank;
     }
     __syncthreads();
-    m = top;
+    m = sm.m[0];
+    for (int q = 1; q < kLpWarps; ++q) m = fmaxf(m, sm.m[q]);
     s = w = 0.f;
     rank = 0;
     for (int q = 0; q < kLpWarps; ++q) {
-      s += sm.s[q];
-      w += sm.w[q];
+      const float e = sm.m[q] == -INFINITY ? 0.f : (sm.m[q] - m) * c2, g = exp2_fast(e);
+      s = fmaf(g, sm.s[q], s);
+      w = fmaf(g, fmaf(e, sm.s[q], sm.w[q]), w);
       rank += sm.rank[q];
     }
   }
-
   if (slices > 1) {
     LpPartial* mine = partials + (size_t)row * slices + slice;
     if (tid == 0) {
@@ -315,18 +408,17 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
       mine->w = w;
       mine->rank = rank;
     }
-    if (tid < k) mine->top[tid] = sm.list[cur][tid];
-    __threadfence();
+    if (tid < k) mine->top[tid] = sm.top[tid];
     __syncthreads();
     if (tid == 0) {
+      __threadfence();  // covers what the block wrote before the barrier
       const bool last = atomicAdd(counters + row, 1u) == (unsigned)slices - 1;
       if (last) counters[row] = 0;  // ready for the next call
       sm.last = last;
-      sm.count = 0;
+      __threadfence();
     }
     __syncthreads();
     if (!sm.last) return;
-    __threadfence();
     const LpPartial* all = partials + (size_t)row * slices;
     // every warp joins the sums alike: lane = slice
     float pm = -INFINITY, ps = 0.f, pw = 0.f;
@@ -350,21 +442,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
       w += __shfl_xor_sync(0xffffffffu, w, o);
       rank += __shfl_xor_sync(0xffffffffu, rank, o);
     }
-    if (k > 0) {
-      // the lists are in order: the first 32 / slices of each are group maxima
-      const int each = 32 / slices;
-      Key head = lane / each < slices && lane % each < k ? __ldcg(&all[lane / each].top[lane % each]) : 0;
-      head = sort_desc(head, lane);
-      const Key thr = max_key(__shfl_sync(0xffffffffu, head, k - 1), 1);
-      for (int i = tid; i < slices * k; i += kLpThreads) {
-        const Key key = __ldcg(&all[i / k].top[i % k]);
-        if (key >= thr) sm.cand[atomicAdd(&sm.count, 1)] = key;  // at most 32 * 32
-      }
-      __syncthreads();
-      place(sm, sm.count, k, sm.list[0]);
-      cur = 0;
-      __syncthreads();
-    }
+    if (k > 0) join_lists(sm, slices, k, all);
   }
 
   const bool empty = m == -INFINITY && s == 0.f;
@@ -380,7 +458,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_token_logprobs(const __grid_c
     if (a.tokens && !has_token && token != -1) atomicOr(a.dev_status, MOE_DEV_INDEX);
   }
   if (tid < k) {
-    const Key key = sm.list[cur][tid];
+    const Key key = sm.top[tid];
     a.top_ids[(long long)row * k + tid] = key ? key_id(key) : -1;
     a.top_logp[(long long)row * k + tid] = key ? (key_logit(key) - m) * a.inv_temperature - log_s : -INFINITY;
   }
@@ -403,13 +481,12 @@ int check(const moe_logprob_args* p) {
   return MOE_OK;
 }
 
-// Slices of a row: while there are SMs to spare (two blocks each) and every thread of a
-// slice still has a vector.
+// Slices of a row: while there are SMs to spare and every thread of a slice has a vector.
 int slices_of(const moe_logprob_args& a) {
-  constexpr int kBlocks = 304;
+  constexpr int kMost = 152 * 2;
   const int per = a.dtype == MOE_F32 ? 4 : 8;
   int s = 1;
-  while (s < kLpMaxSlices && (int64_t)a.n_rows * s * 2 <= kBlocks && a.vocab / per / (2 * s) >= kLpThreads) s *= 2;
+  while (s < kLpMaxSlices && (int64_t)a.n_rows * s * 2 <= kMost && a.vocab / per / (2 * s) >= kLpThreads) s *= 2;
   return s;
 }
 

@@ -13,6 +13,8 @@
 // overflow drops the whole turns; its error is at most |pos| * 2^-52 turns for f_i < 1,
 // 1.4e-9 rad at 10^6 and 3e-6 rad at 2^31.  The top 32 bits go to float as half turns in
 // [-1, 1).
+#include <type_traits>
+
 #include "moe_round_ops.cuh"
 
 namespace moe {
@@ -31,10 +33,10 @@ template <int DT, int D>
 __global__ void __launch_bounds__(kRopeThreads) k_qk_rope(const __grid_constant__ moe_qk_rope_args a) {
   constexpr int L = D / 8, kGroups = kRopeThreads / L;
   __shared__ unsigned long long frac[D / 2];
-  __shared__ float2 trig[2][kRopeRows][D / 2];
+  __shared__ __align__(16) float2 trig[2][kRopeRows][D / 2];
   __shared__ long long where[2][kRopeRows];  // element offset of the row's slot in the cache, or -1
   const int tid = threadIdx.x, p = tid % L, group = tid / L;
-  const int half = a.rot_dim / 2, hq = a.q_heads, hkv = a.kv_heads, heads = hq + 2 * hkv;
+  const int half = a.rot_dim / 2;
   const bool turns = p < a.rot_dim / 8;
   int c0, c1;  // this lane's chunks of four elements
   if (a.interleaved) {
@@ -47,23 +49,90 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_rope(const __grid_constant_
     c0 = a.rot_dim / 4 + 2 * (p - a.rot_dim / 8);
     c1 = c0 + 1;
   }
+  const unsigned members = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((tid & 31) / L * L);
   for (int i = tid; i < half; i += kRopeThreads) frac[i] = turn_fraction(a.inv_freq[i]);
-  const uint2* gq = static_cast<const uint2*>(a.q_gain);
-  const uint2* gk = static_cast<const uint2*>(a.k_gain);
-  uint2 gain_q[2] = {}, gain_k[2] = {};
-  if (gq) {
-    gain_q[0] = gq[c0];
-    gain_q[1] = gq[c1];
-  }
-  if (gk) {
-    gain_k[0] = gk[c0];
-    gain_k[1] = gk[c1];
-  }
+  __syncthreads();
+
+  // Heads [row][head] of one kind, U of them in flight in a group.  (n: rows of the step)
+  const auto heads = [&](auto kind, int n, int row0, int buf, int count, const void* from, int64_t stride,
+                         const void* gain) {
+    constexpr int kQuery = 0, kValue = 2, KIND = decltype(kind)::value;
+    const unsigned mul = ((1u << 20) + count - 1) / count;  // w / count for w < 1024 + 3 * 32
+    float g[8];
+    if (gain) {
+      const uint2 x = static_cast<const uint2*>(gain)[c0], y = static_cast<const uint2*>(gain)[c1];
+      const float2 v[4] = {unpack2<DT>(x.x), unpack2<DT>(x.y), unpack2<DT>(y.x), unpack2<DT>(y.y)};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[2 * j] = v[j].x;
+        g[2 * j + 1] = v[j].y;
+      }
+    }
+    constexpr int U = KIND == kQuery ? kRopeUnroll : 1;
+    for (int w0 = group; w0 < n * count; w0 += kGroups * U) {
+      uint2 x[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int w = w0 + u * kGroups, r = (int)(w * mul >> 20), h = w - r * count;
+        if (w >= n * count) break;
+        const uint16_t* src = static_cast<const uint16_t*>(from) + (row0 + r) * stride + h * D;
+        x[u][0] = __ldcs(reinterpret_cast<const uint2*>(src + 4 * c0));
+        x[u][1] = __ldcs(reinterpret_cast<const uint2*>(src + 4 * c1));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int w = w0 + u * kGroups, r = (int)(w * mul >> 20), h = w - r * count;
+        if (w >= n * count) break;  // a group's lanes agree on w: the shuffles below stay inside the group
+        uint2 y0 = x[u][0], y1 = x[u][1];
+        if constexpr (KIND != kValue) {
+          float2 v[4] = {unpack2<DT>(y0.x), unpack2<DT>(y0.y), unpack2<DT>(y1.x), unpack2<DT>(y1.y)};
+          if (gain) {
+            float ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ss = fmaf(v[j].x, v[j].x, fmaf(v[j].y, v[j].y, ss));
+#pragma unroll
+            for (int o = L / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(members, ss, o);
+            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);  // within 2 units in the last place
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x * inv * g[2 * j], v[j].y * inv * g[2 * j + 1]);
+          }
+          if (turns) {
+            const float4* t = reinterpret_cast<const float4*>(trig[buf][r] + 4 * p);  // cosine, sine, cosine, sine
+            const float4 ta = t[0], tb = t[1];
+            if (a.interleaved) {
+              v[0] = make_float2(v[0].x * ta.x - v[0].y * ta.y, v[0].y * ta.x + v[0].x * ta.y);
+              v[1] = make_float2(v[1].x * ta.z - v[1].y * ta.w, v[1].y * ta.z + v[1].x * ta.w);
+              v[2] = make_float2(v[2].x * tb.x - v[2].y * tb.y, v[2].y * tb.x + v[2].x * tb.y);
+              v[3] = make_float2(v[3].x * tb.z - v[3].y * tb.w, v[3].y * tb.z + v[3].x * tb.w);
+            } else {
+              const float2 a0 = v[0], a1 = v[1], b0 = v[2], b1 = v[3];
+              v[0] = make_float2(a0.x * ta.x - b0.x * ta.y, a0.y * ta.z - b0.y * ta.w);
+              v[1] = make_float2(a1.x * tb.x - b1.x * tb.y, a1.y * tb.z - b1.y * tb.w);
+              v[2] = make_float2(b0.x * ta.x + a0.x * ta.y, b0.y * ta.z + a0.y * ta.w);
+              v[3] = make_float2(b1.x * tb.x + a1.x * tb.y, b1.y * tb.z + a1.y * tb.w);
+            }
+          }
+          y0 = make_uint2(pack2<DT>(v[0].x, v[0].y), pack2<DT>(v[1].x, v[1].y));
+          y1 = make_uint2(pack2<DT>(v[2].x, v[2].y), pack2<DT>(v[3].x, v[3].y));
+        }
+        uint16_t* dst;
+        if constexpr (KIND == kQuery) {
+          dst = static_cast<uint16_t*>(a.q_out) + (row0 + r) * a.q_out_stride + h * D;
+        } else {
+          const long long at = where[buf][r];
+          if (at < 0) continue;
+          dst = static_cast<uint16_t*>(KIND == kValue ? a.cache.v : a.cache.k) + at + h * a.cache.head_stride;
+        }
+        *reinterpret_cast<uint2*>(dst + 4 * c0) = y0;
+        *reinterpret_cast<uint2*>(dst + 4 * c1) = y1;
+      }
+    }
+  };
+
   unsigned flags = 0;
   int buf = 0;
   for (int row0 = blockIdx.x * kRopeRows; row0 < a.n_rows; row0 += gridDim.x * kRopeRows, buf ^= 1) {
     const int rows = min(kRopeRows, a.n_rows - row0);
-    if (row0 == (int)blockIdx.x * kRopeRows) __syncthreads();  // frac
     for (int e = tid; e < rows * half; e += kRopeThreads) {
       const int r = e / half, i = e - r * half;
       const long long pos = a.row_pos[row0 + r];
@@ -84,75 +153,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_rope(const __grid_constant_
       where[buf][tid] = at;
     }
     __syncthreads();  // one a step: the next step writes the other buffer
-    for (int w0 = group; w0 < rows * heads; w0 += kGroups * kRopeUnroll) {
-      uint2 x[kRopeUnroll][2];
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        const int w = w0 + u * kGroups;
-        if (w >= rows * heads) continue;
-        const int r = w / heads, h = w - r * heads;
-        const long long row = row0 + r;
-        const uint16_t* src =
-            h < hq ? static_cast<const uint16_t*>(a.q) + row * a.q_stride + h * D
-            : h < hq + hkv ? static_cast<const uint16_t*>(a.k) + row * a.k_stride + (h - hq) * D
-                           : static_cast<const uint16_t*>(a.v) + row * a.v_stride + (h - hq - hkv) * D;
-        x[u][0] = *reinterpret_cast<const uint2*>(src + 4 * c0);
-        x[u][1] = *reinterpret_cast<const uint2*>(src + 4 * c1);
-      }
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        const int w = w0 + u * kGroups;
-        // a group's lanes agree on w; the shuffles below stay inside the group
-        if (w >= rows * heads) continue;
-        const int r = w / heads, h = w - r * heads;
-        const bool is_q = h < hq, is_v = h >= hq + hkv;
-        uint2 y0 = x[u][0], y1 = x[u][1];
-        if (!is_v) {
-          float2 v[4] = {unpack2<DT>(y0.x), unpack2<DT>(y0.y), unpack2<DT>(y1.x), unpack2<DT>(y1.y)};
-          if (is_q ? gq != nullptr : gk != nullptr) {
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ss = fmaf(v[j].x, v[j].x, fmaf(v[j].y, v[j].y, ss));
-            const unsigned members = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((tid & 31) / L * L);
-#pragma unroll
-            for (int o = L / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(members, ss, o);
-            const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-            const uint2 g0 = is_q ? gain_q[0] : gain_k[0], g1 = is_q ? gain_q[1] : gain_k[1];
-            const float2 g[4] = {unpack2<DT>(g0.x), unpack2<DT>(g0.y), unpack2<DT>(g1.x), unpack2<DT>(g1.y)};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x * inv * g[j].x, v[j].y * inv * g[j].y);
-          }
-          if (turns) {
-            const float2* t = trig[buf][r] + 4 * p;
-            if (a.interleaved) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[j] = make_float2(v[j].x * t[j].x - v[j].y * t[j].y, v[j].y * t[j].x + v[j].x * t[j].y);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float2 t0 = t[2 * j], t1 = t[2 * j + 1], lo = v[j], hi = v[j + 2];
-                v[j] = make_float2(lo.x * t0.x - hi.x * t0.y, lo.y * t1.x - hi.y * t1.y);
-                v[j + 2] = make_float2(hi.x * t0.x + lo.x * t0.y, hi.y * t1.x + lo.y * t1.y);
-              }
-            }
-          }
-          y0 = make_uint2(pack2<DT>(v[0].x, v[0].y), pack2<DT>(v[1].x, v[1].y));
-          y1 = make_uint2(pack2<DT>(v[2].x, v[2].y), pack2<DT>(v[3].x, v[3].y));
-        }
-        uint16_t* dst;
-        if (is_q) {
-          dst = static_cast<uint16_t*>(a.q_out) + (long long)(row0 + r) * a.q_out_stride + h * D;
-        } else {
-          const long long at = where[buf][r];
-          if (at < 0) continue;
-          dst = static_cast<uint16_t*>(is_v ? a.cache.v : a.cache.k) + at +
-                (is_v ? h - hq - hkv : h - hq) * a.cache.head_stride;
-        }
-        *reinterpret_cast<uint2*>(dst + 4 * c0) = y0;
-        *reinterpret_cast<uint2*>(dst + 4 * c1) = y1;
-      }
-    }
+    heads(std::integral_constant<int, 0>{}, rows, row0, buf, a.q_heads, a.q, a.q_stride, a.q_gain);
+    heads(std::integral_constant<int, 1>{}, rows, row0, buf, a.kv_heads, a.k, a.k_stride, a.k_gain);
+    heads(std::integral_constant<int, 2>{}, rows, row0, buf, a.kv_heads, a.v, a.v_stride, nullptr);
   }
   if (flags) atomicOr(a.dev_status, flags);
 }

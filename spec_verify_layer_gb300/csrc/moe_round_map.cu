@@ -17,12 +17,22 @@ constexpr int kMapRows = 4 * kMapThreads;  // rows per block and step: four a th
 constexpr int kMapMaxReq = 16384;
 constexpr int kTree = 64;  // rows of a tree: bits of a mask
 
+// n / page_size for n below 2^31, as a product (integer division is some 20 instructions).
+struct ByPage {
+  unsigned mul;
+  int shift;
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)(((unsigned long long)(unsigned)n * mul) >> shift);
+  }
+  __device__ __forceinline__ int up(int n) const { return n > 0 ? (*this)(n - 1) + 1 : 0; }  // rounded up
+};
+
 // A request's lengths, made consistent.  flags: MOE_DEV_* bits found on the way.
 struct Req {
   int ctx, rows, held, take;  // take: table columns to fill behind the held ones
 };
 
-__device__ __forceinline__ Req request(const moe_map_args& a, int b, unsigned& flags) {
+__device__ __forceinline__ Req request(const moe_map_args& a, ByPage by, int b, unsigned& flags) {
   Req q;
   q.ctx = a.ctx_len[b];
   q.rows = a.new_len[b];
@@ -31,14 +41,13 @@ __device__ __forceinline__ Req request(const moe_map_args& a, int b, unsigned& f
     q.ctx = max(q.ctx, 0);
     q.rows = 0;
   }
-  const int P = a.page_size, W = a.table_width;
-  const int first = (int)(((long long)q.ctx + P - 1) / P);
+  const int W = a.table_width, first = by.up(q.ctx);
   q.held = a.pages_held ? a.pages_held[b] : first;
   if (q.held < first || q.held > W) {
     flags |= MOE_DEV_LENGTH;
     q.held = min(max(q.held, 0), W);
   }
-  int need = (int)(((long long)q.ctx + q.rows + P - 1) / P);
+  int need = by.up(q.ctx + q.rows);
   if (need > W) {
     flags |= MOE_DEV_PAGES;
     need = W;
@@ -53,7 +62,7 @@ __device__ __forceinline__ int checked_page(const moe_map_args& a, int page, uns
   return -1;
 }
 
-__global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant__ moe_map_args a) {
+__global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant__ moe_map_args a, const ByPage by) {
   extern __shared__ uint32_t sm[];
   uint32_t* start = sm;                // [n_req + 1] rows before a request, at most n_rows
   uint32_t* off = sm + a.n_req + 1;    // [n_req + 1] fresh pages before it
@@ -68,7 +77,7 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
     const int b = b0 + tid;
     Req q{0, 0, 0, 0};
     unsigned f = 0;
-    if (b < a.n_req) q = request(a, b, f);
+    if (b < a.n_req) q = request(a, by, b, f);
     uint2 v = make_uint2((uint32_t)q.rows, (uint32_t)q.take), incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -117,7 +126,7 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
   const uint32_t fresh = carry.y;
   for (uint32_t t = blockIdx.x * kMapThreads + tid; t < fresh; t += gridDim.x * kMapThreads) {
     const int b = last_not_above(off, a.n_req, t);
-    const int held = request(a, b, quiet).held;
+    const int held = request(a, by, b, quiet).held;
     a.block_table[(size_t)b * a.table_width + held + (t - off[b])] =
         t < (uint32_t)a.n_free ? checked_page(a, a.free_pages[t], flags) : -1;
   }
@@ -138,7 +147,8 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
     uint64_t mask[4];
     int b = r0 < live ? last_not_above(start, a.n_req, (uint32_t)r0) : 0;
     Req q{0, 0, 0, 0};
-    bool have = false;
+    int off_in = 0, col = 0, page = -1;  // place in the page, table column, page of the row
+    bool have = false;                   // (of request b, up to date for the row before)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = r0 + j;
@@ -151,17 +161,27 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
         ++b;
         have = false;
       }
+      const int s = (int)start[b], i = r - s;
+      bool turn = true;  // another page
       if (!have) {
-        q = request(a, b, quiet);
+        q = request(a, by, b, quiet);
         have = true;
+        col = by(q.ctx + i);
+        off_in = q.ctx + i - col * a.page_size;
+      } else if (++off_in == a.page_size) {
+        off_in = 0;
+        ++col;
+      } else {
+        turn = false;
       }
-      const int s = (int)start[b], i = r - s, p = q.ctx + i, col = p / a.page_size;
-      int page = -1;
-      if (col < q.held) {
-        page = checked_page(a, a.block_table[(size_t)b * a.table_width + col], flags);
-      } else if (col - q.held < q.take) {
-        const uint32_t t = off[b] + (uint32_t)(col - q.held);
-        if (t < (uint32_t)a.n_free) page = checked_page(a, a.free_pages[t], flags);
+      if (turn) {
+        page = -1;
+        if (col < q.held) {
+          page = checked_page(a, a.block_table[(size_t)b * a.table_width + col], flags);
+        } else if (col - q.held < q.take) {
+          const uint32_t t = off[b] + (uint32_t)(col - q.held);
+          if (t < (uint32_t)a.n_free) page = checked_page(a, a.free_pages[t], flags);
+        }
       }
       int depth = i;
       if (a.parents) {
@@ -188,7 +208,7 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
       }
       req[j] = b;
       pos[j] = (int)min((long long)q.ctx + depth, 0x7fffffffLL);
-      slot[j] = page < 0 ? -1 : page * a.page_size + p % a.page_size;
+      slot[j] = page < 0 ? -1 : page * a.page_size + off_in;
     }
     if (r0 + 4 <= a.n_rows) {
       *reinterpret_cast<int4*>(a.row_req + r0) = make_int4(req[0], req[1], req[2], req[3]);
@@ -240,9 +260,14 @@ extern "C" int moe_round_map(const moe_map_args* p, void* stream) {
     const cudaError_t e = cudaFuncSetAttribute(k_round_map, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return launch_status(e);
   }
+  ByPage by;
+  int bits = 0;
+  while ((1 << bits) < a.page_size) ++bits;
+  by.shift = 31 + bits;
+  by.mul = (unsigned)((1ull << by.shift) / (unsigned)a.page_size + 1);
   // one step's rows to a block, up to two blocks an SM: more blocks only repeat the sums
   const int steps = (a.n_rows + kMapRows - 1) / kMapRows;
   const int grid = steps < 1 ? 1 : steps > 2 * sms ? 2 * sms : steps;
-  k_round_map<<<grid, kMapThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  k_round_map<<<grid, kMapThreads, smem, static_cast<cudaStream_t>(stream)>>>(a, by);
   return launch_status(cudaGetLastError());
 }
