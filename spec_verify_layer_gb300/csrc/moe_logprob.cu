@@ -1,7 +1,7 @@
 // Log probabilities of given tokens, entropies, ranks and top alternatives
 // (moe_token_logprobs), one launch and one pass over the logits.
 //
-// A block takes a slice of one row, a chunk at a time: a thread holds four 16-byte vectors
+// A block takes a slice of one row, a chunk at a time: a thread holds three 16-byte vectors
 // of the chunk in registers and updates its own running maximum m (of the logits), sum
 // s = sum 2^u and w = sum 2^u u with u = (x - m) / T * log2(e), two elements an instruction;
 // nothing waits for another warp until the slice ends.  Entropy is ln s - ln 2 * w / s, log
@@ -11,7 +11,7 @@
 // in shared memory.  Of the first chunk it takes what is not below a bound that k entries
 // are known to reach (from the threads' maxima); from then on an entry only counts if it is
 // above the k-th, which few are (k of each doubling of what was seen), so threads append
-// such entries to a buffer and the block merges it in after 1, 2, 4, 8 ... chunks, each
+// such entries to a buffer and the block merges it in after 1, 4, 16 ... chunks, each
 // entry counting the larger ones for its place.  A buffer that runs over (rising logits) has
 // its chunks gone through again, one maximum after the other.  The lists of slices are
 // joined alike: their first entries give the bound.
@@ -27,8 +27,8 @@ namespace moe {
 namespace {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpBlocks = 4;    // of an SM
-constexpr int kLpVecs = 4;      // 16-byte vectors a thread holds of a chunk
+constexpr int kLpBlocks = 5;    // of an SM
+constexpr int kLpVecs = 3;      // 16-byte vectors a thread holds of a chunk
 constexpr int kLpMaxK = 32, kLpMaxSlices = 32;
 constexpr int kLpPend = 480;    // entries that wait to be merged
 using Key = unsigned long long;
@@ -38,12 +38,6 @@ struct LpPartial {  // a slice's result in the workspace
   int rank;
   Key top[kLpMaxK];
 };
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ Key key_of(float x, int id) { return ((Key)order_key(x) << 32) | (uint32_t)~id; }
 __device__ __forceinline__ float key_logit(Key k) { return key_value((unsigned)(k >> 32)); }
@@ -115,33 +109,6 @@ __device__ __forceinline__ Vec<DT> load_vec(const void* row, int first, int voca
   return v;
 }
 
-// Two floats in one register pair.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float x, float y) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-  return p;
-}
-__device__ __forceinline__ float2 split(Pair p) {
-  float2 v;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 __device__ __forceinline__ float one_if_ge(float x, float y) {
   float r;
   asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
@@ -307,7 +274,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     }
     if (top > least) {
 #pragma unroll
-      for (int j = 0; j < kLpVecs; ++j)
+      for (int j = 0; j < kLpVecs; ++j) {
+        float most = x[j].at(0);
+#pragma unroll
+        for (int e = 1; e < N; ++e) most = fmaxf(most, x[j].at(e));
+        if (!(most > least)) continue;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float f = x[j].at(e);
@@ -316,6 +287,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
             if (at < kLpPend) sm.list[at] = key_of(f, (c + j * kLpThreads + tid) * N - lead + e);
           }
         }
+      }
     }
   };
   // What waits is merged with the list so far; chunks [from, to) are where it came from.
@@ -364,7 +336,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     if (k > 0 && (c + kStep == next || c + kStep >= v1)) {
       merge(merged, c + kStep);
       merged = c + kStep;
-      next = v0 + 2 * (merged - v0);
+      next = v0 + 4 * (merged - v0);
     }
   }
 
@@ -481,12 +453,13 @@ int check(const moe_logprob_args* p) {
   return MOE_OK;
 }
 
-// Slices of a row: while there are SMs to spare and every thread of a slice has a vector.
+// Slices of a row: while there are SMs to spare (two blocks each) and every thread of a slice
+// has a vector.  More slices cost more than the last round of blocks: 2,000 rows of 129,283
+// took 208 us uncut, 231 cut in two, 278 in four.
 int slices_of(const moe_logprob_args& a) {
-  constexpr int kMost = 152 * 2;
-  const int per = a.dtype == MOE_F32 ? 4 : 8;
+  const int vecs = a.vocab / (a.dtype == MOE_F32 ? 4 : 8);
   int s = 1;
-  while (s < kLpMaxSlices && (int64_t)a.n_rows * s * 2 <= kMost && a.vocab / per / (2 * s) >= kLpThreads) s *= 2;
+  while (s < kLpMaxSlices && (int64_t)a.n_rows * s * 2 <= 152 * 2 && vecs / (2 * s) >= kLpThreads) s *= 2;
   return s;
 }
 
