@@ -439,7 +439,7 @@ int moe_qk_rope_cache(const moe_qk_rope_args* args, void* stream);
  * dtype MOE_BF16 or MOE_F16; head_dim 64, 128 or 256; kv_heads a divisor of q_heads with
  * a quotient of at most 64; max_tree 1..64; n_req 1..16384; the last element of either
  * cache within 2^35 elements of its first, n_req * kv_heads * (table_width * page_size /
- * 64 + 1) below 2^31.
+ * 64 + 4) below 2^31.
  * MOE_DEV_LENGTH: a negative context, row_start not ascending within n_rows, more rows
  * than max_tree, or a length beyond the table: that request's rows are not computed (out
  * 0, lse -infinity where the rows themselves are valid).  MOE_DEV_INDEX: a needed page

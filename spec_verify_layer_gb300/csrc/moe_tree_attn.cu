@@ -237,10 +237,12 @@ __device__ __forceinline__ float2 tm_load2(uint32_t addr) {
                : "memory");
   return make_float2(__uint_as_float(x), __uint_as_float(y));
 }
-__device__ __forceinline__ void tm_read8(float* r, uint32_t addr) {
+__device__ __forceinline__ void tm_read16(float* r, uint32_t addr) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
       : "r"(addr)
       : "memory");
 }
@@ -271,25 +273,35 @@ __device__ __forceinline__ Req request(const moe_tree_attention_args& a, int b) 
   return q;
 }
 
+// Taking up a head costs about as long as a few tiles (its queries, the first scores, the end
+// of its sums), so in the list each head has kUnit places ahead of those of its tiles.
+constexpr int kUnit = 3;
+
 template <int D>
 struct Walk {  // a block's share, unit (stretch of one head's tiles) after unit
   Req q;
-  int b, h, t0, t1;
-  int left;  // tiles left in the share, this unit's among them
+  int b, h, p0, p1;  // places of the head
+  int t0, t1;        // its tiles; none where the share has only the head's first places
+  int left;          // places left in the share, this unit's among them
+  __device__ __forceinline__ void tiles() {
+    p1 = min(q.tiles + kUnit, p0 + left);
+    t0 = max(0, p0 - kUnit);
+    t1 = max(0, p1 - kUnit);
+  }
   __device__ __forceinline__ void begin(const moe_tree_attention_args& a, int b_, int off, int left_) {
     left = left_;
     b = b_;
     if (left <= 0) return;
     q = request<D>(a, b);
-    h = off / q.tiles;
-    t0 = off - h * q.tiles;
-    t1 = min(q.tiles, t0 + left);
+    h = off / (q.tiles + kUnit);
+    p0 = off - h * (q.tiles + kUnit);
+    tiles();
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(const moe_tree_attention_args& a) {
-    left -= t1 - t0;
+    left -= p1 - p0;
     if (left <= 0) return;
-    t0 = 0;
+    p0 = 0;
     if (++h == a.kv_heads) {
       h = 0;
       do {
@@ -300,7 +312,7 @@ struct Walk {  // a block's share, unit (stretch of one head's tiles) after unit
         q = request<D>(a, b);
       } while (q.tiles == 0);
     }
-    t1 = min(q.tiles, left);
+    tiles();
   }
 };
 
@@ -360,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const auto scan = [&](int b0, const Req& q) {  // lo: places before request b0 + tid, mine: its own
-    mine = q.tiles * a.kv_heads;
+    mine = q.tiles ? (q.tiles + kUnit) * a.kv_heads : 0;
     int incl = mine;
     const int widest = __reduce_max_sync(0xffffffffu, q.tiles ? q.n : 0);
 #pragma unroll
@@ -440,12 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 1;  // the slots start empty
     bool ok = true;
     for (int seq = 0; ok && wk.more(); wk.next(a)) {
-      if (wk.q.n * G <= member * Sh::MG) continue;
+      if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
       const int len = wk.q.ctx + wk.q.n;
       const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
       const long long head_at = wk.h * a.cache.head_stride;
       if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
-        const int at = ct.w1 - wk.left - wk.t0;               // the head's place in the list
+        const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
         const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
         if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
       }
@@ -605,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (; ok && wk.more(); wk.next(a)) {
         const int rows = min(Sh::MG, wk.q.n * G - member * Sh::MG);
-        if (rows <= 0) continue;
+        if (rows <= 0 || wk.t0 == wk.t1) continue;
         const bool two = NS == 2 && rows > 128;
         if (!(ok = bar_wait(&ct.q_ready, q_ph, ct, a.dev_status))) break;
         q_ph ^= 1;
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int seq = 0; ok && wk.more(); wk.next(a)) {
       const int m0 = member * Sh::MG, rows = min(Sh::MG, wk.q.n * G - m0);
-      if (rows <= 0) continue;
+      if (rows <= 0 || wk.t0 == wk.t1) continue;
       const bool two = NS == 2 && rows > 128;
       // the group's queries into the swizzle (a rolled loop: it runs once a unit, and its
       // instructions have to come from memory the first time)
@@ -864,17 +876,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (whole && !two) f0 *= inv, f1 *= inv;  // (rows of two tiles: f0 is 1)
         if (whole && two) f0 = inv;
 #pragma unroll 1
-        for (int col = c0; col < c1; col += 8) {
+        for (int col = c0; col < c1; col += 16) {
           __syncwarp();
-          float x[8];
-          tm_read8(x, lanes + Sh::o_col(two ? wg : 0) + col);
+          float x[16];
+          tm_read16(x, lanes + Sh::o_col(two ? wg : 0) + col);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= f0;
+          for (int j = 0; j < 16; ++j) x[j] *= f0;
           if (add) {
-            float y[8];
-            tm_read8(y, lanes + Sh::o_col(1 % NS) + col);
+            float y[16];
+            tm_read16(y, lanes + Sh::o_col(1 % NS) + col);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = fmaf(y[j], f1, x[j]);
+            for (int j = 0; j < 16; ++j) x[j] = fmaf(y[j], f1, x[j]);
           }
           if (own_bad) {
 #pragma unroll 1
@@ -886,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   static_cast<const uint16_t*>(a.cache.v) + page * a.cache.page_stride +
                   (pos - pc * a.cache.page_size) * a.cache.slot_stride + wk.h * a.cache.head_stride + col);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 const float2 e = unpack2<DT>(v[j]);
                 if (!(fabsf(e.x) < INFINITY)) x[2 * j] += e.x;
                 if (!(fabsf(e.y) < INFINITY)) x[2 * j + 1] += e.y;
@@ -895,11 +907,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (mr < rows) {
             if (whole) {
-              *reinterpret_cast<uint4*>(out + col) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
-                                                                pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+#pragma unroll
+              for (int j = 0; j < 16; j += 8)
+                *reinterpret_cast<uint4*>(out + col + j) =
+                    make_uint4(pack2<DT>(x[j], x[j + 1]), pack2<DT>(x[j + 2], x[j + 3]), pack2<DT>(x[j + 4], x[j + 5]),
+                               pack2<DT>(x[j + 6], x[j + 7]));
             } else {
-              __stcg(to + (col / 4) * p.part_rows, make_float4(x[0], x[1], x[2], x[3]));
-              __stcg(to + (col / 4 + 1) * p.part_rows, make_float4(x[4], x[5], x[6], x[7]));
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                __stcg(to + (col + j) / 4 * p.part_rows, make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]));
             }
           }
         }
@@ -1063,7 +1079,7 @@ int check(const moe_tree_attention_args* p) {
           (a.kv_heads - 1) * a.cache.head_stride >= ((int64_t)8 << 32) - 256)
     return MOE_EUNSUPPORTED;
   // the list of (request, head, tile) is numbered in 32 bits
-  if (((int64_t)a.table_width * a.cache.page_size / 64 + 1) * a.n_req * a.kv_heads >= ((int64_t)1 << 31))
+  if (((int64_t)a.table_width * a.cache.page_size / 64 + 1 + kUnit) * a.n_req * a.kv_heads >= ((int64_t)1 << 31))
     return MOE_EUNSUPPORTED;
   if (!stride_ok(a.q_stride) || !stride_ok(a.out_stride)) return MOE_EINVAL;
   if (!ptr_ok(a.dev_status, 4) || !ptr_ok(a.row_start, 4) || !ptr_ok(a.ctx_len, 4) || !ptr_ok(a.block_table, 4) ||
