@@ -274,7 +274,8 @@ __device__ __forceinline__ Req request(const moe_tree_attention_args& a, int b) 
 }
 
 // Taking up a head costs about as long as a few tiles (its queries, the first scores, the end
-// of its sums), so in the list each head has kUnit places ahead of those of its tiles.
+// of its sums), so in the list each head has kUnit places ahead of those of its tiles: with
+// 0 a ragged batch of 33 requests took 100.5 us, with 2 68.8, with 3 60.8, with 5 60.0.
 constexpr int kUnit = 3;
 
 template <int D>
@@ -487,6 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
         if (t + 1 < wk.t1) look(t + 1);
+        // a row's place to the lanes that copy it; all of them ahead of the copies, which would
+        // otherwise each wait for their own exchange
+        uint32_t from[Sh::STEPS];
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k)
+          from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
         const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
         ok = bar_wait(&ct.empty[slot], phase, ct, a.dev_status) &&
              bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status);
@@ -497,14 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint4* v_src = static_cast<const uint4*>(a.cache.v) + chunk;
           const uint32_t k_dst = kv0 + slot * Sh::kSlot + (chunk >> 3) * kBlk;
           const uint32_t v_dst = kv0 + v_slot * Sh::kSlot + (chunk >> 3) * kBlk;
-#pragma unroll 11
+#pragma unroll
           for (int k = 0; k < Sh::STEPS; ++k) {
-            const int g = k * kProducers + pw, r = g * RPI + sub, mine = k * RPI + sub;
-            const uint32_t from = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], mine & 31);
-            const uint32_t to = r * 128 + (((chunk & 7) ^ (r & 7)) << 4), off = from == kNone ? 0 : from;
-            if (g < KT / RPI) {
-              copy16(k_dst + to, k_src + off, from != kNone);
-              copy16(v_dst + to, v_src + off, from != kNone);
+            const int g = k * kProducers + pw, r = g * RPI + sub;
+            const uint32_t to = r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+            const bool there = from[k] != kNone;
+            const uint32_t off = there ? from[k] : 0;
+            if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
+              copy16(k_dst + to, k_src + off, there);
+              copy16(v_dst + to, v_src + off, there);
             }
           }
         }
