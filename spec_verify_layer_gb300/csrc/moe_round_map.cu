@@ -13,7 +13,8 @@ namespace moe {
 namespace {
 
 constexpr int kMapThreads = 256;
-constexpr int kMapRows = 4 * kMapThreads;  // rows per block and step: four a thread, 16-byte stores
+constexpr int kMapRows = 4 * kMapThreads;  // rows per block and step
+constexpr int kMapPer = 2;  // requests of a thread at a time
 constexpr int kMapMaxReq = 16384;
 constexpr int kTree = 64;  // rows of a tree: bits of a mask
 
@@ -72,13 +73,29 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
   unsigned flags = 0;
   const bool lead = blockIdx.x == 0;
 
+  // the first step's parents travel meanwhile (those of its rows and of the 63 before them,
+  // which may be of the same tree)
+  const auto fetch_parents = [&](int base) {
+    const int lo = max(0, base - (kTree - 1)), hi = min(a.n_rows, base + kMapRows);
+    for (int r = lo + tid; r < hi; r += kMapThreads) par[r - lo] = a.parents[r];
+  };
+  if (a.parents) fetch_parents(blockIdx.x * kMapRows);
+
+  // kMapPer neighbouring requests a thread: their lengths are loaded together
   uint2 carry = make_uint2(0u, 0u);
-  for (int b0 = 0; b0 < a.n_req; b0 += kMapThreads) {
-    const int b = b0 + tid;
-    Req q{0, 0, 0, 0};
+  for (int b0 = 0; b0 < a.n_req; b0 += kMapThreads * kMapPer) {
+    const int b = b0 + tid * kMapPer;
+    Req q[kMapPer];
     unsigned f = 0;
-    if (b < a.n_req) q = request(a, by, b, f);
-    uint2 v = make_uint2((uint32_t)q.rows, (uint32_t)q.take), incl = v;
+    uint2 sum = make_uint2(0u, 0u);
+#pragma unroll
+    for (int j = 0; j < kMapPer; ++j) {
+      q[j] = Req{0, 0, 0, 0};
+      if (b + j < a.n_req) q[j] = request(a, by, b + j, f);
+    }
+#pragma unroll
+    for (int j = 0; j < kMapPer; ++j) sum = make_uint2(add_sat(sum.x, (uint32_t)q[j].rows), add_sat(sum.y, (uint32_t)q[j].take));
+    uint2 incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
@@ -88,27 +105,34 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
       }
     }
     if (lane == 31) wsum[warp] = incl;
+    // what lies before this thread's requests: the lanes below, the warps below, the steps before
+    uint2 before = make_uint2(__shfl_up_sync(0xffffffffu, incl.x, 1), __shfl_up_sync(0xffffffffu, incl.y, 1));
+    if (lane == 0) before = make_uint2(0u, 0u);
     __syncthreads();
-    uint2 before = carry;
+    before = make_uint2(add_sat(before.x, carry.x), add_sat(before.y, carry.y));
+#pragma unroll
     for (int w = 0; w < kMapThreads / 32; ++w) {
       const uint2 s = wsum[w];
       if (w < warp) before = make_uint2(add_sat(before.x, s.x), add_sat(before.y, s.y));
       carry = make_uint2(add_sat(carry.x, s.x), add_sat(carry.y, s.y));
     }
     __syncthreads();
-    incl = make_uint2(add_sat(incl.x, before.x), add_sat(incl.y, before.y));
-    if (b < a.n_req) {
-      const uint32_t end = min(incl.x, (uint32_t)a.n_rows);
-      start[b + 1] = end;
-      off[b + 1] = incl.y;
+#pragma unroll
+    for (int j = 0; j < kMapPer; ++j) {
+      if (b + j >= a.n_req) break;
+      const uint32_t fresh = before.y;
+      before = make_uint2(add_sat(before.x, (uint32_t)q[j].rows), add_sat(before.y, (uint32_t)q[j].take));
+      const uint32_t end = min(before.x, (uint32_t)a.n_rows);
+      start[b + j + 1] = end;
+      off[b + j + 1] = before.y;
       if (lead) {
-        flags |= f;
-        const long long got = min((long long)q.take, max(0LL, (long long)a.n_free - (incl.y - v.y)));
-        if (got < q.take) flags |= MOE_DEV_PAGES;
-        a.row_start[b + 1] = (int)end;
-        a.pages[b] = q.held + (int)got;
+        const long long got = min((long long)q[j].take, max(0LL, (long long)a.n_free - fresh));
+        if (got < q[j].take) flags |= MOE_DEV_PAGES;
+        a.row_start[b + j + 1] = (int)end;
+        a.pages[b + j] = q[j].held + (int)got;
       }
     }
+    if (lead) flags |= f;
   }
   if (tid == 0) {
     start[0] = 0;
@@ -131,102 +155,64 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
         t < (uint32_t)a.n_free ? checked_page(a, a.free_pages[t], flags) : -1;
   }
 
-  // rows, four in a row to a thread
+  // rows: a rolled loop, since a small call is as long as its instructions take to arrive
   const int live = (int)start[a.n_req];
   for (int base = blockIdx.x * kMapRows; base < a.n_rows; base += gridDim.x * kMapRows) {
-    if (a.parents) {  // this step's rows and the 63 before them, which may be of the same tree
+    if (a.parents && base != (int)blockIdx.x * kMapRows) {
       __syncthreads();
-      const int lo = max(0, base - (kTree - 1)), hi = min(live, base + kMapRows);
-      for (int r = lo + tid; r < hi; r += kMapThreads) par[r - lo] = a.parents[r];
+      fetch_parents(base);
       __syncthreads();
     }
-    const int par0 = max(0, base - (kTree - 1));
-    const int r0 = base + 4 * tid;
-    if (r0 >= a.n_rows) continue;
-    int req[4], pos[4], slot[4];
-    uint64_t mask[4];
-    int b = r0 < live ? last_not_above(start, a.n_req, (uint32_t)r0) : 0;
-    Req q{0, 0, 0, 0};
-    int off_in = 0, col = 0, page = -1;  // place in the page, table column, page of the row
-    bool have = false;                   // (of request b, up to date for the row before)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + j;
-      req[j] = -1;
-      pos[j] = 0;
-      slot[j] = -1;
-      mask[j] = 0;
-      if (r >= live) continue;
-      while (r >= (int)start[b + 1]) {
-        ++b;
-        have = false;
-      }
-      const int s = (int)start[b], i = r - s;
-      bool turn = true;  // another page
-      if (!have) {
-        q = request(a, by, b, quiet);
-        have = true;
-        col = by(q.ctx + i);
-        off_in = q.ctx + i - col * a.page_size;
-      } else if (++off_in == a.page_size) {
-        off_in = 0;
-        ++col;
-      } else {
-        turn = false;
-      }
-      if (turn) {
-        page = -1;
+    const int par0 = max(0, base - (kTree - 1)), stop = min(a.n_rows, base + kMapRows);
+    int b = base + tid < live ? last_not_above(start, a.n_req, (uint32_t)(base + tid)) : 0, known = -1;
+    Req q{0, 0, 0, 0};  // of request `known`
+#pragma unroll 1
+    for (int r = base + tid; r < stop; r += kMapThreads) {
+      int req = -1, pos = 0, slot = -1;
+      uint64_t mask = 0;
+      if (r < live) {
+        while (r >= (int)start[b + 1]) ++b;
+        if (b != known) {
+          q = request(a, by, b, quiet);
+          known = b;
+        }
+        req = b;
+        const int s = (int)start[req], i = r - s, p = q.ctx + i, col = by(p);
+        int page = -1;
         if (col < q.held) {
-          page = checked_page(a, a.block_table[(size_t)b * a.table_width + col], flags);
+          page = checked_page(a, a.block_table[(size_t)req * a.table_width + col], flags);
         } else if (col - q.held < q.take) {
-          const uint32_t t = off[b] + (uint32_t)(col - q.held);
+          const uint32_t t = off[req] + (uint32_t)(col - q.held);
           if (t < (uint32_t)a.n_free) page = checked_page(a, a.free_pages[t], flags);
         }
-      }
-      int depth = i;
-      if (a.parents) {
-        if (i < kTree) {
-          uint64_t m = 0;
-          depth = -1;
-          for (int n = i; n >= 0;) {  // n falls with every step
-            m |= 1ull << n;
-            ++depth;
-            const int up = par[s + n - par0];
-            if (up < -1 || up >= n) {
-              flags |= MOE_DEV_INDEX;
-              break;
+        int depth = i;
+        if (a.parents) {
+          if (i < kTree) {
+            depth = -1;
+            for (int n = i; n >= 0;) {  // n falls with every step
+              mask |= 1ull << n;
+              ++depth;
+              const int up = par[s + n - par0];
+              if (up < -1 || up >= n) {
+                flags |= MOE_DEV_INDEX;
+                break;
+              }
+              n = up;
             }
-            n = up;
+          } else {
+            flags |= MOE_DEV_LENGTH;
           }
-          mask[j] = m;
-        } else {
-          flags |= MOE_DEV_LENGTH;
+        } else if (a.tree_mask) {
+          if (i < kTree) mask = i == kTree - 1 ? ~0ull : (2ull << i) - 1;
+          else flags |= MOE_DEV_LENGTH;
         }
-      } else if (a.tree_mask) {
-        if (i < kTree) mask[j] = i == kTree - 1 ? ~0ull : (2ull << i) - 1;
-        else flags |= MOE_DEV_LENGTH;
+        pos = (int)min((long long)q.ctx + depth, 0x7fffffffLL);
+        slot = page < 0 ? -1 : page * a.page_size + (p - col * a.page_size);
       }
-      req[j] = b;
-      pos[j] = (int)min((long long)q.ctx + depth, 0x7fffffffLL);
-      slot[j] = page < 0 ? -1 : page * a.page_size + off_in;
-    }
-    if (r0 + 4 <= a.n_rows) {
-      *reinterpret_cast<int4*>(a.row_req + r0) = make_int4(req[0], req[1], req[2], req[3]);
-      *reinterpret_cast<int4*>(a.row_pos + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(a.row_slot + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-      if (a.tree_mask) {
-        *reinterpret_cast<ulonglong2*>(a.tree_mask + r0) = make_ulonglong2(mask[0], mask[1]);
-        *reinterpret_cast<ulonglong2*>(a.tree_mask + r0 + 2) = make_ulonglong2(mask[2], mask[3]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        if (r0 + j >= a.n_rows) break;
-        a.row_req[r0 + j] = req[j];
-        a.row_pos[r0 + j] = pos[j];
-        a.row_slot[r0 + j] = slot[j];
-        if (a.tree_mask) a.tree_mask[r0 + j] = mask[j];
-      }
+      a.row_req[r] = req;
+      a.row_pos[r] = pos;
+      a.row_slot[r] = slot;
+      if (a.tree_mask) a.tree_mask[r] = mask;
     }
   }
   if (flags) atomicOr(a.dev_status, flags);
@@ -265,9 +251,10 @@ extern "C" int moe_round_map(const moe_map_args* p, void* stream) {
   while ((1 << bits) < a.page_size) ++bits;
   by.shift = 31 + bits;
   by.mul = (unsigned)((1ull << by.shift) / (unsigned)a.page_size + 1);
-  // one step's rows to a block, up to two blocks an SM: more blocks only repeat the sums
+  // one step's rows to a block, up to four blocks an SM: what each repeats of the sums is a
+  // latency that the others share
   const int steps = (a.n_rows + kMapRows - 1) / kMapRows;
-  const int grid = steps < 1 ? 1 : steps > 2 * sms ? 2 * sms : steps;
+  const int grid = steps < 1 ? 1 : steps > 4 * sms ? 4 * sms : steps;
   k_round_map<<<grid, kMapThreads, smem, static_cast<cudaStream_t>(stream)>>>(a, by);
   return launch_status(cudaGetLastError());
 }

@@ -58,6 +58,27 @@ def test_ragged_batches():
         good(TreeCase(seed, ctx.tolist(), n.tolist(), hq=8, hkv=2, d=64, page=16, dtype="bf16"))
 
 
+@pytest.mark.parametrize("req", [383, 384, 385, 900])
+def test_more_requests_than_threads(req):
+    rng = np.random.default_rng(req)
+    ctx = rng.integers(0, 200, req)
+    n = rng.integers(0, 5, req)
+    n[::11] = 0
+    good(TreeCase(req, ctx.tolist(), n.tolist(), hq=4, hkv=1, d=64, page=16, dtype="bf16"))
+
+
+def test_many_groups_of_query_rows():
+    """Sixty-four heads to a key and 64 rows: sixteen groups of 256 query rows, some requests with fewer."""
+    good(TreeCase(19, [700, 40, 0], [64, 9, 33], hq=64, hkv=1, d=128, page=16, dtype="bf16"))
+    good(TreeCase(20, [300, 1], [20, 3], hq=128, hkv=2, d=64, page=16, dtype="f16"))
+    good(TreeCase(21, [3000], [24], hq=64, hkv=1, d=256, page=32, dtype="bf16"))
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_long_contexts_of_other_head_sizes(d):
+    good(TreeCase(22, [15000, 8000], [16, 33], hq=16, hkv=2, d=d, page=24, dtype="f16", layout="hnd"))
+
+
 def test_one_long_request_among_short_ones():
     good(TreeCase(3, [3, 9000, 0, 17, 40], [2, 20, 1, 0, 64], hq=16, hkv=2, d=128, page=32, dtype="bf16"))
 
