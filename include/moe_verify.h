@@ -432,6 +432,9 @@ int moe_qk_rope_cache(const moe_qk_rope_args* args, void* stream);
  * NaN included).  With n_b = 1 this is the decode step of a single token.
  * The softmax weights are rounded to the element type for the product with v (their sum
  * is not); everything else stays in 32 bits until out is rounded.
+ * How the keys of a head are cut up follows the lengths of the whole call, so a row's last
+ * bits may change with the lengths of other requests; not with anything else of them, and
+ * the same call gives the same bits again.
  *   q, out [n_rows][q_heads][D], the strides from row to row in elements (multiples of
  *   8); lse fp32 [n_rows][q_heads] or NULL; row_start [n_req + 1] and ctx_len [n_req] as
  *   moe_round_map writes and reads them (4-byte aligned is enough).  Rows that belong to

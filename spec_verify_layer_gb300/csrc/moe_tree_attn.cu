@@ -28,6 +28,11 @@
 // weights then stay below 2^8 and the sums are exact in relative terms), so the pass over
 // O in tensor memory is rare after the first tiles.
 //
+// Tried and slower: scores of 64 keys in two buffers a stream (full trees 507 us against 372
+// of that time: the tensor cores read a query tile for each product, whatever its width);
+// two threads a row, 16 softmax warps (377 against 304); the softmax unrolled over a whole
+// tile (393: it spills).
+//
 // What is not seen gets the weight 0, but 0 times a cached NaN would still be NaN in the
 // product: slots past the last position are zero-filled, and the values of drafted rows
 // are looked over on their way: what is not finite becomes 0 in the slot and is added at
@@ -795,7 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             const bool far = m == -INFINITY ? top > -INFINITY : (top - m) * c > kRescale;
             if (__any_sync(0xffffffffu, far)) {
-              const float to = fmaxf(m, top), f = m == -INFINITY ? 0.f : exp2_fast((m - to) * c);
+              // row by row: what the rows beside it do leaves a row's bits as they are
+              const float to = far ? top : m, f = !far ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - to) * c);
               if (ti > ti0) {  // O holds something
                 if (!last_product()) break;
 #pragma unroll 1

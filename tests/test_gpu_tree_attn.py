@@ -176,6 +176,16 @@ def test_repeats_are_equal_bit_for_bit():
         assert status == 0 and torch.equal(out, o2) and torch.equal(lse, l2)
 
 
+def test_rows_do_not_depend_on_what_ran_before():
+    """Row counts that leave lanes of a warp without a row: whatever an earlier call left there has no say."""
+    case = TreeCase(23, [2000, 300, 41], [5, 3, 7], hq=6, hkv=2, d=64, page=24, dtype="f16", layout="hnd")
+    out, lse, _ = case.run()
+    for seed in (24, 25):
+        TreeCase(seed, [900, 80], [40, 64], hq=16, hkv=2, d=64, page=16, dtype="f16", q_scale=30.0).run()
+        o2, l2, status = case.run()
+        assert status == 0 and torch.equal(out, o2) and torch.equal(lse, l2)
+
+
 def test_bad_lengths_are_reported_and_left_out():
     case = TreeCase(14, [30, 100, 20], [5, 8, 2], hq=8, hkv=2, d=64, page=16, dtype="bf16")
     out, lse, status = case.run(ctx=i32([30, 10**6, -4]))
