@@ -24,9 +24,11 @@
 // split over blocks leave unnormalised sums with their maximum in the workspace; when the
 // last of its blocks has arrived, each of them joins some of the rows, in block order.
 //
-// Running maximum: O is rescaled only when a row's maximum rises by more than 2^8 (the
-// weights then stay below 2^8 and the sums are exact in relative terms), so the pass over
-// O in tensor memory is rare after the first tiles.
+// Running maximum: it is the largest of the first scores seen, and moves only when a score is
+// above it by more than 2^14 (fp16 weights then stay below their largest value, and sums
+// are as exact relative to themselves).  So a tile's weights need no pass over its scores
+// for the maximum first (full trees 302 us with such a pass, 280 without; 296 with 2^8 as
+// the threshold); a tile that moves a row's maximum is gone through again, with O rescaled.
 //
 // Tried and slower: scores of 64 keys in two buffers a stream (full trees 507 us against 372
 // of that time: the tensor cores read a query tile for each product, whatever its width);
@@ -49,7 +51,7 @@ constexpr int kThreads = 384;  // 8 softmax warps, 3 producer warps, 1 issuing w
 constexpr int kSoftmaxThreads = 256, kProducers = 3;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
-constexpr float kRescale = 8.0f;        // log2 of how far a maximum may lag behind
+constexpr float kRescale = 14.0f;       // log2 of how far a maximum may lag behind
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 
 template <int D>
@@ -211,13 +213,6 @@ __device__ __forceinline__ void tm_read(uint32_t* r, uint32_t addr) {
   tm_wait();
   ready(r);
 }
-__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -280,8 +275,9 @@ __device__ __forceinline__ Req request(const moe_tree_attention_args& a, int b) 
 
 // Taking up a head costs about as long as a few tiles (its queries, the first scores, the end
 // of its sums), so in the list each head has kUnit places ahead of those of its tiles: with
-// 0 a ragged batch of 33 requests took 100.5 us, with 2 68.8, with 3 60.8, with 5 60.0.
-constexpr int kUnit = 3;
+// 0 a ragged batch of 33 requests took 100.5 us, with 2 68.8, with 3 60.8, with 5 60.0; one
+// row over 1,000 keys 14.2 with 3, 13.3 with 4.
+constexpr int kUnit = 4;
 
 template <int D>
 struct Walk {  // a block's share, unit (stretch of one head's tiles) after unit
@@ -685,17 +681,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = member * Sh::MG, rows = min(Sh::MG, wk.q.n * G - m0);
       if (rows <= 0 || wk.t0 == wk.t1) continue;
       const bool two = NS == 2 && rows > 128;
-      // the group's queries into the swizzle (a rolled loop: it runs once a unit, and its
-      // instructions have to come from memory the first time)
+      // the group's queries into the swizzle, zeros in the rows of nobody (a rolled loop: it runs
+      // once a unit, and its instructions have to come from memory the first time)
       const auto q_at = [&](int i) {
         const int r = i / CPR, ch = i % CPR;
         return q0 + (r >> 7) * Sh::kQ + (ch >> 3) * (128 * 128) + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
       };
 #pragma unroll 1
-      for (int i = tid; i < rows * CPR; i += kSoftmaxThreads) {
-        const int mi = m0 + i / CPR, n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, g = mi - n * G;
+      for (int i = tid; i < (two ? 256 : 128) * CPR; i += kSoftmaxThreads) {
+        const int mi = min(m0 + i / CPR, m0 + rows - 1), n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, g = mi - n * G;
         copy16(q_at(i), static_cast<const uint16_t*>(a.q) + (long long)(wk.q.s + n) * a.q_stride + (wk.h * G + g) * D + i % CPR * 8,
-               true);
+               i < rows * CPR);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (p.flip) {
@@ -768,10 +764,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               return bits;
             };
-            // 64 scores of a row in registers at a time: a pass for the maximum, a pass for the
-            // weights, the last keys first (their place is the one that is read already).  The
-            // halves are rolled loops and the mask a branch inside: this code is fetched anew by
-            // every launch, and its length shows in the short ones.
+            // 64 scores of a row in registers at a time, the last keys first (the weights go where
+            // scores were that are read already).  Weights are taken from the running maximum as
+            // it stands, or from the first scores seen; only when a score is above it by more
+            // than the threshold, which the last scores' maximum tells before any weight is
+            // handed over, the tile is gone through again.  The halves are a rolled loop and the
+            // mask a branch inside: this code is fetched anew by every launch, and its length
+            // shows in the short ones.
             uint32_t x[64];
             const auto fetch = [&](int half) {
               const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
@@ -790,54 +789,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             };
-            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-            for (int half = 0; half < Sh::PARTS; ++half) {
-              fetch(half);
-#pragma unroll
-              for (int j = 0; j < 64; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
-            }
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            const bool far = m == -INFINITY ? top > -INFINITY : (top - m) * c > kRescale;
-            if (__any_sync(0xffffffffu, far)) {
-              // row by row: what the rows beside it do leaves a row's bits as they are
-              const float to = far ? top : m, f = !far ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - to) * c);
-              if (ti > ti0) {  // O holds something
-                if (!last_product()) break;
-#pragma unroll 1
-                for (int w = 0; w < D / 32; ++w) {
-                  uint32_t y[32];
-                  tm_read(y, lanes + Sh::o_col(o) + 32 * w);
-#pragma unroll
-                  for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                  tm_store32(lanes + Sh::o_col(o) + 32 * w, y);
-                }
-                tm_wait_store();
-              }
-              l *= f;
-              m = to;
-            }
-            const float shift = m == -INFINITY ? 0.f : m * c;
-            const Pair c2 = pair(c, c), shift2 = pair(-shift, -shift);
+            const Pair c2 = pair(c, c);
             Pair sums[2] = {0, 0};
+            float top = -INFINITY;
+            uint32_t y[32];
 #pragma unroll 1
             for (int half = Sh::PARTS - 1; half >= 0; --half) {
-              if (Sh::PARTS > 1) fetch(half);  // (one part: still there)
+              fetch(half);
+              float tops[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                uint32_t y[16];
+              for (int j = 0; j < 64; ++j) tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
+              top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+              if (m == -INFINITY) m = top;  // every weight so far was 0
+              if (half == 0) {
+                const bool far = mr < rows && (top - m) * c > kRescale;
+                if (__any_sync(0xffffffffu, far)) {
+                  // row by row: what the rows beside it do leaves a row's bits as they are
+                  const float f = far ? exp2_fast((m - top) * c) : 1.f;
+                  if (ti > ti0) {  // O holds something
+                    if (!last_product()) break;
+#pragma unroll 1
+                    for (int w = 0; w < D / 32; ++w) {
+                      tm_read(y, lanes + Sh::o_col(o) + 32 * w);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const int k = 32 * w + 2 * j;
-                  const float2 z = split(fma2(pair(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), c2, shift2));
-                  const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                  sums[j & 1] = add2(sums[j & 1], pair(e0, e1));
-                  y[j] = pack2<DT>(e0, e1);
+                      for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                      tm_store32(lanes + Sh::o_col(o) + 32 * w, y);
+                    }
+                    tm_wait_store();
+                  }
+                  l *= f;
+                  if (far) m = top;
+                  sums[0] = sums[1] = 0;
+                  half = Sh::PARTS;
+                  continue;
                 }
-                tm_store16(lanes + Sh::p_col(buf) + 32 * half + 16 * w, y);
+                if (Sh::PARTS > 1) {
+                  tm_store32(lanes + Sh::p_col(buf) + 32, y);
+                  hand_over(1);
+                }
               }
-              if (half == 1) hand_over(1);
+              const float shift = m == -INFINITY ? 0.f : m * c;
+              const Pair shift2 = pair(-shift, -shift);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float2 z = split(fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, shift2));
+                const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                sums[j & 1] = add2(sums[j & 1], pair(e0, e1));
+                y[j] = pack2<DT>(e0, e1);
+              }
             }
+            if (!ok) break;
+            tm_store32(lanes + Sh::p_col(buf), y);
             const float2 sum = split(add2(sums[0], sums[1]));
             l += sum.x + sum.y;
           } else if (KT == 128) {
