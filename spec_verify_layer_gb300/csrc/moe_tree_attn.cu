@@ -14,7 +14,7 @@
 //   - three producer warps copy key and value rows (cp.async, 16 bytes a lane, page table
 //     looked up per row) into a ring of shared-memory slots in the 128-byte swizzle that
 //     the tensor cores read;
-//   - one thread issues the products: S = Q K^T into tensor memory, and O += P V with P
+//   - one warp issues the products: S = Q K^T into tensor memory, and O += P V with P
 //     read from tensor memory and V from its slot as it lies (no transpose is stored);
 //   - two warpgroups do the softmax, a thread per query row: S out of tensor memory,
 //     running maximum and sum in registers, P back over S as 16-bit weights.
@@ -186,6 +186,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 __device__ __forceinline__ void mma_commit(unsigned long long* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+// One lane of a warp whose lanes are all here.
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
 }
 // The registers of a load are ready after tm_wait; `ready` makes their users wait for it
 // (a volatile statement alone would not keep plain arithmetic behind it).
@@ -573,13 +579,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 10) {
-    // ---------------- issue of the products
-    if (lane == 0) {
+    // ---------------- issue of the products.  The warp goes through the loop as one and one lane
+    // of it issues, so that the operands, which are the same for all lanes, can be held as
+    // such (issued by a thread on its own: full trees 283 us against 258).
+    const auto same = [](auto v) { return __shfl_sync(0xffffffffu, v, 0); };
+    {
       constexpr uint32_t id_s = instruction<DT>(KT, false), id_o = instruction<DT>(D, true);
       const uint64_t kv0 = operand(smem_u32(sm_kv), kBlk), q0 = operand(smem_u32(sm_q), 0);
+      const uint32_t tm = same(tmem);
       int k_slot = 0, v_slot = 1;       // slots of the next key and value tile
       uint32_t k_ph = 0, v_ph = 0, p_par = 0, q_ph = 0;
       bool ok = true;
+      const auto wait = [&](unsigned long long* b, uint32_t parity) {
+        return __all_sync(0xffffffffu, bar_wait(b, parity, ct, a.dev_status)) != 0;
+      };
+      const auto commit = [&](unsigned long long* b) {
+        if (elected()) mma_commit(b);
+        __syncwarp();
+      };
       const auto take = [&](int& s, uint32_t& ph) {  // key and value tiles take turns in the ring
         s += 2;
         if (s >= p.nslot) {
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       const auto wait_p = [&](int buf) {
-        if (!bar_wait(&ct.p_full[buf], p_par >> buf & 1, ct, a.dev_status)) return false;
+        if (!wait(&ct.p_full[buf], p_par >> buf & 1)) return false;
         p_par ^= 1u << buf;
         fence_after();
         return true;
@@ -596,42 +613,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (addresses in descriptors are in units of 16 bytes)
       const auto scores = [&](int buf, int qt) {  // S_buf = Q_qt K^T
         const uint64_t qa = q0 + qt * (Sh::kQ >> 4), kb = kv0 + k_slot * (Sh::kSlot >> 4);
+        if (elected()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + Sh::s_col(buf), qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2,
-                 kb + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, id_s, k > 0);
-        mma_commit(&ct.s_full[buf]);
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tm + Sh::s_col(buf), qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2,
+                   kb + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, id_s, k > 0);
+          mma_commit(&ct.s_full[buf]);
+        }
+        __syncwarp();
       };
       const auto values = [&](int buf, int s, bool first) {  // O_s += P_buf V, as the parts come, the last keys first
         const uint64_t vb = kv0 + v_slot * (Sh::kSlot >> 4);
 #pragma unroll
         for (int part = Sh::PARTS - 1; part >= 0; --part) {
           if (!wait_p(2 * buf + part)) return false;
+          if (elected()) {
 #pragma unroll
-          for (int k = 4 * part; k < 4 * part + 4; ++k)
-            mma_ts(tmem + Sh::o_col(s), tmem + Sh::p_col(buf) + k * 8, vb + k * (2048 >> 4), id_o,
-                   !(first && k == 4 * (Sh::PARTS - 1)));
+            for (int k = 4 * part; k < 4 * part + 4; ++k)
+              mma_ts(tm + Sh::o_col(s), tm + Sh::p_col(buf) + k * 8, vb + k * (2048 >> 4), id_o,
+                     !(first && k == 4 * (Sh::PARTS - 1)));
+            if (part == 0) mma_commit(&ct.o_done[s]);
+          }
+          __syncwarp();
         }
-        mma_commit(&ct.o_done[s]);
         return true;
       };
       const auto wait_tile = [&](int slot, uint32_t ph) {
-        if (!bar_wait(&ct.full[slot], ph, ct, a.dev_status)) return false;
+        if (!wait(&ct.full[slot], ph)) return false;
         fence_async();  // the copies were ordinary writes: order them before the tensor cores' reads
         return true;
       };
       const auto free_tile = [&](int& slot, uint32_t& ph) {
-        mma_commit(&ct.empty[slot]);
+        commit(&ct.empty[slot]);
         take(slot, ph);
       };
       for (; ok && wk.more(); wk.next(a)) {
-        const int rows = min(Sh::MG, wk.q.n * G - member * Sh::MG);
-        if (rows <= 0 || wk.t0 == wk.t1) continue;
+        const int rows = same(min(Sh::MG, wk.q.n * G - member * Sh::MG)), nt = same(wk.t1 - wk.t0);
+        if (rows <= 0 || nt == 0) continue;
         const bool two = NS == 2 && rows > 128;
-        if (!(ok = bar_wait(&ct.q_ready, q_ph, ct, a.dev_status))) break;
+        if (!(ok = wait(&ct.q_ready, q_ph))) break;
         q_ph ^= 1;
         fence_after();
-        const int nt = wk.t1 - wk.t0;
         if (two) {
           // both streams, tile after tile
           for (int t = 0; ok && t <= nt; ++t) {
@@ -665,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      mma_commit(&ct.drain);  // nothing runs on when the block ends
-      bar_wait(&ct.drain, 0, ct, a.dev_status);
+      commit(&ct.drain);  // nothing runs on when the block ends
+      wait(&ct.drain, 0);
     }
   } else {
     // ---------------- softmax
