@@ -30,10 +30,25 @@
 // for the maximum first (full trees 302 us with such a pass, 280 without; 296 with 2^8 as
 // the threshold); a tile that moves a row's maximum is gone through again, with O rescaled.
 //
+// What it takes (GB300, one launch in a stream of them): full trees (40 and 64 rows of 32/4 heads
+// of 128 over 131,071 and 200,001 keys) 255 us, 1,110 TFLOP/s of the 1,975 that a large library
+// product reaches, 2.7 TB/s; 16 rows of one request over 32,768 keys 26.8 us, 2.5 TB/s; 33
+// ragged requests of 16/8 heads of 64, 58 us, 3.5 TB/s; one row over 1,000 keys 12.4 us.
+// Full trees are bound by the chain of a stream (of the 3,110 cycles of a tile in both streams:
+// scores out to weights back 1,700 to 1,900, products and scores of the next 1,200 to 1,400;
+// the tensor cores work 2,048 of them, 64 for each product of 128 x 128 x 16, as operands
+// that come out of shared memory allow).  The others are bound by latency: some 6 us from the launch
+// to the first weights (lengths, page table, keys: one after the other from memory, and code
+// that is fetched for the first time), and 3.5 us for the join of a split head.
+//
 // Tried and slower: scores of 64 keys in two buffers a stream (full trees 507 us against 372
 // of that time: the tensor cores read a query tile for each product, whatever its width);
 // two threads a row, 16 softmax warps (377 against 304); the softmax unrolled over a whole
-// tile (393: it spills).
+// tile (393: it spills); a second issuing warp in the place of a producer (349 against 306);
+// looking at the next barriers between two products (340 against 283: products are issued
+// as they are done, and what stands between them is added to the chain) or at all that a
+// stream waits for in one go (267 against 260); the first half's weights handed over in
+// the middle of the second half's exponentials (263 against 256).
 //
 // What is not seen gets the weight 0, but 0 times a cached NaN would still be NaN in the
 // product: slots past the last position are zero-filled, and the values of drafted rows
@@ -622,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      const auto values = [&](int buf, int s, bool first) {  // O_s += P_buf V, as the parts come, the last keys first
+      const auto values = [&](int buf, int s, bool first, bool last) {  // O_s += P_buf V, as the parts come, the last keys first
         const uint64_t vb = kv0 + v_slot * (Sh::kSlot >> 4);
 #pragma unroll
         for (int part = Sh::PARTS - 1; part >= 0; --part) {
@@ -632,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 4 * part; k < 4 * part + 4; ++k)
               mma_ts(tm + Sh::o_col(s), tm + Sh::p_col(buf) + k * 8, vb + k * (2048 >> 4), id_o,
                      !(first && k == 4 * (Sh::PARTS - 1)));
-            if (part == 0) mma_commit(&ct.o_done[s]);
+            if (part == 0 && (NS == 1 || last)) mma_commit(&ct.o_done[s]);
           }
           __syncwarp();
         }
@@ -660,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
               if (t > 0) {
-                ok = (s == 1 || wait_tile(v_slot, v_ph)) && values(s, s, t == 1);
+                ok = (s == 1 || wait_tile(v_slot, v_ph)) && values(s, s, t == 1, t == nt);
                 if (!ok) break;
                 if (s == 1) free_tile(v_slot, v_ph);
               }
@@ -680,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               free_tile(k_slot, k_ph);
             }
             if (t > 0) {
-              ok = wait_tile(v_slot, v_ph) && values((t - 1) & 1, NS == 2 ? (t - 1) & 1 : 0, t <= NS);
+              ok = wait_tile(v_slot, v_ph) && values((t - 1) & 1, NS == 2 ? (t - 1) & 1 : 0, t <= NS, t >= nt - 1);
               if (!ok) break;
               free_tile(v_slot, v_ph);
             }
@@ -868,13 +883,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             hand_over(1);
           }
           if (!last_product()) break;
-          ++o_cnt;
+          if (NS == 1) ++o_cnt;
           hand_over(0);
         }
       }
       tile_seq += nt;
       // every product of the unit is done when the last of each stream is
       const bool used = NS == 1 ? wg == 0 : two || nt > wg;
+      if (NS == 2 && used) ++o_cnt;  // (the issuing warp says so once a unit)
       if (ok && used)
         ok = __all_sync(0xffffffffu, bar_wait(&ct.o_done[o], (o_cnt - 1) & 1, ct, a.dev_status));
       fence_after();
