@@ -18,6 +18,12 @@
 //
 // With few rows a row is cut into 2^i slices, up to 32; the block that ends last joins the
 // slices' partials in their order, so the result does not depend on which one that is.
+//
+// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 192 us, 5.4
+// TB/s of the 6.8 that a large copy reaches; what is missing is exponentials and
+// comparisons between loads, at five blocks an SM (more slices a row than the SMs need:
+// 231 and 278 us).  16 rows of 131,072 in 16 bits take 12.6 us in a graph and 5 of 32,003
+// 8.0: a chunk's latency, the first list, and the join one after the other.
 #include <type_traits>
 
 #include "moe_common.cuh"

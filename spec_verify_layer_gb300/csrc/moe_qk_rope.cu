@@ -17,6 +17,11 @@
 // overflow drops the whole turns; its error is at most |pos| * 2^-52 turns for f_i < 1,
 // 1.4e-9 rad at 10^6 and 3e-6 rad at 2^31.  The top 32 bits go to float as half turns in
 // [-1, 1).
+//
+// What bounds it (GB300): memory.  16,384 rows of 32 + 2 * 4 heads of 128 (336 MB) take 57.4 us,
+// 5.85 TB/s of the 6.80 that a large copy reaches; a plain copy of this size takes 55.4.  A
+// warp a row took 103 us, values in registers instead of the ring 79.8.  Few rows are
+// bound by latency: one row 3.0 us in a graph, 701 rows of 24 + 2 * 8 heads of 64 (14.4 MB) 4.3.
 #include "moe_round_ops.cuh"
 
 namespace moe {

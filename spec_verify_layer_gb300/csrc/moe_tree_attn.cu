@@ -44,11 +44,10 @@
 // Tried and slower: scores of 64 keys in two buffers a stream (full trees 507 us against 372
 // of that time: the tensor cores read a query tile for each product, whatever its width);
 // two threads a row, 16 softmax warps (377 against 304); the softmax unrolled over a whole
-// tile (393: it spills); a second issuing warp in the place of a producer (349 against 306);
-// looking at the next barriers between two products (340 against 283: products are issued
-// as they are done, and what stands between them is added to the chain) or at all that a
-// stream waits for in one go (267 against 260); the first half's weights handed over in
-// the middle of the second half's exponentials (263 against 256).
+// tile (393: it spills); looking at the next barriers between two products (340 against 283:
+// products are issued as they are done, and what stands between them is added to the
+// chain) or at all that a stream waits for in one go (267 against 260); the first half's
+// weights handed over in the middle of the second half's exponentials (263 against 256).
 //
 // What is not seen gets the weight 0, but 0 times a cached NaN would still be NaN in the
 // product: slots past the last position are zero-filled, and the values of drafted rows
