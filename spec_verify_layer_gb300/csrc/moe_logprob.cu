@@ -1,8 +1,9 @@
 // Log probabilities of given tokens, entropies, ranks and top alternatives
 // (moe_token_logprobs), one launch and one pass over the logits.
 //
-// A block takes a slice of one row, a chunk at a time: a thread holds three 16-byte vectors
-// of the chunk in registers and updates its own running maximum m (of the logits), sum
+// A block takes a slice of one row, a chunk at a time: a thread takes three 16-byte vectors
+// of the chunk, asked for two chunks ahead into shared memory (a thread reads only what it
+// asked for itself, so nothing else has to wait), and updates its own running maximum m (of the logits), sum
 // s = sum 2^u and w = sum 2^u u with u = (x - m) / T * log2(e), two elements an instruction;
 // nothing waits for another warp until the slice ends.  Entropy is ln s - ln 2 * w / s, log
 // probabilities (x - m) / T - ln s.
@@ -19,11 +20,14 @@
 // With few rows a row is cut into 2^i slices, up to 32; the block that ends last joins the
 // slices' partials in their order, so the result does not depend on which one that is.
 //
-// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 192 us, 5.4
-// TB/s of the 6.8 that a large copy reaches; what is missing is exponentials and
-// comparisons between loads, at five blocks an SM (more slices a row than the SMs need:
-// 231 and 278 us).  16 rows of 131,072 in 16 bits take 12.6 us in a graph and 5 of 32,003
-// 8.0: a chunk's latency, the first list, and the join one after the other.
+// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 173 us, 6.0
+// TB/s of the 6.8 that a large copy reaches; what is missing is the last wave of rows (a row a
+// block, four blocks an SM) and the first list of each.  With the vectors loaded straight
+// into registers, five blocks an SM, 191 us; one chunk ahead 183; three of two
+// vectors a thread 182; three blocks an SM 185; more slices a row than the SMs need cost a
+// first list each (231 and 278 of that time's 208).  16 rows of 131,072 in 16 bits take 12.6
+// us in a graph and 5 of 32,003 8.0: a chunk's latency, the first list, and the join one
+// after the other.
 #include <type_traits>
 
 #include "moe_common.cuh"
@@ -33,8 +37,9 @@ namespace moe {
 namespace {
 
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
-constexpr int kLpBlocks = 5;    // of an SM
+constexpr int kLpBlocks = 4;    // of an SM
 constexpr int kLpVecs = 3;      // 16-byte vectors a thread holds of a chunk
+constexpr int kLpStages = 3;    // chunks in shared memory, asked for ahead of their turn
 constexpr int kLpMaxK = 32, kLpMaxSlices = 32;
 constexpr int kLpPend = 480;    // entries that wait to be merged
 using Key = unsigned long long;
@@ -169,6 +174,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
                      LpPartial* partials) {
   constexpr int N = Vec<DT>::N;
   __shared__ LpShared sm;
+  __shared__ uint4 ring[kLpStages][kLpVecs][kLpThreads];  // chunks to come; a thread reads what it asked for itself
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.top_k;
   const int row = blockIdx.x / slices, slice = blockIdx.x - row * slices;
   const char* base = static_cast<const char*>(a.logits) + (long long)row * a.stride * (16 / N);
@@ -186,15 +192,33 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
   float kth = -INFINITY;  // the k-th logit so far: later entries have to be above it
   if (tid < kLpMaxK) sm.top[tid] = 0;
   if (tid == 0) sm.count = 0;
-  __syncthreads();
 
+  constexpr int kStep = kLpThreads * kLpVecs;
+  const auto full = [&](int c) {  // every vector of the chunk lies in the slice and in the row
+    const int first = c * N - lead;
+    return c + kStep <= v1 && first >= 0 && first + kStep * N <= a.vocab;
+  };
+  int stage = 0;
+  const auto ask = [&](int c, int to) {
+    if (full(c)) {
+#pragma unroll
+      for (int j = 0; j < kLpVecs; ++j)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&ring[to][j][tid])),
+                     "l"(base + (long long)((c + j * kLpThreads + tid) * N - lead) * (16 / N))
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kLpStages - 1; ++i) ask(v0 + i * kStep, i);
+  __syncthreads();
   const auto chunk = [&](int c, auto inner) {  // inner: every vector is there in full, the token in none
     Vec<DT> x[kLpVecs];
 #pragma unroll
     for (int j = 0; j < kLpVecs; ++j) {
       const int v = c + j * kLpThreads + tid;
       if constexpr (inner.value)
-        x[j].raw = __ldcs(reinterpret_cast<const uint4*>(base + (long long)(v * N - lead) * (16 / N)));
+        x[j].raw = ring[stage][j][tid];
       else if (v < v1) x[j] = load_vec<DT>(base, v * N - lead, a.vocab);
       else x[j].raw = make_uint4(Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone);
     }
@@ -333,12 +357,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     kth = last ? key_logit(last) : -INFINITY;
     __syncthreads();
   };
-  constexpr int kStep = kLpThreads * kLpVecs;
   int merged = v0, next = v0 + kStep;
   for (int c = v0; c < v1; c += kStep) {
     const int first = c * N - lead, last = first + kStep * N;
-    if (c + kStep <= v1 && first >= 0 && last <= a.vocab && (token < first || token >= last)) chunk(c, std::true_type{});
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLpStages - 2) : "memory");
+    ask(c + (kLpStages - 1) * kStep, stage == 0 ? kLpStages - 1 : stage - 1);
+    if (full(c) && (token < first || token >= last)) chunk(c, std::true_type{});
     else chunk(c, std::false_type{});
+    stage = stage == kLpStages - 1 ? 0 : stage + 1;
     if (k > 0 && (c + kStep == next || c + kStep >= v1)) {
       merge(merged, c + kStep);
       merged = c + kStep;

@@ -146,6 +146,22 @@ def test_the_maximum_comes_last():
     good(case)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,n", [(64, 4), (64, 40), (128, 4), (128, 40), (256, 4), (256, 40)])
+@pytest.mark.parametrize("levels", ["rise", "fall", "rise within tiles", "saw"])
+def test_scores_in_steps(dtype, d, n, levels):
+    """Scores that go up or down by far more than a weight's range, between tiles and inside them; rows of the
+    same request see them with either sign, or not at all."""
+    case = TreeCase(26, [900, 40], [n, 3], hq=4, hkv=1, d=d, page=16, dtype=dtype, q_scale=0.5)
+    pos = torch.arange(900 + n, device=DEV)
+    level = {"rise": 12 * (pos // 64), "fall": -12 * (pos // 64), "rise within tiles": 40 * (pos // 32 % 4),
+             "saw": 60 * (pos // 64 % 2) + pos // 128}[levels].float()
+    p, o = case.where(0, np.arange(900 + n))
+    case.k[p, o, 0, 0] = level.to(case.dt)
+    case.q[:, :, 0] = (torch.tensor([1.0, -1.0, 0.0, 1.0], device=DEV) * d ** 0.5).to(case.dt)
+    good(case)
+
+
 def test_strided_queries_and_padding_rows():
     case = TreeCase(11, [30, 100], [5, 8], hq=6, hkv=2, d=64, page=16, dtype="bf16", pad_rows=4, q_pad=128)
     out, lse, status = case.run()
