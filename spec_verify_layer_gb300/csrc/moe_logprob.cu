@@ -25,8 +25,8 @@
 // block, four blocks an SM) and the first list of each.  With the vectors loaded straight
 // into registers, five blocks an SM, 191 us; one chunk ahead 183; three of two
 // vectors a thread 182; three blocks an SM 185; more slices a row than the SMs need cost a
-// first list each (231 and 278 of that time's 208).  16 rows of 131,072 in 16 bits take 12.6
-// us in a graph and 5 of 32,003 8.0: a chunk's latency, the first list, and the join one
+// first list each (231 and 278 of that time's 208).  16 rows of 131,072 in 16 bits take 11.6
+// us in a graph and 5 of 32,003 7.0: a chunk's latency, the first list, and the join one
 // after the other.
 #include <type_traits>
 
@@ -153,20 +153,32 @@ __device__ __forceinline__ void place(LpShared& sm, int n, int k) {
 
 // The first k entries of the slices' lists (descending, 2^i of them, 32 at most) into sm.top.
 // The 32 / n first entries of each are maxima of 32 groups, so nothing below the k-th largest
-// of them is among the first k.  (All threads call.)
-__device__ __forceinline__ void join_lists(LpShared& sm, int n, int k, const LpPartial* all) {
-  const int tid = threadIdx.x, lane = tid & 31, each = 32 / n;
-  if (tid == 0) sm.count = 0;
-  const Key head = sort_desc(lane % each < k ? __ldcg(&all[lane / each].top[lane % each]) : 0, lane);
-  const Key thr = max_key(__shfl_sync(0xffffffffu, head, k - 1), 1);
-  __syncthreads();
-  for (int i = tid; i < n * k; i += kLpThreads) {
-    const Key key = __ldcg(&all[i / k].top[i % k]);
-    if (key >= thr) sm.list[atomicAdd(&sm.count, 1)] = key;
+// of them is among the first k.  All threads make one and call; what is read is asked for
+// when it is made.
+struct LpLists {
+  static constexpr int kPer = kLpMaxSlices * kLpMaxK / kLpThreads;
+  Key head, mine[kPer];
+  __device__ __forceinline__ LpLists(int n, int k, const LpPartial* all) {
+    const int tid = threadIdx.x, lane = tid & 31, each = 32 / n;
+    head = lane % each < k ? __ldcg(&all[lane / each].top[lane % each]) : 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid + j * kLpThreads;
+      mine[j] = i < n * k ? __ldcg(&all[i / k].top[i % k]) : 0;
+    }
   }
-  __syncthreads();
-  place(sm, sm.count, k);
-}
+  __device__ __forceinline__ void join(LpShared& sm, int k) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) sm.count = 0;
+    const Key thr = max_key(__shfl_sync(0xffffffffu, sort_desc(head, lane), k - 1), 1);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (mine[j] >= thr) sm.list[atomicAdd(&sm.count, 1)] = mine[j];
+    __syncthreads();
+    place(sm, sm.count, k);
+  }
+};
 
 template <int DT>
 __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
@@ -415,16 +427,18 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     if (tid < k) mine->top[tid] = sm.top[tid];
     __syncthreads();
     if (tid == 0) {
-      __threadfence();  // covers what the block wrote before the barrier
-      const bool last = atomicAdd(counters + row, 1u) == (unsigned)slices - 1;
+      // releases what the block wrote before the barrier, acquires what the others did
+      unsigned before;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(counters + row) : "memory");
+      const bool last = before == (unsigned)slices - 1;
       if (last) counters[row] = 0;  // ready for the next call
       sm.last = last;
-      __threadfence();
     }
     __syncthreads();
     if (!sm.last) return;
     const LpPartial* all = partials + (size_t)row * slices;
     // every warp joins the sums alike: lane = slice
+    LpLists lists(slices, max(k, 1), all);
     float pm = -INFINITY, ps = 0.f, pw = 0.f;
     int pr = 0;
     if (lane < slices) {
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
       w += __shfl_xor_sync(0xffffffffu, w, o);
       rank += __shfl_xor_sync(0xffffffffu, rank, o);
     }
-    if (k > 0) join_lists(sm, slices, k, all);
+    if (k > 0) lists.join(sm, k);
   }
 
   const bool empty = m == -INFINITY && s == 0.f;
