@@ -33,7 +33,8 @@
 // What it takes (GB300, one launch in a stream of them): full trees (40 and 64 rows of 32/4 heads
 // of 128 over 131,071 and 200,001 keys) 255 us, 1,110 TFLOP/s of the 1,975 that a large library
 // product reaches, 2.7 TB/s; 16 rows of one request over 32,768 keys 26.8 us, 2.5 TB/s; 33
-// ragged requests of 16/8 heads of 64, 58 us, 3.5 TB/s; one row over 1,000 keys 12.4 us.
+// ragged requests of 16/8 heads of 64, 54.3 us, 3.8 TB/s; one row over 1,000 keys 12.6 us
+// (10.2 in a graph).
 // Full trees are bound by the chain of a stream (of the 3,110 cycles of a tile in both streams:
 // scores out to weights back 1,700 to 1,900, products and scores of the next 1,200 to 1,400;
 // the tensor cores work 2,048 of them, 64 for each product of 128 x 128 x 16, as operands
@@ -979,10 +980,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!whole) {
         named_sync(1, kSoftmaxThreads);
-        if (tid == 0) {  // one fence covers what the block wrote before the barrier
-          __threadfence();
-          atomicAdd(p.arrive + ct.split[wk.t0 == 0].first * ct.groups + member, 1u);
-        }
+        if (tid == 0)  // releases what the block wrote before the barrier
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.arrive + ct.split[wk.t0 == 0].first * ct.groups + member)
+                       : "memory");
       }
       ++seq;
     }
@@ -1035,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int block0 = (sp.first * ct.groups + member) * 2;
         const float4* from = p.part + ((long long)block0 * (D / 4) + c4) * p.part_rows + r;
         const float2* from_ml = p.part_ml + (long long)block0 * p.part_rows + r;
-        constexpr int kAhead = 10;
+        constexpr int kAhead = 4;  // parts of a lane on their way (10: 53.3 us for the ragged batch against 51.9)
 #pragma unroll 1
         for (int k0 = mine_k; k0 < sp.parts && here; k0 += tw * kAhead) {
           float2 ml[kAhead];
@@ -1089,7 +1089,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (atomicAdd(done, 1u) == (unsigned)sp.parts - 1) {  // all have seen the count: ready for the next call
           *arrive = 0;
           *done = 0;
-          __threadfence();
         }
       }
     }
