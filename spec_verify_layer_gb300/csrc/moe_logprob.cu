@@ -20,13 +20,13 @@
 // With few rows a row is cut into 2^i slices, up to 32; the block that ends last joins the
 // slices' partials in their order, so the result does not depend on which one that is.
 //
-// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 173 us, 6.0
+// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 174 us, 5.9
 // TB/s of the 6.8 that a large copy reaches; what is missing is the last wave of rows (a row a
 // block, four blocks an SM) and the first list of each.  With the vectors loaded straight
 // into registers, five blocks an SM, 191 us; one chunk ahead 183; three of two
 // vectors a thread 182; three blocks an SM 185; more slices a row than the SMs need cost a
-// first list each (231 and 278 of that time's 208).  16 rows of 131,072 in 16 bits take 11.6
-// us in a graph and 5 of 32,003 7.0: a chunk's latency, the first list, and the join one
+// first list each (231 and 278 of that time's 208).  16 rows of 131,072 in 16 bits take 11.8
+// us in a graph and 5 of 32,003 7.1: a chunk's latency, the first list, and the join one
 // after the other.
 #include <type_traits>
 

@@ -10,7 +10,7 @@
 //
 // What bounds it (GB300): latency.  Six requests with trees take 3.9 us in a graph (an empty
 // launch 0.6): two dependent reads, a prefix sum, the tree's parents and masks.  1,500
-// prompts of up to 1,000 tokens (9.6 MB) take 13 us: the prefix sums of the requests, and then
+// prompts of up to 1,000 tokens (9.6 MB) take 12 us: the prefix sums of the requests, and then
 // a binary search a row for its request; the traffic alone would take 1.4.
 #include "moe_round_ops.cuh"
 

@@ -31,10 +31,10 @@
 // the threshold); a tile that moves a row's maximum is gone through again, with O rescaled.
 //
 // What it takes (GB300, one launch in a stream of them): full trees (40 and 64 rows of 32/4 heads
-// of 128 over 131,071 and 200,001 keys) 255 us, 1,110 TFLOP/s of the 1,975 that a large library
-// product reaches, 2.7 TB/s; 16 rows of one request over 32,768 keys 26.8 us, 2.5 TB/s; 33
-// ragged requests of 16/8 heads of 64, 54.3 us, 3.8 TB/s; one row over 1,000 keys 12.6 us
-// (10.2 in a graph).
+// of 128 over 131,071 and 200,001 keys) 258 us, 1,090 TFLOP/s of the 1,975 that a large library
+// product reaches, 2.7 TB/s; 16 rows of one request over 32,768 keys 26.7 us, 2.5 TB/s; 33
+// ragged requests of 16/8 heads of 64, 55.5 us, 3.7 TB/s; one row over 1,000 keys 12.3 us
+// (10.4 in a graph).
 // Full trees are bound by the chain of a stream (of the 3,110 cycles of a tile in both streams:
 // scores out to weights back 1,700 to 1,900, products and scores of the next 1,200 to 1,400;
 // the tensor cores work 2,048 of them, 64 for each product of 128 x 128 x 16, as operands
