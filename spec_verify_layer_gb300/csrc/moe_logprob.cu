@@ -25,7 +25,7 @@
 // block, four blocks an SM) and the first list of each.  With the vectors loaded straight
 // into registers, five blocks an SM, 191 us; one chunk ahead 183; three of two
 // vectors a thread 182; three blocks an SM 185; more slices a row than the SMs need cost a
-// first list each (231 and 278 of that time's 208).  16 rows of 131,072 in 16 bits take 11.8
+// first list each (201 cut in two, 246 in four).  16 rows of 131,072 in 16 bits take 11.8
 // us in a graph and 5 of 32,003 7.1: a chunk's latency, the first list, and the join one
 // after the other.
 #include <type_traits>
@@ -501,7 +501,7 @@ int check(const moe_logprob_args* p) {
 
 // Slices of a row: while there are SMs to spare (two blocks each) and every thread of a slice
 // has a vector.  More slices cost more than the last round of blocks: 2,000 rows of 129,283
-// took 208 us uncut, 231 cut in two, 278 in four.
+// take 174 us uncut, 201 cut in two, 246 in four.
 int slices_of(const moe_logprob_args& a) {
   const int vecs = a.vocab / (a.dtype == MOE_F32 ? 4 : 8);
   int s = 1;
