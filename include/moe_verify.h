@@ -309,8 +309,10 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const u
  *     MOE_DEV_* bits into it and never clears it; the caller does.
  *   - Nothing outside the described buffers is read or written whatever the device-side
  *     maps hold: an entry that does not fit is skipped and raises its bit.
- *   - The calls allocate nothing and synchronise with nothing; workspaces are passed in.
- *     Calls that share a workspace must not overlap.
+ *   - The calls allocate nothing and synchronise with nothing; workspaces are passed in, set
+ *     to zero once before their first use.  One buffer may serve any calls that are not
+ *     under way at the same time, of other shapes and of either kind, if it is as large as
+ *     the largest needs.
  *   - Outputs do not depend on the order in which thread blocks finish (bitwise).
  *   - Element types: MOE_BF16, MOE_F16, and MOE_F32 where a call says so.  Sums, softmax
  *     statistics and norms are held in 32 bits; results are rounded once.
@@ -448,9 +450,10 @@ int moe_qk_rope_cache(const moe_qk_rope_args* args, void* stream);
  * 0, lse -infinity where the rows themselves are valid).  MOE_DEV_INDEX: a needed page
  * outside the cache; its positions count as not seen.  MOE_DEV_TIMEOUT: thread blocks
  * that share a request's context waited for each other for more than 2 s.
- * ws: moe_tree_attention_workspace_bytes (0 for arguments that the call would refuse),
- * 16-byte aligned, set to zero once before its first use; a call that ends without
- * MOE_DEV_TIMEOUT leaves it ready for the next. */
+ * ws: moe_tree_attention_workspace_bytes (it goes by head_dim and, up to a bound, by
+ * max_tree * q_heads / kv_heads; 0 for arguments that the call would refuse), 16-byte
+ * aligned, set to zero once before its first use; a call that ends without
+ * MOE_DEV_TIMEOUT leaves it ready for the next, whatever its shape. */
 typedef struct moe_tree_attention_args {
   const void* q;
   void* out;
@@ -484,9 +487,9 @@ int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_
  *   logits [n_rows][vocab] of MOE_F32, MOE_BF16 or MOE_F16, stride from row to row in
  *   elements, any alignment of the element type; tokens [n_rows] (NULL if neither logp nor
  *   rank is asked for).  vocab 1..2^24, top_k 0..32, inv_temperature > 0 and finite.
- * ws: moe_token_logprobs_workspace_bytes (0 for arguments that the call would refuse),
- * 16-byte aligned, set to zero once before its first use; every call leaves it ready for
- * the next. */
+ * ws: moe_token_logprobs_workspace_bytes (some 84 KB, the same for all arguments; 0 for those
+ * that the call would refuse), 16-byte aligned, set to zero once before its first use;
+ * every call leaves it ready for the next, whatever its shape. */
 typedef struct moe_logprob_args {
   const void* logits;
   const int32_t* tokens;

@@ -42,6 +42,7 @@ constexpr int kLpVecs = 3;      // 16-byte vectors a thread holds of a chunk
 constexpr int kLpStages = 3;    // chunks in shared memory, asked for ahead of their turn
 constexpr int kLpMaxK = 32, kLpMaxSlices = 32;
 constexpr int kLpPend = 480;    // entries that wait to be merged
+constexpr int kLpSliced = 304;  // blocks up to which rows are cut into slices
 using Key = unsigned long long;
 
 struct LpPartial {  // a slice's result in the workspace
@@ -499,17 +500,19 @@ int check(const moe_logprob_args* p) {
   return MOE_OK;
 }
 
-// Slices of a row: while there are SMs to spare (two blocks each) and every thread of a slice
-// has a vector.  More slices cost more than the last round of blocks: 2,000 rows of 129,283
+// Slices of a row: while there are SMs to spare (kLpSliced blocks, two for each of 152) and every
+// thread of a slice has a vector.  More slices cost more than the last round of blocks: 2,000 rows of 129,283
 // take 174 us uncut, 201 cut in two, 246 in four.
 int slices_of(const moe_logprob_args& a) {
   const int vecs = a.vocab / (a.dtype == MOE_F32 ? 4 : 8);
   int s = 1;
-  while (s < kLpMaxSlices && (int64_t)a.n_rows * s * 2 <= 152 * 2 && vecs / (2 * s) >= kLpThreads) s *= 2;
+  while (s < kLpMaxSlices && (int64_t)a.n_rows * s * 2 <= kLpSliced && vecs / (2 * s) >= kLpThreads) s *= 2;
   return s;
 }
 
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+// Counters of the rows that are cut (at most kLpSliced / 2), partials of their slices (at most kLpSliced).
+constexpr size_t kLpWorkspace = kCounterBytes + kLpSliced * sizeof(LpPartial);
+static_assert(kLpSliced / 2 * sizeof(unsigned) <= kCounterBytes && kCounterBytes % alignof(LpPartial) == 0, "counters");
 
 }  // namespace
 }  // namespace moe
@@ -517,24 +520,21 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 using namespace moe;
 
 extern "C" size_t moe_token_logprobs_workspace_bytes(const moe_logprob_args* args) {
-  if (check(args) != MOE_OK) return 0;
-  const int s = slices_of(*args);
-  if (s == 1) return 256;
-  return up256((size_t)args->n_rows * 4) + (size_t)args->n_rows * s * sizeof(LpPartial);
+  return check(args) == MOE_OK ? kLpWorkspace : 0;
 }
 
 extern "C" int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, void* stream) {
   const int rc = check(args);
   if (rc != MOE_OK) return rc;
   if (!ptr_ok(ws, 16)) return MOE_EINVAL;
-  if (ws_bytes < moe_token_logprobs_workspace_bytes(args)) return MOE_EWORKSPACE;
+  if (ws_bytes < kLpWorkspace) return MOE_EWORKSPACE;
   const moe_logprob_args& a = *args;
   if (a.n_rows == 0) return MOE_OK;
   const int s = slices_of(a), per = a.dtype == MOE_F32 ? 4 : 8;
   const int vecs = (a.vocab + 2 * per - 2) / per;  // wherever a row starts
   const int slice_vecs = (vecs + s - 1) / s;
   unsigned* counters = static_cast<unsigned*>(ws);
-  LpPartial* partials = reinterpret_cast<LpPartial*>(static_cast<char*>(ws) + up256((size_t)a.n_rows * 4));
+  LpPartial* partials = reinterpret_cast<LpPartial*>(static_cast<char*>(ws) + kCounterBytes);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)a.n_rows * s;
   if (a.dtype == MOE_F32) k_token_logprobs<MOE_F32><<<grid, kLpThreads, 0, st>>>(a, s, slice_vecs, counters, partials);

@@ -40,6 +40,11 @@ inline int current_sms() {
   return n;
 }
 
+// A workspace begins with its call's counters, which are zero between calls, in an area of one size
+// whatever the arguments are; what lies behind it is written before it is read.  So one buffer
+// serves calls of any shape, one after the other, and of either call that takes one.
+constexpr size_t kCounterBytes = 1280;
+
 // What the launch itself reported; a failed launch leaves no error behind for the caller's next call.
 inline int launch_status(cudaError_t e) {
   if (e == cudaSuccess) return MOE_OK;

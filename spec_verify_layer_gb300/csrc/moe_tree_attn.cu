@@ -1149,13 +1149,13 @@ int group_rows(const moe_tree_attention_args& a) {  // query rows of a group, as
 }
 
 struct Workspace {
-  size_t counters, ml, part, total;
+  size_t ml, part, total;
 };
 Workspace layout(const moe_tree_attention_args& a) {
   Workspace w{};
   const size_t rows = (size_t)kMaxBlocks * 2 * group_rows(a);
-  w.counters = 0;
-  w.ml = up256((size_t)2 * kMaxBlocks * 4);
+  static_assert(2 * kMaxBlocks * sizeof(unsigned) <= kCounterBytes && kCounterBytes % 256 == 0, "counters");
+  w.ml = kCounterBytes;
   w.part = w.ml + up256(rows * 8);
   w.total = w.part + up256(rows * a.head_dim * 4);
   return w;

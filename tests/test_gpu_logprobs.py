@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import spec_verify_layer_gb300 as mv
-from round_ops_helpers import DEV, DT, at, stream, word
+from round_ops_helpers import DEV, DT, TreeCase, at, stream, word
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +200,59 @@ def test_captured():
         torch.cuda.synchronize()
         want, _ = run(x, t, 0)
         assert torch.equal(o["logp"], want["logp"]) and torch.equal(o["rank"], want["rank"])
+
+
+def call(x, token, k, ws):
+    """One call over a given workspace; all outputs."""
+    code = {torch.bfloat16: mv.MOE_BF16, torch.float16: mv.MOE_F16, torch.float32: mv.MOE_F32}[x.dtype]
+    rows, vocab = x.shape
+    f = lambda *s: torch.full(s, 9.0, device=DEV)  # noqa: E731
+    o = dict(logp=f(rows), entropy=f(rows), rank=torch.full((rows,), -9, dtype=torch.int32, device=DEV),
+             top_ids=torch.full((rows, k), -9, dtype=torch.int32, device=DEV), top_logp=f(rows, k))
+    status = word()
+    args = mv.make_logprob_args(n_rows=rows, vocab=vocab, dtype=code, logits=at(x), stride=x.stride(0),
+                                dev_status=at(status), tokens=at(token), top_k=k, **{n: at(t) for n, t in o.items()})
+    mv.moe_token_logprobs(args, at(ws), ws.numel(), stream())
+    assert int(status.item()) == 0
+    return o
+
+
+SHAPES = [(16, 131072, 20, "bf16"), (100, 32003, 5, "f32"), (5, 60001, 32, "f32"), (140, 40000, 3, "f32"),
+          (1, 262144, 1, "f16"), (152, 33000, 8, "f32"), (200, 9001, 4, "bf16"), (16, 131072, 20, "bf16"),
+          (77, 131072, 2, "bf16"), (152, 33000, 8, "f32")]
+
+
+def test_one_workspace_serves_calls_of_any_shape():
+    """Set to zero once, then used by rounds of other row counts, vocabularies and list lengths."""
+    inputs = [sample(20 + i, rows, vocab, dtype) + (k,) for i, (rows, vocab, k, dtype) in enumerate(SHAPES)]
+    size = max(mv.moe_token_logprobs_workspace_bytes(mv.make_logprob_args(
+        n_rows=x.shape[0], vocab=x.shape[1], dtype=DT[shape[3]][1], logits=at(x), stride=x.stride(0), dev_status=at(t),
+        tokens=at(t), logp=at(t))) for (x, t, _), shape in zip(inputs, SHAPES))
+    shared = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    for (x, t, k), shape in zip(inputs, SHAPES):
+        want = call(x, t, k, torch.zeros_like(shared))
+        got = call(x, t, k, shared)
+        for n in want:
+            assert torch.equal(got[n], want[n]), (shape, n)
+
+
+def test_a_workspace_shared_with_the_attention():
+    """The attention's and this call's workspaces may be one buffer, as long as the calls do not overlap."""
+    case = TreeCase(30, [5000, 12, 700], [16, 3, 30], hq=16, hkv=2, d=128, page=16, dtype="bf16")
+    out, lse, status = case.run()
+    assert status == 0
+    x, t = sample(31, 140, 40000, "f32")
+    few, few_t = sample(32, 3, 100000, "bf16")
+    o2, l2 = case.outputs()
+    flag = word()
+    args = case.args(o2, l2, flag)
+    shared = torch.zeros(max(1 << 20, mv.moe_tree_attention_workspace_bytes(args)), dtype=torch.uint8, device=DEV)
+    want, few_want = (call(a, b, 8, torch.zeros_like(shared)) for a, b in ((x, t), (few, few_t)))
+    for _ in range(3):
+        o2.fill_(float("nan"))
+        mv.moe_tree_attention(args, at(shared), shared.numel(), stream())
+        assert int(flag.item()) == 0 and torch.equal(o2, out) and torch.equal(l2, lse)
+        for (a, b), w in (((x, t), want), ((few, few_t), few_want)):
+            got = call(a, b, 8, shared)
+            for n in w:
+                assert torch.equal(got[n], w[n]), n

@@ -149,3 +149,11 @@ def test_errors_raise_with_their_code():
     with pytest.raises(mv.MoeError) as e:
         mv.moe_tree_attention(tree_args(), P, 0, 0)
     assert e.value.code == mv.MOE_EWORKSPACE
+
+
+def test_a_logprob_workspace_serves_every_shape():
+    """One size for all: a workspace made for the widest round is enough for narrower ones, and the other way round."""
+    sizes = {mv.moe_token_logprobs_workspace_bytes(logp_args(n_rows=n, vocab=v, stride=v, dtype=t, top_k=k))
+             for n in (0, 1, 5, 64, 65, 77, 152, 153, 5000) for v in (1, 1000, 131072, 1 << 24)
+             for t in (mv.MOE_F32, mv.MOE_BF16) for k in (0, 32)}
+    assert len(sizes) == 1 and sizes.pop() > 0
