@@ -127,6 +127,12 @@ __device__ __forceinline__ float one_if_ge(float x, float y) {
   return r;
 }
 
+// The exponent that takes sums from a maximum to a larger one.  A maximum of the type's lowest
+// numbers (masked entries) is so far below that the difference may be -infinity; bounded, the
+// factor 2^d is 0 all the same, and d itself times a sum stays a number.  (A NaN is in the
+// sums already when it is one here.)
+__device__ __forceinline__ float lower(float from, float to, float c2) { return fmaxf((from - to) * c2, -300.f); }
+
 struct LpShared {
   Key list[kLpMaxSlices * kLpMaxK];  // what waits to be merged; candidates of the join of slices
   Key top[kLpMaxK];                  // the block's first k so far, in order; 0 where there are fewer
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     const float top = fmaxf(tops[0], tops[1]);
     if (top > m) {
       if (m > -INFINITY) {
-        const float d = (m - top) * c2, f = exp2_fast(d);
+        const float d = lower(m, top, c2), f = exp2_fast(d);
         w = f * fmaf(d, s, w);
         s *= f;
       }
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     float top = m;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float d = m == -INFINITY ? 0.f : (m - top) * c2, f = exp2_fast(d);
+    const float d = m == -INFINITY ? 0.f : lower(m, top, c2), f = exp2_fast(d);
     w = f * fmaf(d, s, w);
     s *= f;
 #pragma unroll
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     s = w = 0.f;
     rank = 0;
     for (int q = 0; q < kLpWarps; ++q) {
-      const float e = sm.m[q] == -INFINITY ? 0.f : (sm.m[q] - m) * c2, g = exp2_fast(e);
+      const float e = sm.m[q] == -INFINITY ? 0.f : lower(sm.m[q], m, c2), g = exp2_fast(e);
       s = fmaf(g, sm.s[q], s);
       w = fmaf(g, fmaf(e, sm.s[q], sm.w[q]), w);
       rank += sm.rank[q];
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
     m = pm;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float d = pm == -INFINITY ? 0.f : (pm - m) * c2, f = exp2_fast(d);
+    const float d = pm == -INFINITY ? 0.f : lower(pm, m, c2), f = exp2_fast(d);
     w = f * fmaf(d, ps, pw);
     s = f * ps;
     rank = pr;

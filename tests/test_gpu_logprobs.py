@@ -256,3 +256,17 @@ def test_a_workspace_shared_with_the_attention():
             got = call(a, b, 8, shared)
             for n in w:
                 assert torch.equal(got[n], w[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,vocab", [(6, 5003), (6, 70001), (162, 9001)])
+def test_masks_of_the_lowest_value(dtype, rows, vocab):
+    """Masked entries that hold the type's lowest finite number, alone in a thread's part, a warp's, a slice or at
+    a row's start: finite logits have finite entropies."""
+    x, t = sample(33, rows, vocab, dtype)
+    i = torch.arange(vocab, device=DEV)
+    masks = [(i != 17) & (i != vocab // 2) & (i != vocab - 3), i < vocab // 2, i >= vocab // 2, i % 2 == 0,
+             i // 4096 % 2 == 0, i != vocab - 1]
+    for r in range(rows):
+        x[r, masks[r % 6]] = torch.finfo(x.dtype).min
+    check(x, t, 5)
