@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocks)
   const bool has_token = token >= 0 && token < a.vocab;
   const float xt = has_token ? logit_at<DT>(base, token) : INFINITY;
   const float above = nextafterf(xt, INFINITY);  // what entries behind the token have to reach
-  const float c2 = a.inv_temperature * 1.4426950408889634f;
+  // (finite: 0 times an infinity would be NaN)
+  const float c2 = fminf(a.inv_temperature * 1.4426950408889634f, 3.402823466e38f);
   float m = -INFINITY, s = 0.f, w = 0.f;
   int rank = 0;
   float kth = -INFINITY;  // the k-th logit so far: later entries have to be above it

@@ -270,3 +270,18 @@ def test_masks_of_the_lowest_value(dtype, rows, vocab):
     for r in range(rows):
         x[r, masks[r % 6]] = torch.finfo(x.dtype).min
     check(x, t, 5)
+
+
+@pytest.mark.parametrize("inv_t", [1e-30, 1e6, 1e30, 2.3e38, 3e38, 3.4e38])
+def test_extreme_temperatures(inv_t):
+    """Down to the largest factor that 32 bits hold, where the first entry has all the probability."""
+    x, t = sample(34, 4, 20011, "f32")
+    t[0], t[1] = x[0].argmax(), x[1].argmax()
+    o, status = run(x, t, 2, inv_t)
+    assert status == 0
+    if inv_t < 1:
+        check(x, t, 2, inv_t)
+        return
+    assert o["logp"].tolist()[:2] == [0.0, 0.0] and (o["logp"][2:] < -1e3).all()
+    assert (o["entropy"] == 0).all() and (o["top_logp"][:, 0] == 0).all() and (o["top_logp"][:, 1] < -1e3).all()
+    assert torch.equal(o["top_ids"][:, 0].long(), x.argmax(1))
