@@ -350,7 +350,8 @@ typedef struct moe_kv_cache {
  * takes max(0, need_b - held_b) pages from free_pages, in request order, and they are
  * written behind its held ones: block_table[b][held_b ..].  Other table entries stay.
  *   row_start [n_req + 1]  first row of each request; row_start[n_req] = all rows
- *   pages     [n_req]      pages the request holds now (the next call's pages_held)
+ *   pages     [n_req]      pages the request holds now (the next call's pages_held; the two
+ *                          may be one array, for which a second small launch is made)
  *   n_taken   [1]          pages taken: free_pages[0 .. n_taken) are in use now
  *   row_req   [n_rows]     request of the row
  *   row_pos   [n_rows]     ctx_len + depth of the row in its tree (the rotation's position)
@@ -362,7 +363,8 @@ typedef struct moe_kv_cache {
  * bring at most 64 rows.  NULL: each row follows the one before it (a chain, or a
  * prompt); tree_mask is then the chain's, for at most 64 rows.
  * n_rows is the capacity of the row arrays: rows that no request brings get row_req -1,
- * row_pos 0, row_slot -1 and an empty mask, so a captured round can keep its width.
+ * row_pos 0, row_slot -1 and an empty mask, so a captured round can keep its width.  No
+ * output may overlap an input or another output otherwise.
  * Raised bits: MOE_DEV_PAGES (too few free pages, or more than table_width columns
  * needed: rows without a page get slot -1, fresh table entries without one -1);
  * MOE_DEV_LENGTH (a negative length or one past 2^31 - 1, taken as 0; pages_held below

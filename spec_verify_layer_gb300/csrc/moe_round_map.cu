@@ -6,7 +6,10 @@
 // request from L2) instead of waiting for another block or a second launch, and then
 // fills its share of the row arrays and of the fresh table entries; a row's page is read
 // from the table where the request held it before the call and from the free list where
-// it is fresh, so no block reads what another writes.
+// it is fresh, so no block reads what another writes.  `pages` may be `pages_held` itself: blocks
+// read that one from their first look to their last, so it is written by a second launch then,
+// of one block, which only goes through the requests (each thread reads an entry before it
+// writes it).
 //
 // What bounds it (GB300): latency.  Six requests with trees take 3.9 us in a graph (an empty
 // launch 0.6): two dependent reads, a prefix sum, the tree's parents and masks.  1,500
@@ -68,7 +71,12 @@ __device__ __forceinline__ int checked_page(const moe_map_args& a, int page, uns
   return -1;
 }
 
-__global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant__ moe_map_args a, const ByPage by) {
+// What a launch writes: the counts of pages, everything else, or (as it is unless they lie over
+// what the requests held) both.
+enum { kMapPages = 1, kMapRest = 2 };
+
+__global__ void __launch_bounds__(kMapThreads)
+    k_round_map(const __grid_constant__ moe_map_args a, const ByPage by, const int what) {
   extern __shared__ uint32_t sm[];
   uint32_t* start = sm;                // [n_req + 1] rows before a request, at most n_rows
   uint32_t* off = sm + a.n_req + 1;    // [n_req + 1] fresh pages before it
@@ -84,7 +92,7 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
     const int lo = max(0, base - (kTree - 1)), hi = min(a.n_rows, base + kMapRows);
     for (int r = lo + tid; r < hi; r += kMapThreads) par[r - lo] = a.parents[r];
   };
-  if (a.parents) fetch_parents(blockIdx.x * kMapRows);
+  if (a.parents && what != kMapPages) fetch_parents(blockIdx.x * kMapRows);
 
   // kMapPer neighbouring requests a thread: their lengths are loaded together
   uint2 carry = make_uint2(0u, 0u);
@@ -133,12 +141,13 @@ __global__ void __launch_bounds__(kMapThreads) k_round_map(const __grid_constant
       if (lead) {
         const long long got = min((long long)q[j].take, max(0LL, (long long)a.n_free - fresh));
         if (got < q[j].take) flags |= MOE_DEV_PAGES;
-        a.row_start[b + j + 1] = (int)end;
-        a.pages[b + j] = q[j].held + (int)got;
+        if (what & kMapRest) a.row_start[b + j + 1] = (int)end;
+        if (what & kMapPages) a.pages[b + j] = q[j].held + (int)got;
       }
     }
     if (lead) flags |= f;
   }
+  if (what == kMapPages) return;  // (what is wrong with the lengths the other launch reports)
   if (tid == 0) {
     start[0] = 0;
     off[0] = 0;
@@ -238,6 +247,9 @@ extern "C" int moe_round_map(const moe_map_args* p, void* stream) {
       !ptr_ok(a.dev_status, 4))
     return MOE_EINVAL;
   if (a.n_free > 0 && !ptr_ok(a.free_pages, 4)) return MOE_EINVAL;
+  // pages_held in place, or apart from it
+  const uintptr_t held = reinterpret_cast<uintptr_t>(a.pages_held), pages = reinterpret_cast<uintptr_t>(a.pages);
+  if (held && held != pages && (held < pages ? pages - held : held - pages) < (uintptr_t)a.n_req * 4) return MOE_EINVAL;
   if (a.n_rows > 0 && (!ptr_ok(a.row_req, 16) || !ptr_ok(a.row_pos, 16) || !ptr_ok(a.row_slot, 16) ||
                        !opt_ok(a.tree_mask, 16)))
     return MOE_EINVAL;
@@ -260,6 +272,9 @@ extern "C" int moe_round_map(const moe_map_args* p, void* stream) {
   // latency that the others share
   const int steps = (a.n_rows + kMapRows - 1) / kMapRows;
   const int grid = steps < 1 ? 1 : steps > 4 * sms ? 4 * sms : steps;
-  k_round_map<<<grid, kMapThreads, smem, static_cast<cudaStream_t>(stream)>>>(a, by);
+  const bool in_place = held == pages;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  k_round_map<<<grid, kMapThreads, smem, st>>>(a, by, in_place ? kMapRest : kMapRest | kMapPages);
+  if (in_place) k_round_map<<<1, kMapThreads, smem, st>>>(a, by, kMapPages);
   return launch_status(cudaGetLastError());
 }

@@ -3,7 +3,8 @@ import numpy as np
 import pytest
 import torch
 
-from round_ops_helpers import MapCase
+import spec_verify_layer_gb300 as mv
+from round_ops_helpers import DEV, MapCase, at, i32, word
 from spec_verify_layer_gb300 import MOE_DEV_INDEX, MOE_DEV_LENGTH, MOE_DEV_PAGES
 
 pytestmark = pytest.mark.gpu
@@ -160,3 +161,80 @@ def test_a_captured_map_follows_its_lengths():
         for t, name in zip([table] + outs, ("table", "row_start", "pages", "taken", "row_req", "row_pos", "row_slot")):
             np.testing.assert_array_equal(t.cpu().numpy(), want[name], err_msg=name)
     assert int(status.item()) == 0 and DEV == "cuda"
+
+
+class Map:
+    """A case's tensors and its descriptor, for calls that are made more than once."""
+
+    def __init__(self, case, in_place=False):
+        self.ctx, self.new, self.held, self.table = (i32(getattr(case, n)) for n in ("ctx", "new", "held", "table"))
+        self.free, self.status, B, rows = i32(case.free), word(), len(case.ctx), case.rows
+        self.parents = None if case.parents is None else i32(case.parents)
+        self.row_start, self.taken = i32([-7] * (B + 1)), i32([-7])
+        self.pages = self.held if in_place else i32([-7] * B)
+        self.row_req, self.row_pos, self.row_slot = (i32([-7] * rows) for _ in range(3))
+        self.mask = torch.zeros(rows, dtype=torch.int64, device=DEV)
+        self.args = mv.make_map_args(
+            n_req=B, n_rows=rows, page_size=case.page, n_pages=case.n_pages, table_width=case.width,
+            n_free=self.free.numel(), ctx_len=at(self.ctx), new_len=at(self.new), pages_held=at(self.held),
+            free_pages=at(self.free), parents=at(self.parents), block_table=at(self.table),
+            row_start=at(self.row_start), pages=at(self.pages), n_taken=at(self.taken), row_req=at(self.row_req),
+            row_pos=at(self.row_pos), row_slot=at(self.row_slot), tree_mask=at(self.mask) if self.parents is not None else 0,
+            dev_status=at(self.status))
+
+    def call(self, side=None):
+        mv.moe_round_map(self.args, (side or torch.cuda.current_stream()).cuda_stream)
+
+    def got(self):
+        names = ("table", "row_start", "pages", "taken", "row_req", "row_pos", "row_slot", "mask")
+        return {n: getattr(self, n).cpu().numpy().astype(np.int64) for n in names}
+
+
+@pytest.mark.parametrize("req,new,page,tree", [(6, 16, 16, True), (700, 900, 16, False), (130, 61, 8, True),
+                                               (5200, 3, 16, False), (3, 0, 4, False)])
+def test_held_pages_in_place(req, new, page, tree):
+    """`pages` over `pages_held`: every block reads what was held, whichever has ended."""
+    rng = np.random.default_rng(req)
+    case = MapCase(18, rng.integers(0, 300, req), rng.integers(0, new + 1, req), page, extra=2, tree=tree, pad=3)
+    t = Map(case, in_place=True)
+    t.call()
+    got, want = t.got(), case.plain()
+    for name in got:
+        if name != "mask" or tree:
+            np.testing.assert_array_equal(got[name], want[name], err_msg=name)
+    assert int(t.status.item()) == 0
+
+
+def test_rounds_in_place_in_a_graph():
+    """Round after round of one captured call: what a round leaves in the held pages is the next one's input."""
+    case = MapCase(19, [0] * 40, [37] * 40, 8, spare=2000, width=64)
+    t = Map(case, in_place=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        mv.moe_round_map(t.args, torch.cuda.current_stream().cuda_stream)
+    for _ in range(6):
+        want = case.plain()
+        t.free.copy_(i32(np.resize(case.free, t.free.numel())))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = t.got()
+        for name in got:
+            if name != "mask":
+                np.testing.assert_array_equal(got[name], want[name], err_msg=name)
+        case.ctx, case.held, case.table = case.ctx + case.new, want["pages"], want["table"]
+        case.free = case.free[int(want["taken"][0]):]
+        t.ctx.copy_(i32(case.ctx))
+    assert int(t.status.item()) == 0
+
+
+def test_counts_of_pages_in_place_when_free_pages_run_out():
+    case = MapCase(20, [10, 20, 30], [40, 50, 60], 8, spare=0)
+    case.free = case.free[:7]
+    t = Map(case, in_place=True)
+    t.call()
+    want = case.plain()
+    assert int(t.status.item()) == MOE_DEV_PAGES
+    np.testing.assert_array_equal(t.got()["pages"], want["pages"])
+    np.testing.assert_array_equal(t.got()["table"], want["table"])

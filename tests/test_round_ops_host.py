@@ -157,3 +157,9 @@ def test_a_logprob_workspace_serves_every_shape():
              for n in (0, 1, 5, 64, 65, 77, 152, 153, 5000) for v in (1, 1000, 131072, 1 << 24)
              for t in (mv.MOE_F32, mv.MOE_BF16) for k in (0, 32)}
     assert len(sizes) == 1 and sizes.pop() > 0
+
+
+@pytest.mark.parametrize("held", [P - 4, P + 4, P - 4 * 255, P + 4 * 255])
+def test_held_pages_partly_over_pages(held):
+    """In place or apart (that a call in place runs is tested on the GPU)."""
+    refused("moe_round_map", map_args(n_req=256, pages=P, pages_held=held), mv.MOE_EINVAL, None)
