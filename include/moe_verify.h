@@ -450,8 +450,9 @@ int moe_qk_rope_cache(const moe_qk_rope_args* args, void* stream);
  * MOE_DEV_LENGTH: a negative context, row_start not ascending within n_rows, more rows
  * than max_tree, or a length beyond the table: that request's rows are not computed (out
  * 0, lse -infinity where the rows themselves are valid).  MOE_DEV_INDEX: a needed page
- * outside the cache; its positions count as not seen.  MOE_DEV_TIMEOUT: thread blocks
- * that share a request's context waited for each other for more than 2 s.
+ * outside the cache; its positions count as not seen.  MOE_DEV_TIMEOUT: a wait inside a
+ * thread block, or between blocks that share a request's context, gave up after 2 s; the
+ * outputs are incomplete, and ws has to be set to zero before its next use.
  * ws: moe_tree_attention_workspace_bytes (it goes by head_dim and, up to a bound, by
  * max_tree * q_heads / kv_heads; 0 for arguments that the call would refuse), 16-byte
  * aligned, set to zero once before its first use; a call that ends without
@@ -470,6 +471,12 @@ typedef struct moe_tree_attention_args {
   int32_t n_req, n_rows, max_tree, table_width, q_heads, kv_heads, head_dim, dtype;
   float scale;
 } moe_tree_attention_args;
+/* Bound on the device-side waits of every later moe_tree_attention call of the process
+ * (default 2 s; 0 restores it; a captured call keeps the bound of its capture).  As with
+ * moe_set_wait_limit_ns a tiny bound makes waits give up at once, and the call ends its
+ * products in flight under the default bound and returns, so tests can see
+ * MOE_DEV_TIMEOUT without any hang. */
+int moe_set_attention_wait_limit_ns(uint64_t ns);
 size_t moe_tree_attention_workspace_bytes(const moe_tree_attention_args* args);
 int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_bytes, void* stream);
 

@@ -27,6 +27,7 @@ ABI_SYMBOLS = (
     "moe_profile_phases", "moe_decode_layer_noalloc", "moe_prefill_workspace_bytes",
     "moe_prefill_layer", "moe_strerror",
     "moe_round_map", "moe_qk_rope_cache", "moe_tree_attention_workspace_bytes", "moe_tree_attention",
+    "moe_set_attention_wait_limit_ns",
     "moe_token_logprobs_workspace_bytes", "moe_token_logprobs",
 )
 MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2  # element types of the attention-side calls
@@ -152,6 +153,8 @@ _lib.moe_tree_attention_workspace_bytes.argtypes = [ctypes.POINTER(moe_tree_atte
 _lib.moe_tree_attention_workspace_bytes.restype = _sz
 _lib.moe_tree_attention.argtypes = [ctypes.POINTER(moe_tree_attention_args), _vp, _sz, _vp]
 _lib.moe_tree_attention.restype = ctypes.c_int
+_lib.moe_set_attention_wait_limit_ns.argtypes = [ctypes.c_uint64]
+_lib.moe_set_attention_wait_limit_ns.restype = ctypes.c_int
 _lib.moe_token_logprobs_workspace_bytes.argtypes = [ctypes.POINTER(moe_logprob_args)]
 _lib.moe_token_logprobs_workspace_bytes.restype = _sz
 _lib.moe_token_logprobs.argtypes = [ctypes.POINTER(moe_logprob_args), _vp, _sz, _vp]
@@ -358,6 +361,10 @@ def moe_qk_rope_cache(args: moe_qk_rope_args, stream: int) -> None:
 
 def moe_tree_attention_workspace_bytes(args: moe_tree_attention_args) -> int:
     return int(_lib.moe_tree_attention_workspace_bytes(args))
+
+
+def moe_set_attention_wait_limit_ns(ns: int) -> None:
+    _check(_lib.moe_set_attention_wait_limit_ns(int(ns)), "moe_set_attention_wait_limit_ns")
 
 
 def moe_tree_attention(args: moe_tree_attention_args, ws: int, ws_bytes: int, stream: int) -> None:

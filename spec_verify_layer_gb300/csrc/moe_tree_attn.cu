@@ -54,6 +54,7 @@
 // product: slots past the last position are zero-filled, and the values of drafted rows
 // are looked over on their way: what is not finite becomes 0 in the slot and is added at
 // the end to the rows that see it.
+#include <atomic>
 #include <type_traits>
 
 #include "moe_round_ops.cuh"
@@ -67,7 +68,9 @@ constexpr int kSoftmaxThreads = 256, kProducers = 3;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 constexpr float kRescale = 14.0f;       // log2 of how far a maximum may lag behind
-constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
+constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after 2 s
+constexpr long long kCyclesPerNs = 2;  // waits count SM cycles: ns at 2 GHz, a few times ns at lower clocks
+std::atomic<unsigned long long> g_wait_ns{kWaitNs};
 
 template <int D>
 struct Shape {
@@ -101,6 +104,7 @@ struct Plan {  // host-computed, the same for every block
   float2* part_ml;   // [blocks][2][part_rows]: maximum, sum
   unsigned* arrive;  // [blocks]
   unsigned* done;    // [blocks]
+  long long wait_cycles;  // bound of a wait
 };
 
 struct Split {  // a head that is split over blocks: its request's rows, its first block, how many
@@ -119,6 +123,7 @@ struct Control {
   Split split[2];  // of the share's units: one that began in a share before, one that goes on in the next
   unsigned tmem;
   int abort;
+  long long wait_cycles;  // as the plan's
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -141,12 +146,12 @@ __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
   return ok != 0;
 }
 // Waits for the phase of `parity` to end; false once any wait of the block gave up.
-__device__ __forceinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, int* abort_flag, unsigned* status) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, Control& ct, unsigned* status) {
   const long long t0 = clock64();
   while (!bar_try(b, parity)) {
-    if (*(volatile int*)abort_flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *(volatile int*)abort_flag = 1;
+    if (*(volatile int*)&ct.abort) return false;
+    if (clock64() - t0 > *(volatile long long*)&ct.wait_cycles) {
+      *(volatile int*)&ct.abort = 1;
       atomicOr(status, MOE_DEV_TIMEOUT);
       return false;
     }
@@ -155,7 +160,18 @@ __device__ __forceinline__ bool bar_wait_slow(uint32_t b, uint32_t parity, int* 
 }
 __device__ __forceinline__ bool bar_wait(unsigned long long* b, uint32_t parity, Control& ct, unsigned* status) {
   if (bar_try(smem_u32(b), parity)) return true;
-  return bar_wait_slow(smem_u32(b), parity, &ct.abort, status);
+  return bar_wait_slow(smem_u32(b), parity, ct, status);
+}
+// The last wait, for products in flight: they end by themselves, whatever other waits of the block
+// gave up, and until they have the block may neither free tensor memory nor leave.
+__device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned* status) {
+  const long long t0 = clock64();
+  while (!bar_try(smem_u32(b), 0)) {
+    if (clock64() - t0 > (long long)kWaitNs * kCyclesPerNs) {
+      atomicOr(status, MOE_DEV_TIMEOUT);
+      return;
+    }
+  }
 }
 // Barrier of the softmax warps; true if all of them said so.
 __device__ __forceinline__ bool named_all(int id, int threads, bool v) {
@@ -388,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&ct.q_ready, kSoftmaxThreads / 32);
       bar_init(&ct.drain, 1);
       ct.abort = 0;
+      ct.wait_cycles = p.wait_cycles;
       ct.split[0].parts = ct.split[1].parts = 0;
     }
     if (lane < 8) ct.bad[lane] = 0;
@@ -702,8 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      commit(&ct.drain);  // nothing runs on when the block ends
-      wait(&ct.drain, 0);
+      commit(&ct.drain);  // nothing runs on when the block ends, also where a wait gave up
+      bar_drain(&ct.drain, a.dev_status);
+      __syncwarp();
     }
   } else {
     // ---------------- softmax
@@ -998,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned v;
         do {
           asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrive) : "memory");
-          if (clock64() - t0 > kWaitCycles) {
+          if (v < (unsigned)sp.parts && clock64() - t0 > p.wait_cycles) {
             atomicOr(a.dev_status, MOE_DEV_TIMEOUT);
             *(volatile int*)&ct.abort = 1;
             break;
@@ -1092,6 +1110,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    __syncwarp();
+    tm_wait_store();  // (a wait that gave up leaves some on their way)
   }
   __syncthreads();
   __syncwarp();
@@ -1200,6 +1220,11 @@ extern "C" size_t moe_tree_attention_workspace_bytes(const moe_tree_attention_ar
   return check(args) == MOE_OK ? layout(*args).total : 0;
 }
 
+extern "C" int moe_set_attention_wait_limit_ns(uint64_t ns) {
+  g_wait_ns.store(ns ? ns : kWaitNs, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
 extern "C" int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_bytes, void* stream) {
   const int rc = check(args);
   if (rc != MOE_OK) return rc;
@@ -1224,6 +1249,8 @@ extern "C" int moe_tree_attention(const moe_tree_attention_args* args, void* ws,
   p.c = (a.scale == 0.f ? 1.f : std::fabs(a.scale)) * 1.4426950408889634f;
   p.arrive = reinterpret_cast<unsigned*>(base);
   p.done = p.arrive + kMaxBlocks;
+  const unsigned long long ns = g_wait_ns.load(std::memory_order_relaxed);
+  p.wait_cycles = (long long)(ns < (1ull << 40) ? ns : 1ull << 40) * kCyclesPerNs;
   p.part_ml = reinterpret_cast<float2*>(base + w.ml);
   p.part = reinterpret_cast<float4*>(base + w.part);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -274,3 +274,21 @@ def test_offsets_past_32_bits():
     case.k, case.v, case.n_pages = k, v, n_pages
     case.table = np.where(case.table >= 0, case.table + far, -1)
     good(case)
+
+
+def test_waits_that_give_up_are_reported_and_the_next_call_is_whole():
+    """A bound of 1 ns makes waits give up in every role of the kernel and between blocks: the call ends, says so, and
+    leaves nothing behind but its workspace's counters."""
+    cases = [TreeCase(29, [9000, 300, 17], [16, 40, 3], hq=16, hkv=2, d=d, page=24, dtype="bf16") for d in (64, 128, 256)]
+    for case in cases:
+        want, want_lse, status = case.run()
+        assert status == 0
+        try:
+            mv.moe_set_attention_wait_limit_ns(1)
+            for _ in range(3):
+                _, _, status = case.run()
+                assert status == mv.MOE_DEV_TIMEOUT
+        finally:
+            mv.moe_set_attention_wait_limit_ns(0)
+        out, lse, status = case.run()
+        assert status == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
