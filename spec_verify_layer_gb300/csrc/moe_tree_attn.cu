@@ -25,10 +25,9 @@
 // last of its blocks has arrived, each of them joins some of the rows, in block order.
 //
 // Running maximum: it is the largest of the first scores seen, and moves only when a score is
-// above it by more than 2^14 (fp16 weights then stay below their largest value, and sums
-// are as exact relative to themselves).  So a tile's weights need no pass over its scores
-// for the maximum first (full trees 302 us with such a pass, 280 without; 296 with 2^8 as
-// the threshold); a tile that moves a row's maximum is gone through again, with O rescaled.
+// above it by more than 2^14 (bf16) or 2^8 (fp16, see kBias).  So a tile's weights need no pass
+// over its scores for the maximum first (full trees 302 us with such a pass, 280 without;
+// 296 with 2^8 as the threshold); a tile that moves a row's maximum is gone through again, with O rescaled.
 //
 // What it takes (GB300, one launch in a stream of them): full trees (40 and 64 rows of 32/4 heads
 // of 128 over 131,071 and 200,001 keys) 258 us, 1,090 TFLOP/s of the 1,975 that a large library
@@ -67,7 +66,17 @@ constexpr int kThreads = 384;  // 8 softmax warps, 3 producer warps, 1 issuing w
 constexpr int kSoftmaxThreads = 256, kProducers = 3;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
-constexpr float kRescale = 14.0f;       // log2 of how far a maximum may lag behind
+// Weights are 2^(score - maximum + kBias), and a maximum may lag 2^kRescale behind.  fp16 has few
+// places below 1: a weight under 2^-14 loses bits and one under 2^-25 would be 0, while the sum,
+// in 32 bits, holds it, so a long flat tail beside one strong key would vanish from the result
+// alone.  The places above 1 are used for it (2^15 at most, then): what is lost are weights under
+// 2^-32 of the largest.  (A smaller lag leaves room for a larger bias, but more tiles are gone
+// through again: 33 ragged requests 55.6 us with 8 and 7, 57.3 with 7 and 8, 62.1 with 5 and
+// 10; 55.0 with 14 and none.)  bf16 has the exponents of 32 bits and needs no bias.
+template <int DT>
+constexpr float kBias = DT == MOE_F16 ? 7.0f : 0.0f;
+template <int DT>
+constexpr float kRescale = DT == MOE_F16 ? 8.0f : 14.0f;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after 2 s
 constexpr long long kCyclesPerNs = 2;  // waits count SM cycles: ns at 2 GHz, a few times ns at lower clocks
 std::atomic<unsigned long long> g_wait_ns{kWaitNs};
@@ -857,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
               if (m == -INFINITY) m = top;  // every weight so far was 0
               if (half == 0) {
-                const bool far = mr < rows && (top - m) * c > kRescale;
+                const bool far = mr < rows && (top - m) * c > kRescale<DT>;
                 if (__any_sync(0xffffffffu, far)) {
                   // row by row: what the rows beside it do leaves a row's bits as they are
                   const float f = far ? exp2_fast((m - top) * c) : 1.f;
@@ -883,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   hand_over(1);
                 }
               }
-              const float shift = m == -INFINITY ? 0.f : m * c;
+              const float shift = m == -INFINITY ? 0.f : fmaf(m, c, -kBias<DT>);
               const Pair shift2 = pair(-shift, -shift);
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
@@ -993,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (mr < rows && c0 == 0) {
           if (!whole) __stcg(p.part_ml + slot * p.part_rows + mr, make_float2(m, l));
-          else if (a.lse) a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+          else if (a.lse) a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (fmaf(m, c, -kBias<DT>) + log2f(l)) * 0.6931471805599453f;
         }
       }
       if (!whole) {
@@ -1098,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * a.out_stride + (long long)head * D + 4 * c4) =
               make_uint2(pack2<DT>(acc.x * inv, acc.y * inv), pack2<DT>(acc.z * inv, acc.w * inv));
           if (c4 == 0 && a.lse)
-            a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (top * p.c + log2f(l)) * 0.6931471805599453f;
+            a.lse[orow * a.q_heads + head] = l == 0.f ? -INFINITY : (fmaf(top, p.c, -kBias<DT>) + log2f(l)) * 0.6931471805599453f;
         }
       }
       named_sync(1, kSoftmaxThreads);

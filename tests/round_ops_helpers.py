@@ -233,8 +233,9 @@ class TreeCase:
                 seen[i, ctx + j] = bool((word_ >> j) & 1)
         return seen
 
-    def check(self, out, lse, only=None):
-        """Every request's rows against float64, within the bound that the roundings add up to."""
+    def check(self, out, lse, only=None, weight_step=2**-25):
+        """Every request's rows against float64, within the bound that the roundings add up to (weight_step: what an
+        fp16 weight below its smallest normal number may be off by, as a share of the largest)."""
         u = torch.finfo(self.dt).eps / 2
         group = self.hq // self.hkv
         for b in range(len(self.ctx)) if only is None else only:
@@ -259,7 +260,7 @@ class TreeCase:
                 hidden_free = torch.where(seen.any(0)[:, None], v, 0)
                 ref, mass = w @ hidden_free, w @ hidden_free.abs()
                 # weights rounded to the element type (below its smallest normal number: absolutely)
-                tiny = 2**-25 * hidden_free.abs().sum(0) if self.dt == torch.float16 else 0.0
+                tiny = weight_step * hidden_free.abs().sum(0) if self.dt == torch.float16 else 0.0
                 bound = u * (ref.abs() + mass * (1 + u)) + mass * (2 * ds[..., None] + 1e-5) + tiny + (
                     2**-24 if self.dt == torch.float16 else 0.0)
                 got = out[r0:r1, h * group:(h + 1) * group].double()

@@ -292,3 +292,31 @@ def test_waits_that_give_up_are_reported_and_the_next_call_is_whole():
             mv.moe_set_attention_wait_limit_ns(0)
         out, lse, status = case.run()
         assert status == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("d,n", [(64, 3), (128, 2), (128, 40), (256, 3)])
+@pytest.mark.parametrize("strong", [0, 3000, 5999])
+def test_a_flat_tail_beside_one_strong_key(d, n, strong):
+    """Weights of 2^-25.6 beside one of 1 in fp16: six thousand of them are the whole result where the strong key's
+    value is 0.  A weight may be off by 2^-32 of the largest beside the half step of its type."""
+    case = TreeCase(27, [6000] * 20, [n] * 20, hq=2, hkv=2, d=d, page=64, dtype="f16")
+    case.q.zero_()
+    case.q[:, :, 0] = d ** 0.5
+    case.k[:, :, :, 0] = 0
+    case.v[torch.isfinite(case.v)] = 1.0
+    for b in range(20):
+        p, o = case.where(b, np.array([strong]))
+        case.k[p, o, :, 0] = 17.75
+        case.v[p, o] = 0
+    out, lse, status = case.run()
+    assert status == 0
+    case.check(out, lse, weight_step=2**-32)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_small_weights_keep_their_bits(d):
+    """Spread scores: most weights are far below the largest one."""
+    case = TreeCase(28, [9000, 700, 0], [7, 33, 20], hq=4, hkv=1, d=d, page=24, dtype="f16", q_scale=4.0, layout="hnd")
+    out, lse, status = case.run()
+    assert status == 0
+    case.check(out, lse, weight_step=2**-32)
