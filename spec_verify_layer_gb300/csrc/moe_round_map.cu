@@ -260,7 +260,9 @@ extern "C" int moe_round_map(const moe_map_args* p, void* stream) {
   if (sms < 1) return MOE_ECUDA;
   const size_t smem = (size_t)(a.n_req + 1) * 8;
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k_round_map, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most that any call takes: the limit is the kernel's, not the call's, and calls of other
+    // threads may lie between this and the launch
+    const cudaError_t e = cudaFuncSetAttribute(k_round_map, cudaFuncAttributeMaxDynamicSharedMemorySize, (kMapMaxReq + 1) * 8);
     if (e != cudaSuccess) return launch_status(e);
   }
   ByPage by;

@@ -238,3 +238,30 @@ def test_counts_of_pages_in_place_when_free_pages_run_out():
     assert int(t.status.item()) == MOE_DEV_PAGES
     np.testing.assert_array_equal(t.got()["pages"], want["pages"])
     np.testing.assert_array_equal(t.got()["table"], want["table"])
+
+
+def test_calls_of_different_sizes_from_two_threads():
+    """Calls with many requests, which take more shared memory than the default, of different counts side by side."""
+    import threading
+    cases = [MapCase(16, [5] * 16384, [0] * 16383 + [3], 16), MapCase(17, [5] * 5200, [0] * 5199 + [3], 16)]
+    errors, go = [], threading.Barrier(2)
+
+    def work(case):
+        try:
+            t = Map(case)
+            side = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            go.wait()
+            for _ in range(3000):
+                t.call(side)
+            side.synchronize()
+            assert int(t.status.item()) == 0
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
