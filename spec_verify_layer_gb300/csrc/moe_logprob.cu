@@ -544,8 +544,8 @@ extern "C" int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t
   LpPartial* partials = reinterpret_cast<LpPartial*>(static_cast<char*>(ws) + kCounterBytes);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)a.n_rows * s;
-  if (a.dtype == MOE_F32) k_token_logprobs<MOE_F32><<<grid, kLpThreads, 0, st>>>(a, s, slice_vecs, counters, partials);
-  else if (a.dtype == MOE_BF16) k_token_logprobs<MOE_BF16><<<grid, kLpThreads, 0, st>>>(a, s, slice_vecs, counters, partials);
-  else k_token_logprobs<MOE_F16><<<grid, kLpThreads, 0, st>>>(a, s, slice_vecs, counters, partials);
-  return launch_status(cudaGetLastError());
+  const auto fn = a.dtype == MOE_F32    ? k_token_logprobs<MOE_F32>
+                  : a.dtype == MOE_BF16 ? k_token_logprobs<MOE_BF16>
+                                        : k_token_logprobs<MOE_F16>;
+  return launch_status(launch_kernel(fn, grid, kLpThreads, 0, st, a, s, slice_vecs, counters, partials));
 }

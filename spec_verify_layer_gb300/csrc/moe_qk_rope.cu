@@ -260,8 +260,7 @@ cudaError_t launch(const moe_qk_rope_args& a, int sms, cudaStream_t st) {
   runs.page_mul = (unsigned)((1ull << runs.page_shift) / (unsigned)a.cache.page_size + 1);
   const size_t smem = (size_t)kRopeStages * runs.length * a.head_dim * 2;
   const auto fn = a.head_dim == 64 ? k_qk_rope<DT, 64> : a.head_dim == 128 ? k_qk_rope<DT, 128> : k_qk_rope<DT, 256>;
-  fn<<<grid, kRopeThreads, smem, st>>>(a, runs);
-  return cudaGetLastError();
+  return launch_kernel(fn, grid, kRopeThreads, smem, st, a, runs);
 }
 
 }  // namespace

@@ -276,7 +276,7 @@ extern "C" int moe_round_map(const moe_map_args* p, void* stream) {
   const int grid = steps < 1 ? 1 : steps > 4 * sms ? 4 * sms : steps;
   const bool in_place = held == pages;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  k_round_map<<<grid, kMapThreads, smem, st>>>(a, by, in_place ? kMapRest : kMapRest | kMapPages);
-  if (in_place) k_round_map<<<1, kMapThreads, smem, st>>>(a, by, kMapPages);
-  return launch_status(cudaGetLastError());
+  const cudaError_t e = launch_kernel(k_round_map, grid, kMapThreads, smem, st, a, by, (int)(in_place ? kMapRest : kMapRest | kMapPages));
+  if (e != cudaSuccess || !in_place) return launch_status(e);
+  return launch_status(launch_kernel(k_round_map, 1, kMapThreads, smem, st, a, by, (int)kMapPages));
 }

@@ -54,6 +54,17 @@ inline int launch_status(cudaError_t e) {
 
 #ifdef __CUDACC__
 
+// A launch and its own status (the runtime's last error may be that of an earlier call).
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*fn)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 // A 32-bit word of two elements <-> two floats.
 template <int DT>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
