@@ -305,6 +305,8 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const u
  *     memory, read during the call, and its pointers are device memory.  Lengths, maps
  *     and masks are read on the device, so a captured graph follows their contents.
  *   - Device pointers are 16-byte aligned except where a field says otherwise.
+ *   - Strides are below 2^40 elements, and such that a buffer's last row or slot begins less
+ *     than 2^60 elements behind its first.
  *   - dev_status: a caller-owned device word, required, 4-byte aligned.  A kernel ORs
  *     MOE_DEV_* bits into it and never clears it; the caller does.
  *   - Nothing outside the described buffers is read or written whatever the device-side
@@ -371,7 +373,8 @@ typedef struct moe_kv_cache {
  * what the context needs or outside the table; more rows than n_rows, the rest is left
  * out; a tree of more than 64 rows, its later rows get an empty mask); MOE_DEV_INDEX (a
  * page outside [0, n_pages), treated as none; a parent outside [-1, row), treated as -1).
- * Limits: 1 <= n_req <= 16384, 0 <= n_rows, 1 <= table_width, 0 <= n_free. */
+ * Limits: 1 <= n_req <= 16384, 0 <= n_rows <= 2^30, 1 <= table_width, n_req * table_width
+ * below 2^31, 0 <= n_free. */
 typedef struct moe_map_args {
   const int32_t* ctx_len;
   const int32_t* new_len;
@@ -405,8 +408,8 @@ int moe_round_map(const moe_map_args* args, void* stream);
  *   row, in elements (multiples of 8), so the three may lie in one projection's output.
  *   q_out may be q itself (same stride); k and v must not lie in the cache.
  * dtype: MOE_BF16 or MOE_F16, of every element array.  head_dim 64, 128 or 256; rot_dim a
- * multiple of 16, 16..head_dim, or 0 (no rotation); q_heads and kv_heads 1..256;
- * eps >= 0. */
+ * multiple of 16, 16..head_dim, or 0 (no rotation); q_heads and kv_heads 1..256; n_rows
+ * 0..2^24; eps >= 0. */
 typedef struct moe_qk_rope_args {
   const void* q;
   const void* k;
@@ -444,9 +447,10 @@ int moe_qk_rope_cache(const moe_qk_rope_args* args, void* stream);
  *   moe_round_map writes and reads them (4-byte aligned is enough).  Rows that belong to
  *   no request are not written.
  * dtype MOE_BF16 or MOE_F16; head_dim 64, 128 or 256; kv_heads a divisor of q_heads with
- * a quotient of at most 64; max_tree 1..64; n_req 1..16384; the last element of either
- * cache within 2^35 elements of its first, n_req * kv_heads * (table_width * page_size /
- * 64 + 4) below 2^31.
+ * a quotient of at most 64; q_heads 1..1024; max_tree 1..64; n_req 1..16384; n_rows
+ * 0..2^20; the last head of either cache's last slot less than 2^35 - 256 elements behind
+ * its first element; n_req * kv_heads * (table_width * page_size / 64, rounded up, + 4)
+ * below 2^31.
  * MOE_DEV_LENGTH: a negative context, row_start not ascending within n_rows, more rows
  * than max_tree, or a length beyond the table: that request's rows are not computed (out
  * 0, lse -infinity where the rows themselves are valid).  MOE_DEV_INDEX: a needed page
@@ -495,7 +499,8 @@ int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_
  * and top_logp NaN and its ids unspecified.
  *   logits [n_rows][vocab] of MOE_F32, MOE_BF16 or MOE_F16, stride from row to row in
  *   elements, any alignment of the element type; tokens [n_rows] (NULL if neither logp nor
- *   rank is asked for).  vocab 1..2^24, top_k 0..32, inv_temperature > 0 and finite.
+ *   rank is asked for).  n_rows 0..2^24, vocab 1..2^24, top_k 0..32, inv_temperature > 0
+ *   and finite.
  * ws: moe_token_logprobs_workspace_bytes (some 84 KB, the same for all arguments; 0 for those
  * that the call would refuse), 16-byte aligned, set to zero once before its first use;
  * every call leaves it ready for the next, whatever its shape. */

@@ -496,7 +496,8 @@ int check(const moe_logprob_args* p) {
   if (a.n_rows < 0 || a.vocab < 1 || a.top_k < 0 || a.stride < 0) return MOE_EINVAL;
   if (!(a.inv_temperature > 0.f) || !std::isfinite(a.inv_temperature)) return MOE_EINVAL;
   if (a.dtype != MOE_BF16 && a.dtype != MOE_F16 && a.dtype != MOE_F32) return MOE_EINVAL;
-  if (a.vocab > (1 << 24) || a.top_k > kLpMaxK || a.n_rows > (1 << 24) || a.stride >= ((int64_t)1 << 40))
+  if (a.vocab > (1 << 24) || a.top_k > kLpMaxK || a.n_rows > (1 << 24) || a.stride >= ((int64_t)1 << 40) ||
+      !rows_ok(a.n_rows, a.stride))
     return MOE_EUNSUPPORTED;
   if (!ptr_ok(a.dev_status, 4)) return MOE_EINVAL;
   if (a.n_rows == 0) return MOE_OK;

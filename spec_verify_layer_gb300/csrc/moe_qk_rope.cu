@@ -277,10 +277,13 @@ extern "C" int moe_qk_rope_cache(const moe_qk_rope_args* p, void* stream) {
   if (a.dtype != MOE_BF16 && a.dtype != MOE_F16) return a.dtype == MOE_F32 ? MOE_EUNSUPPORTED : MOE_EINVAL;
   if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return MOE_EUNSUPPORTED;
   if (a.rot_dim % 16 || a.q_heads > 256 || a.kv_heads > 256 || a.n_rows > (1 << 24)) return MOE_EUNSUPPORTED;
-  const int rc = check_cache(a.cache);
+  const int rc = check_cache(a.cache, a.kv_heads);
   if (rc != MOE_OK) return rc;
   if (!stride_ok(a.q_stride) || !stride_ok(a.k_stride) || !stride_ok(a.v_stride) || !stride_ok(a.q_out_stride))
     return MOE_EINVAL;
+  if (!rows_ok(a.n_rows, a.q_stride) || !rows_ok(a.n_rows, a.k_stride) || !rows_ok(a.n_rows, a.v_stride) ||
+      !rows_ok(a.n_rows, a.q_out_stride))
+    return MOE_EUNSUPPORTED;
   if (!ptr_ok(a.dev_status, 4) || !opt_ok(a.q_gain, 16) || !opt_ok(a.k_gain, 16)) return MOE_EINVAL;
   if (a.rot_dim > 0 && !ptr_ok(a.inv_freq, 8)) return MOE_EINVAL;
   if (a.n_rows == 0) return MOE_OK;

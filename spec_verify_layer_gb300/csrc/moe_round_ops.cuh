@@ -18,14 +18,25 @@ inline bool ptr_ok(const void* p, unsigned align) { return p && (reinterpret_cas
 // NULL, or aligned
 inline bool opt_ok(const void* p, unsigned align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) == 0; }
 
-// strides of a cache in elements: multiples of 8, not negative, and no offset past 2^62
+// strides in elements: multiples of 8, not negative
 inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < ((int64_t)1 << 40); }
 
-inline int check_cache(const moe_kv_cache& c) {
+// Offsets in elements, products of counts and strides: in 128 bits, since a descriptor may hold
+// any, and far enough below 2^63 for bytes.
+using Wide = __int128;
+constexpr Wide kMaxOffset = (Wide)1 << 60;
+inline bool rows_ok(int64_t rows, int64_t stride) { return (Wide)(rows - 1) * stride < kMaxOffset; }
+// of the first element of the last head of the last slot
+inline Wide cache_span(const moe_kv_cache& c, int heads) {
+  return (Wide)(c.n_pages - 1) * c.page_stride + (Wide)(c.page_size - 1) * c.slot_stride + (Wide)(heads - 1) * c.head_stride;
+}
+
+inline int check_cache(const moe_kv_cache& c, int heads) {
   if (!ptr_ok(c.k, 16) || !ptr_ok(c.v, 16)) return MOE_EINVAL;
   if (c.n_pages < 1 || c.page_size < 1) return MOE_EINVAL;
   if (!stride_ok(c.page_stride) || !stride_ok(c.slot_stride) || !stride_ok(c.head_stride)) return MOE_EINVAL;
-  if (c.page_size > 65536 || (int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31)) return MOE_EUNSUPPORTED;
+  if (c.page_size > 65536 || (int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31) || cache_span(c, heads) >= kMaxOffset)
+    return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 

@@ -1153,16 +1153,15 @@ int check(const moe_tree_attention_args* p) {
   if (a.max_tree > kTree || a.q_heads / a.kv_heads > 64 || a.q_heads > 1024 || a.n_req > 16384 ||
       a.n_rows > (1 << 20))
     return MOE_EUNSUPPORTED;
-  const int rc = check_cache(a.cache);
+  const int rc = check_cache(a.cache, a.kv_heads);
   if (rc != MOE_OK) return rc;
   // offsets in the cache travel in units of 16 bytes, in 32 bits
-  if ((a.cache.n_pages - 1) * a.cache.page_stride + (a.cache.page_size - 1) * a.cache.slot_stride +
-          (a.kv_heads - 1) * a.cache.head_stride >= ((int64_t)8 << 32) - 256)
-    return MOE_EUNSUPPORTED;
+  if (cache_span(a.cache, a.kv_heads) >= ((int64_t)8 << 32) - 256) return MOE_EUNSUPPORTED;
   // the list of (request, head, tile) is numbered in 32 bits
-  if (((int64_t)a.table_width * a.cache.page_size / 64 + 1 + kUnit) * a.n_req * a.kv_heads >= ((int64_t)1 << 31))
+  if ((Wide)(((int64_t)a.table_width * a.cache.page_size + 63) / 64 + kUnit) * a.n_req * a.kv_heads >= ((int64_t)1 << 31))
     return MOE_EUNSUPPORTED;
   if (!stride_ok(a.q_stride) || !stride_ok(a.out_stride)) return MOE_EINVAL;
+  if (!rows_ok(a.n_rows, a.q_stride) || !rows_ok(a.n_rows, a.out_stride)) return MOE_EUNSUPPORTED;
   if (!ptr_ok(a.dev_status, 4) || !ptr_ok(a.row_start, 4) || !ptr_ok(a.ctx_len, 4) || !ptr_ok(a.block_table, 4) ||
       !opt_ok(a.lse, 4) || !opt_ok(a.tree_mask, 8))
     return MOE_EINVAL;

@@ -163,3 +163,44 @@ def test_a_logprob_workspace_serves_every_shape():
 def test_held_pages_partly_over_pages(held):
     """In place or apart (that a call in place runs is tested on the GPU)."""
     refused("moe_round_map", map_args(n_req=256, pages=P, pages_held=held), mv.MOE_EINVAL, None)
+
+
+# products of counts and strides that pass 64 bits, or come round to something small there
+WRAPPED_CACHES = [dict(n_pages=1 << 26, page_size=16, page_stride=1 << 38), dict(n_pages=(1 << 26) + 1, page_stride=1 << 39),
+                  dict(page_size=65536, n_pages=8, slot_stride=(1 << 40) - 8),
+                  dict(n_pages=(1 << 27) - 1, page_stride=(1 << 40) - 8, slot_stride=(1 << 40) - 8)]
+
+
+@pytest.mark.parametrize("kw", WRAPPED_CACHES)
+def test_caches_whose_offsets_pass_64_bits(kw):
+    a = tree_args(cache=cache(**kw))
+    assert mv.moe_tree_attention_workspace_bytes(a) == 0
+    refused("moe_tree_attention", a, mv.MOE_EUNSUPPORTED, P, 1 << 40, None)
+    if kw.get("page_size") != 65536:  # (2^56 elements: an address space would hold them)
+        refused("moe_qk_rope_cache", rope_args(cache=cache(**kw)), mv.MOE_EUNSUPPORTED, None)
+
+
+@pytest.mark.parametrize("name", ["q_stride", "k_stride", "v_stride", "q_out_stride"])
+def test_rows_whose_offsets_pass_64_bits(name):
+    refused("moe_qk_rope_cache", rope_args(n_rows=1 << 24, **{name: (1 << 40) - 8}), mv.MOE_EUNSUPPORTED, None)
+
+
+def test_logits_whose_offsets_pass_64_bits():
+    a = logp_args(n_rows=1 << 24, stride=(1 << 40) - 1)
+    assert mv.moe_token_logprobs_workspace_bytes(a) == 0
+    refused("moe_token_logprobs", a, mv.MOE_EUNSUPPORTED, P, 1 << 40, None)
+
+
+@pytest.mark.parametrize("width,page,ok", [(131067, 64, True), (131068, 64, False), (8388287, 1, True), (8388288, 1, True),
+                                           (8388289, 1, False), (2**31 - 1, 65536, False)])
+def test_the_limit_of_the_attentions_list(width, page, ok):
+    """n_req * kv_heads * (table_width * page_size / 64, rounded up, + 4) below 2^31: up to 131,071 for 16,384 requests."""
+    a = tree_args(n_req=16384, q_heads=1, kv_heads=1, table_width=width, cache=cache(page_size=page))
+    assert (mv.moe_tree_attention_workspace_bytes(a) > 0) == ok
+    if not ok:
+        refused("moe_tree_attention", a, mv.MOE_EUNSUPPORTED, P, 1 << 40, None)
+
+
+def test_a_list_whose_length_passes_64_bits():
+    a = tree_args(n_req=16384, q_heads=1024, kv_heads=1024, table_width=2**31 - 1, cache=cache(page_size=65536, n_pages=8))
+    assert mv.moe_tree_attention_workspace_bytes(a) == 0
