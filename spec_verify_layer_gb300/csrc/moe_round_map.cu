@@ -14,7 +14,8 @@
 // What bounds it (GB300): latency.  Six requests with trees take 3.9 us in a graph (an empty
 // launch 0.6): two dependent reads, a prefix sum, the tree's parents and masks.  1,500
 // prompts of up to 1,000 tokens (9.6 MB) take 12 us: the prefix sums of the requests, and then
-// a binary search a row for its request; the traffic alone would take 1.4.
+// a binary search a row for its request, in two steps of rows for 125 of the 608 blocks; the
+// traffic alone would take 1.4.  In place the six requests take 9.5 us in a stream, apart 7.0.
 #include "moe_round_ops.cuh"
 
 namespace moe {

@@ -31,15 +31,20 @@
 //
 // What it takes (GB300, one launch in a stream of them): full trees (40 and 64 rows of 32/4 heads
 // of 128 over 131,071 and 200,001 keys) 258 us, 1,090 TFLOP/s of the 1,975 that a large library
-// product reaches, 2.7 TB/s; 16 rows of one request over 32,768 keys 26.7 us, 2.5 TB/s; 33
-// ragged requests of 16/8 heads of 64, 55.5 us, 3.7 TB/s; one row over 1,000 keys 12.3 us
-// (10.4 in a graph).
+// product reaches, 2.7 TB/s; the same of 16/2 heads of 256, 322 us; 64 requests of one row over
+// 8,192 keys each 177.6 us, 6.0 TB/s; 16 rows of one request over 32,768 keys 26.7 us, 2.5
+// TB/s; 33 ragged requests of 16/8 heads of 64 in fp16, 55.9 us, 3.7 TB/s; one row over 1,000
+// keys 12.3 us (10.4 in a graph).
 // Full trees are bound by the chain of a stream (of the 3,110 cycles of a tile in both streams:
-// scores out to weights back 1,700 to 1,900, products and scores of the next 1,200 to 1,400;
-// the tensor cores work 2,048 of them, 64 for each product of 128 x 128 x 16, as operands
-// that come out of shared memory allow).  The others are bound by latency: some 6 us from the launch
-// to the first weights (lengths, page table, keys: one after the other from memory, and code
-// that is fetched for the first time), and 3.5 us for the join of a split head.
+// scores out to weights back 1,700 to 1,900, products and scores of the next 1,200 to 1,400).
+// The tensor cores work 2,048 of them, 64 for each product of 128 x 128 x 16, which is their
+// full rate (8,192 operations a cycle); in the rest no product is in flight, since a stream's
+// softmax, which waits for its own loads, maxima and exponentials one after the other, takes
+// longer than the 1,024 cycles of the other stream's products.  Ragged batches pay for 128 rows
+// where a group has 48 at most and 24 on average.  The others are bound by latency: some 6 us
+// from the launch to the first weights (lengths, page table, keys and, on the same barrier,
+// values: one after the other from memory, and code that is fetched for the first time), and
+// 3.5 us for the join of a split head.
 //
 // Tried and slower: scores of 64 keys in two buffers a stream (full trees 507 us against 372
 // of that time: the tensor cores read a query tile for each product, whatever its width);
@@ -54,7 +59,6 @@
 // are looked over on their way: what is not finite becomes 0 in the slot and is added at
 // the end to the rows that see it.
 #include <atomic>
-#include <type_traits>
 
 #include "moe_round_ops.cuh"
 
