@@ -371,8 +371,9 @@ typedef struct moe_kv_cache {
  * needed: rows without a page get slot -1, fresh table entries without one -1);
  * MOE_DEV_LENGTH (a negative length, or lengths past 2^31 - 1 together: the request brings no
  * rows, and a negative context counts as 0; pages_held below what the context needs or
- * outside the table; more rows than n_rows, the rest is left out; a tree of more than 64 rows, its later rows get an empty mask); MOE_DEV_INDEX (a
- * page outside [0, n_pages), treated as none; a parent outside [-1, row), treated as -1).
+ * outside the table; more rows than n_rows, the rest is left out; a tree of more than 64
+ * rows, its later rows get an empty mask); MOE_DEV_INDEX (a page outside [0, n_pages),
+ * treated as none; a parent outside [-1, row), treated as -1).
  * Limits: 1 <= n_req <= 16384, 0 <= n_rows <= 2^30, 1 <= table_width, n_req * table_width
  * below 2^31, 0 <= n_free. */
 typedef struct moe_map_args {
@@ -401,8 +402,8 @@ int moe_round_map(const moe_map_args* args, void* stream);
  * (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved.  inv_freq, in 64 bits, is taken
  * modulo one turn a position and multiplied in fixed point, so whole turns drop out without a
  * rounding; the angle is off by at most |row_pos| * 2^-52 turns for frequencies below one turn
- * (1.4e-9 rad at 10^6, 3e-6 at 2^31) and 1e-7 rad of its 32-bit form.  Queries go to q_out; keys go to the cache at the row's slot, and so do the
- * values, as they are.  A row with slot -1 has its queries written and nothing cached;
+ * (1.4e-9 rad at 10^6, 3e-6 at 2^31) and 1e-7 rad of its 32-bit form.  Queries go to
+ * q_out; keys go to the cache at the row's slot, and so do the values, as they are.  A row with slot -1 has its queries written and nothing cached;
  * other slots outside the cache raise MOE_DEV_INDEX and are skipped.  Two rows must not
  * share a slot.
  *   q [n_rows][q_heads][D], k and v [n_rows][kv_heads][D]: the strides are from row to

@@ -22,8 +22,8 @@
 // With few rows a row is cut into 2^i slices, up to 32; the block that ends last joins the
 // slices' partials in their order, so the result does not depend on which one that is.
 //
-// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 177 us, 5.85
-// TB/s of the 6.8 that a large copy reaches; what is missing is the last wave of rows (a row a
+// What bounds it (GB300): 2,000 rows of 129,283 logits in 32 bits (1.03 GB) take 173 to 177 us by machine,
+// 5.85 to 5.95 TB/s of the 6.8 that a large copy reaches; what is missing is the last wave of rows (a row a
 // block, four blocks an SM) and the first list of each.  With the vectors loaded straight
 // into registers, five blocks an SM, 191 us; one chunk ahead 183; three of two
 // vectors a thread 182; three blocks an SM 185; more slices a row than the SMs need cost a
