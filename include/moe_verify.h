@@ -295,8 +295,9 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const u
  * What a round runs around its expert layers: the page and slot map of the rows to come
  * (moe_round_map), the norms and rotation of their queries and keys with the write into
  * the paged cache (moe_qk_rope_cache), the attention of the drafted rows over that cache
- * (moe_tree_attention), and the log probabilities of the drafted tokens under the logits
- * (moe_token_logprobs).  The pages leave these steps to the surrounding engine; their
+ * (moe_tree_attention), the log probabilities of the drafted tokens under the logits
+ * (moe_token_logprobs), and which of them stand (moe_verify_drafts).  The cache may be in 8
+ * bits (moe_cache8_append, moe_cache8_read, moe_tree_attention8).  The pages leave these steps to the surrounding engine; their
  * definitions here are this library's own.
  *
  * Conventions, besides those at the top of this file:
@@ -321,13 +322,15 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const u
  * ====================================================================================== */
 
 enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+enum { MOE_E4M3 = 3, MOE_I8 = 4 }; /* codes of a cache in 8 bits (moe_kv_cache8) */
 
 enum {
   MOE_DEV_TIMEOUT = 1, /* a bounded device wait gave up: outputs are incomplete */
   MOE_DEV_SLOT = 2,    /* an expert table entry outside the bank (expert layer calls) */
   MOE_DEV_PAGES = 4,   /* free pages or table columns ran out */
   MOE_DEV_LENGTH = 8,  /* a length that is negative, too long or does not fit the rest */
-  MOE_DEV_INDEX = 16   /* a page, slot, parent or token index outside its range */
+  MOE_DEV_INDEX = 16,  /* a page, slot, parent or token index outside its range */
+  MOE_DEV_VALUE = 32   /* a value that is not finite, or a scale that is not one, where the call says so */
 };
 
 /* A paged cache of keys and values, DEVICE pointers.  The element (page, slot in page,
@@ -486,6 +489,94 @@ int moe_set_attention_wait_limit_ns(uint64_t ns);
 size_t moe_tree_attention_workspace_bytes(const moe_tree_attention_args* args);
 int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_bytes, void* stream);
 
+/* A paged cache of keys and values in 8 bits, DEVICE pointers: codes, and a scale for each
+ * block of block_size tokens and head, of keys and of values apart.  A value is the 32-bit
+ * product code * scale.  The code (page, slot in page, head, e) of either is at the byte
+ * page * page_stride + slot * slot_stride + head * head_stride + e (strides multiples of
+ * 16, not negative), its scale at the float page * scale_page_stride + (slot /
+ * block_size) * scale_block_stride + head * scale_head_stride (not negative).  block_size: a
+ * power of two, 1..128, that divides page_size; 1 is a scale a token.
+ *   format MOE_E4M3: 1 sign, 4 exponent (bias 7) and 3 mantissa bits; all codes are numbers
+ *   here, 0x7f and 0xff, which the calls never write, +-480.  MOE_I8: two's complement; the
+ *   calls write -127..127.
+ * A scale is 0 or a finite positive normal number; any other counts as 0 and raises
+ * MOE_DEV_VALUE where a position that a call reads goes by it.  So no cached bits are
+ * infinite or NaN.  moe_cache8_append writes powers of two; a program's own calibrated
+ * scales may be any.  Pages are numbered as in moe_kv_cache. */
+typedef struct moe_kv_cache8 {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, slot_stride, head_stride;
+  int64_t scale_page_stride, scale_block_stride, scale_head_stride;
+  int32_t n_pages, page_size, block_size, format;
+} moe_kv_cache8;
+
+/* Rows into a cache of 8 bits (moe_cache8_append) and out of it (moe_cache8_read).  Row
+ * i of request b, row_start[b] + i, is its position ctx_len[b] + i: behind the context
+ * where rows are appended, anywhere (0 for a whole prefix) where they are read.
+ *   append: per block of tokens that rows fall into, and per head, of keys and of values, let
+ *   a be the largest magnitude, finite ones only, of the block's new rows and of what it holds
+ *   from before (the positions of the block that are below ctx_len[b]; what lies behind
+ *   them, as of drafts that were rejected, has no influence).  The block's scale becomes 2^e
+ *   with the least e >= -126 for which a <= Q * 2^e, Q = 448 (MOE_E4M3) or 127 (MOE_I8).
+ *   Rows are rounded to the nearest code (ties to even) of x / 2^e; what the block holds
+ *   is rounded again from its values where the scale has changed.  With MOE_E4M3 that is
+ *   exact but for codes that fall below the smallest normal one; with MOE_I8 a value
+ *   that was rounded again is off by less than one step of its present scale (rounded once:
+ *   half a step).  Infinities become the largest code with their sign, NaN 0, and both raise
+ *   MOE_DEV_VALUE.  The last block of a context is written as a whole, so it must not be shared
+ *   with another request (a shared prefix ends with a block); no two rows of a call may
+ *   fall into one slot.
+ *   read: k, v = code * scale, rounded once to dtype.
+ *   k, v [n_rows][kv_heads][D] of MOE_BF16, MOE_F16 or MOE_F32, the strides from row to row in
+ *   elements (multiples of 8); they must not lie in the cache.  Rows that belong to no request
+ *   are neither read nor written.
+ * head_dim 64, 128 or 256; kv_heads 1..256; n_req 1..16384; n_rows 0..2^24;
+ * MOE_DEV_LENGTH: a negative context, row_start not ascending within n_rows, or a length
+ * beyond the table: that request is left out (its rows are not written).  MOE_DEV_INDEX: a
+ * page outside the cache: what would lie there is not cached, and read as 0. */
+typedef struct moe_cache8_args {
+  void* k; /* append: read; read: written */
+  void* v;
+  const int32_t* row_start;
+  const int32_t* ctx_len;
+  const int32_t* block_table; /* [n_req][table_width] */
+  unsigned* dev_status;
+  moe_kv_cache8 cache;
+  int64_t k_stride, v_stride;
+  int32_t n_req, n_rows, table_width, kv_heads, head_dim, dtype;
+} moe_cache8_args;
+int moe_cache8_append(const moe_cache8_args* args, void* stream);
+int moe_cache8_read(const moe_cache8_args* args, void* stream);
+
+/* moe_tree_attention over a cache of 8 bits: the same rows, masks, lengths, outputs, limits,
+ * raised bits and workspace rules, with keys and values code * scale (a scale that is not
+ * one counts as 0 and raises MOE_DEV_VALUE).  dtype is that of q and out.  Inside, codes are
+ * 16-bit numbers (exactly), queries 16-bit numbers with a power of two for each row and
+ * head (exactly, but for elements below 2^-38 of its largest), the softmax weights, with the
+ * values' scale in them, are rounded to fp16 for the product with the codes (what is lost
+ * are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  The span of
+ * either cache is below 2^36 - 2048 bytes here.
+ * Waits go by moe_set_attention_wait_limit_ns. */
+typedef struct moe_tree_attention8_args {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* row_start;
+  const int32_t* ctx_len;
+  const int32_t* block_table; /* [n_req][table_width] */
+  const uint64_t* tree_mask;  /* [n_rows] or NULL */
+  unsigned* dev_status;
+  moe_kv_cache8 cache;
+  int64_t q_stride, out_stride;
+  int32_t n_req, n_rows, max_tree, table_width, q_heads, kv_heads, head_dim, dtype;
+  float scale;
+} moe_tree_attention8_args;
+size_t moe_tree_attention8_workspace_bytes(const moe_tree_attention8_args* args);
+int moe_tree_attention8(const moe_tree_attention8_args* args, void* ws, size_t ws_bytes, void* stream);
+
 /* Log probabilities of given tokens under rows of logits.  With z = logit *
  * inv_temperature and lse = log(sum exp(z)) over the row:
  *   logp     [n_rows]         z[token] - lse
@@ -526,6 +617,67 @@ typedef struct moe_logprob_args {
 } moe_logprob_args;
 size_t moe_token_logprobs_workspace_bytes(const moe_logprob_args* args);
 int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* Which drafted tokens stand, and which token follows.  Request b's rows are row_start[b] ..
+ * row_start[b + 1] - 1, at most 64: row 0 is the token that was there before (its own
+ * token is not read), the others are drafts, each behind its parent (parents[row], an index
+ * within the request less than the row's own; NULL: the row before it).  logits[r] is what
+ * the target says behind row r, p_r = softmax(logits[r] * inv_temperature).  From r = row
+ * 0 on, the children of r are tried in the order of their rows:
+ *   without draft_probs (the drafts were looked up, or are a drafter's likeliest): child c
+ *   with token x is taken if p_r(x) > 0 and uniform[c] * (1 - the sum of p_r over the tokens
+ *   of the children rejected before it) < p_r(x); a token that was rejected already is not
+ *   taken.  After the last rejection the rest is p_r without their tokens;
+ *   with draft_probs (chains only, parents NULL; draft_probs[c] the probabilities q_c that
+ *   c's token was drawn from): c is taken if uniform[c] * q_c(x) < p_r(x), the rest after
+ *   a rejection is max(p_r - q_c, 0);
+ *   inv_temperature = +infinity (greedy): c is taken if x is the largest logit's token (of
+ *   equal ones the lowest); the token that follows is that token; uniform, noise and
+ *   draft_probs are not read and may be NULL.
+ * r goes on with the child that was taken; where none was, or there is none (the rest is
+ * p_r then), the token that follows is the one with the largest rest(x) / noise[b][x], of
+ * equal ones the lowest: a draw from rest if noise is exponentially distributed, entries
+ * that are not positive cannot be drawn.  Where nothing of the rest is left, p_r is drawn
+ * from.  So, with uniform in [0, 1), the tokens are distributed as the target's own.
+ *   accepted   [n_req]   drafts that stand
+ *   path       [n_rows]  path[row_start[b] + i]: the i-th row that stands (path[row_start[b]]
+ *                        is 0), as an index within the request; -1 behind the last
+ *   next_token [n_req]   the token that follows
+ * A request without rows gets accepted 0 and next_token -1.  A draft of token -1 stands for
+ * none and is not taken (its draft_probs are not read); other tokens outside the
+ * vocabulary are not taken either and raise MOE_DEV_INDEX, as does a parent outside
+ * [-1, row), taken as -1: such rows, but for row 0, hang on nothing and are not tried.  Logits of
+ * -infinity are tokens that cannot occur.  Where the row that is drawn from has no other or
+ * holds NaN or +infinity, next_token is -1; the latter raise MOE_DEV_VALUE, and no child of a
+ * row with them is taken.  MOE_DEV_LENGTH: row_start not ascending within n_rows, or more
+ * than 64 rows: the request gets accepted 0, next_token -1, and its path is not written.
+ * Decisions come from sums in 32 bits joined in 64; a uniform number within some 1e-6 of
+ * its border may fall on either side of it.
+ *   logits [n_rows][vocab] of MOE_F32, MOE_BF16 or MOE_F16, stride from row to row in
+ *   elements; draft_probs [n_rows][vocab] of draft_dtype, draft_stride; uniform [n_rows] and
+ *   noise [n_req][vocab] (noise_stride) fp32; any alignment of their element types.  n_req
+ *   1..16384, n_rows 0..2^20, vocab 1..2^24, inv_temperature > 0.
+ * ws: moe_verify_drafts_workspace_bytes (it goes by n_req and n_rows; 0 for arguments that the
+ * call would refuse), 16-byte aligned, set to zero once before its first use; every call
+ * leaves it ready for the next, whatever its shape. */
+typedef struct moe_verify_args {
+  const void* logits;
+  const void* draft_probs; /* or NULL */
+  const int32_t* row_start;
+  const int32_t* parents; /* or NULL */
+  const int32_t* tokens;
+  const float* uniform;
+  const float* noise;
+  int32_t* accepted;
+  int32_t* path;
+  int32_t* next_token;
+  unsigned* dev_status;
+  int64_t stride, draft_stride, noise_stride;
+  int32_t n_req, n_rows, vocab, dtype, draft_dtype;
+  float inv_temperature;
+} moe_verify_args;
+size_t moe_verify_drafts_workspace_bytes(const moe_verify_args* args);
+int moe_verify_drafts(const moe_verify_args* args, void* ws, size_t ws_bytes, void* stream);
 
 const char* moe_strerror(int code);
 

@@ -29,10 +29,13 @@ ABI_SYMBOLS = (
     "moe_round_map", "moe_qk_rope_cache", "moe_tree_attention_workspace_bytes", "moe_tree_attention",
     "moe_set_attention_wait_limit_ns",
     "moe_token_logprobs_workspace_bytes", "moe_token_logprobs",
+    "moe_cache8_append", "moe_cache8_read", "moe_tree_attention8_workspace_bytes", "moe_tree_attention8",
+    "moe_verify_drafts_workspace_bytes", "moe_verify_drafts",
 )
 MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2  # element types of the attention-side calls
+MOE_E4M3, MOE_I8 = 3, 4  # codes of a cache in 8 bits
 # bits of their device status word
-MOE_DEV_TIMEOUT, MOE_DEV_SLOT, MOE_DEV_PAGES, MOE_DEV_LENGTH, MOE_DEV_INDEX = 1, 2, 4, 8, 16
+MOE_DEV_TIMEOUT, MOE_DEV_SLOT, MOE_DEV_PAGES, MOE_DEV_LENGTH, MOE_DEV_INDEX, MOE_DEV_VALUE = 1, 2, 4, 8, 16, 32
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 KIND_ROUND = 0
 MMA_ROWS = 13  # rounds of at least this many rows run on the tensor cores
@@ -91,6 +94,34 @@ class moe_tree_attention_args(ctypes.Structure):
 class moe_logprob_args(ctypes.Structure):
     _fields_ = _fields([("p", "logits tokens logp entropy rank top_ids top_logp dev_status"), ("l", "stride"),
                         ("i", "n_rows vocab top_k dtype"), ("f", "inv_temperature")])
+
+
+class moe_kv_cache8(ctypes.Structure):
+    _fields_ = _fields([("p", "k v k_scale v_scale"),
+                        ("l", "page_stride slot_stride head_stride scale_page_stride scale_block_stride "
+                              "scale_head_stride"),
+                        ("i", "n_pages page_size block_size format")])
+
+
+class moe_cache8_args(ctypes.Structure):
+    _fields_ = (_fields([("p", "k v row_start ctx_len block_table dev_status")])
+                + [("cache", moe_kv_cache8)]
+                + _fields([("l", "k_stride v_stride"), ("i", "n_req n_rows table_width kv_heads head_dim dtype")]))
+
+
+class moe_tree_attention8_args(ctypes.Structure):
+    _fields_ = (_fields([("p", "q out lse row_start ctx_len block_table tree_mask dev_status")])
+                + [("cache", moe_kv_cache8)]
+                + _fields([("l", "q_stride out_stride"),
+                           ("i", "n_req n_rows max_tree table_width q_heads kv_heads head_dim dtype"),
+                           ("f", "scale")]))
+
+
+class moe_verify_args(ctypes.Structure):
+    _fields_ = _fields([("p", "logits draft_probs row_start parents tokens uniform noise accepted path next_token "
+                              "dev_status"),
+                        ("l", "stride draft_stride noise_stride"), ("i", "n_req n_rows vocab dtype draft_dtype"),
+                        ("f", "inv_temperature")])
 
 
 class MoeError(RuntimeError):
@@ -159,6 +190,18 @@ _lib.moe_token_logprobs_workspace_bytes.argtypes = [ctypes.POINTER(moe_logprob_a
 _lib.moe_token_logprobs_workspace_bytes.restype = _sz
 _lib.moe_token_logprobs.argtypes = [ctypes.POINTER(moe_logprob_args), _vp, _sz, _vp]
 _lib.moe_token_logprobs.restype = ctypes.c_int
+_lib.moe_cache8_append.argtypes = [ctypes.POINTER(moe_cache8_args), _vp]
+_lib.moe_cache8_append.restype = ctypes.c_int
+_lib.moe_cache8_read.argtypes = [ctypes.POINTER(moe_cache8_args), _vp]
+_lib.moe_cache8_read.restype = ctypes.c_int
+_lib.moe_tree_attention8_workspace_bytes.argtypes = [ctypes.POINTER(moe_tree_attention8_args)]
+_lib.moe_tree_attention8_workspace_bytes.restype = _sz
+_lib.moe_tree_attention8.argtypes = [ctypes.POINTER(moe_tree_attention8_args), _vp, _sz, _vp]
+_lib.moe_tree_attention8.restype = ctypes.c_int
+_lib.moe_verify_drafts_workspace_bytes.argtypes = [ctypes.POINTER(moe_verify_args)]
+_lib.moe_verify_drafts_workspace_bytes.restype = _sz
+_lib.moe_verify_drafts.argtypes = [ctypes.POINTER(moe_verify_args), _vp, _sz, _vp]
+_lib.moe_verify_drafts.restype = ctypes.c_int
 _lib.moe_strerror.argtypes = [ctypes.c_int]
 _lib.moe_strerror.restype = ctypes.c_char_p
 
@@ -377,3 +420,66 @@ def moe_token_logprobs_workspace_bytes(args: moe_logprob_args) -> int:
 
 def moe_token_logprobs(args: moe_logprob_args, ws: int, ws_bytes: int, stream: int) -> None:
     _check(_lib.moe_token_logprobs(args, ws, ws_bytes, stream), "moe_token_logprobs")
+
+
+# ---- a cache in 8 bits, and the end of the round ----
+
+def make_kv_cache8(k: int, v: int, k_scale: int, v_scale: int, *, n_pages: int, page_size: int, block_size: int,
+                   format: int, page_stride: int, slot_stride: int, head_stride: int, scale_page_stride: int,
+                   scale_block_stride: int, scale_head_stride: int) -> moe_kv_cache8:
+    """A paged key/value cache in 8 bits (MOE_E4M3 or MOE_I8) by device addresses; strides in elements."""
+    return moe_kv_cache8(k, v, k_scale, v_scale, page_stride, slot_stride, head_stride, scale_page_stride,
+                         scale_block_stride, scale_head_stride, n_pages, page_size, block_size, format)
+
+
+def make_cache8_args(*, n_req: int, n_rows: int, kv_heads: int, head_dim: int, dtype: int, k: int, v: int,
+                     k_stride: int, v_stride: int, row_start: int, ctx_len: int, block_table: int, table_width: int,
+                     cache: moe_kv_cache8, dev_status: int) -> moe_cache8_args:
+    """Descriptor of moe_cache8_append and moe_cache8_read; strides in elements from row to row."""
+    return moe_cache8_args(k or None, v or None, row_start, ctx_len, block_table, dev_status, cache, k_stride, v_stride,
+                           n_req, n_rows, table_width, kv_heads, head_dim, dtype)
+
+
+def make_tree_attention8_args(*, n_req: int, n_rows: int, max_tree: int, q_heads: int, kv_heads: int, head_dim: int,
+                              dtype: int, q: int, q_stride: int, out: int, out_stride: int, row_start: int,
+                              ctx_len: int, block_table: int, table_width: int, cache: moe_kv_cache8, scale: float,
+                              dev_status: int, tree_mask: int = 0, lse: int = 0) -> moe_tree_attention8_args:
+    """Descriptor of moe_tree_attention8; strides in elements from row to row."""
+    return moe_tree_attention8_args(q or None, out or None, lse or None, row_start, ctx_len, block_table,
+                                    tree_mask or None, dev_status, cache, q_stride, out_stride, n_req, n_rows,
+                                    max_tree, table_width, q_heads, kv_heads, head_dim, dtype, scale)
+
+
+def make_verify_args(*, n_req: int, n_rows: int, vocab: int, dtype: int, logits: int, stride: int, row_start: int,
+                     tokens: int, accepted: int, path: int, next_token: int, dev_status: int,
+                     inv_temperature: float = 1.0, parents: int = 0, uniform: int = 0, noise: int = 0,
+                     noise_stride: int = 0, draft_probs: int = 0, draft_dtype: int = MOE_F32,
+                     draft_stride: int = 0) -> moe_verify_args:
+    """Descriptor of moe_verify_drafts; strides in elements from row to row, inv_temperature math.inf: greedy."""
+    return moe_verify_args(logits or None, draft_probs or None, row_start, parents or None, tokens or None,
+                           uniform or None, noise or None, accepted, path or None, next_token, dev_status, stride,
+                           draft_stride, noise_stride, n_req, n_rows, vocab, dtype, draft_dtype, inv_temperature)
+
+
+def moe_cache8_append(args: moe_cache8_args, stream: int) -> None:
+    _check(_lib.moe_cache8_append(args, stream), "moe_cache8_append")
+
+
+def moe_cache8_read(args: moe_cache8_args, stream: int) -> None:
+    _check(_lib.moe_cache8_read(args, stream), "moe_cache8_read")
+
+
+def moe_tree_attention8_workspace_bytes(args: moe_tree_attention8_args) -> int:
+    return int(_lib.moe_tree_attention8_workspace_bytes(args))
+
+
+def moe_tree_attention8(args: moe_tree_attention8_args, ws: int, ws_bytes: int, stream: int) -> None:
+    _check(_lib.moe_tree_attention8(args, ws, ws_bytes, stream), "moe_tree_attention8")
+
+
+def moe_verify_drafts_workspace_bytes(args: moe_verify_args) -> int:
+    return int(_lib.moe_verify_drafts_workspace_bytes(args))
+
+
+def moe_verify_drafts(args: moe_verify_args, ws: int, ws_bytes: int, stream: int) -> None:
+    _check(_lib.moe_verify_drafts(args, ws, ws_bytes, stream), "moe_verify_drafts")

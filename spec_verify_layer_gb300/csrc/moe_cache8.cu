@@ -1,0 +1,323 @@
+// Rows into a paged cache of 8 bits and out of it (moe_cache8_append, moe_cache8_read), one
+// launch each: each row is read once and written once.
+//
+// Append.  A task is one block of tokens of one head, of keys or of values: its largest magnitude,
+// the least power of two that holds it, the codes.  With powers of two x / 2^e is exact, so a
+// row is rounded once, and for e4m3, which has the same relative precision at every scale,
+// they cost one binade of range and no precision; what a block holds from before is carried to another scale without
+// a further rounding (int8: with half a step of its own).  The rows of a block lie next to each
+// other in the call, so a thread block takes kRows consecutive rows, finds their requests, and
+// works through the blocks that begin among them; a group of 8, 16 or 32 lanes takes a task, in
+// 16-byte loads.
+//
+// Read.  A thread takes 16 codes; a row's request, page and scales are looked up once a thread block.
+#include "moe_round_ops.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRows = 16;  // of a thread block
+
+struct Request {
+  int s, n, ctx;  // first row, rows, context; n < 0: not a request that can be worked on
+};
+
+__device__ __forceinline__ Request request(const moe_cache8_args& a, int b) {
+  Request q;
+  q.s = __ldg(a.row_start + b);
+  const int e = __ldg(a.row_start + b + 1);
+  q.ctx = __ldg(a.ctx_len + b);
+  const bool ok = q.s >= 0 && e >= q.s && e <= a.n_rows && q.ctx >= 0 &&
+                  (long long)q.ctx + (e - q.s) <= min((long long)a.table_width * a.cache.page_size, 0x7fffffffll - 256);
+  q.n = ok ? e - q.s : -1;
+  return q;
+}
+
+__device__ __forceinline__ unsigned bad_requests(const moe_cache8_args& a) {
+  unsigned flags = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(a.row_start) != 0) flags |= MOE_DEV_LENGTH;
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.n_req; b += gridDim.x * kThreads)
+    if (request(a, b).n < 0) flags |= MOE_DEV_LENGTH;
+  return flags;
+}
+
+// A row's eight elements in 32 bits.
+template <int DT>
+struct Row8 {
+  uint4 raw[DT == MOE_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, long long element) {
+    if constexpr (DT == MOE_F32) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + element);
+      raw[0] = p[0];
+      raw[1] = p[1];
+    } else {
+      raw[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + element);
+    }
+  }
+  __device__ __forceinline__ void floats(float* x) const {
+    if constexpr (DT == MOE_F32) {
+      const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(w[j]);
+    } else {
+      const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack2<DT>(w[j]);
+        x[2 * j] = v.x;
+        x[2 * j + 1] = v.y;
+      }
+    }
+  }
+};
+
+// The values of four codes (a product by a power of two where the code's exponent is put into
+// that of a 32-bit number).
+__device__ __forceinline__ void decode4(uint32_t w, bool i8, float* x) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = (int8_t)(w >> (8 * j));
+    x[j] = i8 ? (float)c : __uint_as_float(((uint32_t)c & 0x80000000u) | ((uint32_t)(c & 0x7f) << 20)) * 1.329227995784916e36f;  // 2^120
+  }
+}
+
+__device__ __forceinline__ uint32_t encode4(const float* x, float inv, bool i8) {
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = x[j] == x[j] ? x[j] * inv : 0.f;
+  if (i8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w |= ((uint32_t)max(-127, min(127, __float2int_rn(y[j]))) & 0xffu) << (8 * j);
+    return w;
+  }
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+// e of the least power of two 2^e, e >= -126, with most <= Q 2^e: most = 1.f * 2^E is at most
+// 448 * 2^(E - 8) where 1.f <= 1.75, at most 127 * 2^(E - 6) where 1.f <= 127 / 64.
+__device__ __forceinline__ int scale_exponent(float most, bool i8) {
+  const uint32_t bits = __float_as_uint(most), f = bits & 0x7fffffu;
+  const int E = (int)(bits >> 23) - 127, e = i8 ? E - 6 + (f > 0x7e0000u) : E - 8 + (f > 0x600000u);
+  return max(e, -126);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ moe_cache8_args a, PageDivide pd, int lanes) {
+  constexpr int CPR = D / 8;  // chunks of eight elements of a row
+  struct Begin {              // a block of tokens that begins among these rows
+    long long codes, scales;  // of its first slot, and of its scale, head 0
+    int row, held, rows;      // first row, slots before it, rows
+  };
+  __shared__ Begin begin[kRows];
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.cache.block_size;
+  const bool i8 = a.cache.format == MOE_I8;
+  unsigned flags = bad_requests(a);
+  if (tid == 0) count = 0;
+  __syncthreads();
+  for (int i = warp; i < kRows; i += kWarps) {
+    const int r = blockIdx.x * kRows + i;
+    if (r >= a.n_rows) break;
+    const int b = last_not_above_warp(a.row_start, a.n_req, r);
+    const Request q = request(a, b);
+    const int pos = q.ctx + r - q.s, in_block = pos & (B - 1);
+    if (r < q.s || r - q.s >= q.n || (r > q.s && in_block)) continue;
+    const int col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
+    const int page = __ldg(a.block_table + (long long)b * a.table_width + col);
+    if (page < 0 || page >= a.cache.n_pages) {
+      flags |= MOE_DEV_INDEX;
+      continue;
+    }
+    const int slot = pos - in_block - col * a.cache.page_size;
+    if (lane == 0)
+      begin[atomicAdd(&count, 1)] = {page * a.cache.page_stride + slot * a.cache.slot_stride,
+                                     page * a.cache.scale_page_stride + slot / B * a.cache.scale_block_stride,
+                                     r, in_block, min(B - in_block, q.n - (r - q.s))};
+  }
+  __syncthreads();
+  const int heads = a.kv_heads, tasks = count * 2 * heads, group = tid / lanes, groups = kThreads / lanes, at = tid & (lanes - 1);
+  const unsigned members = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & ~(lanes - 1));
+  for (int t = group; t < tasks; t += groups) {
+    const int head = t % heads, kv = t / heads & 1;
+    const Begin g = begin[t / (2 * heads)];
+    const void* x = kv ? a.v : a.k;
+    const long long x0 = g.row * (kv ? a.v_stride : a.k_stride) + head * D, x_stride = kv ? a.v_stride : a.k_stride;
+    uint8_t* codes = static_cast<uint8_t*>(kv ? a.cache.v : a.cache.k) + g.codes + head * a.cache.head_stride;
+    float* scale = (kv ? a.cache.v_scale : a.cache.k_scale) + g.scales + head * a.cache.scale_head_stride;
+    const float old = g.held ? scale_of(*scale, flags) : 0.f;
+    float most = 0.f;
+    bool odd = false;
+    const auto look = [&](const float* v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = fabsf(v[j]);
+        if (m < INFINITY) most = fmaxf(most, m);
+        else odd = true;
+      }
+    };
+    for (int c = at; c < g.held * CPR; c += lanes) {
+      const uint2 w = *reinterpret_cast<const uint2*>(codes + c / CPR * a.cache.slot_stride + c % CPR * 8);
+      float v[8];
+      decode4(w.x, i8, v);
+      decode4(w.y, i8, v + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= old;
+      look(v);
+    }
+#pragma unroll 4
+    for (int c = at; c < g.rows * CPR; c += lanes) {
+      Row8<DT> y;
+      y.load(x, x0 + c / CPR * x_stride + c % CPR * 8);
+      float v[8];
+      y.floats(v);
+      look(v);
+    }
+    for (int o = lanes >> 1; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(members, most, o));
+    if (odd) flags |= MOE_DEV_VALUE;
+    const int e = scale_exponent(most, i8);
+    const float now = __uint_as_float((uint32_t)(e + 127) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (now != old)
+      for (int c = at; c < g.held * CPR; c += lanes) {
+        uint2* p = reinterpret_cast<uint2*>(codes + c / CPR * a.cache.slot_stride + c % CPR * 8);
+        const uint2 w = *p;
+        float v[8];
+        decode4(w.x, i8, v);
+        decode4(w.y, i8, v + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= old;
+        *p = make_uint2(encode4(v, inv, i8), encode4(v + 4, inv, i8));
+      }
+#pragma unroll 4
+    for (int c = at; c < g.rows * CPR; c += lanes) {
+      Row8<DT> y;
+      y.load(x, x0 + c / CPR * x_stride + c % CPR * 8);
+      float v[8];
+      y.floats(v);
+      *reinterpret_cast<uint2*>(codes + (g.held + c / CPR) * a.cache.slot_stride + c % CPR * 8) =
+          make_uint2(encode4(v, inv, i8), encode4(v + 4, inv, i8));
+    }
+    if (at == 0) *scale = now;
+  }
+  if (flags) atomicOr(a.dev_status, flags);
+}
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ moe_cache8_args a, PageDivide pd) {
+  constexpr int CPR = D / 16;
+  __shared__ long long from[kRows], scales[kRows];  // -1: not a row of a request, -2: nothing cached
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool i8 = a.cache.format == MOE_I8;
+  unsigned flags = bad_requests(a);
+  const int r0 = blockIdx.x * kRows, rows = min(kRows, a.n_rows - r0);
+  for (int i = warp; i < rows; i += kWarps) {
+    const int r = r0 + i, b = last_not_above_warp(a.row_start, a.n_req, r);
+    const Request q = request(a, b);
+    long long at = -1, scale = 0;
+    if (r >= q.s && r - q.s < q.n) {
+      const int pos = q.ctx + r - q.s, col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
+      const int page = __ldg(a.block_table + (long long)b * a.table_width + col), slot = pos - col * a.cache.page_size;
+      if (page < 0 || page >= a.cache.n_pages) {
+        flags |= MOE_DEV_INDEX;
+        at = -2;
+      } else {
+        at = page * a.cache.page_stride + slot * a.cache.slot_stride;
+        scale = page * a.cache.scale_page_stride + slot / a.cache.block_size * a.cache.scale_block_stride;
+      }
+    }
+    if (lane == 0) {
+      from[i] = at;
+      scales[i] = scale;
+    }
+  }
+  __syncthreads();
+  const int per_row = 2 * a.kv_heads * CPR;
+#pragma unroll 2
+  for (int t = tid; t < rows * per_row; t += kThreads) {
+    const int i = t / per_row, h2 = t % per_row / CPR, c = t % CPR, kv = h2 >= a.kv_heads, head = h2 - (kv ? a.kv_heads : 0);
+    if (from[i] == -1) continue;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    float s = 0.f;
+    if (from[i] >= 0) {
+      w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? a.cache.v : a.cache.k) + from[i] +
+                                          head * a.cache.head_stride + c * 16);
+      s = scale_of((kv ? a.cache.v_scale : a.cache.k_scale)[scales[i] + head * a.cache.scale_head_stride], flags);
+    }
+    const long long to = (long long)(r0 + i) * (kv ? a.v_stride : a.k_stride) + head * D + c * 16;
+    float x[16];
+    decode4(w.x, i8, x);
+    decode4(w.y, i8, x + 4);
+    decode4(w.z, i8, x + 8);
+    decode4(w.w, i8, x + 12);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] *= s;
+    if constexpr (DT == MOE_F32) {
+      float4* out = reinterpret_cast<float4*>(static_cast<float*>(kv ? a.v : a.k) + to);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) out[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    } else {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? a.v : a.k) + to);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        out[j] = make_uint4(pack2<DT>(x[8 * j], x[8 * j + 1]), pack2<DT>(x[8 * j + 2], x[8 * j + 3]),
+                            pack2<DT>(x[8 * j + 4], x[8 * j + 5]), pack2<DT>(x[8 * j + 6], x[8 * j + 7]));
+    }
+  }
+  if (flags) atomicOr(a.dev_status, flags);
+}
+
+int check(const moe_cache8_args* p) {
+  if (!p) return MOE_EINVAL;
+  const moe_cache8_args& a = *p;
+  if (a.n_req < 1 || a.n_rows < 0 || a.table_width < 1 || a.kv_heads < 1 || a.head_dim < 1) return MOE_EINVAL;
+  if (a.dtype != MOE_BF16 && a.dtype != MOE_F16 && a.dtype != MOE_F32) return MOE_EINVAL;
+  if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256) return MOE_EUNSUPPORTED;
+  if (a.n_req > 16384 || a.n_rows > (1 << 24) || a.kv_heads > 256) return MOE_EUNSUPPORTED;
+  const int rc = check_cache(a.cache, a.kv_heads);
+  if (rc != MOE_OK) return rc;
+  if (!stride_ok(a.k_stride) || !stride_ok(a.v_stride)) return MOE_EINVAL;
+  if (!rows_ok(a.n_rows, a.k_stride) || !rows_ok(a.n_rows, a.v_stride)) return MOE_EUNSUPPORTED;
+  if (!ptr_ok(a.dev_status, 4) || !ptr_ok(a.row_start, 4) || !ptr_ok(a.ctx_len, 4) || !ptr_ok(a.block_table, 4)) return MOE_EINVAL;
+  if (a.n_rows > 0 && (!ptr_ok(a.k, 16) || !ptr_ok(a.v, 16))) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+template <int DT>
+cudaError_t append(const moe_cache8_args& a, cudaStream_t st) {
+  // lanes of a task: no more than it has chunks of eight elements
+  const int chunks = a.cache.block_size * a.head_dim / 8, lanes = chunks >= 32 ? 32 : chunks;
+  const auto fn = a.head_dim == 64 ? k_append<DT, 64> : a.head_dim == 128 ? k_append<DT, 128> : k_append<DT, 256>;
+  return launch_kernel(fn, (a.n_rows + kRows - 1) / kRows, kThreads, 0, st, a, page_divide(a.cache.page_size), lanes);
+}
+template <int DT>
+cudaError_t read(const moe_cache8_args& a, cudaStream_t st) {
+  const auto fn = a.head_dim == 64 ? k_read<DT, 64> : a.head_dim == 128 ? k_read<DT, 128> : k_read<DT, 256>;
+  return launch_kernel(fn, (a.n_rows + kRows - 1) / kRows, kThreads, 0, st, a, page_divide(a.cache.page_size));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_cache8_append(const moe_cache8_args* args, void* stream) {
+  const int rc = check(args);
+  if (rc != MOE_OK || args->n_rows == 0) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(args->dtype == MOE_BF16  ? append<MOE_BF16>(*args, st)
+                       : args->dtype == MOE_F16 ? append<MOE_F16>(*args, st)
+                                                : append<MOE_F32>(*args, st));
+}
+
+extern "C" int moe_cache8_read(const moe_cache8_args* args, void* stream) {
+  const int rc = check(args);
+  if (rc != MOE_OK || args->n_rows == 0) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(args->dtype == MOE_BF16  ? read<MOE_BF16>(*args, st)
+                       : args->dtype == MOE_F16 ? read<MOE_F16>(*args, st)
+                                                : read<MOE_F32>(*args, st));
+}

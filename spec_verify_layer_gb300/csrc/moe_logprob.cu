@@ -32,8 +32,7 @@
 // after the other.
 #include <type_traits>
 
-#include "moe_common.cuh"
-#include "moe_round_ops.cuh"
+#include "moe_vocab.cuh"
 
 namespace moe {
 namespace {
@@ -45,19 +44,12 @@ constexpr int kLpStages = 3;    // chunks in shared memory, asked for ahead of t
 constexpr int kLpMaxK = 32, kLpMaxSlices = 32;
 constexpr int kLpPend = 480;    // entries that wait to be merged
 constexpr int kLpSliced = 304;  // blocks up to which rows are cut into slices
-using Key = unsigned long long;
 
 struct LpPartial {  // a slice's result in the workspace
   float m, s, w;
   int rank;
   Key top[kLpMaxK];
 };
-
-__device__ __forceinline__ Key key_of(float x, int id) { return ((Key)order_key(x) << 32) | (uint32_t)~id; }
-__device__ __forceinline__ float key_logit(Key k) { return key_value((unsigned)(k >> 32)); }
-__device__ __forceinline__ int key_id(Key k) { return (int)~(uint32_t)k; }
-
-__device__ __forceinline__ Key max_key(Key a, Key b) { return a > b ? a : b; }
 
 // 32 keys of a warp in descending order over the lanes
 __device__ __forceinline__ Key sort_desc(Key v, int lane) {
@@ -69,57 +61,6 @@ __device__ __forceinline__ Key sort_desc(Key v, int lane) {
       const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
       v = keep_max ? (v > x ? v : x) : (v < x ? v : x);
     }
-  return v;
-}
-
-template <int DT>
-struct Vec {
-  static constexpr int N = DT == MOE_F32 ? 4 : 8;
-  static constexpr uint32_t kNone = DT == MOE_F32 ? 0xff800000u : DT == MOE_BF16 ? 0xff80ff80u : 0xfc00fc00u;
-  uint4 raw;
-  __device__ __forceinline__ float at(int e) const {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    if constexpr (DT == MOE_F32) {
-      return __uint_as_float(w[e]);
-    } else {
-      const float2 p = unpack2<DT>(w[e >> 1]);
-      return (e & 1) ? p.y : p.x;
-    }
-  }
-};
-
-template <int DT>
-__device__ __forceinline__ float logit_at(const void* base, long long i) {
-  if constexpr (DT == MOE_F32) {
-    return static_cast<const float*>(base)[i];
-  } else {
-    const uint32_t w = static_cast<const uint16_t*>(base)[i];
-    return unpack2<DT>(w).x;
-  }
-}
-
-// A vector whose first element is entry `first` of the row; entries outside [0, vocab) -infinity.
-template <int DT>
-__device__ __forceinline__ Vec<DT> load_vec(const void* row, int first, int vocab) {
-  Vec<DT> v;
-  constexpr int N = Vec<DT>::N, size = 16 / N;
-  if (first >= 0 && first + N <= vocab) {
-    v.raw = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (long long)first * size));
-    return v;
-  }
-  uint32_t w[4] = {Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone};
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int i = first + e;
-    if (i < 0 || i >= vocab) continue;
-    if constexpr (DT == MOE_F32) {
-      w[e] = static_cast<const uint32_t*>(row)[i];
-    } else {
-      const uint32_t x = static_cast<const uint16_t*>(row)[i];
-      w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | (x << 16) : (w[e >> 1] & 0xffff0000u) | x;
-    }
-  }
-  v.raw = make_uint4(w[0], w[1], w[2], w[3]);
   return v;
 }
 

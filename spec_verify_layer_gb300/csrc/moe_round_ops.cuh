@@ -1,6 +1,6 @@
 // Shared by the attention-side operators of a verify round (moe_round_map.cu,
-// moe_qk_rope.cu, moe_tree_attn.cu, moe_logprob.cu): argument checks and the element
-// types.  Internal; not part of the public ABI.
+// moe_qk_rope.cu, moe_tree_attn.cuh, moe_logprob.cu, moe_cache8.cu, moe_verify_drafts.cu):
+// argument checks and the element types.  Internal; not part of the public ABI.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,6 +38,40 @@ inline int check_cache(const moe_kv_cache& c, int heads) {
   if (c.page_size > 65536 || (int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31) || cache_span(c, heads) >= kMaxOffset)
     return MOE_EUNSUPPORTED;
   return MOE_OK;
+}
+
+// strides of codes: multiples of 16 bytes, not negative
+inline bool code_stride_ok(int64_t s) { return s >= 0 && s % 16 == 0 && s < ((int64_t)1 << 40); }
+inline bool scale_stride_ok(int64_t s) { return s >= 0 && s < ((int64_t)1 << 40); }
+inline Wide cache_span(const moe_kv_cache8& c, int heads) {
+  return (Wide)(c.n_pages - 1) * c.page_stride + (Wide)(c.page_size - 1) * c.slot_stride + (Wide)(heads - 1) * c.head_stride;
+}
+
+inline int check_cache(const moe_kv_cache8& c, int heads) {
+  if (!ptr_ok(c.k, 16) || !ptr_ok(c.v, 16) || !ptr_ok(c.k_scale, 4) || !ptr_ok(c.v_scale, 4)) return MOE_EINVAL;
+  if (c.n_pages < 1 || c.page_size < 1 || c.block_size < 1 || c.page_size % c.block_size ||
+      (c.block_size & (c.block_size - 1)) || (c.format != MOE_E4M3 && c.format != MOE_I8))
+    return MOE_EINVAL;
+  if (!code_stride_ok(c.page_stride) || !code_stride_ok(c.slot_stride) || !code_stride_ok(c.head_stride) ||
+      !scale_stride_ok(c.scale_page_stride) || !scale_stride_ok(c.scale_block_stride) || !scale_stride_ok(c.scale_head_stride))
+    return MOE_EINVAL;
+  const Wide scales = (Wide)(c.n_pages - 1) * c.scale_page_stride +
+                      (Wide)(c.page_size / c.block_size - 1) * c.scale_block_stride + (Wide)(heads - 1) * c.scale_head_stride;
+  if (c.block_size > 128 || c.page_size > 65536 || (int64_t)c.n_pages * c.page_size >= ((int64_t)1 << 31) ||
+      cache_span(c, heads) >= kMaxOffset || scales >= kMaxOffset)
+    return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+// n / page_size = (n * mul) >> shift for every n below 2^31
+struct PageDivide {
+  unsigned mul;
+  int shift;
+};
+inline PageDivide page_divide(int page_size) {
+  int bits = 0;
+  while ((1 << bits) < page_size) ++bits;
+  return {(unsigned)((1ull << (31 + bits)) / (unsigned)page_size + 1), 31 + bits};
 }
 
 // The current device's SM count; 0 if there is no usable device.
@@ -134,6 +168,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
   const uint32_t s = a + b;
   return s < a ? 0xffffffffu : s;
+}
+
+// A scale of a cache in 8 bits: 0 and finite positive normal numbers are one, others count as 0.
+__device__ __forceinline__ float scale_of(float s, unsigned& flags) {
+  if (s >= 1.1754943508222875e-38f && s < INFINITY) return s;
+  if (s != 0.f) flags |= MOE_DEV_VALUE;
+  return 0.f;
+}
+
+// Largest b in [0, n) with start[b] <= x, for start ascending with start[0] <= x, found by a warp
+// with 32 probes at a time; some b in range where start is not ascending.  All lanes call.
+__device__ __forceinline__ int last_not_above_warp(const int32_t* start, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {  // the answer is in [lo, lo + n)
+    const int step = (n + 31) >> 5, at = lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, at < n && __ldg(start + lo + at) <= x);
+    const int k = max(0, 31 - __clz(below));  // (lane 0's first probe is taken for granted)
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
 }
 
 // Largest b in [0, n) with start[b] <= x, for start ascending with start[0] <= x.

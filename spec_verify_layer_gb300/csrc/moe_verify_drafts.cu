@@ -1,0 +1,576 @@
+// Which drafted tokens stand and which token follows (moe_verify_drafts), two launches.
+//
+// k_sums: one pass over the logits of the rows that drafts hang on (greedy: of all rows); a block
+// takes a slice of a row, a thread running maximum m and sum s = sum 2^((x - m) c), c = log2(e) / T
+// (greedy: the largest logit's key).  Rows without drafts behind them need no sums and are
+// left out.
+//
+// k_draw: a request's blocks each join its rows' sums and walk down its drafts (a few dozen numbers, in
+// 64 bits; cheaper done in each block than handed from one to the others), then scan a slice of the
+// row where the walk ended for the largest rest(x) / noise(x): an exponential race, so the
+// draw needs one pass, no prefix sums, and no order between slices.  The request's block that
+// ends last joins the slices, by (ratio, lower id), so it does not matter which one that is.
+//
+// The exponent (x - m) c is taken with c in two parts (c >= hi, lo > 0, so that -infinity stays
+// what it is): with c rounded to 32 bits probabilities far from the maximum would be off by
+// some 1e-6, and a decision lies that near its border far more often than by the 1e-7 of the
+// rounded sums.
+#include "moe_vocab.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTree = 64;
+constexpr int kVecs = 4;         // vectors a thread has on their way
+constexpr int kMaxSlices = 32;
+constexpr int kBlocks = 608;     // four of an SM: rows and requests are cut into slices up to there
+constexpr int kSliceMin = 2048;  // entries of a slice at least
+constexpr int kCounters = (int)(kCounterBytes / sizeof(unsigned));
+
+struct Drawn {  // a slice's candidates: of the rest, and of p for where nothing of the rest is left
+  float m, best, best_p;
+  int id, id_p, bad;
+};
+
+struct Plan {
+  int row_slices, row_vecs;    // slices of a row in k_sums, vectors of a slice
+  int draw_slices, draw_vecs;  // of the row that is drawn from
+  float hi, lo;                // c
+  double inv_t;
+  float2* sums;    // [rows][row_slices]: m, s
+  Key* keys;       // greedy: [rows][row_slices]
+  Drawn* drawn;    // [requests][draw_slices]
+  unsigned* left;  // [requests]
+};
+
+__device__ __forceinline__ float2 exponent(float2 x, float m, const Plan& p) {
+  const Pair d = add2(pair(x), pair(-m, -m));
+  return split(fma2(d, pair(p.hi, p.hi), mul2(d, pair(p.lo, p.lo))));
+}
+__device__ __forceinline__ float factor(float from, float to, const Plan& p) {  // of sums that go from one maximum to a larger
+  const float d = from - to;
+  return exp2_fast(fmaf(d, p.hi, d * p.lo));
+}
+__device__ __forceinline__ float element(const void* base, int dt, long long i) {
+  return dt == MOE_F32 ? logit_at<MOE_F32>(base, i) : dt == MOE_BF16 ? logit_at<MOE_BF16>(base, i) : logit_at<MOE_F16>(base, i);
+}
+
+template <int DT>
+struct Row {  // a row of logits in vectors
+  static constexpr int N = Vec<DT>::N;
+  const char* base;
+  int lead, vecs;
+  __device__ __forceinline__ Row(const moe_verify_args& a, int row) {
+    base = static_cast<const char*>(a.logits) + (long long)row * a.stride * (16 / N);
+    lead = (int)((reinterpret_cast<uintptr_t>(base) & 15) / (16 / N));
+    vecs = (a.vocab + lead + N - 1) / N;
+  }
+};
+
+template <int DT, bool GREEDY>
+__global__ void __launch_bounds__(kThreads) k_sums(const __grid_constant__ moe_verify_args a, const __grid_constant__ Plan p) {
+  constexpr int N = Vec<DT>::N;
+  __shared__ float m_of[kWarps], s_of[kWarps];
+  __shared__ Key k_of[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = blockIdx.x / p.row_slices, slice = blockIdx.x - row * p.row_slices;
+  {
+    // every warp finds the row's request and looks for its children
+    const int b = last_not_above_warp(a.row_start, a.n_req, row);
+    const int s = __ldg(a.row_start + b), e = __ldg(a.row_start + b + 1), n = e - s, i = row - s;
+    if (s < 0 || i < 0 || row >= e || e > a.n_rows || n > kTree) return;  // k_draw says so
+    if (!GREEDY) {
+      bool child = false;
+      for (int j = i + 1 + lane; j < n; j += 32) child |= a.parents ? __ldg(a.parents + s + j) == i : j == i + 1;
+      if (!__any_sync(0xffffffffu, child)) return;
+    }
+  }
+  const Row<DT> r(a, row);
+  const int v0 = slice * p.row_vecs, v1 = min(v0 + p.row_vecs, r.vecs);
+  float m = -INFINITY, s = 0.f;
+  int id = 0;
+  bool bad = false;
+  for (int v = v0 + tid; v < v1; v += kThreads * kVecs) {
+    Vec<DT> x[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      x[j].raw = make_uint4(Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone, Vec<DT>::kNone);
+      if (v + j * kThreads < v1) x[j] = load_vec<DT>(r.base, (v + j * kThreads) * N - r.lead, a.vocab);
+    }
+    if constexpr (GREEDY) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float f = x[j].at(e);
+          bad |= !(f < INFINITY);
+          if (f > m) {
+            m = f;
+            id = (v + j * kThreads) * N - r.lead + e;
+          }
+        }
+    } else {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int e = 0; e < N; ++e) top = fmaxf(top, x[j].at(e));
+      if (top > m) {
+        if (m > -INFINITY) s *= factor(m, top, p);
+        m = top;
+      }
+      const float shift = m == -INFINITY ? 0.f : m;
+      Pair sum = 0;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+          const float2 u = exponent(make_float2(x[j].at(e), x[j].at(e + 1)), shift, p);
+          sum = add2(sum, pair(exp2_fast(u.x), exp2_fast(u.y)));
+        }
+      const float2 both = split(sum);
+      s += both.x + both.y;
+    }
+  }
+  if constexpr (GREEDY) {
+    Key key = bad ? ~0ull : m == -INFINITY ? 0 : key_of(m, id);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) key = max_key(key, __shfl_xor_sync(0xffffffffu, key, o));
+    if (lane == 0) k_of[warp] = key;
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) key = max_key(key, k_of[w]);
+      p.keys[blockIdx.x] = key;
+    }
+  } else {
+    const auto join = [&](float om, float os) {
+      const float to = fmaxf(m, om);
+      if (m < to) s = m == -INFINITY ? s : s * factor(m, to, p);  // (nothing so far: 0, or NaN that has to stay)
+      if (om < to) os = om == -INFINITY ? os : os * factor(om, to, p);
+      s += os;
+      m = to;
+    };
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+      join(om, os);
+    }
+    if (lane == 0) {
+      m_of[warp] = m;
+      s_of[warp] = s;
+    }
+    __syncthreads();
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) join(m_of[w], s_of[w]);
+      p.sums[blockIdx.x] = make_float2(m, s);
+    }
+  }
+}
+
+struct Walk {  // of one request, in shared memory
+  double prob[kTree], S[kTree], border[kTree];
+  float m[kTree], u[kTree];
+  int parent[kTree], token[kTree], best[kTree], inner[kTree];
+  bool again[kTree];
+  int order[kTree];
+  int out[kTree], n_out;  // tokens that were rejected behind the last row
+  int last, stands, child;
+};
+
+// N consecutive entries of a row from `first` on, in 32 bits; `other` outside [0, n).
+template <int N>
+__device__ __forceinline__ void entries(const void* row, int dt, int first, int n, float other, float* x) {
+  const int size = dt == MOE_F32 ? 4 : 2;
+  const char* at = static_cast<const char*>(row) + (long long)first * size;
+  if (first >= 0 && first + N <= n && (reinterpret_cast<uintptr_t>(at) & (N * size >= 16 ? 15 : 7)) == 0) {
+    if (dt == MOE_F32) {
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(at) + j);
+        x[4 * j] = v.x;
+        x[4 * j + 1] = v.y;
+        x[4 * j + 2] = v.z;
+        x[4 * j + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(at) + j);
+        const float2 lo = dt == MOE_BF16 ? unpack2<MOE_BF16>(w.x) : unpack2<MOE_F16>(w.x);
+        const float2 hi = dt == MOE_BF16 ? unpack2<MOE_BF16>(w.y) : unpack2<MOE_F16>(w.y);
+        x[4 * j] = lo.x;
+        x[4 * j + 1] = lo.y;
+        x[4 * j + 2] = hi.x;
+        x[4 * j + 3] = hi.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) x[j] = first + j >= 0 && first + j < n ? element(row, dt, first + j) : other;
+}
+
+// One warp goes down the drafts of rows [s, s + n).
+template <int DT>
+__device__ __forceinline__ unsigned walk_down(const moe_verify_args& a, const Plan& p, Walk& w, int s, int n, bool greedy) {
+  const int lane = threadIdx.x & 31;
+  unsigned flags = 0;
+  for (int i = lane; i < n; i += 32) {
+    int up = i - 1, token = i ? __ldg(a.tokens + s + i) : -1;
+    if (a.parents && i) {
+      up = __ldg(a.parents + s + i);
+      if (up < -1 || up >= i) {
+        flags |= MOE_DEV_INDEX;
+        up = -1;
+      }
+    }
+    if (token < -1 || token >= a.vocab) {
+      flags |= MOE_DEV_INDEX;
+      token = -1;
+    }
+    w.parent[i] = up;
+    w.token[i] = token;
+    w.u[i] = greedy || !i ? 0.f : __ldg(a.uniform + s + i);
+    w.inner[i] = 0;
+  }
+  __syncwarp();
+  for (int i = lane; i < n; i += 32)
+    if (w.parent[i] >= 0) w.inner[w.parent[i]] = 1;
+  __syncwarp();
+  for (int i = lane; i < n; i += 32) {
+    w.best[i] = -1;
+    w.m[i] = -INFINITY;
+    w.S[i] = 0.;
+    if (greedy) {
+      const Key* key = p.keys + (long long)(s + i) * p.row_slices;
+      Key top = 0;
+      for (int j = 0; j < p.row_slices; ++j) top = max_key(top, key[j]);
+      w.best[i] = top == 0 ? -1 : top == ~0ull ? -2 : key_id(top);
+    } else if (w.inner[i]) {
+      const float2* part = p.sums + (long long)(s + i) * p.row_slices;
+      float m = -INFINITY;
+#pragma unroll 4
+      for (int j = 0; j < p.row_slices; ++j) m = fmaxf(m, part[j].x);
+      double S = 0.;
+#pragma unroll 4
+      for (int j = 0; j < p.row_slices; ++j) {
+        const float2 v = part[j];
+        S += v.x == -INFINITY ? (double)v.y : (double)v.y * factor(v.x, m, p);
+      }
+      w.m[i] = m;
+      w.S[i] = S;
+    }
+  }
+  __syncwarp();
+  for (int i = lane; i < n; i += 32) {
+    const int up = w.parent[i], token = w.token[i];
+    double prob = 0., border = 1.;
+    bool again = false;
+    if (up >= 0 && token >= 0) {
+      if (greedy) {
+        prob = w.best[up] == token ? 1. : 0.;
+        border = 0.;
+      } else {
+        const float x = logit_at<DT>(static_cast<const char*>(a.logits), (long long)(s + up) * a.stride + token);
+        const double S = w.S[up];
+        if (S != 0.) prob = exp(((double)x - (double)w.m[up]) * p.inv_t) / S;
+        if (a.draft_probs) {
+          border = (double)w.u[i] * (double)element(a.draft_probs, a.draft_dtype, (long long)(s + i) * a.draft_stride + token);
+        } else {
+          for (int j = 0; j < i; ++j) again |= w.parent[j] == up && w.token[j] == token;
+        }
+      }
+    }
+    w.prob[i] = again ? 0. : prob;
+    w.border[i] = border;
+  }
+  __syncwarp();
+  // the walk itself, by all lanes alike
+  int last = 0, stands = 0;
+  double rest = 1.;
+  const bool chain = greedy || a.draft_probs;
+  for (int i = 1; i < n; ++i) {
+    if (w.parent[i] != last) continue;
+    const double prob = w.prob[i], border = chain ? w.border[i] : (double)w.u[i] * rest;
+    if (prob > 0. && border < prob) {
+      last = i;
+      rest = 1.;
+      ++stands;
+      if (lane == 0) w.order[stands] = i;
+    } else {
+      rest -= prob;
+    }
+  }
+  if (lane == 0) {
+    w.order[0] = 0;
+    w.last = last;
+    w.stands = stands;
+    w.child = -1;
+    w.n_out = 0;
+    for (int i = last + 1; i < n; ++i)
+      if (w.parent[i] == last && w.token[i] >= 0) {
+        w.child = i;
+        w.out[w.n_out++] = w.token[i];
+      }
+  }
+  return flags;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_verify_args a, const __grid_constant__ Plan p) {
+  constexpr int N = Vec<DT>::N;
+  __shared__ Walk w;
+  __shared__ Drawn all[kWarps];
+  __shared__ int ends;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.draw_slices, slice = blockIdx.x - b * p.draw_slices;
+  const bool greedy = isinf(a.inv_temperature);
+  const int s = __ldg(a.row_start + b), e = __ldg(a.row_start + b + 1), n = e - s;
+  if (b == 0 && slice == 0 && tid == 0 && s != 0) atomicOr(a.dev_status, MOE_DEV_LENGTH);
+  if (s < 0 || e < s || e > a.n_rows || n > kTree || n == 0) {
+    if (slice == 0 && tid == 0) {
+      a.accepted[b] = 0;
+      a.next_token[b] = -1;
+      if (n != 0 || s < 0 || e > a.n_rows) atomicOr(a.dev_status, MOE_DEV_LENGTH);
+    }
+    return;
+  }
+  if (warp == 0) {
+    const unsigned flags = walk_down<DT>(a, p, w, s, n, greedy);
+    if (flags && slice == 0) atomicOr(a.dev_status, flags);
+  }
+  __syncthreads();
+  const int last = w.last;
+  if (slice == 0) {
+    for (int i = tid; i < n; i += kThreads) a.path[s + i] = i <= w.stands ? w.order[i] : -1;
+    if (tid == 0) a.accepted[b] = w.stands;
+  }
+  const bool inner = w.inner[last] != 0;
+  const double S = w.S[last];
+  if (greedy || (inner && !(S > 0.))) {  // known already, or nothing to draw from
+    if (slice == 0 && tid == 0) {
+      a.next_token[b] = greedy ? max(w.best[last], -1) : -1;
+      if (greedy ? w.best[last] == -2 : S != 0.) atomicOr(a.dev_status, MOE_DEV_VALUE);
+    }
+    return;
+  }
+
+  const Row<DT> r(a, s + last);
+  const float* noise = a.noise + b * a.noise_stride;
+  const int child = w.child, n_out = a.draft_probs ? 0 : w.n_out;
+  const char* q = a.draft_probs && child >= 0
+                      ? static_cast<const char*>(a.draft_probs) + (long long)(s + child) * a.draft_stride * (a.draft_dtype == MOE_F32 ? 4 : 2)
+                      : nullptr;
+  const bool residual = q || n_out > 0;
+  const float inv_S = inner ? (float)(1. / S) : 1.f;
+  Drawn d{inner ? w.m[last] : -INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
+  const int v0 = slice * p.draw_vecs, v1 = min(v0 + p.draw_vecs, r.vecs);
+#pragma unroll 1
+  for (int v = v0 + tid; v < v1; v += 2 * kThreads) {
+    Vec<DT> x[2];
+    float race[2][N], from[2][N];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int at = v + j * kThreads, first = at < v1 ? at * N - r.lead : a.vocab;
+      x[j] = load_vec<DT>(r.base, first, a.vocab);
+      entries<N>(noise, MOE_F32, first, a.vocab, 0.f, race[j]);
+      if (q) entries<N>(q, a.draft_dtype, first, a.vocab, 0.f, from[j]);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float f = x[j].at(i);
+        d.bad |= !(f < INFINITY);
+        top = fmaxf(top, f);
+      }
+    if (top > d.m) {
+      if (d.m > -INFINITY) d.best_p *= factor(d.m, top, p);
+      d.m = top;
+    }
+    const float shift = d.m == -INFINITY ? 0.f : d.m;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 u = exponent(make_float2(x[j].at(i), x[j].at(i + 1)), shift, p);
+        const int id = (v + j * kThreads) * N - r.lead + i;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mass = exp2_fast(h ? u.y : u.x) * inv_S, noisy = race[j][i + h];
+          const float ratio = noisy > 0.f ? __fdividef(mass, noisy) : 0.f;
+          if (ratio > d.best_p) {
+            d.best_p = ratio;
+            d.id_p = id + h;
+          }
+          if (residual && ratio > d.best) {  // (the rest is no more than p)
+            const float rest = q ? mass - fmaxf(from[j][i + h], 0.f) : mass;
+            const float left = noisy > 0.f && rest > 0.f ? __fdividef(rest, noisy) : 0.f;
+            bool out = false;
+            if (left > d.best) {
+              for (int k = 0; k < n_out; ++k) out |= w.out[k] == id + h;
+              if (!out) {
+                d.best = left;
+                d.id = id + h;
+              }
+            }
+          }
+        }
+      }
+  }
+  // joined: the larger ratio, of equal ones the lower id.  (Where the maxima differ, no rest is asked for.)
+  const auto join = [&](const Drawn& o) {
+    const float to = fmaxf(d.m, o.m);
+    if (o.best > d.best || (o.best == d.best && o.id < d.id)) {
+      d.best = o.best;
+      d.id = o.id;
+    }
+    const float mine = d.m < to && d.m > -INFINITY ? d.best_p * factor(d.m, to, p) : d.best_p;
+    const float other = o.m < to && o.m > -INFINITY ? o.best_p * factor(o.m, to, p) : o.best_p;
+    d.best_p = fmaxf(mine, other);
+    if (other > mine || (other == mine && o.id_p < d.id_p)) d.id_p = o.id_p;
+    d.m = to;
+    d.bad |= o.bad;
+  };
+  const auto warp_join = [&]() {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      Drawn x;
+      x.m = __shfl_xor_sync(0xffffffffu, d.m, o);
+      x.best = __shfl_xor_sync(0xffffffffu, d.best, o);
+      x.best_p = __shfl_xor_sync(0xffffffffu, d.best_p, o);
+      x.id = __shfl_xor_sync(0xffffffffu, d.id, o);
+      x.id_p = __shfl_xor_sync(0xffffffffu, d.id_p, o);
+      x.bad = __shfl_xor_sync(0xffffffffu, d.bad, o);
+      join(x);
+    }
+  };
+  warp_join();
+  if (lane == 0) all[warp] = d;
+  __syncthreads();
+  if (warp != 0) return;
+  d = lane < kWarps ? all[lane] : Drawn{-INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
+  warp_join();
+  if (p.draw_slices > 1) {
+    if (lane == 0) {
+      p.drawn[blockIdx.x] = d;
+      unsigned before;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.left + b) : "memory");
+      ends = before == (unsigned)p.draw_slices - 1;
+    }
+    __syncwarp();
+    if (!ends) return;
+    d = Drawn{-INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
+    if (lane < p.draw_slices) {
+      const Drawn* o = p.drawn + (long long)b * p.draw_slices + lane;
+      d = Drawn{__ldcg(&o->m), __ldcg(&o->best), __ldcg(&o->best_p), __ldcg(&o->id), __ldcg(&o->id_p), __ldcg(&o->bad)};
+    }
+    warp_join();
+    if (lane == 0) p.left[b] = 0;  // ready for the next call
+  }
+  if (lane == 0) {
+    a.next_token[b] = d.bad ? -1 : d.best > 0.f ? d.id : d.best_p > 0.f ? d.id_p : -1;
+    if (d.bad) atomicOr(a.dev_status, MOE_DEV_VALUE);
+  }
+}
+
+int check(const moe_verify_args* args) {
+  if (!args) return MOE_EINVAL;
+  const moe_verify_args& a = *args;
+  if (a.n_req < 1 || a.n_rows < 0 || a.vocab < 1 || !(a.inv_temperature > 0.f)) return MOE_EINVAL;
+  const auto type_ok = [](int t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_F32; };
+  if (!type_ok(a.dtype) || (a.draft_probs && !type_ok(a.draft_dtype))) return MOE_EINVAL;
+  const auto count_ok = [](int64_t s) { return s >= 0 && s < ((int64_t)1 << 40); };
+  if (!count_ok(a.stride) || (a.draft_probs && !count_ok(a.draft_stride)) || (a.noise && !count_ok(a.noise_stride))) return MOE_EINVAL;
+  if (a.n_req > 16384 || a.n_rows > (1 << 20) || a.vocab > (1 << 24)) return MOE_EUNSUPPORTED;
+  if (a.draft_probs && a.parents) return MOE_EUNSUPPORTED;
+  if (!rows_ok(a.n_rows, a.stride) || (a.draft_probs && !rows_ok(a.n_rows, a.draft_stride)) ||
+      (a.noise && !rows_ok(a.n_req, a.noise_stride)))
+    return MOE_EUNSUPPORTED;
+  if (!ptr_ok(a.dev_status, 4) || !ptr_ok(a.row_start, 4) || !ptr_ok(a.accepted, 4) || !ptr_ok(a.next_token, 4)) return MOE_EINVAL;
+  if (!opt_ok(a.parents, 4) || !opt_ok(a.uniform, 4) || !opt_ok(a.noise, 4)) return MOE_EINVAL;
+  if (a.n_rows > 0) {
+    const bool greedy = std::isinf(a.inv_temperature);
+    if (!ptr_ok(a.logits, a.dtype == MOE_F32 ? 4 : 2) || !ptr_ok(a.tokens, 4) || !ptr_ok(a.path, 4)) return MOE_EINVAL;
+    if (!greedy && (!a.uniform || !a.noise)) return MOE_EINVAL;
+    if (!opt_ok(a.draft_probs, a.draft_dtype == MOE_F32 ? 4 : 2)) return MOE_EINVAL;
+  }
+  return MOE_OK;
+}
+
+int slices_for(int64_t rows, int vocab) {
+  int n = 1;
+  while (n < kMaxSlices && rows * n < kBlocks && vocab / (2 * n) >= kSliceMin) n *= 2;
+  return n;
+}
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct Workspace {
+  int row_slices, draw_slices;
+  size_t sums, drawn, total;
+};
+Workspace layout(const moe_verify_args& a) {
+  Workspace w{};
+  w.row_slices = slices_for(a.n_rows, a.vocab);
+  w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab) : 1;
+  w.sums = kCounterBytes;
+  w.drawn = w.sums + up256((size_t)a.n_rows * w.row_slices * sizeof(Key));
+  w.total = w.drawn + up256((size_t)a.n_req * w.draw_slices * sizeof(Drawn));
+  return w;
+}
+
+template <int DT>
+cudaError_t launch(const moe_verify_args& a, const Plan& p, bool greedy, cudaStream_t st) {
+  if (a.n_rows > 0) {
+    const auto fn = greedy ? k_sums<DT, true> : k_sums<DT, false>;
+    const cudaError_t e = launch_kernel(fn, (unsigned)a.n_rows * p.row_slices, kThreads, 0, st, a, p);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(k_draw<DT>, (unsigned)a.n_req * p.draw_slices, kThreads, 0, st, a, p);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_verify_drafts_workspace_bytes(const moe_verify_args* args) {
+  return check(args) == MOE_OK ? layout(*args).total : 0;
+}
+
+extern "C" int moe_verify_drafts(const moe_verify_args* args, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check(args);
+  if (rc != MOE_OK) return rc;
+  moe_verify_args a = *args;
+  if (!ptr_ok(ws, 16)) return MOE_EINVAL;
+  const Workspace w = layout(a);
+  if (ws_bytes < w.total) return MOE_EWORKSPACE;
+  const bool greedy = std::isinf(a.inv_temperature);
+  if (greedy) a.draft_probs = nullptr;
+  char* base = static_cast<char*>(ws);
+  Plan p{};
+  const int N = a.dtype == MOE_F32 ? 4 : 8, vecs = (a.vocab + 2 * N - 2) / N;  // a row that begins off a vector's start has one more
+  p.row_slices = w.row_slices;
+  p.row_vecs = (vecs + w.row_slices - 1) / w.row_slices;
+  p.draw_slices = w.draw_slices;
+  p.draw_vecs = (vecs + w.draw_slices - 1) / w.draw_slices;
+  const double c = (double)a.inv_temperature * 1.4426950408889634;
+  float hi = c < 3.0e38 ? (float)c : 3.0e38f;
+  if ((double)hi > c) hi = std::nextafter(hi, 0.f);
+  const float lo = greedy || hi >= 3.0e38f ? 0.f : (float)(c - (double)hi);
+  p.hi = hi;
+  p.lo = lo > 1e-30f ? lo : 1e-30f;
+  p.inv_t = (double)a.inv_temperature;
+  p.left = reinterpret_cast<unsigned*>(base);
+  p.sums = reinterpret_cast<float2*>(base + w.sums);
+  p.keys = reinterpret_cast<Key*>(base + w.sums);
+  p.drawn = reinterpret_cast<Drawn*>(base + w.drawn);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return launch_status(a.dtype == MOE_BF16  ? launch<MOE_BF16>(a, p, greedy, st)
+                       : a.dtype == MOE_F16 ? launch<MOE_F16>(a, p, greedy, st)
+                                            : launch<MOE_F32>(a, p, greedy, st));
+}
