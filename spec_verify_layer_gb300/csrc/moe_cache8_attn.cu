@@ -4,6 +4,22 @@
 
 using namespace moe;
 
+namespace {
+
+// Blocks of 16 tokens and more have one scale for each run of 16 keys of a tile; smaller ones are taken key by key.
+template <int FMT>
+int choose(const moe_tree_attention8_args& a, const Plan& p, int sms, cudaStream_t st) {
+  using A = moe_tree_attention8_args;
+  const bool coarse = a.cache.block_size >= 16;
+  switch (a.head_dim) {
+    case 64: return coarse ? launch<A, FMT, 64, true>(a, p, sms, st) : launch<A, FMT, 64, false>(a, p, sms, st);
+    case 128: return coarse ? launch<A, FMT, 128, true>(a, p, sms, st) : launch<A, FMT, 128, false>(a, p, sms, st);
+    default: return coarse ? launch<A, FMT, 256, true>(a, p, sms, st) : launch<A, FMT, 256, false>(a, p, sms, st);
+  }
+}
+
+}  // namespace
+
 extern "C" size_t moe_tree_attention8_workspace_bytes(const moe_tree_attention8_args* args) {
   return check(args) == MOE_OK ? layout(*args).total : 0;
 }
@@ -13,17 +29,11 @@ extern "C" int moe_tree_attention8(const moe_tree_attention8_args* args, void* w
   int sms = 0;
   const int rc = prepare(args, ws, ws_bytes, p, sms);
   if (rc != MOE_OK || args->n_rows == 0) return rc;
-  using A = moe_tree_attention8_args;
-  const A& a = *args;
+  const moe_tree_attention8_args& a = *args;
   p.flip = 0;  // the sign of the scale goes with the rows' factors
   p.c = 1.f;
-  p.score = a.scale * 1.4426950408889634f * (a.cache.format == MOE_E4M3 ? 256.f : 1.f);
+  p.score = a.scale * 1.4426950408889634f;
   while ((1 << p.block_shift) < a.cache.block_size) ++p.block_shift;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // products are of fp16 numbers whatever the type of q and out
-  switch (a.head_dim) {
-    case 64: return launch<A, MOE_F16, 64>(a, p, sms, st);
-    case 128: return launch<A, MOE_F16, 128>(a, p, sms, st);
-    default: return launch<A, MOE_F16, 256>(a, p, sms, st);
-  }
+  return a.cache.format == MOE_E4M3 ? choose<MOE_E4M3>(a, p, sms, st) : choose<MOE_I8>(a, p, sms, st);
 }

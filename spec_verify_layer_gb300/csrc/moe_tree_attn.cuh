@@ -72,7 +72,8 @@ inline std::atomic<unsigned long long> g_attention_wait_ns{2000000000ull};
 namespace {
 
 constexpr int kTree = 64;
-constexpr int kSoftmaxThreads = 256;
+constexpr int kThreads = 384;  // 8 softmax warps, 3 producer warps, 1 issuing warp: 168 registers a thread
+constexpr int kSoftmaxThreads = 256, kProducers = 3;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 // Weights are 2^(score - maximum + kBias), and a maximum may lag 2^kRescale behind.  fp16 has few
@@ -99,10 +100,6 @@ constexpr bool kQ8 = std::is_same_v<A, moe_tree_attention8_args>;
 
 template <typename A, int D>
 struct Shape {
-  // 8 softmax warps, 1 issuing warp, producer warps.  16-bit cache: 168 registers a thread.  Codes:
-  // what is on its way from memory stands in the producers' registers, so there are more of them;
-  // the registers go over to the softmax warps when the roles are taken (kSoftmaxRegs, kOtherRegs).
-  static constexpr int kProducers = kQ8<A> ? 7 : 3, kThreads = kQ8<A> ? 512 : 384;
   static constexpr int KT = kKeyTile<D>;
   static constexpr int NS = D == 256 ? 1 : 2;          // streams (tensor memory holds 512 columns)
   static constexpr int PARTS = KT / 64;                // the weights are handed over 64 keys at a time
@@ -121,8 +118,6 @@ struct Shape {
   __host__ __device__ static constexpr int p_col(int buf) { return s_col(buf) + KT / 2; }
   __host__ __device__ static constexpr int o_col(int s) { return NS == 2 ? 256 * s + 128 : 256; }
 };
-
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88, kLaunchRegs = 128;  // 256 * 168 + 256 * 88 = 512 * 128
 
 struct Plan {  // host-computed, the same for every block
   int nq;      // query tiles held
@@ -151,8 +146,8 @@ struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes: one)
-  int red[16], redn[16];
+  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows
+  int red[kThreads / 32], redn[kThreads / 32];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;
   int start_b, gangs, groups, gang, member;
@@ -403,15 +398,15 @@ __device__ __forceinline__ int gang_of(int total, int gangs, int x) {
 
 // ---- codes ------------------------------------------------------------------------------
 
-// Eight codes (two words) as fp16 numbers.  e4m3: the code's exponent and mantissa put into those of
-// an fp16 are its value times 2^-8, subnormal ones included.  int8: 1024 + (code + 128) has the
-// code in its last bits; 1152 is taken off again, exactly.
-__device__ __forceinline__ uint4 codes_to_half(uint32_t a, uint32_t b, bool i8) {
+// Eight codes (two words) as fp16 numbers, exactly.  int8: 1024 + (code + 128) has the code in its
+// last bits; 1152 is taken off again.
+template <int FMT>
+__device__ __forceinline__ uint4 codes_to_half(uint32_t a, uint32_t b) {
   uint32_t r[4];
   const uint32_t w[2] = {a, b};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    if (i8) {
+    if constexpr (FMT == MOE_I8) {
       const uint32_t u = w[j] ^ 0x80808080u;
       const __half2 off = __half2half2(__ushort_as_half(0x6480));
       const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
@@ -419,12 +414,17 @@ __device__ __forceinline__ uint4 codes_to_half(uint32_t a, uint32_t b, bool i8) 
       r[2 * j] = *reinterpret_cast<const uint32_t*>(&x);
       r[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&y);
     } else {
-      const uint32_t lo = __byte_perm(w[j], 0, 0x1404), hi = __byte_perm(w[j], 0, 0x3424);
-      r[2 * j] = (lo & 0x80008000u) | ((lo >> 1) & 0x3f803f80u);
-      r[2 * j + 1] = (hi & 0x80008000u) | ((hi >> 1) & 0x3f803f80u);
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+          : "=r"(r[2 * j]), "=r"(r[2 * j + 1])
+          : "r"(w[j]));
     }
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// Bytes of four e4m3 codes that are NaN, as 0xff.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  const uint32_t high = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return (high >> 7) * 0xffu;
 }
 __device__ __forceinline__ uint4 load_codes(const void* p) {
   uint4 v;
@@ -434,12 +434,14 @@ __device__ __forceinline__ uint4 load_codes(const void* p) {
 
 // ---- the kernel -------------------------------------------------------------------------
 
-template <typename A, int DT, int D>
-__global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
+// FMT: the type of q, cache and out (16-bit cache), or of the codes.  COARSE: a scale stands for 16 keys or more.
+template <typename A, int FMT, int D, bool COARSE>
+__global__ void __launch_bounds__(kThreads, 1)
     k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p) {
   using Sh = Shape<A, D>;
   constexpr bool Q8 = kQ8<A>;
-  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kThreads = Sh::kThreads, kProducers = Sh::kProducers;
+  constexpr int DT = Q8 ? MOE_F16 : FMT;  // of the products
+  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI;
   constexpr uint32_t kBlk = KT * 128;  // bytes of a 64-element block of a key or value tile
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -555,22 +557,27 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
   const int member = ct.member;
   wk.begin(a, ct.start_b, ct.start_off, ct.w1 - ct.w0);
 
-  if (warp >= 8) {
-    if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp != 10) {
+  if (warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
     // ---------------- producers of codes: a warp's rows of a tile are dealt out as below, 16 codes a
     // lane and step.  A tile's codes are asked for while the tile before is turned into fp16, keys
     // and values in turn, and its table entries a tile ahead of that.
-    const int pw = warp < 10 ? warp - 8 : warp - 9, chunk = lane % CC, sub = lane / CC;
-    const int own = (lane / RPI * kProducers + pw) * RPI + lane % RPI;  // the row that this lane looks up
-    const bool owns = lane < Sh::STEPS * RPI && own < KT, i8 = a.cache.format == MOE_I8;
+    // Eight lanes side by side take four chunks each of two rows: their stores meet eight different
+    // banks of the swizzle.
+    constexpr int kBlocks = CC / 4;  // 64-element blocks of a row
+    const int pw = warp == 11 ? 2 : warp - 8, chunk = (lane & 3) | ((lane >> 3) & (kBlocks - 1)) << 2;
+    const int sub = (lane >> 2 & 1) | (lane / (8 * kBlocks)) << 1;
+    constexpr int LOOKS = (Sh::STEPS * RPI + 31) / 32;  // rows of a warp that a lane looks up
+    const auto row_of = [&](int j) {                    // the j-th of them; KT and more: none
+      const int mine = 32 * j + lane;
+      return (mine / RPI * kProducers + pw) * RPI + mine % RPI;
+    };
     constexpr uint32_t kNone = 0xffffffffu;
     const uint32_t kv0 = smem_u32(sm_kv);
     int slot = 0, tile_seq = 0;
     uint32_t phase = 1;  // the slots start empty
     bool ok = true;
-    for (; ok && wk.more(); wk.next(a)) {
+    for (int seq = 0; ok && wk.more(); wk.next(a)) {
       if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
       const int len = wk.q.ctx + wk.q.n;
       const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
@@ -580,56 +587,72 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
         const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
         if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
       }
-      int page = 0;
-      unsigned hole = 0;
-      float ks = 0.f, vs = 0.f;
-      uint32_t from[Sh::STEPS];
+      int page[LOOKS];
+      unsigned hole[2] = {0, 0};
+      float ks[LOOKS], vs[LOOKS];
+      uint32_t at[LOOKS];  // in units of 16 bytes
       uint4 keys[Sh::STEPS], values[Sh::STEPS];
       const auto look = [&](int t) {
-        const int pos = t * KT + own;
-        page = 0;
-        if (owns && pos < len) page = __ldg(table + (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift));
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          const int r = row_of(j), pos = t * KT + r;
+          page[j] = 0;
+          if (r < KT && pos < len) page[j] = __ldg(table + (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift));
+        }
       };
       const auto place = [&](int t) {  // tile t's rows, from their pages, and their scales
-        const int pos = t * KT + own, col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
-        const int in_page = pos - col * a.cache.page_size;
-        const bool there = owns && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
-        const uint32_t at = good ? (uint32_t)((page * a.cache.page_stride + in_page * a.cache.slot_stride + head_at) >> 4) : kNone;
-        ks = vs = 0.f;
-        if (good) {
-          const long long sc = page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
-          ks = __ldg(a.cache.k_scale + sc);
-          vs = __ldg(a.cache.v_scale + sc);
-        }
-        hole = __ballot_sync(0xffffffffu, there && !good);
 #pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k) from[k] = __shfl_sync(0xffffffffu, at, (k * RPI + sub) & 31);
+        for (int j = 0; j < LOOKS; ++j) {
+          const int r = row_of(j), pos = t * KT + r, col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
+          const int in_page = pos - col * a.cache.page_size;
+          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
+          at[j] = kNone;
+          ks[j] = vs[j] = 0.f;
+          if (good) {
+            at[j] = (uint32_t)((page[j] * a.cache.page_stride + in_page * a.cache.slot_stride + head_at) >> 4);
+            const long long sc = page[j] * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
+            ks[j] = __ldg(a.cache.k_scale + sc);
+            vs[j] = __ldg(a.cache.v_scale + sc);
+          }
+          hole[j] = __ballot_sync(0xffffffffu, there && !good);
+        }
       };
       const auto ask = [&](const void* base, uint4 (&to)[Sh::STEPS]) {
 #pragma unroll
         for (int k = 0; k < Sh::STEPS; ++k) {
           const int g = k * kProducers + pw;
+          const uint32_t from = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
           to[k] = make_uint4(0, 0, 0, 0);
-          if (((k + 1) * kProducers <= KT / RPI || g < KT / RPI) && from[k] != kNone)
-            to[k] = load_codes(static_cast<const uint4*>(base) + from[k] + chunk);
+          if (((k + 1) * kProducers <= KT / RPI || g < KT / RPI) && from != kNone)
+            to[k] = load_codes(static_cast<const uint4*>(base) + from + chunk);
         }
       };
-      const auto put = [&](const uint4 (&x)[Sh::STEPS], int slot, unsigned zero) {
-        // lanes whose block of 64 elements is an odd one write their second eight first, so that the
-        // eight lanes of a store meet eight different banks of the swizzle
-        const int odd = CC > 4 ? chunk >> 2 & 1 : 0;
+      const auto put = [&](const uint4 (&x)[Sh::STEPS], int slot) {
         const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
 #pragma unroll
         for (int k = 0; k < Sh::STEPS; ++k) {
           const int g = k * kProducers + pw, r = g * RPI + sub;
           if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
-            uint4 w = x[k];
-            if (zero >> (k * RPI + sub) & 1) w = make_uint4(0, 0, 0, 0);
-            if (odd) w = make_uint4(w.z, w.w, w.x, w.y);
-            const uint32_t at = dst + r * 128, c = (2 * (chunk & 3) + odd) ^ (r & 7);
-            const uint4 lo = codes_to_half(w.x, w.y, i8), hi = codes_to_half(w.z, w.w, i8);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (c << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + ((c ^ 1) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+            const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
+            const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+          }
+        }
+      };
+      // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
+      // are noted, and added at the end to the rows that see them.
+      const auto clean = [&](const unsigned (&zero)[2], int node0) {
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k) {
+          const int r = (k * kProducers + pw) * RPI + sub;
+          if (zero[k * RPI >> 5] >> ((k * RPI + sub) & 31) & 1) values[k] = make_uint4(0, 0, 0, 0);
+          if (FMT == MOE_E4M3 && r >= node0 && r < KT) {
+            const uint4 n = make_uint4(nan_codes(values[k].x), nan_codes(values[k].y), nan_codes(values[k].z), nan_codes(values[k].w));
+            if (n.x | n.y | n.z | n.w) {
+              values[k] = make_uint4(values[k].x & ~n.x, values[k].y & ~n.y, values[k].z & ~n.z, values[k].w & ~n.w);
+              atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
+            }
           }
         }
       };
@@ -648,17 +671,22 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
         const bool more = t + 1 < wk.t1;
         ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
         if (!ok) break;
-        const float key_scale = scale_of(ks, flags), value_scale = scale_of(vs, flags);
-        const unsigned zero = __ballot_sync(0xffffffffu, value_scale == 0.f);  // such values are zeros, at scale 1
-        float* sc = sm_scale + (tile_seq & 7) * 3 * KT;
-        if (owns) {
-          sc[own] = key_scale;
-          sc[KT + own] = value_scale == 0.f ? 0.f : log2f(value_scale) + (i8 ? 0.f : 8.f);
-          sc[2 * KT + own] = value_scale == 0.f ? 1.f : (i8 ? 1.f : 0.00390625f) / value_scale;
+        unsigned zero[2] = {0, 0};
+        float* const sc = sm_scale + (tile_seq & 7) * 3 * KT;
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          const int r = row_of(j);
+          const float key = scale_of(ks[j], flags), value = scale_of(vs[j], flags);
+          zero[j] = __ballot_sync(0xffffffffu, value == 0.f);  // such values are zeros, at scale 1
+          if (r < KT) {
+            sc[r] = key;
+            sc[KT + r] = value == 0.f ? 0.f : log2f(value);
+            sc[2 * KT + r] = value == 0.f ? 1.f : 1.f / value;
+          }
         }
-        if (hole) flags |= MOE_DEV_INDEX;
-        if (lane == 0) ct.hole[tile_seq & 7][pw] = hole;
-        put(keys, slot, 0);
+        if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
+        if (lane == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
+        put(keys, slot);
         if (more) {
           place(t + 1);
           ask(a.cache.k, keys);
@@ -666,7 +694,9 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
         filled(slot);
         ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status));
         if (!ok) break;
-        put(values, v_slot, zero);
+        const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+        if ((zero[0] | zero[1]) || (FMT == MOE_E4M3 && node0 < KT)) clean(zero, node0);
+        put(values, v_slot);
         if (more) ask(a.cache.v, values);
         filled(v_slot);
         if (t + 2 < wk.t1) look(t + 2);
@@ -676,6 +706,7 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
           phase ^= 1;
         }
       }
+      ++seq;
     }
     } else {
     // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
@@ -807,7 +838,7 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     }
-  } else {
+  } else if (warp == 10) {
     // ---------------- issue of the products.  The warp goes through the loop as one and one lane
     // of it issues, so that the operands, which are the same for all lanes, can be held as
     // such (issued by a thread on its own: full trees 283 us against 258).
@@ -920,9 +951,7 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
       bar_drain(&ct.drain, a.dev_status);
       __syncwarp();
     }
-  }
   } else {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------- softmax
     const int wg = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes of tensor memory
@@ -1027,8 +1056,8 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
             // which of the tile's keys this row sees, unless it is all
             const unsigned* hole = ct.hole[(tile_seq + ti) & 7];
             const uint4 hole_a = *reinterpret_cast<const uint4*>(hole);
-            const uint4 hole_b = *reinterpret_cast<const uint4*>(hole + 4);
-            const bool holes = (hole_a.x | hole_a.y | hole_a.z | hole_a.w | hole_b.x | hole_b.y | hole_b.z | hole_b.w) != 0;
+            const uint2 hole_b = *reinterpret_cast<const uint2*>(hole + 4);
+            const bool holes = (hole_a.x | hole_a.y | hole_a.z | hole_a.w | hole_b.x | hole_b.y) != 0;
             const bool all = base + KT <= wk.q.ctx && !holes;
             const auto seen = [&](int w) {  // of keys 32 w .. 32 w + 31
               const int k = wk.q.ctx - base - 32 * w;  // context keys of the word
@@ -1040,7 +1069,7 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < 32; ++j) {
                   const int r = 32 * w + j, g = r / RPI, q = g / kProducers * RPI + r % RPI;
-                  if (hole[Q8 ? g % kProducers : 2 * (g % kProducers) + (q >> 5)] >> (q & 31) & 1) bits &= ~(1u << j);
+                  if (hole[2 * (g % kProducers) + (q >> 5)] >> (q & 31) & 1) bits &= ~(1u << j);
                 }
               }
               return bits;
@@ -1054,6 +1083,11 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
             // shows in the short ones.
             uint32_t x[64];
             const float4* const scales = reinterpret_cast<const float4*>(sm_scale + ((tile_seq + ti) & 7) * 3 * KT);
+            const auto scaled = [](uint32_t* x, Pair factor, Pair more) {
+              const float2 y = split(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), factor, more));
+              x[0] = __float_as_uint(y.x);
+              x[1] = __float_as_uint(y.y);
+            };
             const auto fetch = [&](int half) {
               const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
               tm_load(x, at);
@@ -1064,18 +1098,19 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
               if constexpr (Q8) {
                 // to powers of two with the value's scale in them: s * key's scale * row's factor +
                 // log2(value's scale)
-                const Pair row2 = pair(row_factor, row_factor);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float4 ks = scales[16 * half + j], lv = scales[KT / 4 + 16 * half + j];
-                  const float2 y = split(fma2(pair(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])),
-                                              mul2(pair(ks.x, ks.y), row2), pair(lv.x, lv.y)));
-                  const float2 z = split(fma2(pair(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])),
-                                              mul2(pair(ks.z, ks.w), row2), pair(lv.z, lv.w)));
-                  x[4 * j] = __float_as_uint(y.x);
-                  x[4 * j + 1] = __float_as_uint(y.y);
-                  x[4 * j + 2] = __float_as_uint(z.x);
-                  x[4 * j + 3] = __float_as_uint(z.y);
+                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {
+                  const float4* const ks = scales + (64 * half + j) / 4;
+                  if constexpr (COARSE) {
+                    const float f = ks->x * row_factor, lv = ks[KT / 4].x;
+                    const Pair f2 = pair(f, f), lv2 = pair(lv, lv);
+#pragma unroll
+                    for (int i = j; i < j + 16; i += 2) scaled(x + i, f2, lv2);
+                  } else {
+                    const float4 s = *ks, lv = ks[KT / 4];
+                    scaled(x + j, pair(s.x * row_factor, s.y * row_factor), pair(lv.x, lv.y));
+                    scaled(x + j + 2, pair(s.z * row_factor, s.w * row_factor), pair(lv.z, lv.w));
+                  }
                 }
               }
               if (!all) {
@@ -1131,14 +1166,24 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
               const Pair shift2 = pair(-shift, -shift);
               if constexpr (Q8) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {  // the sum is of the weights without the values' scales
-                  const float4 iv = scales[2 * (KT / 4) + 16 * half + j];
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const float2 z = split(add2(pair(__uint_as_float(x[4 * j + 2 * h]), __uint_as_float(x[4 * j + 2 * h + 1])), shift2));
+                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {  // the sum is of the weights without the values' scales
+                  const float4* const iv = scales + 2 * (KT / 4) + (64 * half + j) / 4;
+                  const auto weights = [&](int i, Pair inv, Pair& sum) {
+                    const float2 z = split(add2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), shift2));
                     const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                    sums[h] = fma2(pair(e0, e1), h ? pair(iv.z, iv.w) : pair(iv.x, iv.y), sums[h]);
-                    y[2 * j + h] = pack2<DT>(e0, e1);
+                    sum = COARSE ? add2(sum, pair(e0, e1)) : fma2(pair(e0, e1), inv, sum);
+                    y[i / 2] = pack2<DT>(e0, e1);
+                  };
+                  if constexpr (COARSE) {
+                    Pair part[2] = {0, 0};
+#pragma unroll
+                    for (int i = j; i < j + 16; i += 2) weights(i, 0, part[i / 2 & 1]);
+                    const float inv = iv->x;
+                    sums[0] = fma2(add2(part[0], part[1]), pair(inv, inv), sums[0]);
+                  } else {
+                    const float4 v = *iv;
+                    weights(j, pair(v.x, v.y), sums[0]);
+                    weights(j + 2, pair(v.z, v.w), sums[1]);
                   }
                 }
               } else {
@@ -1192,7 +1237,7 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
         l = x.y * f0 + y.y * f1;
       }
       const bool whole = wk.t0 == 0 && wk.t1 == wk.q.tiles;
-      const unsigned long long bad = Q8 ? 0 : *(volatile unsigned long long*)&ct.bad[seq & 7];
+      const unsigned long long bad = Q8 && FMT == MOE_I8 ? 0 : *(volatile unsigned long long*)&ct.bad[seq & 7];
       if (live) {
         const int c0 = two ? 0 : wg * (D / 2), c1 = two ? D : c0 + D / 2;
         const int part = wk.t0 == 0;
@@ -1218,21 +1263,31 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) x[j] = fmaf(y[j], f1, x[j]);
           }
-          if constexpr (!Q8)
           if (own_bad) {
 #pragma unroll 1
             for (int nd = 0; nd < kTree; ++nd) {
               if (!(own_bad >> nd & 1)) continue;
               const int pos = wk.q.ctx + nd, pc = pos / a.cache.page_size;
               const int page = __ldg(a.block_table + (long long)wk.b * a.table_width + pc);
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  static_cast<const uint16_t*>(a.cache.v) + page * a.cache.page_stride +
-                  (pos - pc * a.cache.page_size) * a.cache.slot_stride + wk.h * a.cache.head_stride + col);
+              const long long from = page * a.cache.page_stride + (pos - pc * a.cache.page_size) * a.cache.slot_stride +
+                                     wk.h * a.cache.head_stride + col;
+              if constexpr (Q8) {
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.cache.v) + from);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float2 e = unpack2<DT>(v[j]);
-                if (!(fabsf(e.x) < INFINITY)) x[2 * j] += e.x;
-                if (!(fabsf(e.y) < INFINITY)) x[2 * j + 1] += e.y;
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t n = nan_codes(v[j]);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    if (n >> (8 * i) & 1) x[4 * j + i] = __uint_as_float(0x7fffffffu);
+                }
+              } else {
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.cache.v) + from);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float2 e = unpack2<DT>(v[j]);
+                  if (!(fabsf(e.x) < INFINITY)) x[2 * j] += e.x;
+                  if (!(fabsf(e.y) < INFINITY)) x[2 * j + 1] += e.y;
+                }
               }
             }
           }
@@ -1443,7 +1498,7 @@ Workspace layout(const A& a) {
   return w;
 }
 
-template <typename A, int DT, int D>
+template <typename A, int FMT, int D, bool COARSE = true>
 int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   using Sh = Shape<A, D>;
   constexpr int kSmem = 227 * 1024;
@@ -1456,20 +1511,13 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
-    e = cudaFuncSetAttribute(k_tree_attn<A, DT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (kQ8<A> && e == cudaSuccess) {
-      // the softmax warps' larger share comes out of what the block is launched with: never ask for more
-      static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * kLaunchRegs, "registers");
-      cudaFuncAttributes attr;
-      e = cudaFuncGetAttributes(&attr, k_tree_attn<A, DT, D>);
-      if (e == cudaSuccess && attr.numRegs != kLaunchRegs) return MOE_EUNSUPPORTED;
-    }
+    e = cudaFuncSetAttribute(k_tree_attn<A, FMT, D, COARSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < kMaxBlocks ? sms : kMaxBlocks);
-  cfg.blockDim = dim3(Sh::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1477,7 +1525,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, DT, D>, a, p));
+  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, COARSE>, a, p));
 }
 
 // Checks, workspace and what the host computes, alike for both caches.
