@@ -110,8 +110,15 @@ struct Shape {
   static constexpr int CC = kQ8<A> ? D / 16 : D / 8;   // and of a cached row
   static constexpr int RPI = 32 / CC;                  // rows that a warp copies with one instruction
   static constexpr int STEPS = (KT / RPI + kProducers - 1) / kProducers;  // instructions of a producer for a tile
-  // codes: scale of the key, logarithm and reciprocal of the value's scale, of each key of 8 tiles; a factor a query row
-  static constexpr int kScales = kQ8<A> ? 8 * 3 * KT * 4 + 256 * 4 : 0;
+  // Codes: scale of the key, logarithm and reciprocal of the value's scale, of each key of kRing tiles (a
+  // tile's are written when its slot of keys is free, up to half the slots ahead of the softmax); a
+  // factor a query row; page and scales of the rows that a producer's lane looks up, twice; codes on
+  // their way, a stage for a tile's keys or values.
+  static constexpr int LOOKS = (STEPS * RPI + 31) / 32;  // rows of a producer that a lane looks up
+  static constexpr int kRing = D == 64 ? 8 : 4;
+  static constexpr int kRaw = KT * D, kRawStages = 3;
+  static constexpr int kLooked = kProducers * 2 * 3 * LOOKS * 32;
+  static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kLooked) * 4 + kRawStages * kRaw : 0;
   // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
   // there is one stream); the weights, in 16 bits, go over the second half of their scores.
   __host__ __device__ static constexpr int s_col(int buf) { return NS == 2 ? 256 * buf : 64 * buf; }
@@ -426,10 +433,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   const uint32_t high = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
   return (high >> 7) * 0xffu;
 }
-__device__ __forceinline__ uint4 load_codes(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -448,8 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* sm_q = smem;
   unsigned char* sm_kv = smem + (size_t)p.nq * Sh::kQ;
   Control& ct = *reinterpret_cast<Control*>(sm_kv + (size_t)p.nslot * Sh::kSlot);
-  float* const sm_scale = reinterpret_cast<float*>(&ct + 1);  // [8][3][KT]
-  float* const sm_row = sm_scale + 8 * 3 * KT;                // [256]
+  float* const sm_scale = reinterpret_cast<float*>(&ct + 1);  // [kRing][3][KT]
+  float* const sm_row = sm_scale + Sh::kRing * 3 * KT;        // [256]
+  unsigned char* const sm_looked = reinterpret_cast<unsigned char*>(sm_row + 256), *const sm_raw = sm_looked + Sh::kLooked * 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.group;
   const auto result2 = [&](float x, float y) {
@@ -559,22 +565,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
-    // ---------------- producers of codes: a warp's rows of a tile are dealt out as below, 16 codes a
-    // lane and step.  A tile's codes are asked for while the tile before is turned into fp16, keys
-    // and values in turn, and its table entries a tile ahead of that.
+    // ---------------- producers of codes.  A warp's rows of a tile are dealt out as below, 16 codes
+    // a lane and step: they are copied into a ring of stages (keys and values of a tile in turn),
+    // read back by the lane that copied them, and written as fp16 into the tile's slot.  All that
+    // comes from memory comes by asynchronous copies, table entries and scales too: a register that
+    // waits for memory holds up every exchange and barrier behind it (they share few counters),
+    // 263 us against 438 with the codes in registers for 64 requests of one row over up to 8,192 keys
+    // with these in better and in worse order.
     // Eight lanes side by side take four chunks each of two rows: their stores meet eight different
     // banks of the swizzle.
     constexpr int kBlocks = CC / 4;  // 64-element blocks of a row
     const int pw = warp == 11 ? 2 : warp - 8, chunk = (lane & 3) | ((lane >> 3) & (kBlocks - 1)) << 2;
     const int sub = (lane >> 2 & 1) | (lane / (8 * kBlocks)) << 1;
-    constexpr int LOOKS = (Sh::STEPS * RPI + 31) / 32;  // rows of a warp that a lane looks up
-    const auto row_of = [&](int j) {                    // the j-th of them; KT and more: none
+    constexpr int LOOKS = Sh::LOOKS;
+    const auto row_of = [&](int j) {  // the j-th row that this lane looks up; KT and more: none
       const int mine = 32 * j + lane;
       return (mine / RPI * kProducers + pw) * RPI + mine % RPI;
     };
     constexpr uint32_t kNone = 0xffffffffu;
-    const uint32_t kv0 = smem_u32(sm_kv);
-    int slot = 0, tile_seq = 0;
+    const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw) + lane * 16, looked0 = smem_u32(sm_looked);
+    int slot = 0, tile_seq = 0, ask_stage = 0, put_stage = 0;
     uint32_t phase = 1;  // the slots start empty
     bool ok = true;
     for (int seq = 0; ok && wk.more(); wk.next(a)) {
@@ -587,70 +597,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
         if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
       }
-      int page[LOOKS];
-      unsigned hole[2] = {0, 0};
-      float ks[LOOKS], vs[LOOKS];
+      unsigned hole[2], next_hole[2] = {0, 0};
       uint32_t at[LOOKS];  // in units of 16 bytes
-      uint4 keys[Sh::STEPS], values[Sh::STEPS];
+      // page (0), key's (1) and value's scale (2) of the j-th row, of odd and even tiles
+      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 3 + what) * LOOKS + j) * 32 + lane; };
       const auto look = [&](int t) {
 #pragma unroll
         for (int j = 0; j < LOOKS; ++j) {
           const int r = row_of(j), pos = t * KT + r;
-          page[j] = 0;
-          if (r < KT && pos < len) page[j] = __ldg(table + (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift));
+          const bool there = r < KT && pos < len;
+          const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
+          copy4(looked0 + looked(t, 0, j) * 4, table + (there ? col : 0), there);
         }
       };
-      const auto place = [&](int t) {  // tile t's rows, from their pages, and their scales
+      const auto ask = [&](const void* base) {  // the tile that `at` is of, into the next stage
+        uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j), pos = t * KT + r, col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
-          const int in_page = pos - col * a.cache.page_size;
-          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
-          at[j] = kNone;
-          ks[j] = vs[j] = 0.f;
-          if (good) {
-            at[j] = (uint32_t)((page[j] * a.cache.page_stride + in_page * a.cache.slot_stride + head_at) >> 4);
-            const long long sc = page[j] * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
-            ks[j] = __ldg(a.cache.k_scale + sc);
-            vs[j] = __ldg(a.cache.v_scale + sc);
-          }
-          hole[j] = __ballot_sync(0xffffffffu, there && !good);
-        }
-      };
-      const auto ask = [&](const void* base, uint4 (&to)[Sh::STEPS]) {
+        for (int k = 0; k < Sh::STEPS; ++k)
+          from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
+        const uint32_t dst = raw0 + ask_stage * Sh::kRaw + pw * 512;
+        const uint4* const src = static_cast<const uint4*>(base) + chunk;
 #pragma unroll
         for (int k = 0; k < Sh::STEPS; ++k) {
           const int g = k * kProducers + pw;
-          const uint32_t from = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
-          to[k] = make_uint4(0, 0, 0, 0);
-          if (((k + 1) * kProducers <= KT / RPI || g < KT / RPI) && from != kNone)
-            to[k] = load_codes(static_cast<const uint4*>(base) + from + chunk);
+          const bool there = from[k] != kNone;
+          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI)
+            copy16(dst + k * kProducers * 512, src + (there ? from[k] : 0), there);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++ask_stage == Sh::kRawStages) ask_stage = 0;
       };
-      const auto put = [&](const uint4 (&x)[Sh::STEPS], int slot) {
+      // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
+      const auto ask_keys = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          const int r = row_of(j), pos = t * KT + r, col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
+          const int in_page = pos - col * a.cache.page_size, page = *reinterpret_cast<volatile int*>(sm_looked + looked(t, 0, j) * 4);
+          const bool there = r < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
+          const long long sc = good ? page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at : 0;
+          at[j] = good ? (uint32_t)((page * a.cache.page_stride + in_page * a.cache.slot_stride + head_at) >> 4) : kNone;
+          copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
+          copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
+          next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
+        }
+        if (t + 1 < wk.t1) look(t + 1);
+        ask(a.cache.k);
+      };
+      const auto put = [&](int slot) {  // the next stage's codes into a slot
         const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
+        const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
 #pragma unroll
         for (int k = 0; k < Sh::STEPS; ++k) {
           const int g = k * kProducers + pw, r = g * RPI + sub;
           if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
             const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
-            const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
+            const uint4 lo = codes_to_half<FMT>(x.x, x.y), hi = codes_to_half<FMT>(x.z, x.w);
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
           }
         }
+        if (++put_stage == Sh::kRawStages) put_stage = 0;
       };
       // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
       // are noted, and added at the end to the rows that see them.
       const auto clean = [&](const unsigned (&zero)[2], int node0) {
-#pragma unroll
+        unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+#pragma unroll 1
         for (int k = 0; k < Sh::STEPS; ++k) {
-          const int r = (k * kProducers + pw) * RPI + sub;
-          if (zero[k * RPI >> 5] >> ((k * RPI + sub) & 31) & 1) values[k] = make_uint4(0, 0, 0, 0);
-          if (FMT == MOE_E4M3 && r >= node0 && r < KT) {
-            const uint4 n = make_uint4(nan_codes(values[k].x), nan_codes(values[k].y), nan_codes(values[k].z), nan_codes(values[k].w));
+          const int r = (k * kProducers + pw) * RPI + sub, mine = k * RPI + sub;
+          if (r >= KT) break;
+          uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
+          if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
+          if (FMT == MOE_E4M3 && r >= node0) {
+            const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
             if (n.x | n.y | n.z | n.w) {
-              values[k] = make_uint4(values[k].x & ~n.x, values[k].y & ~n.y, values[k].z & ~n.z, values[k].w & ~n.w);
+              *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
               atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
             }
           }
@@ -662,44 +684,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bar_arrive(&ct.full[slot]);
       };
       look(wk.t0);
-      place(wk.t0);
-      ask(a.cache.k, keys);
-      ask(a.cache.v, values);
-      if (wk.t0 + 1 < wk.t1) look(wk.t0 + 1);
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      ask_keys(wk.t0);
+      ask(a.cache.v);
       for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
         const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
         const bool more = t + 1 < wk.t1;
+        // keys, scales, and the next tile's pages are there; its values are on their way
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        hole[0] = next_hole[0];
+        hole[1] = next_hole[1];
+        float key[LOOKS], value[LOOKS];
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          key[j] = *reinterpret_cast<volatile float*>(sm_looked + looked(t, 1, j) * 4);
+          value[j] = *reinterpret_cast<volatile float*>(sm_looked + looked(t, 2, j) * 4);
+        }
+        if (more) ask_keys(t + 1);
         ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
         if (!ok) break;
         unsigned zero[2] = {0, 0};
-        float* const sc = sm_scale + (tile_seq & 7) * 3 * KT;
+        float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
 #pragma unroll
         for (int j = 0; j < LOOKS; ++j) {
           const int r = row_of(j);
-          const float key = scale_of(ks[j], flags), value = scale_of(vs[j], flags);
-          zero[j] = __ballot_sync(0xffffffffu, value == 0.f);  // such values are zeros, at scale 1
+          const float ks = scale_of(key[j], flags), vs = scale_of(value[j], flags);
+          zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);  // such values are zeros, at scale 1
           if (r < KT) {
-            sc[r] = key;
-            sc[KT + r] = value == 0.f ? 0.f : log2f(value);
-            sc[2 * KT + r] = value == 0.f ? 1.f : 1.f / value;
+            float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
+            asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
+            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
+            sc[r] = ks;
+            sc[KT + r] = vs == 0.f ? 0.f : log;
+            sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
           }
         }
         if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
         if (lane == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
-        put(keys, slot);
-        if (more) {
-          place(t + 1);
-          ask(a.cache.k, keys);
-        }
+        put(slot);
         filled(slot);
+        if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
         ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status));
         if (!ok) break;
         const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
         if ((zero[0] | zero[1]) || (FMT == MOE_E4M3 && node0 < KT)) clean(zero, node0);
-        put(values, v_slot);
-        if (more) ask(a.cache.v, values);
+        if (more) ask(a.cache.v);  // (into the keys' stage)
+        put(v_slot);
         filled(v_slot);
-        if (t + 2 < wk.t1) look(t + 2);
         slot += 2;
         if (slot >= p.nslot) {
           slot -= p.nslot;
@@ -708,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++seq;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
     // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
     // g = k * kProducers + its number
@@ -1082,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // mask a branch inside: this code is fetched anew by every launch, and its length
             // shows in the short ones.
             uint32_t x[64];
-            const float4* const scales = reinterpret_cast<const float4*>(sm_scale + ((tile_seq + ti) & 7) * 3 * KT);
+            const float4* const scales = reinterpret_cast<const float4*>(sm_scale + ((tile_seq + ti) & (Sh::kRing - 1)) * 3 * KT);
             const auto scaled = [](uint32_t* x, Pair factor, Pair more) {
               const float2 y = split(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), factor, more));
               x[0] = __float_as_uint(y.x);
@@ -1506,7 +1539,9 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   p.nq = Sh::NS == 2 && need > 128 ? 2 : 1;
   p.nslot = (kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - p.nq * Sh::kQ) / Sh::kSlot;
   if (p.nslot > kMaxSlots) p.nslot = kMaxSlots;
-  static_assert((kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - Sh::NS * Sh::kQ) / Sh::kSlot >= 4, "ring");
+  static_assert(kMaxSlots / 2 + 1 <= 8, "holes");
+  if (kQ8<A> && p.nslot > 2 * Sh::kRing - 2) p.nslot = 2 * Sh::kRing - 2;
+  static_assert((kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - Sh::NS * Sh::kQ) / Sh::kSlot >= (kQ8<A> ? 3 : 4), "ring");
   static thread_local int ready = -1;  // device whose shared-memory limit this thread has set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
