@@ -117,7 +117,7 @@ struct Shape {
   static constexpr int LOOKS = (STEPS * RPI + 31) / 32;  // rows of a producer that a lane looks up
   static constexpr int kRing = D == 64 ? 8 : 4;
   static constexpr int kRaw = KT * D, kRawStages = 3;
-  static constexpr int kLooked = kProducers * 2 * 3 * LOOKS * 32;
+  static constexpr int kLooked = kProducers * 2 * 4 * LOOKS * 32;
   static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kLooked) * 4 + kRawStages * kRaw : 0;
   // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
   // there is one stream); the weights, in 16 bits, go over the second half of their scores.
@@ -428,6 +428,14 @@ __device__ __forceinline__ uint4 codes_to_half(uint32_t a, uint32_t b) {
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
+// A value's scale: 2^-48 .. 2^48.  The weights' sum is taken from the weights with the scales in them, so
+// these may not lie further apart than 32-bit exponents reach; smaller ones count as 0 (their
+// values are below 1.6e-12), larger ones too and are reported.
+__device__ __forceinline__ float value_scale(float s, unsigned& flags) {
+  s = scale_of(s, flags);
+  if (s > 281474976710656.f) flags |= MOE_DEV_VALUE;
+  return s >= 3.552713678800501e-15f && s <= 281474976710656.f ? s : 0.f;
+}
 // Bytes of four e4m3 codes that are NaN, as 0xff.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   const uint32_t high = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
@@ -584,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     constexpr uint32_t kNone = 0xffffffffu;
     const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw) + lane * 16, looked0 = smem_u32(sm_looked);
+    const uint32_t page_units = (uint32_t)(a.cache.page_stride >> 4), slot_units = (uint32_t)(a.cache.slot_stride >> 4);
     int slot = 0, tile_seq = 0, ask_stage = 0, put_stage = 0;
     uint32_t phase = 1;  // the slots start empty
     bool ok = true;
@@ -591,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
       const int len = wk.q.ctx + wk.q.n;
       const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-      const long long head_at = wk.h * a.cache.head_stride, scale_at = wk.h * a.cache.scale_head_stride;
+      const uint32_t head_units = (uint32_t)(wk.h * a.cache.head_stride >> 4);
+      const long long scale_at = wk.h * a.cache.scale_head_stride;
       if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
         const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
         const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
@@ -599,16 +609,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       unsigned hole[2], next_hole[2] = {0, 0};
       uint32_t at[LOOKS];  // in units of 16 bytes
-      // page (0), key's (1) and value's scale (2) of the j-th row, of odd and even tiles
-      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 3 + what) * LOOKS + j) * 32 + lane; };
+      // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
+      // scale.  COARSE: lanes 0 .. KT/8 - 1 look up the scale of keys, then of values, of a run of 16 keys
+      // each: its page (3) and scale (1).
+      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 4 + what) * LOOKS + j) * 32 + lane; };
+      const auto column = [&](int pos) { return (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift); };
+      const auto look_at = [&](int t, int r, int what, int j) {
+        const int pos = t * KT + r;
+        const bool there = r < KT && pos < len;
+        copy4(looked0 + looked(t, what, j) * 4, table + (there ? column(pos) : 0), there);
+      };
+      const int run = lane < KT / 8 ? (lane & (KT / 16 - 1)) * 16 : KT;
       const auto look = [&](int t) {
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j), pos = t * KT + r;
-          const bool there = r < KT && pos < len;
-          const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
-          copy4(looked0 + looked(t, 0, j) * 4, table + (there ? col : 0), there);
-        }
+        for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
+        if constexpr (COARSE) look_at(t, run, 3, 0);
+      };
+      const auto read = [&](int t, int what, int j) { return *reinterpret_cast<volatile int*>(sm_looked + looked(t, what, j) * 4); };
+      const auto scale_place = [&](int page, int in_page) {
+        return page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
       };
       const auto ask = [&](const void* base) {  // the tile that `at` is of, into the next stage
         uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
@@ -629,15 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
       const auto ask_keys = [&](int t) {
+        int page[LOOKS];
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) page[j] = read(t, 0, j);
+        if constexpr (COARSE) {
+          const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, run_page = read(t, 3, 0);
+          const bool good = run < KT && pos < len && run_page >= 0 && run_page < a.cache.n_pages;
+          copy4(looked0 + looked(t, 1, 0) * 4, (lane < KT / 16 ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(run_page, in_page) : 0), good);
+        }
 #pragma unroll
         for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j), pos = t * KT + r, col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
-          const int in_page = pos - col * a.cache.page_size, page = *reinterpret_cast<volatile int*>(sm_looked + looked(t, 0, j) * 4);
-          const bool there = r < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
-          const long long sc = good ? page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at : 0;
-          at[j] = good ? (uint32_t)((page * a.cache.page_stride + in_page * a.cache.slot_stride + head_at) >> 4) : kNone;
-          copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
-          copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
+          const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size;
+          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
+          // (below 2^32, so the product may be taken in 32 bits)
+          at[j] = good ? (uint32_t)page[j] * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
+          if constexpr (!COARSE) {
+            const long long sc = good ? scale_place(page[j], in_page) : 0;
+            copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
+            copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
+          }
           next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
         }
         if (t + 1 < wk.t1) look(t + 1);
@@ -646,13 +675,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto put = [&](int slot) {  // the next stage's codes into a slot
         const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
         const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+        uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k)
+          if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
+            x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
 #pragma unroll
         for (int k = 0; k < Sh::STEPS; ++k) {
           const int g = k * kProducers + pw, r = g * RPI + sub;
           if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
             const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
-            const uint4 lo = codes_to_half<FMT>(x.x, x.y), hi = codes_to_half<FMT>(x.z, x.w);
+            const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
           }
@@ -665,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
 #pragma unroll 1
         for (int k = 0; k < Sh::STEPS; ++k) {
-          const int r = (k * kProducers + pw) * RPI + sub, mine = k * RPI + sub;
+          const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r >> 4 : k * RPI + sub;
           if (r >= KT) break;
           uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
           if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
@@ -676,6 +709,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
             }
           }
+        }
+      };
+      // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum
+      // and in their products alike); values of scale 0 are zeros at scale 1
+      const auto put_scale = [&](float* sc, float s, bool of_value) {
+        float log, inv;
+        asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(s));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        if (of_value) {
+          sc[KT] = s == 0.f ? 0.f : log;
+          sc[2 * KT] = s == 0.f ? 1.f : inv;
+        } else {
+          sc[0] = s;
         }
       };
       const auto filled = [&](int slot) {  // what the lanes wrote, before the tensor cores read it
@@ -697,26 +743,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         float key[LOOKS], value[LOOKS];
 #pragma unroll
         for (int j = 0; j < LOOKS; ++j) {
-          key[j] = *reinterpret_cast<volatile float*>(sm_looked + looked(t, 1, j) * 4);
-          value[j] = *reinterpret_cast<volatile float*>(sm_looked + looked(t, 2, j) * 4);
+          if (j == 0 || !COARSE) key[j] = __int_as_float(read(t, 1, j));
+          if (!COARSE) value[j] = __int_as_float(read(t, 2, j));
         }
         if (more) ask_keys(t + 1);
         ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
         if (!ok) break;
         unsigned zero[2] = {0, 0};
         float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
+        if constexpr (COARSE) {
+          const bool of_value = lane >= KT / 16;
+          const float s = of_value ? value_scale(key[0], flags) : scale_of(key[0], flags);
+          zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> (KT / 16);
+          if (run < KT) put_scale(sc + run, s, of_value);
+        } else {
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j);
-          const float ks = scale_of(key[j], flags), vs = scale_of(value[j], flags);
-          zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);  // such values are zeros, at scale 1
-          if (r < KT) {
-            float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
-            asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
-            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
-            sc[r] = ks;
-            sc[KT + r] = vs == 0.f ? 0.f : log;
-            sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
+          for (int j = 0; j < LOOKS; ++j) {
+            const int r = row_of(j);
+            const float ks = scale_of(key[j], flags), vs = value_scale(value[j], flags);
+            zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);
+            if (r < KT) {
+              put_scale(sc + r, ks, false);
+              put_scale(sc + r, vs, true);
+            }
           }
         }
         if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
