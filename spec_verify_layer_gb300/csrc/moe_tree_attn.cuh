@@ -60,6 +60,8 @@
 // the end to the rows that see it.
 #pragma once
 
+#include <cuda.h>
+
 #include <atomic>
 #include <type_traits>
 
@@ -110,15 +112,14 @@ struct Shape {
   static constexpr int CC = kQ8<A> ? D / 16 : D / 8;   // and of a cached row
   static constexpr int RPI = 32 / CC;                  // rows that a warp copies with one instruction
   static constexpr int STEPS = (KT / RPI + kProducers - 1) / kProducers;  // instructions of a producer for a tile
-  // Codes: scale of the key, logarithm and reciprocal of the value's scale, of each key of kRing tiles (a
-  // tile's are written when its slot of keys is free, up to half the slots ahead of the softmax); a
-  // factor a query row; page and scales of the rows that a producer's lane looks up, twice; codes on
-  // their way, a stage for a tile's keys or values.
-  static constexpr int LOOKS = (STEPS * RPI + 31) / 32;  // rows of a producer that a lane looks up
+  // Codes: stages of raw codes, a tile's keys or values each; scale of the key, logarithm and reciprocal of
+  // the value's scale, of each key of kRing tiles (a tile's are written when its slot of keys is free, up
+  // to half the slots ahead of the softmax); a factor a query row; and, of two tiles, pages and raw
+  // scales as they were looked up.
   static constexpr int kRing = D == 64 ? 8 : 4;
   static constexpr int kRaw = KT * D, kRawStages = 3;
-  static constexpr int kLooked = kProducers * 2 * 4 * LOOKS * 32;
-  static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kLooked) * 4 + kRawStages * kRaw : 0;
+  static constexpr int kPages = 2 * KT;
+  static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kPages + 2 * 2 * KT) * 4 + kRawStages * kRaw : 0;
   // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
   // there is one stream); the weights, in 16 bits, go over the second half of their scores.
   __host__ __device__ static constexpr int s_col(int buf) { return NS == 2 ? 256 * buf : 64 * buf; }
@@ -138,6 +139,8 @@ struct Plan {  // host-computed, the same for every block
   float c;     // |scale| * log2(e); codes: 1 (scores are made powers of two key by key)
   float score; // codes: scale * log2(e), times what a code's fp16 number has to be multiplied with
   int block_shift;  // codes: log2 of the tokens of a block
+  int head_first;   // the tensor maps' order
+  int box;          // rows that a box of the tensor map has, 16 .. the tile's keys
   float4* part;      // [blocks][2: as Control::split][D / 4][part_rows]: a warp's rows side by side
   float2* part_ml;   // [blocks][2][part_rows]: maximum, sum
   unsigned* arrive;  // [blocks]
@@ -152,8 +155,9 @@ struct Split {  // a head that is split over blocks: its request's rows, its fir
 struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
+  unsigned long long raw_full[3], raw_empty[3], scale_full[2];  // codes
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows
+  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes: a bit a row)
   int red[kThreads / 32], redn[kThreads / 32];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;
@@ -200,11 +204,11 @@ __device__ __forceinline__ bool bar_wait(unsigned long long* b, uint32_t parity,
   if (bar_try(smem_u32(b), parity)) return true;
   return bar_wait_slow(smem_u32(b), parity, ct, status);
 }
-// The last wait, for products in flight: they end by themselves, whatever other waits of the block
+// The last wait, for products or copies in flight: they end by themselves, whatever other waits of the block
 // gave up, and until they have the block may neither free tensor memory nor leave.
-__device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned* status) {
+__device__ __forceinline__ void bar_drain(unsigned long long* b, uint32_t parity, unsigned* status) {
   const long long t0 = clock64();
-  while (!bar_try(smem_u32(b), 0)) {
+  while (!bar_try(smem_u32(b), parity)) {
     if (clock64() - t0 > (long long)kWaitNs * kCyclesPerNs) {
       atomicOr(status, MOE_DEV_TIMEOUT);
       return;
@@ -441,8 +445,279 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   const uint32_t high = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
   return (high >> 7) * 0xffu;
 }
+// Codes come into a ring of raw stages, a tile's keys and values in turn, by the tensor memory
+// accelerator: the third producer asks for them.  COARSE (the page is a multiple of 16 rows): boxes of
+// rows that lie in one page, by a tensor map; otherwise row by row.
+struct Maps {
+  CUtensorMap k, v;  // [page][head][slot][D], bytes; slot and head in the order of their strides
+};
+struct NoMaps {};
+template <typename A>
+using MapsOf = std::conditional_t<kQ8<A>, Maps, NoMaps>;
+
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int y, int z, int page, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(y), "r"(z), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void copy_row(uint32_t dst, const void* src, int bytes, unsigned long long* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned long long* b, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
+// The three producers' work for a block's share.  Each turns a third of a tile's rows into fp16, 16 codes
+// a lane and step; the third one (pw 2) asks for a tile's keys while the tile before is worked
+// on, and for its values when the keys before have been read.  Its own look-ups (pages a tile ahead,
+// scales with the keys) are asynchronous copies too: a register that waits for memory holds up every
+// exchange and barrier behind it, since they share few counters.
+template <typename A, int FMT, int D, bool COARSE>
+__device__ __forceinline__ void produce_codes(const A& a, const Plan& p, const Maps& maps, Control& ct, unsigned char* sm_kv,
+                                              unsigned char* sm_raw, float* sm_scale, unsigned char* sm_looked, Walk<A, D>& wk, int pw,
+                                              int member, unsigned& flags) {
+  using Sh = Shape<A, D>;
+  constexpr int KT = Sh::KT, CC = Sh::CC, RPI = Sh::RPI, RUNS = KT / 16, WORDS = KT / 32;
+  constexpr uint32_t kBlk = KT * 128;
+  const int lane = threadIdx.x & 31, chunk = lane % CC, sub = lane / CC;
+  const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw), looked0 = smem_u32(sm_looked);
+  volatile float* const raw_scale = reinterpret_cast<volatile float*>(sm_looked + Sh::kPages * 4);  // [2][keys, values][KT]
+  int slot = 0, tile_seq = 0, put_stage = 0, ask_stage = 0;
+  uint32_t phase = 1, put_ph = 0, ask_ph = 1;  // slots and stages start empty
+  int asked = 0, got = 0;                      // stages
+  bool ok = true;
+  const auto wait = [&](unsigned long long* b, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, bar_wait(b, parity, ct, a.dev_status));
+    return ok;
+  };
+  for (int seq = 0; ok && wk.more(); wk.next(a)) {
+    if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
+    const int len = wk.q.ctx + wk.q.n;
+    const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
+    if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
+      const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
+      const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
+      if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
+    }
+    // ---- the third producer: what it looks up is the page of a run of 16 rows (COARSE; lanes 0 ..
+    // RUNS - 1), or of the rows lane, lane + 32 ...
+    constexpr int LOOKS = COARSE ? 1 : WORDS;
+    const auto row_of = [&](int j) { return COARSE ? (lane < RUNS ? lane * 16 : KT) : j * 32 + lane; };
+    const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
+    int page[LOOKS] = {}, in_page[LOOKS] = {};  // of the tile that is asked for; page n_pages: none
+    const auto look = [&](int t) {
+#pragma unroll
+      for (int j = 0; j < LOOKS; ++j) {
+        const int r = row_of(j), pos = t * KT + r;
+        const bool there = r < KT && pos < len;
+        copy4(looked0 + (((t & 1) * LOOKS + j) * 32 + lane) * 4, table + (there ? column(pos) : 0), there);
+      }
+    };
+    const auto ask = [&](bool values) {  // the tile of `page`, keys or values
+      if (!wait(&ct.raw_empty[ask_stage], ask_ph)) return;
+      unsigned long long* const full = &ct.raw_full[ask_stage];
+      const uint32_t dst = raw0 + ask_stage * Sh::kRaw;
+      if constexpr (COARSE) {
+        // (what lies past the end or has no page is asked for at a page that is not there: zeros)
+        if (lane == 0) bar_expect(full, Sh::kRaw);
+        __syncwarp();
+        if (lane < RUNS && lane * 16 % p.box == 0)
+          copy_box(dst + lane * 16 * D, values ? &maps.v : &maps.k, p.head_first ? wk.h : in_page[0], p.head_first ? in_page[0] : wk.h, page[0], full);
+      } else {
+        int rows = 0;
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) rows += __popc(__ballot_sync(0xffffffffu, page[j] < a.cache.n_pages));
+        if (lane == 0) bar_expect(full, rows * D);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j)
+          if (page[j] < a.cache.n_pages)
+            copy_row(dst + (j * 32 + lane) * D,
+                     static_cast<const uint8_t*>(values ? a.cache.v : a.cache.k) + page[j] * a.cache.page_stride +
+                         in_page[j] * a.cache.slot_stride + wk.h * a.cache.head_stride,
+                     D, full);
+      }
+      ++asked;
+      if (++ask_stage == Sh::kRawStages) {
+        ask_stage = 0;
+        ask_ph ^= 1;
+      }
+    };
+    const auto ask_keys = [&](int t, int tile) {  // tile t of the head, the block's tile-th; its pages are there
+      unsigned missing[LOOKS];
+#pragma unroll
+      for (int j = 0; j < LOOKS; ++j) {
+        const int r = row_of(j), pos = t * KT + r;
+        const bool there = r < KT && pos < len;
+        page[j] = *reinterpret_cast<volatile int*>(sm_looked + (((t & 1) * LOOKS + j) * 32 + lane) * 4);
+        in_page[j] = pos - column(pos) * a.cache.page_size;
+        const bool good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
+        if (!good) page[j] = a.cache.n_pages;
+        missing[j] = __ballot_sync(0xffffffffu, there && !good);
+        const long long sc = good ? page[j] * a.cache.scale_page_stride + (in_page[j] >> p.block_shift) * a.cache.scale_block_stride +
+                                        wk.h * a.cache.scale_head_stride
+                                  : 0;
+        const uint32_t to = looked0 + (Sh::kPages + (tile & 1) * 2 * KT + (COARSE ? lane : r)) * 4;
+        if (r < KT) {
+          copy4(to, a.cache.k_scale + sc, good);
+          copy4(to + KT * 4, a.cache.v_scale + sc, good);
+        }
+      }
+      if (lane < WORDS) {  // the tile's rows without a page
+        unsigned word = missing[0];
+        if constexpr (COARSE) word = (word >> (2 * lane) & 1 ? 0xffffu : 0u) | (word >> (2 * lane + 1) & 1 ? 0xffff0000u : 0u);
+        else
+#pragma unroll
+          for (int j = 1; j < LOOKS; ++j) word = lane == j ? missing[j] : word;
+        ct.hole[tile & 7][lane] = word;
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&ct.scale_full[tile & 1])) : "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(&ct.scale_full[tile & 1]);  // behind the holes
+      if (t + 1 < wk.t1) look(t + 1);
+      ask(false);
+    };
+    // ---- all three
+    const auto put = [&](int slot) {  // the next stage's codes into a slot
+      const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
+      const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+      // lanes whose block of 64 elements is an odd one write their second eight first, so that the eight
+      // lanes of a store meet eight different banks of the swizzle
+      const int odd = CC > 4 ? chunk >> 2 & 1 : 0;
+      uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
+#pragma unroll
+      for (int k = 0; k < Sh::STEPS; ++k)
+        if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
+          x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
+#pragma unroll
+      for (int k = 0; k < Sh::STEPS; ++k) {
+        const int g = k * kProducers + pw, r = g * RPI + sub;
+        if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
+          const uint32_t to = dst + r * 128 + (((2 * (chunk & 3) + odd) ^ (r & 7)) << 4);
+          const uint4 lo = codes_to_half<FMT>(odd ? x[k].z : x[k].x, odd ? x[k].w : x[k].y);
+          const uint4 hi = codes_to_half<FMT>(odd ? x[k].x : x[k].z, odd ? x[k].y : x[k].w);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+        }
+      }
+      fence_async();  // what the lanes wrote, before the tensor cores read it
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(&ct.full[slot]);
+        bar_arrive(&ct.raw_empty[put_stage]);
+      }
+      if (++put_stage == Sh::kRawStages) {
+        put_stage = 0;
+        put_ph ^= 1;
+      }
+      ++got;
+    };
+    // Values past the end, without a page or of a scale that counts as 0 are zeros, and so are, in
+    // drafted rows, codes that are NaN: those are noted, and added at the end to the rows that see them.
+    const auto clean = [&](const unsigned* zero, int t) {
+      unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+      const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+#pragma unroll 1
+      for (int k = 0; k < Sh::STEPS; ++k) {
+        const int r = (k * kProducers + pw) * RPI + sub;
+        if (r >= KT) break;
+        uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
+        unsigned word = zero[0];
+        if constexpr (!COARSE)
+#pragma unroll
+          for (int j = 1; j < WORDS; ++j) word = r >> 5 == j ? zero[j] : word;
+        const bool gone = word >> (COARSE ? r >> 4 : r & 31) & 1 || ct.hole[tile_seq & 7][r >> 5] >> (r & 31) & 1;
+        if (gone || t * KT + r >= len) {
+          *v = make_uint4(0, 0, 0, 0);
+        } else if (FMT == MOE_E4M3 && r >= node0) {
+          const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
+          if (n.x | n.y | n.z | n.w) {
+            *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+            atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
+          }
+        }
+      }
+      __syncwarp();
+    };
+    if (pw == 2) {
+      look(wk.t0);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      ask_keys(wk.t0, tile_seq);
+      if (ok) ask(true);
+    }
+    for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
+      const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
+      const bool more = t + 1 < wk.t1;
+      if (pw == 2 && more) {
+        asm volatile("cp.async.wait_all;" ::: "memory");  // the next tile's pages, asked for a tile ago
+        ask_keys(t + 1, tile_seq + 1);
+        if (!ok) break;
+      }
+      if (!wait(&ct.scale_full[tile_seq & 1], tile_seq >> 1 & 1)) break;
+      const volatile float* const rs = raw_scale + (tile_seq & 1) * 2 * KT;
+      unsigned zero[LOOKS], any = 0;
+#pragma unroll
+      for (int j = 0; j < LOOKS; ++j) {
+        const int r = row_of(j);
+        unsigned seen = 0;
+        const float s = r < KT ? value_scale(rs[KT + (COARSE ? lane : r)], seen) : 1.f;
+        zero[j] = __ballot_sync(0xffffffffu, t * KT + r < len && s == 0.f);
+        any |= zero[j];
+      }
+      unsigned holes = 0;
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) holes |= *(volatile unsigned*)&ct.hole[tile_seq & 7][w];
+      if (holes) flags |= MOE_DEV_INDEX;
+      if (!wait(&ct.empty[slot], phase)) break;
+      if (pw == 0) {
+        float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          const int r = row_of(j);
+          if (r < KT) {
+            const float ks = scale_of(rs[COARSE ? lane : r], flags), vs = value_scale(rs[KT + (COARSE ? lane : r)], flags);
+            float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
+            asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
+            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
+            sc[r] = ks;
+            sc[KT + r] = vs == 0.f ? 0.f : log;  // values of scale 0 are zeros at scale 1
+            sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
+          }
+        }
+      }
+      if (!wait(&ct.raw_full[put_stage], put_ph)) break;
+      put(slot);
+      if (pw == 2 && more) {  // into the stage of the keys
+        ask(true);
+        if (!ok) break;
+      }
+      if (!wait(&ct.raw_full[put_stage], put_ph)) break;
+      if (!wait(&ct.empty[v_slot], phase ^ (v_slot == 0))) break;
+      if (any || holes || (t + 1) * KT > len || (FMT == MOE_E4M3 && (t + 1) * KT > wk.q.ctx)) clean(zero, t);
+      put(v_slot);
+      slot += 2;
+      if (slot >= p.nslot) {
+        slot -= p.nslot;
+        phase ^= 1;
+      }
+    }
+    ++seq;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // a wait that gave up: copies in flight end by themselves, and the block does not leave before
+  for (; pw == 2 && got < asked; ++got) {
+    bar_drain(&ct.raw_full[put_stage], put_ph, a.dev_status);
+    if (++put_stage == Sh::kRawStages) {
+      put_stage = 0;
+      put_ph ^= 1;
+    }
+  }
 }
 
 // ---- the kernel -------------------------------------------------------------------------
@@ -450,7 +725,7 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there)
 // FMT: the type of q, cache and out (16-bit cache), or of the codes.  COARSE: a scale stands for 16 keys or more.
 template <typename A, int FMT, int D, bool COARSE>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p) {
+    k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p, const __grid_constant__ MapsOf<A> maps) {
   using Sh = Shape<A, D>;
   constexpr bool Q8 = kQ8<A>;
   constexpr int DT = Q8 ? MOE_F16 : FMT;  // of the products
@@ -460,10 +735,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sm_q = smem;
   unsigned char* sm_kv = smem + (size_t)p.nq * Sh::kQ;
-  Control& ct = *reinterpret_cast<Control*>(sm_kv + (size_t)p.nslot * Sh::kSlot);
+  unsigned char* const sm_raw = sm_kv + (size_t)p.nslot * Sh::kSlot;
+  Control& ct = *reinterpret_cast<Control*>(sm_raw + (Q8 ? Sh::kRawStages * Sh::kRaw : 0));
   float* const sm_scale = reinterpret_cast<float*>(&ct + 1);  // [kRing][3][KT]
   float* const sm_row = sm_scale + Sh::kRing * 3 * KT;        // [256]
-  unsigned char* const sm_looked = reinterpret_cast<unsigned char*>(sm_row + 256), *const sm_raw = sm_looked + Sh::kLooked * 4;
+  unsigned char* const sm_looked = reinterpret_cast<unsigned char*>(sm_row + 256);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.group;
   const auto result2 = [&](float x, float y) {
@@ -493,6 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bar_init(&ct.q_ready, kSoftmaxThreads / 32);
       bar_init(&ct.drain, 1);
+      if constexpr (Q8) {
+        for (int i = 0; i < Sh::kRawStages; ++i) {
+          bar_init(&ct.raw_full[i], 1);
+          bar_init(&ct.raw_empty[i], kProducers);
+        }
+        for (int i = 0; i < 2; ++i) bar_init(&ct.scale_full[i], 33);
+      }
       ct.abort = 0;
       ct.wait_cycles = p.wait_cycles;
       ct.split[0].parts = ct.split[1].parts = 0;
@@ -573,223 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
-    // ---------------- producers of codes.  A warp's rows of a tile are dealt out as below, 16 codes
-    // a lane and step: they are copied into a ring of stages (keys and values of a tile in turn),
-    // read back by the lane that copied them, and written as fp16 into the tile's slot.  All that
-    // comes from memory comes by asynchronous copies, table entries and scales too: a register that
-    // waits for memory holds up every exchange and barrier behind it (they share few counters),
-    // 263 us against 438 with the codes in registers for 64 requests of one row over up to 8,192 keys
-    // with these in better and in worse order.
-    // Eight lanes side by side take four chunks each of two rows: their stores meet eight different
-    // banks of the swizzle.
-    constexpr int kBlocks = CC / 4;  // 64-element blocks of a row
-    const int pw = warp == 11 ? 2 : warp - 8, chunk = (lane & 3) | ((lane >> 3) & (kBlocks - 1)) << 2;
-    const int sub = (lane >> 2 & 1) | (lane / (8 * kBlocks)) << 1;
-    constexpr int LOOKS = Sh::LOOKS;
-    const auto row_of = [&](int j) {  // the j-th row that this lane looks up; KT and more: none
-      const int mine = 32 * j + lane;
-      return (mine / RPI * kProducers + pw) * RPI + mine % RPI;
-    };
-    constexpr uint32_t kNone = 0xffffffffu;
-    const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw) + lane * 16, looked0 = smem_u32(sm_looked);
-    const uint32_t page_units = (uint32_t)(a.cache.page_stride >> 4), slot_units = (uint32_t)(a.cache.slot_stride >> 4);
-    int slot = 0, tile_seq = 0, ask_stage = 0, put_stage = 0;
-    uint32_t phase = 1;  // the slots start empty
-    bool ok = true;
-    for (int seq = 0; ok && wk.more(); wk.next(a)) {
-      if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
-      const int len = wk.q.ctx + wk.q.n;
-      const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-      const uint32_t head_units = (uint32_t)(wk.h * a.cache.head_stride >> 4);
-      const long long scale_at = wk.h * a.cache.scale_head_stride;
-      if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
-        const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
-        const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
-        if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
-      }
-      unsigned hole[2], next_hole[2] = {0, 0};
-      uint32_t at[LOOKS];  // in units of 16 bytes
-      // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
-      // scale.  COARSE: lanes 0 .. KT/8 - 1 look up the scale of keys, then of values, of a run of 16 keys
-      // each: its page (3) and scale (1).
-      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 4 + what) * LOOKS + j) * 32 + lane; };
-      const auto column = [&](int pos) { return (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift); };
-      const auto look_at = [&](int t, int r, int what, int j) {
-        const int pos = t * KT + r;
-        const bool there = r < KT && pos < len;
-        copy4(looked0 + looked(t, what, j) * 4, table + (there ? column(pos) : 0), there);
-      };
-      const int run = lane < KT / 8 ? (lane & (KT / 16 - 1)) * 16 : KT;
-      const auto look = [&](int t) {
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
-        if constexpr (COARSE) look_at(t, run, 3, 0);
-      };
-      const auto read = [&](int t, int what, int j) { return *reinterpret_cast<volatile int*>(sm_looked + looked(t, what, j) * 4); };
-      const auto scale_place = [&](int page, int in_page) {
-        return page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
-      };
-      const auto ask = [&](const void* base) {  // the tile that `at` is of, into the next stage
-        uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k)
-          from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
-        const uint32_t dst = raw0 + ask_stage * Sh::kRaw + pw * 512;
-        const uint4* const src = static_cast<const uint4*>(base) + chunk;
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int g = k * kProducers + pw;
-          const bool there = from[k] != kNone;
-          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI)
-            copy16(dst + k * kProducers * 512, src + (there ? from[k] : 0), there);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (++ask_stage == Sh::kRawStages) ask_stage = 0;
-      };
-      // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
-      const auto ask_keys = [&](int t) {
-        int page[LOOKS];
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) page[j] = read(t, 0, j);
-        if constexpr (COARSE) {
-          const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, run_page = read(t, 3, 0);
-          const bool good = run < KT && pos < len && run_page >= 0 && run_page < a.cache.n_pages;
-          copy4(looked0 + looked(t, 1, 0) * 4, (lane < KT / 16 ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(run_page, in_page) : 0), good);
-        }
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size;
-          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
-          // (below 2^32, so the product may be taken in 32 bits)
-          at[j] = good ? (uint32_t)page[j] * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
-          if constexpr (!COARSE) {
-            const long long sc = good ? scale_place(page[j], in_page) : 0;
-            copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
-            copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
-          }
-          next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
-        }
-        if (t + 1 < wk.t1) look(t + 1);
-        ask(a.cache.k);
-      };
-      const auto put = [&](int slot) {  // the next stage's codes into a slot
-        const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
-        const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
-        uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k)
-          if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
-            x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int g = k * kProducers + pw, r = g * RPI + sub;
-          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
-            const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
-            const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
-          }
-        }
-        if (++put_stage == Sh::kRawStages) put_stage = 0;
-      };
-      // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
-      // are noted, and added at the end to the rows that see them.
-      const auto clean = [&](const unsigned (&zero)[2], int node0) {
-        unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
-#pragma unroll 1
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r >> 4 : k * RPI + sub;
-          if (r >= KT) break;
-          uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
-          if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
-          if (FMT == MOE_E4M3 && r >= node0) {
-            const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
-            if (n.x | n.y | n.z | n.w) {
-              *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-              atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
-            }
-          }
-        }
-      };
-      // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum
-      // and in their products alike); values of scale 0 are zeros at scale 1
-      const auto put_scale = [&](float* sc, float s, bool of_value) {
-        float log, inv;
-        asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(s));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        if (of_value) {
-          sc[KT] = s == 0.f ? 0.f : log;
-          sc[2 * KT] = s == 0.f ? 1.f : inv;
-        } else {
-          sc[0] = s;
-        }
-      };
-      const auto filled = [&](int slot) {  // what the lanes wrote, before the tensor cores read it
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&ct.full[slot]);
-      };
-      look(wk.t0);
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-      ask_keys(wk.t0);
-      ask(a.cache.v);
-      for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
-        const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
-        const bool more = t + 1 < wk.t1;
-        // keys, scales, and the next tile's pages are there; its values are on their way
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        hole[0] = next_hole[0];
-        hole[1] = next_hole[1];
-        float key[LOOKS], value[LOOKS];
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          if (j == 0 || !COARSE) key[j] = __int_as_float(read(t, 1, j));
-          if (!COARSE) value[j] = __int_as_float(read(t, 2, j));
-        }
-        if (more) ask_keys(t + 1);
-        ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
-        if (!ok) break;
-        unsigned zero[2] = {0, 0};
-        float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
-        if constexpr (COARSE) {
-          const bool of_value = lane >= KT / 16;
-          const float s = of_value ? value_scale(key[0], flags) : scale_of(key[0], flags);
-          zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> (KT / 16);
-          if (run < KT) put_scale(sc + run, s, of_value);
-        } else {
-#pragma unroll
-          for (int j = 0; j < LOOKS; ++j) {
-            const int r = row_of(j);
-            const float ks = scale_of(key[j], flags), vs = value_scale(value[j], flags);
-            zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);
-            if (r < KT) {
-              put_scale(sc + r, ks, false);
-              put_scale(sc + r, vs, true);
-            }
-          }
-        }
-        if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
-        if (lane == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
-        put(slot);
-        filled(slot);
-        if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-        ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status));
-        if (!ok) break;
-        const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
-        if ((zero[0] | zero[1]) || (FMT == MOE_E4M3 && node0 < KT)) clean(zero, node0);
-        if (more) ask(a.cache.v);  // (into the keys' stage)
-        put(v_slot);
-        filled(v_slot);
-        slot += 2;
-        if (slot >= p.nslot) {
-          slot -= p.nslot;
-          phase ^= 1;
-        }
-      }
-      ++seq;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+      produce_codes<A, FMT, D, COARSE>(a, p, maps, ct, sm_kv, sm_raw, sm_scale, sm_looked, wk, warp == 11 ? 2 : warp - 8, member, flags);
     } else {
     // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
     // g = k * kProducers + its number
@@ -1030,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       commit(&ct.drain);  // nothing runs on when the block ends, also where a wait gave up
-      bar_drain(&ct.drain, a.dev_status);
+      bar_drain(&ct.drain, 0, a.dev_status);
       __syncwarp();
     }
   } else {
@@ -1147,7 +1214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
               const int v = len - base - 32 * w;  // positions of the word
               bits = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
-              if (holes) {
+              if (Q8) {
+                bits &= ~hole[w];
+              } else if (holes) {
 #pragma unroll 1
                 for (int j = 0; j < 32; ++j) {
                   const int r = 32 * w + j, g = r / RPI, q = g / kProducers * RPI + r % RPI;
@@ -1581,7 +1650,7 @@ Workspace layout(const A& a) {
 }
 
 template <typename A, int FMT, int D, bool COARSE = true>
-int launch(const A& a, Plan p, int sms, cudaStream_t st) {
+int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps = {}) {
   using Sh = Shape<A, D>;
   constexpr int kSmem = 227 * 1024;
   const int need = a.max_tree * p.group;
@@ -1609,7 +1678,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, COARSE>, a, p));
+  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, COARSE>, a, p, maps));
 }
 
 // Checks, workspace and what the host computes, alike for both caches.
