@@ -38,18 +38,18 @@ bool encode(CUtensorMap* map, void* base, const moe_tree_attention8_args& a, int
                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks of 16 tokens and more have one scale for each run of 16 keys of a tile, and pages whose rows come
-// in boxes by a tensor map; smaller blocks, and strides that make no map, are taken row by row.
+// Blocks of 16 tokens and more have one scale for each run of 16 keys of a tile, smaller ones are taken key
+// by key.  Pages that are a multiple of 8 rows come in boxes, as far as their strides make a tensor map.
 template <int FMT>
 int choose(const moe_tree_attention8_args& a, Plan p, int sms, cudaStream_t st) {
   using A = moe_tree_attention8_args;
-  Maps maps;
-  bool coarse = a.cache.block_size >= 16;
-  if (coarse) {
-    p.box = 16;
+  Maps maps = {};
+  const bool coarse = a.cache.block_size >= 16;
+  if (a.cache.page_size % 8 == 0) {
+    p.box = 8;
     while (2 * p.box <= (a.head_dim == 256 ? 64 : 128) && a.cache.page_size % (2 * p.box) == 0) p.box *= 2;
     p.head_first = a.cache.head_stride < a.cache.slot_stride;
-    coarse = encode(&maps.k, a.cache.k, a, p.box, p.head_first) && encode(&maps.v, a.cache.v, a, p.box, p.head_first);
+    if (!encode(&maps.k, a.cache.k, a, p.box, p.head_first) || !encode(&maps.v, a.cache.v, a, p.box, p.head_first)) p.box = 0;
   }
   switch (a.head_dim) {
     case 64: return coarse ? launch<A, FMT, 64, true>(a, p, sms, st, maps) : launch<A, FMT, 64, false>(a, p, sms, st, maps);
@@ -70,7 +70,7 @@ extern "C" int moe_tree_attention8(const moe_tree_attention8_args* args, void* w
   const int rc = prepare(args, ws, ws_bytes, p, sms);
   if (rc != MOE_OK || args->n_rows == 0) return rc;
   const moe_tree_attention8_args& a = *args;
-  p.flip = 0;  // the sign of the scale goes with the rows' factors
+  p.flip = 0;
   p.c = 1.f;
   p.score = a.scale * 1.4426950408889634f;
   while ((1 << p.block_shift) < a.cache.block_size) ++p.block_shift;

@@ -74,8 +74,7 @@ inline std::atomic<unsigned long long> g_attention_wait_ns{2000000000ull};
 namespace {
 
 constexpr int kTree = 64;
-constexpr int kThreads = 384;  // 8 softmax warps, 3 producer warps, 1 issuing warp: 168 registers a thread
-constexpr int kSoftmaxThreads = 256, kProducers = 3;
+constexpr int kSoftmaxThreads = 256, kProducers = 3, kConverters = 6;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 // Weights are 2^(score - maximum + kBias), and a maximum may lag 2^kRescale behind.  fp16 has few
@@ -102,6 +101,9 @@ constexpr bool kQ8 = std::is_same_v<A, moe_tree_attention8_args>;
 
 template <typename A, int D>
 struct Shape {
+  // 8 softmax warps, 1 issuing warp, and 3 producer warps (168 registers a thread) or, of codes, 1 loader
+  // and 6 converters (128 registers)
+  static constexpr int kThreads = kQ8<A> ? 512 : 384;
   static constexpr int KT = kKeyTile<D>;
   static constexpr int NS = D == 256 ? 1 : 2;          // streams (tensor memory holds 512 columns)
   static constexpr int PARTS = KT / 64;                // the weights are handed over 64 keys at a time
@@ -140,7 +142,7 @@ struct Plan {  // host-computed, the same for every block
   float score; // codes: scale * log2(e), times what a code's fp16 number has to be multiplied with
   int block_shift;  // codes: log2 of the tokens of a block
   int head_first;   // the tensor maps' order
-  int box;          // rows that a box of the tensor map has, 16 .. the tile's keys
+  int box;          // rows that a box of the tensor map has, 8 .. the tile's keys; 0: no boxes
   float4* part;      // [blocks][2: as Control::split][D / 4][part_rows]: a warp's rows side by side
   float2* part_ml;   // [blocks][2][part_rows]: maximum, sum
   unsigned* arrive;  // [blocks]
@@ -155,10 +157,11 @@ struct Split {  // a head that is split over blocks: its request's rows, its fir
 struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
-  unsigned long long raw_full[3], raw_empty[3], scale_full[2];  // codes
+  unsigned long long raw_full[3], raw_empty[3], known[2];  // codes
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
+  unsigned gone[8][4];                // codes, per tile: rows whose values are zeros
   __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes: a bit a row)
-  int red[kThreads / 32], redn[kThreads / 32];
+  int red[16], redn[16];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;
   int start_b, gangs, groups, gang, member;
@@ -303,6 +306,13 @@ __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tm_store2(uint32_t addr, float x, float y) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(__float_as_uint(x)),
                "r"(__float_as_uint(y))
@@ -445,9 +455,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   const uint32_t high = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
   return (high >> 7) * 0xffu;
 }
-// Codes come into a ring of raw stages, a tile's keys and values in turn, by the tensor memory
-// accelerator: the third producer asks for them.  COARSE (the page is a multiple of 16 rows): boxes of
-// rows that lie in one page, by a tensor map; otherwise row by row.
+// Codes come into a ring of raw stages, a tile's keys and values in turn; one warp asks for them, six turn
+// them into fp16.
 struct Maps {
   CUtensorMap k, v;  // [page][head][slot][D], bytes; slot and head in the order of their strides
 };
@@ -461,36 +470,173 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
       "l"(map), "r"(0), "r"(y), "r"(z), "r"(page), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void copy_row(uint32_t dst, const void* src, int bytes, unsigned long long* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
-               "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ void bar_expect(unsigned long long* b, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_copies(unsigned long long* b) {  // an arrival when this thread's copies so far are there
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
-// The three producers' work for a block's share.  Each turns a third of a tile's rows into fp16, 16 codes
-// a lane and step; the third one (pw 2) asks for a tile's keys while the tile before is worked
-// on, and for its values when the keys before have been read.  Its own look-ups (pages a tile ahead,
-// scales with the keys) are asynchronous copies too: a register that waits for memory holds up every
-// exchange and barrier behind it, since they share few counters.
+// The loader: looks up pages (a tile ahead) and scales, asks for a tile's keys while the tile before is
+// worked on and for its values when a stage is free, and writes down what the softmax and the
+// converters have to know of the tile.  Where a page is a multiple of 8 rows (p.box) the rows of a
+// page come as boxes of a tensor map, otherwise by 16-byte copies.  All that it looks up are asynchronous
+// copies too: a register that waits for memory holds up every exchange and barrier behind it.
 template <typename A, int FMT, int D, bool COARSE>
-__device__ __forceinline__ void produce_codes(const A& a, const Plan& p, const Maps& maps, Control& ct, unsigned char* sm_kv,
-                                              unsigned char* sm_raw, float* sm_scale, unsigned char* sm_looked, Walk<A, D>& wk, int pw,
-                                              int member, unsigned& flags) {
+__device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps& maps, Control& ct, unsigned char* sm_raw, float* sm_scale,
+                                           unsigned char* sm_looked, Walk<A, D>& wk, int member, unsigned& flags) {
   using Sh = Shape<A, D>;
-  constexpr int KT = Sh::KT, CC = Sh::CC, RPI = Sh::RPI, RUNS = KT / 16, WORDS = KT / 32;
+  constexpr int KT = Sh::KT, WORDS = KT / 32, CC = Sh::CC;
+  const int lane = threadIdx.x & 31;
+  const uint32_t raw0 = smem_u32(sm_raw), looked0 = smem_u32(sm_looked);
+  volatile int* const pages = reinterpret_cast<volatile int*>(sm_looked);
+  volatile float* const raw_scale = reinterpret_cast<volatile float*>(sm_looked + Sh::kPages * 4);  // [2: tiles][keys, values][KT]
+  int tile_seq = 0, stage = 0, asked = 0;
+  uint32_t ph = 1;  // stages start empty
+  bool ok = true;
+  const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
+  for (; ok && wk.more(); wk.next(a)) {
+    if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
+    const int len = wk.q.ctx + wk.q.n;
+    const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
+    if (!(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {        // who shares this head: read when the unit ends
+      const int at = ct.w1 - wk.left - wk.p0 + kUnit;  // the place of the head's first tile
+      const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
+      if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
+    }
+    // pages are looked up of runs of 8 rows, a lane each, or (without boxes) of the rows lane, lane + 32 ...
+    const auto look = [&](int t) {
+#pragma unroll
+      for (int j = 0; j < WORDS; ++j) {
+        if (j > 0 && p.box) break;
+        const int r = p.box ? lane * 8 : j * 32 + lane, pos = t * KT + r;
+        const bool there = r < KT && pos < len;
+        copy4(looked0 + (((t & 1) * WORDS + j) * 32 + lane) * 4, table + (there ? column(pos) : 0), there);
+      }
+    };
+    const auto page_of = [&](int t, int r) { return pages[((t & 1) * WORDS * 32) + (p.box ? r >> 3 : r)]; };
+    const auto ask = [&](int t, bool values) {  // the next stage: keys or values of tile t, whose pages are there
+      ok = __all_sync(0xffffffffu, bar_wait(&ct.raw_empty[stage], ph, ct, a.dev_status));
+      if (!ok) return;
+      unsigned long long* const full = &ct.raw_full[stage];
+      const uint32_t dst = raw0 + stage * Sh::kRaw;
+      if (p.box) {
+        // (what lies past the end or has no page is asked for at a page that is not there: zeros)
+        if (lane == 0) bar_expect(full, Sh::kRaw);
+        __syncwarp();
+        const int r = lane * 8, pos = t * KT + r;
+        if (r < KT && r % p.box == 0) {
+          const int page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
+          const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
+          copy_box(dst + r * D, values ? &maps.v : &maps.k, p.head_first ? wk.h : in_page, p.head_first ? in_page : wk.h,
+                   good ? page : a.cache.n_pages, full);
+        }
+      } else {
+        const uint8_t* const base = static_cast<const uint8_t*>(values ? a.cache.v : a.cache.k) + wk.h * a.cache.head_stride + lane % CC * 16;
+#pragma unroll 2
+        for (int r = lane / CC; r < KT; r += 32 / CC) {
+          const int pos = t * KT + r, page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
+          const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
+          copy16(dst + r * D + lane % CC * 16, base + (good ? page * a.cache.page_stride + in_page * a.cache.slot_stride : 0), good);
+        }
+        bar_copies(full);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++asked;
+      if (++stage == Sh::kRawStages) {
+        stage = 0;
+        ph ^= 1;
+      }
+    };
+    const auto ask_tile = [&](int t, int tile) {  // tile t of the head, the block's tile-th
+#pragma unroll
+      for (int j = 0; j < (COARSE ? 1 : WORDS); ++j) {
+        const int r = COARSE ? lane * 16 : j * 32 + lane, pos = t * KT + r;
+        if (r < KT) {
+          const int page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
+          const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
+          const long long sc = good ? page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride +
+                                          wk.h * a.cache.scale_head_stride
+                                    : 0;
+          const uint32_t to = looked0 + (Sh::kPages + (tile & 1) * 2 * KT + r) * 4;
+          copy4(to, a.cache.k_scale + sc, good);
+          copy4(to + KT * 4, a.cache.v_scale + sc, good);
+        }
+      }
+      if (t + 1 < wk.t1) look(t + 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      ask(t, false);
+      if (ok) ask(t, true);
+    };
+    // scales as the softmax takes them, and the rows whose values are zeros: without a page, past the end,
+    // or of a scale that counts as 0
+    const auto write_down = [&](int t) {
+      const volatile float* const rs = raw_scale + (tile_seq & 1) * 2 * KT;
+      float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
+      unsigned missing = 0, any = 0, gone = 0;
+#pragma unroll
+      for (int j = 0; j < WORDS; ++j) {
+        const int r = j * 32 + lane, pos = t * KT + r, page = page_of(t, r);
+        const bool there = pos < len, good = there && page >= 0 && page < a.cache.n_pages;
+        const unsigned m = __ballot_sync(0xffffffffu, there && !good);
+        const float vs = value_scale(rs[KT + (COARSE ? r & ~15 : r)], flags);
+        const unsigned g = __ballot_sync(0xffffffffu, !there || !good || vs == 0.f);
+        missing = lane == j ? m : missing;
+        gone = lane == j ? g : gone;
+        any |= m;
+        if (!COARSE || (r & 15) == 0) {
+          const float ks = scale_of(rs[r], flags);
+          float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
+          asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
+          asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
+          sc[r] = ks;
+          sc[KT + r] = vs == 0.f ? 0.f : log;  // values of scale 0 are zeros at scale 1
+          sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
+        }
+      }
+      if (any) flags |= MOE_DEV_INDEX;
+      if (lane < WORDS) {
+        ct.hole[tile_seq & 7][lane] = missing;
+        ct.gone[tile_seq & 7][lane] = gone;
+      }
+    };
+    look(wk.t0);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    ask_tile(wk.t0, tile_seq);
+    for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
+      asm volatile("cp.async.wait_group 2;" ::: "memory");  // all but the codes: this tile's scales and the next one's pages
+      __syncwarp();
+      write_down(t);
+      __syncwarp();
+      if (lane == 0) bar_arrive(&ct.known[tile_seq & 1]);
+      if (t + 1 < wk.t1) ask_tile(t + 1, tile_seq + 1);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // a wait that gave up: boxes in flight end by themselves, and the block does not leave before
+  for (int i = 1; !ok && i <= Sh::kRawStages && i <= asked; ++i)
+    bar_drain(&ct.raw_full[(asked - i) % Sh::kRawStages], (asked - i) / Sh::kRawStages & 1, a.dev_status);
+}
+
+// The converters: each turns a sixth of a tile's rows into fp16, 16 codes a lane and step, in the
+// 128-byte swizzle that the tensor cores read.
+template <typename A, int FMT, int D>
+__device__ __forceinline__ void convert_codes(const A& a, const Plan& p, Control& ct, unsigned char* sm_kv, unsigned char* sm_raw,
+                                              Walk<A, D>& wk, int cw, int member) {
+  using Sh = Shape<A, D>;
+  constexpr int KT = Sh::KT, CC = Sh::CC, RPI = Sh::RPI, WORDS = KT / 32, STEPS = (KT / RPI + kConverters - 1) / kConverters;
   constexpr uint32_t kBlk = KT * 128;
   const int lane = threadIdx.x & 31, chunk = lane % CC, sub = lane / CC;
-  const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw), looked0 = smem_u32(sm_looked);
-  volatile float* const raw_scale = reinterpret_cast<volatile float*>(sm_looked + Sh::kPages * 4);  // [2][keys, values][KT]
-  int slot = 0, tile_seq = 0, put_stage = 0, ask_stage = 0;
-  uint32_t phase = 1, put_ph = 0, ask_ph = 1;  // slots and stages start empty
-  int asked = 0, got = 0;                      // stages
+  const uint32_t kv0 = smem_u32(sm_kv);
+  // lanes whose block of 64 elements is an odd one write their second eight first, so that the eight lanes
+  // of a store meet eight different banks of the swizzle
+  const int odd = CC > 4 ? chunk >> 2 & 1 : 0;
+  int slot = 0, tile_seq = 0, stage = 0;
+  uint32_t phase = 1, ph = 0;  // slots start empty
   bool ok = true;
   const auto wait = [&](unsigned long long* b, uint32_t parity) {
     ok = __all_sync(0xffffffffu, bar_wait(b, parity, ct, a.dev_status));
@@ -498,107 +644,18 @@ __device__ __forceinline__ void produce_codes(const A& a, const Plan& p, const M
   };
   for (int seq = 0; ok && wk.more(); wk.next(a)) {
     if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
-    const int len = wk.q.ctx + wk.q.n;
-    const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-    if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
-      const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
-      const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
-      if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
-    }
-    // ---- the third producer: what it looks up is the page of a run of 16 rows (COARSE; lanes 0 ..
-    // RUNS - 1), or of the rows lane, lane + 32 ...
-    constexpr int LOOKS = COARSE ? 1 : WORDS;
-    const auto row_of = [&](int j) { return COARSE ? (lane < RUNS ? lane * 16 : KT) : j * 32 + lane; };
-    const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
-    int page[LOOKS] = {}, in_page[LOOKS] = {};  // of the tile that is asked for; page n_pages: none
-    const auto look = [&](int t) {
-#pragma unroll
-      for (int j = 0; j < LOOKS; ++j) {
-        const int r = row_of(j), pos = t * KT + r;
-        const bool there = r < KT && pos < len;
-        copy4(looked0 + (((t & 1) * LOOKS + j) * 32 + lane) * 4, table + (there ? column(pos) : 0), there);
-      }
-    };
-    const auto ask = [&](bool values) {  // the tile of `page`, keys or values
-      if (!wait(&ct.raw_empty[ask_stage], ask_ph)) return;
-      unsigned long long* const full = &ct.raw_full[ask_stage];
-      const uint32_t dst = raw0 + ask_stage * Sh::kRaw;
-      if constexpr (COARSE) {
-        // (what lies past the end or has no page is asked for at a page that is not there: zeros)
-        if (lane == 0) bar_expect(full, Sh::kRaw);
-        __syncwarp();
-        if (lane < RUNS && lane * 16 % p.box == 0)
-          copy_box(dst + lane * 16 * D, values ? &maps.v : &maps.k, p.head_first ? wk.h : in_page[0], p.head_first ? in_page[0] : wk.h, page[0], full);
-      } else {
-        int rows = 0;
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) rows += __popc(__ballot_sync(0xffffffffu, page[j] < a.cache.n_pages));
-        if (lane == 0) bar_expect(full, rows * D);
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j)
-          if (page[j] < a.cache.n_pages)
-            copy_row(dst + (j * 32 + lane) * D,
-                     static_cast<const uint8_t*>(values ? a.cache.v : a.cache.k) + page[j] * a.cache.page_stride +
-                         in_page[j] * a.cache.slot_stride + wk.h * a.cache.head_stride,
-                     D, full);
-      }
-      ++asked;
-      if (++ask_stage == Sh::kRawStages) {
-        ask_stage = 0;
-        ask_ph ^= 1;
-      }
-    };
-    const auto ask_keys = [&](int t, int tile) {  // tile t of the head, the block's tile-th; its pages are there
-      unsigned missing[LOOKS];
-#pragma unroll
-      for (int j = 0; j < LOOKS; ++j) {
-        const int r = row_of(j), pos = t * KT + r;
-        const bool there = r < KT && pos < len;
-        page[j] = *reinterpret_cast<volatile int*>(sm_looked + (((t & 1) * LOOKS + j) * 32 + lane) * 4);
-        in_page[j] = pos - column(pos) * a.cache.page_size;
-        const bool good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
-        if (!good) page[j] = a.cache.n_pages;
-        missing[j] = __ballot_sync(0xffffffffu, there && !good);
-        const long long sc = good ? page[j] * a.cache.scale_page_stride + (in_page[j] >> p.block_shift) * a.cache.scale_block_stride +
-                                        wk.h * a.cache.scale_head_stride
-                                  : 0;
-        const uint32_t to = looked0 + (Sh::kPages + (tile & 1) * 2 * KT + (COARSE ? lane : r)) * 4;
-        if (r < KT) {
-          copy4(to, a.cache.k_scale + sc, good);
-          copy4(to + KT * 4, a.cache.v_scale + sc, good);
-        }
-      }
-      if (lane < WORDS) {  // the tile's rows without a page
-        unsigned word = missing[0];
-        if constexpr (COARSE) word = (word >> (2 * lane) & 1 ? 0xffffu : 0u) | (word >> (2 * lane + 1) & 1 ? 0xffff0000u : 0u);
-        else
-#pragma unroll
-          for (int j = 1; j < LOOKS; ++j) word = lane == j ? missing[j] : word;
-        ct.hole[tile & 7][lane] = word;
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&ct.scale_full[tile & 1])) : "memory");
-      __syncwarp();
-      if (lane == 0) bar_arrive(&ct.scale_full[tile & 1]);  // behind the holes
-      if (t + 1 < wk.t1) look(t + 1);
-      ask(false);
-    };
-    // ---- all three
     const auto put = [&](int slot) {  // the next stage's codes into a slot
       const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
-      const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
-      // lanes whose block of 64 elements is an odd one write their second eight first, so that the eight
-      // lanes of a store meet eight different banks of the swizzle
-      const int odd = CC > 4 ? chunk >> 2 & 1 : 0;
-      uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
+      const unsigned char* const src = sm_raw + stage * Sh::kRaw + cw * 512 + lane * 16;
+      uint4 x[STEPS];  // (all loads ahead of the stores)
 #pragma unroll
-      for (int k = 0; k < Sh::STEPS; ++k)
-        if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
-          x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
+      for (int k = 0; k < STEPS; ++k)
+        if ((k + 1) * kConverters <= KT / RPI || k * kConverters + cw < KT / RPI)
+          x[k] = *reinterpret_cast<const uint4*>(src + k * kConverters * 512);
 #pragma unroll
-      for (int k = 0; k < Sh::STEPS; ++k) {
-        const int g = k * kProducers + pw, r = g * RPI + sub;
-        if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
+      for (int k = 0; k < STEPS; ++k) {
+        const int g = k * kConverters + cw, r = g * RPI + sub;
+        if ((k + 1) * kConverters <= KT / RPI || g < KT / RPI) {
           const uint32_t to = dst + r * 128 + (((2 * (chunk & 3) + odd) ^ (r & 7)) << 4);
           const uint4 lo = codes_to_half<FMT>(odd ? x[k].z : x[k].x, odd ? x[k].w : x[k].y);
           const uint4 hi = codes_to_half<FMT>(odd ? x[k].x : x[k].z, odd ? x[k].y : x[k].w);
@@ -610,30 +667,23 @@ __device__ __forceinline__ void produce_codes(const A& a, const Plan& p, const M
       __syncwarp();
       if (lane == 0) {
         bar_arrive(&ct.full[slot]);
-        bar_arrive(&ct.raw_empty[put_stage]);
+        bar_arrive(&ct.raw_empty[stage]);
       }
-      if (++put_stage == Sh::kRawStages) {
-        put_stage = 0;
-        put_ph ^= 1;
+      if (++stage == Sh::kRawStages) {
+        stage = 0;
+        ph ^= 1;
       }
-      ++got;
     };
-    // Values past the end, without a page or of a scale that counts as 0 are zeros, and so are, in
-    // drafted rows, codes that are NaN: those are noted, and added at the end to the rows that see them.
-    const auto clean = [&](const unsigned* zero, int t) {
-      unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
-      const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+    // Values that are not there are zeros, and so are, in drafted rows, codes that are NaN: those are
+    // noted, and added at the end to the rows that see them.
+    const auto clean = [&](int node0) {
+      unsigned char* const src = sm_raw + stage * Sh::kRaw + cw * 512 + lane * 16;
 #pragma unroll 1
-      for (int k = 0; k < Sh::STEPS; ++k) {
-        const int r = (k * kProducers + pw) * RPI + sub;
+      for (int k = 0; k < STEPS; ++k) {
+        const int r = (k * kConverters + cw) * RPI + sub;
         if (r >= KT) break;
-        uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
-        unsigned word = zero[0];
-        if constexpr (!COARSE)
-#pragma unroll
-          for (int j = 1; j < WORDS; ++j) word = r >> 5 == j ? zero[j] : word;
-        const bool gone = word >> (COARSE ? r >> 4 : r & 31) & 1 || ct.hole[tile_seq & 7][r >> 5] >> (r & 31) & 1;
-        if (gone || t * KT + r >= len) {
+        uint4* const v = reinterpret_cast<uint4*>(src + k * kConverters * 512);
+        if (ct.gone[tile_seq & 7][r >> 5] >> (r & 31) & 1) {
           *v = make_uint4(0, 0, 0, 0);
         } else if (FMT == MOE_E4M3 && r >= node0) {
           const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
@@ -645,61 +695,19 @@ __device__ __forceinline__ void produce_codes(const A& a, const Plan& p, const M
       }
       __syncwarp();
     };
-    if (pw == 2) {
-      look(wk.t0);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      ask_keys(wk.t0, tile_seq);
-      if (ok) ask(true);
-    }
-    for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
+    for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
       const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
-      const bool more = t + 1 < wk.t1;
-      if (pw == 2 && more) {
-        asm volatile("cp.async.wait_all;" ::: "memory");  // the next tile's pages, asked for a tile ago
-        ask_keys(t + 1, tile_seq + 1);
-        if (!ok) break;
-      }
-      if (!wait(&ct.scale_full[tile_seq & 1], tile_seq >> 1 & 1)) break;
-      const volatile float* const rs = raw_scale + (tile_seq & 1) * 2 * KT;
-      unsigned zero[LOOKS], any = 0;
-#pragma unroll
-      for (int j = 0; j < LOOKS; ++j) {
-        const int r = row_of(j);
-        unsigned seen = 0;
-        const float s = r < KT ? value_scale(rs[KT + (COARSE ? lane : r)], seen) : 1.f;
-        zero[j] = __ballot_sync(0xffffffffu, t * KT + r < len && s == 0.f);
-        any |= zero[j];
-      }
-      unsigned holes = 0;
-#pragma unroll
-      for (int w = 0; w < WORDS; ++w) holes |= *(volatile unsigned*)&ct.hole[tile_seq & 7][w];
-      if (holes) flags |= MOE_DEV_INDEX;
+      if (!wait(&ct.known[tile_seq & 1], tile_seq >> 1 & 1)) break;
+      if (!wait(&ct.raw_full[stage], ph)) break;
       if (!wait(&ct.empty[slot], phase)) break;
-      if (pw == 0) {
-        float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j);
-          if (r < KT) {
-            const float ks = scale_of(rs[COARSE ? lane : r], flags), vs = value_scale(rs[KT + (COARSE ? lane : r)], flags);
-            float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
-            asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
-            asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
-            sc[r] = ks;
-            sc[KT + r] = vs == 0.f ? 0.f : log;  // values of scale 0 are zeros at scale 1
-            sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
-          }
-        }
-      }
-      if (!wait(&ct.raw_full[put_stage], put_ph)) break;
       put(slot);
-      if (pw == 2 && more) {  // into the stage of the keys
-        ask(true);
-        if (!ok) break;
-      }
-      if (!wait(&ct.raw_full[put_stage], put_ph)) break;
+      unsigned gone = 0;
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) gone |= *(volatile unsigned*)&ct.gone[tile_seq & 7][w];
+      if (!wait(&ct.raw_full[stage], ph)) break;
       if (!wait(&ct.empty[v_slot], phase ^ (v_slot == 0))) break;
-      if (any || holes || (t + 1) * KT > len || (FMT == MOE_E4M3 && (t + 1) * KT > wk.q.ctx)) clean(zero, t);
+      const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+      if (gone || (FMT == MOE_E4M3 && node0 < KT)) clean(node0);
       put(v_slot);
       slot += 2;
       if (slot >= p.nslot) {
@@ -709,27 +717,18 @@ __device__ __forceinline__ void produce_codes(const A& a, const Plan& p, const M
     }
     ++seq;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  // a wait that gave up: copies in flight end by themselves, and the block does not leave before
-  for (; pw == 2 && got < asked; ++got) {
-    bar_drain(&ct.raw_full[put_stage], put_ph, a.dev_status);
-    if (++put_stage == Sh::kRawStages) {
-      put_stage = 0;
-      put_ph ^= 1;
-    }
-  }
 }
 
 // ---- the kernel -------------------------------------------------------------------------
 
 // FMT: the type of q, cache and out (16-bit cache), or of the codes.  COARSE: a scale stands for 16 keys or more.
 template <typename A, int FMT, int D, bool COARSE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
     k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p, const __grid_constant__ MapsOf<A> maps) {
   using Sh = Shape<A, D>;
   constexpr bool Q8 = kQ8<A>;
   constexpr int DT = Q8 ? MOE_F16 : FMT;  // of the products
-  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI;
+  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kThreads = Sh::kThreads;
   constexpr uint32_t kBlk = KT * 128;  // bytes of a 64-element block of a key or value tile
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -758,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == 11) {
     if (lane < p.nslot) {
-      bar_init(&ct.full[lane], Q8 ? kProducers : 33 * kProducers);  // a warp's copies, and what its first lane wrote
+      bar_init(&ct.full[lane], Q8 ? kConverters : 33 * kProducers);  // a warp's copies, and what its first lane wrote
       bar_init(&ct.empty[lane], 1);
     }
     if (lane < 4) bar_init(&ct.p_full[lane], 4);
@@ -771,10 +770,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&ct.drain, 1);
       if constexpr (Q8) {
         for (int i = 0; i < Sh::kRawStages; ++i) {
-          bar_init(&ct.raw_full[i], 1);
-          bar_init(&ct.raw_empty[i], kProducers);
+          bar_init(&ct.raw_full[i], p.box ? 1 : 32);
+          bar_init(&ct.raw_empty[i], kConverters);
         }
-        for (int i = 0; i < 2; ++i) bar_init(&ct.scale_full[i], 33);
+        for (int i = 0; i < 2; ++i) bar_init(&ct.known[i], 1);
       }
       ct.abort = 0;
       ct.wait_cycles = p.wait_cycles;
@@ -854,9 +853,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int member = ct.member;
   wk.begin(a, ct.start_b, ct.start_off, ct.w1 - ct.w0);
 
-  if (warp == 8 || warp == 9 || warp == 11) {
+  if (Q8 ? warp >= 8 && warp != 10 : warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
-      produce_codes<A, FMT, D, COARSE>(a, p, maps, ct, sm_kv, sm_raw, sm_scale, sm_looked, wk, warp == 11 ? 2 : warp - 8, member, flags);
+      if (warp == 8) load_codes<A, FMT, D, COARSE>(a, p, maps, ct, sm_raw, sm_scale, sm_looked, wk, member, flags);
+      else convert_codes<A, FMT, D>(a, p, ct, sm_kv, sm_raw, wk, warp == 9 ? 0 : warp - 10, member);
     } else {
     // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
     // g = k * kProducers + its number
@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int o = CPR / 2; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
           const bool bf = a.dtype == MOE_BF16;
           const int k = min(126, 14 - (bf ? (int)(most >> 7) - 127 : (int)(most >> 10) - 15));
-          const float by = __uint_as_float((uint32_t)(k + 127) << 23);
+          const float by = __uint_as_float((uint32_t)(k + 127) << 23 | (p.score < 0.f ? 0x80000000u : 0u));
           uint32_t y[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -1145,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             y[j] = pack2<MOE_F16>(v.x * by, v.y * by);
           }
           *reinterpret_cast<uint4*>(smem + (q_at(i) - q0)) = make_uint4(y[0], y[1], y[2], y[3]);
-          if (i % CPR == 0) sm_row[i / CPR] = p.score * __uint_as_float((uint32_t)(127 - k) << 23);
+          if (i % CPR == 0) sm_row[i / CPR] = fabsf(p.score) * __uint_as_float((uint32_t)(127 - k) << 23);
         } else
         copy16(q_at(i), static_cast<const uint16_t*>(a.q) + (long long)(wk.q.s + n) * a.q_stride + (wk.h * G + g) * D + i % CPR * 8,
                i < rows * CPR);
@@ -1232,13 +1232,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             // handed over, the tile is gone through again.  The halves are a rolled loop and the
             // mask a branch inside: this code is fetched anew by every launch, and its length
             // shows in the short ones.
+            if constexpr (Q8) {
+              // Codes: scores become powers of two with the value's scale in them, s * key's scale *
+              // row's factor + log2(value's scale) (the factor is not negative).  First their maximum, 64 at a
+              // time, then weights, 32 at a time and the last keys first: that needs fewer registers than
+              // the way below, so that there is room for converters.
+              const float* const scales = sm_scale + ((tile_seq + ti) & (Sh::kRing - 1)) * 3 * KT;
+              float top = -INFINITY;
+              {
+                uint32_t x[64];
+#pragma unroll 1
+                for (int half = 0; half < Sh::PARTS; ++half) {
+                  const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
+                  tm_load(x, at);
+                  tm_load(x + 32, at + 32);
+                  tm_wait();
+                  ready(x);
+                  ready(x + 32);
+                  if (!all) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                      const unsigned bits = seen(2 * half + w);
+#pragma unroll
+                      for (int j = 0; j < 32; ++j)
+                        if (!(bits >> j & 1)) x[32 * w + j] = 0xff800000u;
+                    }
+                  }
+                  const float* const sc = scales + 64 * half;
+#pragma unroll
+                  for (int j = 0; j < 64; j += COARSE ? 16 : 1) {
+                    float most = __uint_as_float(x[j]);
+                    if constexpr (COARSE)
+#pragma unroll
+                      for (int i = 1; i < 16; ++i) most = fmaxf(most, __uint_as_float(x[j + i]));
+                    // (a factor of 0 would make NaN of what is not seen)
+                    if (most > -INFINITY) top = fmaxf(top, fmaf(most, sc[j] * row_factor, sc[KT + j]));
+                  }
+                }
+              }
+              if (m == -INFINITY) m = top;  // every weight so far was 0
+              const bool far = mr < rows && top - m > kRescale<DT>;
+              if (__any_sync(0xffffffffu, far)) {
+                // row by row: what the rows beside it do leaves a row's bits as they are
+                const float f = far ? exp2_fast(m - top) : 1.f;
+                if (ti > ti0) {  // O holds something
+                  if (!last_product()) break;
+                  uint32_t y[32];
+#pragma unroll 1
+                  for (int w = 0; w < D / 32; ++w) {
+                    tm_read(y, lanes + Sh::o_col(o) + 32 * w);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                    tm_store32(lanes + Sh::o_col(o) + 32 * w, y);
+                  }
+                  tm_wait_store();
+                }
+                l *= f;
+                if (far) m = top;
+              }
+              const float shift = m == -INFINITY ? 0.f : m - kBias<DT>;
+#pragma unroll 1
+              for (int w = KT / 32 - 1; w >= 0; --w) {
+                uint32_t x[32], y[16];
+                tm_read(x, lanes + Sh::s_col(buf) + 32 * w);
+                const unsigned bits = all ? 0xffffffffu : seen(w);
+                const float* const sc = scales + 32 * w;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; j += COARSE ? 16 : 4) {
+                  Pair part[2] = {0, 0};
+                  float4 f4, v4;
+                  float inv = 0.f;
+                  if constexpr (COARSE) {
+                    const float f = sc[j] * row_factor, v = sc[KT + j] - shift;
+                    f4 = make_float4(f, f, f, f);
+                    v4 = make_float4(v, v, v, v);
+                    inv = sc[2 * KT + j];
+                  } else {
+                    f4 = *reinterpret_cast<const float4*>(sc + j);
+                    v4 = *reinterpret_cast<const float4*>(sc + KT + j);
+                    f4 = make_float4(f4.x * row_factor, f4.y * row_factor, f4.z * row_factor, f4.w * row_factor);
+                    v4 = make_float4(v4.x - shift, v4.y - shift, v4.z - shift, v4.w - shift);
+                  }
+#pragma unroll
+                  for (int i = j; i < j + (COARSE ? 16 : 4); i += 2) {
+                    const bool second = !COARSE && (i & 2);
+                    float2 z = split(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), second ? pair(f4.z, f4.w) : pair(f4.x, f4.y),
+                                          second ? pair(v4.z, v4.w) : pair(v4.x, v4.y)));
+                    if (!all) {
+                      if (!(bits >> i & 1)) z.x = -INFINITY;
+                      if (!(bits >> (i + 1) & 1)) z.y = -INFINITY;
+                    }
+                    const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                    y[i / 2] = pack2<DT>(e0, e1);
+                    if constexpr (COARSE) {
+                      part[i / 2 & 1] = add2(part[i / 2 & 1], pair(e0, e1));
+                    } else {
+                      const float2 iv = *reinterpret_cast<const float2*>(sc + 2 * KT + i);
+                      part[i / 2 & 1] = mul2(pair(e0, e1), pair(iv));
+                    }
+                  }
+                  const float2 both = split(add2(part[0], part[1]));
+                  sum = COARSE ? fmaf(both.x + both.y, inv, sum) : sum + (both.x + both.y);
+                }
+                l += sum;
+                tm_store16(lanes + Sh::p_col(buf) + 16 * w, y);
+                if (w == 2 && Sh::PARTS > 1) hand_over(1);
+              }
+            } else {
             uint32_t x[64];
-            const float4* const scales = reinterpret_cast<const float4*>(sm_scale + ((tile_seq + ti) & (Sh::kRing - 1)) * 3 * KT);
-            const auto scaled = [](uint32_t* x, Pair factor, Pair more) {
-              const float2 y = split(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), factor, more));
-              x[0] = __float_as_uint(y.x);
-              x[1] = __float_as_uint(y.y);
-            };
             const auto fetch = [&](int half) {
               const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
               tm_load(x, at);
@@ -1246,24 +1348,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               tm_wait();
               ready(x);
               ready(x + 32);
-              if constexpr (Q8) {
-                // to powers of two with the value's scale in them: s * key's scale * row's factor +
-                // log2(value's scale)
-#pragma unroll
-                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {
-                  const float4* const ks = scales + (64 * half + j) / 4;
-                  if constexpr (COARSE) {
-                    const float f = ks->x * row_factor, lv = ks[KT / 4].x;
-                    const Pair f2 = pair(f, f), lv2 = pair(lv, lv);
-#pragma unroll
-                    for (int i = j; i < j + 16; i += 2) scaled(x + i, f2, lv2);
-                  } else {
-                    const float4 s = *ks, lv = ks[KT / 4];
-                    scaled(x + j, pair(s.x * row_factor, s.y * row_factor), pair(lv.x, lv.y));
-                    scaled(x + j + 2, pair(s.z * row_factor, s.w * row_factor), pair(lv.z, lv.w));
-                  }
-                }
-              }
               if (!all) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
@@ -1315,29 +1399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               const float shift = m == -INFINITY ? 0.f : fmaf(m, c, -kBias<DT>);
               const Pair shift2 = pair(-shift, -shift);
-              if constexpr (Q8) {
-#pragma unroll
-                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {  // the sum is of the weights without the values' scales
-                  const float4* const iv = scales + 2 * (KT / 4) + (64 * half + j) / 4;
-                  const auto weights = [&](int i, Pair inv, Pair& sum) {
-                    const float2 z = split(add2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), shift2));
-                    const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                    sum = COARSE ? add2(sum, pair(e0, e1)) : fma2(pair(e0, e1), inv, sum);
-                    y[i / 2] = pack2<DT>(e0, e1);
-                  };
-                  if constexpr (COARSE) {
-                    Pair part[2] = {0, 0};
-#pragma unroll
-                    for (int i = j; i < j + 16; i += 2) weights(i, 0, part[i / 2 & 1]);
-                    const float inv = iv->x;
-                    sums[0] = fma2(add2(part[0], part[1]), pair(inv, inv), sums[0]);
-                  } else {
-                    const float4 v = *iv;
-                    weights(j, pair(v.x, v.y), sums[0]);
-                    weights(j + 2, pair(v.z, v.w), sums[1]);
-                  }
-                }
-              } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float2 z = split(fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, shift2));
@@ -1345,12 +1406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sums[j & 1] = add2(sums[j & 1], pair(e0, e1));
                 y[j] = pack2<DT>(e0, e1);
               }
-              }
             }
             if (!ok) break;
             tm_store32(lanes + Sh::p_col(buf), y);
             const float2 sum = split(add2(sums[0], sums[1]));
             l += sum.x + sum.y;
+            }
           } else if (KT == 128) {
             hand_over(1);
           }
@@ -1658,7 +1719,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps =
   p.nslot = (kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - p.nq * Sh::kQ) / Sh::kSlot;
   if (p.nslot > kMaxSlots) p.nslot = kMaxSlots;
   static_assert(kMaxSlots / 2 + 1 <= 8, "holes");
-  if (kQ8<A> && p.nslot > 2 * Sh::kRing - 2) p.nslot = 2 * Sh::kRing - 2;
+  if (kQ8<A> && p.nslot > 2 * Sh::kRing - 3) p.nslot = 2 * Sh::kRing - 3;
   static_assert((kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - Sh::NS * Sh::kQ) / Sh::kSlot >= (kQ8<A> ? 3 : 4), "ring");
   static thread_local int ready = -1;  // device whose shared-memory limit this thread has set
   int dev = 0;
@@ -1670,7 +1731,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps =
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < kMaxBlocks ? sms : kMaxBlocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
