@@ -74,7 +74,7 @@ inline std::atomic<unsigned long long> g_attention_wait_ns{2000000000ull};
 namespace {
 
 constexpr int kTree = 64;
-constexpr int kSoftmaxThreads = 256, kProducers = 3, kConverters = 6;
+constexpr int kSoftmaxThreads = 256, kProducers = 3, kConverters = 3;  // (of keys, and as many of values)
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 // Weights are 2^(score - maximum + kBias), and a maximum may lag 2^kRescale behind.  fp16 has few
@@ -502,6 +502,7 @@ __device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps
     if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
     const int len = wk.q.ctx + wk.q.n;
     const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
+    const long long scale_at = wk.h * a.cache.scale_head_stride;
     if (!(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {        // who shares this head: read when the unit ends
       const int at = ct.w1 - wk.left - wk.p0 + kUnit;  // the place of the head's first tile
       const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
@@ -518,6 +519,7 @@ __device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps
       }
     };
     const auto page_of = [&](int t, int r) { return pages[((t & 1) * WORDS * 32) + (p.box ? r >> 3 : r)]; };
+    int box_page = 0, box_row = 0;  // of this lane's box
     const auto ask = [&](int t, bool values) {  // the next stage: keys or values of tile t, whose pages are there
       ok = __all_sync(0xffffffffu, bar_wait(&ct.raw_empty[stage], ph, ct, a.dev_status));
       if (!ok) return;
@@ -527,13 +529,8 @@ __device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps
         // (what lies past the end or has no page is asked for at a page that is not there: zeros)
         if (lane == 0) bar_expect(full, Sh::kRaw);
         __syncwarp();
-        const int r = lane * 8, pos = t * KT + r;
-        if (r < KT && r % p.box == 0) {
-          const int page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
-          const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
-          copy_box(dst + r * D, values ? &maps.v : &maps.k, p.head_first ? wk.h : in_page, p.head_first ? in_page : wk.h,
-                   good ? page : a.cache.n_pages, full);
-        }
+        if (lane * 8 < KT && lane * 8 % p.box == 0)
+          copy_box(dst + lane * 8 * D, values ? &maps.v : &maps.k, p.head_first ? wk.h : box_row, p.head_first ? box_row : wk.h, box_page, full);
       } else {
         const uint8_t* const base = static_cast<const uint8_t*>(values ? a.cache.v : a.cache.k) + wk.h * a.cache.head_stride + lane % CC * 16;
 #pragma unroll 2
@@ -551,20 +548,21 @@ __device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps
         ph ^= 1;
       }
     };
+    // Scales stand for runs of the block's tokens, 16 at most: keys' first, then values'.
+    const int run_log = min(p.block_shift, 4), runs = KT >> run_log;
     const auto ask_tile = [&](int t, int tile) {  // tile t of the head, the block's tile-th
-#pragma unroll
-      for (int j = 0; j < (COARSE ? 1 : WORDS); ++j) {
-        const int r = COARSE ? lane * 16 : j * 32 + lane, pos = t * KT + r;
-        if (r < KT) {
-          const int page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
-          const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
-          const long long sc = good ? page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride +
-                                          wk.h * a.cache.scale_head_stride
-                                    : 0;
-          const uint32_t to = looked0 + (Sh::kPages + (tile & 1) * 2 * KT + r) * 4;
-          copy4(to, a.cache.k_scale + sc, good);
-          copy4(to + KT * 4, a.cache.v_scale + sc, good);
-        }
+#pragma unroll 1
+      for (int i = lane; i < 2 * runs; i += 32) {
+        const int r = (i < runs ? i : i - runs) << run_log, pos = t * KT + r;
+        const int page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
+        const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
+        const long long sc = good ? page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at : 0;
+        copy4(looked0 + (Sh::kPages + (tile & 1) * 2 * KT + i) * 4, (i < runs ? a.cache.k_scale : a.cache.v_scale) + sc, good);
+      }
+      if (p.box) {
+        const int pos = t * KT + lane * 8, page = lane * 8 < KT ? page_of(t, lane * 8) : -1;
+        box_page = pos < len && page >= 0 && page < a.cache.n_pages ? page : a.cache.n_pages;
+        box_row = pos - column(pos) * a.cache.page_size;
       }
       if (t + 1 < wk.t1) look(t + 1);
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -576,31 +574,50 @@ __device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps
     const auto write_down = [&](int t) {
       const volatile float* const rs = raw_scale + (tile_seq & 1) * 2 * KT;
       float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
-      unsigned missing = 0, any = 0, gone = 0;
-#pragma unroll
-      for (int j = 0; j < WORDS; ++j) {
-        const int r = j * 32 + lane, pos = t * KT + r, page = page_of(t, r);
-        const bool there = pos < len, good = there && page >= 0 && page < a.cache.n_pages;
-        const unsigned m = __ballot_sync(0xffffffffu, there && !good);
-        const float vs = value_scale(rs[KT + (COARSE ? r & ~15 : r)], flags);
-        const unsigned g = __ballot_sync(0xffffffffu, !there || !good || vs == 0.f);
-        missing = lane == j ? m : missing;
-        gone = lane == j ? g : gone;
-        any |= m;
-        if (!COARSE || (r & 15) == 0) {
-          const float ks = scale_of(rs[r], flags);
-          float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
-          asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
-          asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
-          sc[r] = ks;
-          sc[KT + r] = vs == 0.f ? 0.f : log;  // values of scale 0 are zeros at scale 1
-          sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
+      const int left = len - t * KT;  // rows up to the end
+      unsigned missing = 0, gone = 0;  // of the word that this lane writes
+      if (p.box && run_log >= 3) {
+        // by runs of 8 rows, a bit each, which are spread to a byte
+        const int r = lane * 8;
+        const bool here = r < KT, there = here && r < left;
+        const int page = here ? page_of(t, r) : 0;
+        const bool good = there && page >= 0 && page < a.cache.n_pages;
+        unsigned seen = 0;  // (reported where the scales are written)
+        const float vs = good ? value_scale(rs[runs + (r >> run_log)], seen) : 0.f;
+        const auto spread = [&](unsigned m) {
+          m = m >> (4 * lane & 31) & 15;
+          return ((m | m << 7 | m << 14 | m << 21) & 0x01010101u) * 0xffu;
+        };
+        missing = spread(__ballot_sync(0xffffffffu, there && !good));
+        gone = spread(__ballot_sync(0xffffffffu, here && vs == 0.f));
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < WORDS; ++j) {
+          const int r = j * 32 + lane, page = page_of(t, r);
+          const bool there = r < left, good = there && page >= 0 && page < a.cache.n_pages;
+          unsigned seen = 0;
+          const float vs = good ? value_scale(rs[runs + (r >> run_log)], seen) : 0.f;
+          const unsigned m = __ballot_sync(0xffffffffu, there && !good), g = __ballot_sync(0xffffffffu, vs == 0.f);
+          missing = lane == j ? m : missing;
+          gone = lane == j ? g : gone;
         }
       }
-      if (any) flags |= MOE_DEV_INDEX;
       if (lane < WORDS) {
+        const int n = left - 32 * lane;  // (of a run that the end cuts)
+        if (n < 32) gone |= n <= 0 ? 0xffffffffu : ~0u << n;
         ct.hole[tile_seq & 7][lane] = missing;
         ct.gone[tile_seq & 7][lane] = gone;
+        if (missing) flags |= MOE_DEV_INDEX;
+      }
+#pragma unroll 1
+      for (int r = COARSE ? lane * 16 : lane; r < KT; r += COARSE ? KT : 32) {
+        const float ks = scale_of(rs[r >> run_log], flags), vs = value_scale(rs[runs + (r >> run_log)], flags);
+        float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
+        asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
+        sc[r] = ks;
+        sc[KT + r] = vs == 0.f ? 0.f : log;  // values of scale 0 are zeros at scale 1
+        sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
       }
     };
     look(wk.t0);
@@ -622,11 +639,11 @@ __device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps
     bar_drain(&ct.raw_full[(asked - i) % Sh::kRawStages], (asked - i) / Sh::kRawStages & 1, a.dev_status);
 }
 
-// The converters: each turns a sixth of a tile's rows into fp16, 16 codes a lane and step, in the
-// 128-byte swizzle that the tensor cores read.
+// The converters, three for keys and three for values: each turns a third of their rows into fp16, 16
+// codes a lane and step, in the 128-byte swizzle that the tensor cores read.
 template <typename A, int FMT, int D>
 __device__ __forceinline__ void convert_codes(const A& a, const Plan& p, Control& ct, unsigned char* sm_kv, unsigned char* sm_raw,
-                                              Walk<A, D>& wk, int cw, int member) {
+                                              Walk<A, D>& wk, bool values, int cw, int member) {
   using Sh = Shape<A, D>;
   constexpr int KT = Sh::KT, CC = Sh::CC, RPI = Sh::RPI, WORDS = KT / 32, STEPS = (KT / RPI + kConverters - 1) / kConverters;
   constexpr uint32_t kBlk = KT * 128;
@@ -635,8 +652,8 @@ __device__ __forceinline__ void convert_codes(const A& a, const Plan& p, Control
   // lanes whose block of 64 elements is an odd one write their second eight first, so that the eight lanes
   // of a store meet eight different banks of the swizzle
   const int odd = CC > 4 ? chunk >> 2 & 1 : 0;
-  int slot = 0, tile_seq = 0, stage = 0;
-  uint32_t phase = 1, ph = 0;  // slots start empty
+  int slot = values, tile_seq = 0, stage = values;  // keys and values take turns in both rings
+  uint32_t phase = 1, ph = 0;                       // slots start empty
   bool ok = true;
   const auto wait = [&](unsigned long long* b, uint32_t parity) {
     ok = __all_sync(0xffffffffu, bar_wait(b, parity, ct, a.dev_status));
@@ -644,14 +661,44 @@ __device__ __forceinline__ void convert_codes(const A& a, const Plan& p, Control
   };
   for (int seq = 0; ok && wk.more(); wk.next(a)) {
     if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
-    const auto put = [&](int slot) {  // the next stage's codes into a slot
-      const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
-      const unsigned char* const src = sm_raw + stage * Sh::kRaw + cw * 512 + lane * 16;
+#pragma unroll 1
+    for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
+      if (!wait(&ct.known[tile_seq & 1], tile_seq >> 1 & 1)) break;
+      if (!wait(&ct.raw_full[stage], ph)) break;
+      unsigned char* const src = sm_raw + stage * Sh::kRaw + cw * 512 + lane * 16;
+      if (values) {
+        // Values that are not there are zeros, and so are, in drafted rows, codes that are NaN: those are
+        // noted, and added at the end to the rows that see them.
+        unsigned gone = 0;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) gone |= *(volatile unsigned*)&ct.gone[tile_seq & 7][w];
+        const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+        if (gone || (FMT == MOE_E4M3 && node0 < KT)) {
+#pragma unroll 1
+          for (int k = 0; k < STEPS; ++k) {
+            const int r = (k * kConverters + cw) * RPI + sub;
+            if (r >= KT) break;
+            uint4* const v = reinterpret_cast<uint4*>(src + k * kConverters * 512);
+            if (ct.gone[tile_seq & 7][r >> 5] >> (r & 31) & 1) {
+              *v = make_uint4(0, 0, 0, 0);
+            } else if (FMT == MOE_E4M3 && r >= node0) {
+              const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
+              if (n.x | n.y | n.z | n.w) {
+                *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+                atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
       uint4 x[STEPS];  // (all loads ahead of the stores)
 #pragma unroll
       for (int k = 0; k < STEPS; ++k)
         if ((k + 1) * kConverters <= KT / RPI || k * kConverters + cw < KT / RPI)
           x[k] = *reinterpret_cast<const uint4*>(src + k * kConverters * 512);
+      if (!wait(&ct.empty[slot], phase)) break;
+      const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) {
         const int g = k * kConverters + cw, r = g * RPI + sub;
@@ -669,46 +716,11 @@ __device__ __forceinline__ void convert_codes(const A& a, const Plan& p, Control
         bar_arrive(&ct.full[slot]);
         bar_arrive(&ct.raw_empty[stage]);
       }
-      if (++stage == Sh::kRawStages) {
-        stage = 0;
+      stage += 2;
+      if (stage >= Sh::kRawStages) {
+        stage -= Sh::kRawStages;
         ph ^= 1;
       }
-    };
-    // Values that are not there are zeros, and so are, in drafted rows, codes that are NaN: those are
-    // noted, and added at the end to the rows that see them.
-    const auto clean = [&](int node0) {
-      unsigned char* const src = sm_raw + stage * Sh::kRaw + cw * 512 + lane * 16;
-#pragma unroll 1
-      for (int k = 0; k < STEPS; ++k) {
-        const int r = (k * kConverters + cw) * RPI + sub;
-        if (r >= KT) break;
-        uint4* const v = reinterpret_cast<uint4*>(src + k * kConverters * 512);
-        if (ct.gone[tile_seq & 7][r >> 5] >> (r & 31) & 1) {
-          *v = make_uint4(0, 0, 0, 0);
-        } else if (FMT == MOE_E4M3 && r >= node0) {
-          const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
-          if (n.x | n.y | n.z | n.w) {
-            *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-            atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
-          }
-        }
-      }
-      __syncwarp();
-    };
-    for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
-      const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
-      if (!wait(&ct.known[tile_seq & 1], tile_seq >> 1 & 1)) break;
-      if (!wait(&ct.raw_full[stage], ph)) break;
-      if (!wait(&ct.empty[slot], phase)) break;
-      put(slot);
-      unsigned gone = 0;
-#pragma unroll
-      for (int w = 0; w < WORDS; ++w) gone |= *(volatile unsigned*)&ct.gone[tile_seq & 7][w];
-      if (!wait(&ct.raw_full[stage], ph)) break;
-      if (!wait(&ct.empty[v_slot], phase ^ (v_slot == 0))) break;
-      const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
-      if (gone || (FMT == MOE_E4M3 && node0 < KT)) clean(node0);
-      put(v_slot);
       slot += 2;
       if (slot >= p.nslot) {
         slot -= p.nslot;
@@ -856,7 +868,7 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
   if (Q8 ? warp >= 8 && warp != 10 : warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
       if (warp == 8) load_codes<A, FMT, D, COARSE>(a, p, maps, ct, sm_raw, sm_scale, sm_looked, wk, member, flags);
-      else convert_codes<A, FMT, D>(a, p, ct, sm_kv, sm_raw, wk, warp == 9 ? 0 : warp - 10, member);
+      else convert_codes<A, FMT, D>(a, p, ct, sm_kv, sm_raw, wk, warp >= 13, warp == 9 ? 0 : (warp - 10) % 3, member);
     } else {
     // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
     // g = k * kProducers + its number
@@ -1238,37 +1250,48 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
               // time, then weights, 32 at a time and the last keys first: that needs fewer registers than
               // the way below, so that there is room for converters.
               const float* const scales = sm_scale + ((tile_seq + ti) & (Sh::kRing - 1)) * 3 * KT;
+              const uint32_t s_at = lanes + Sh::s_col(buf);
               float top = -INFINITY;
-              {
-                uint32_t x[64];
-#pragma unroll 1
-                for (int half = 0; half < Sh::PARTS; ++half) {
-                  const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
-                  tm_load(x, at);
-                  tm_load(x + 32, at + 32);
-                  tm_wait();
-                  ready(x);
-                  ready(x + 32);
-                  if (!all) {
+              uint32_t x[32], ahead[32];
+              const auto most_of = [&](uint32_t (&x)[32], int w) {
+                if (!all) {
+                  const unsigned bits = seen(w);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                      const unsigned bits = seen(2 * half + w);
+                  for (int j = 0; j < 32; ++j)
+                    if (!(bits >> j & 1)) x[j] = 0xff800000u;
+                }
+                const float* const sc = scales + 32 * w;
 #pragma unroll
-                      for (int j = 0; j < 32; ++j)
-                        if (!(bits >> j & 1)) x[32 * w + j] = 0xff800000u;
-                    }
-                  }
-                  const float* const sc = scales + 64 * half;
-#pragma unroll
-                  for (int j = 0; j < 64; j += COARSE ? 16 : 1) {
+                for (int j = 0; j < 32; j += COARSE ? 16 : 4) {
+                  if constexpr (COARSE) {
                     float most = __uint_as_float(x[j]);
-                    if constexpr (COARSE)
 #pragma unroll
-                      for (int i = 1; i < 16; ++i) most = fmaxf(most, __uint_as_float(x[j + i]));
+                    for (int i = 1; i < 16; ++i) most = fmaxf(most, __uint_as_float(x[j + i]));
                     // (a factor of 0 would make NaN of what is not seen)
                     if (most > -INFINITY) top = fmaxf(top, fmaf(most, sc[j] * row_factor, sc[KT + j]));
+                  } else {
+                    const float4 f = *reinterpret_cast<const float4*>(sc + j), v = *reinterpret_cast<const float4*>(sc + KT + j);
+                    const float f_of[4] = {f.x, f.y, f.z, f.w}, v_of[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const float s = __uint_as_float(x[j + i]);
+                      if (s > -INFINITY) top = fmaxf(top, fmaf(s, f_of[i] * row_factor, v_of[i]));
+                    }
                   }
                 }
+              };
+              // (the next 32 on their way while these are gone through)
+              tm_read(x, s_at);
+#pragma unroll 1
+              for (int w = 0; w < KT / 32; w += 2) {
+                tm_load(ahead, s_at + 32 * (w + 1));
+                most_of(x, w);
+                tm_wait();
+                ready(ahead);
+                tm_load(x, s_at + 32 * (w + 2 < KT / 32 ? w + 2 : KT / 32 - 1));  // (the last: for the weights)
+                most_of(ahead, w + 1);
+                tm_wait();
+                ready(x);
               }
               if (m == -INFINITY) m = top;  // every weight so far was 0
               const bool far = mr < rows && top - m > kRescale<DT>;
@@ -1291,10 +1314,8 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
                 if (far) m = top;
               }
               const float shift = m == -INFINITY ? 0.f : m - kBias<DT>;
-#pragma unroll 1
-              for (int w = KT / 32 - 1; w >= 0; --w) {
-                uint32_t x[32], y[16];
-                tm_read(x, lanes + Sh::s_col(buf) + 32 * w);
+              const auto weigh = [&](uint32_t (&x)[32], int w) {
+                uint32_t y[16];
                 const unsigned bits = all ? 0xffffffffu : seen(w);
                 const float* const sc = scales + 32 * w;
                 float sum = 0.f;
@@ -1337,7 +1358,18 @@ __global__ void __launch_bounds__(Shape<A, D>::kThreads, 1)
                 }
                 l += sum;
                 tm_store16(lanes + Sh::p_col(buf) + 16 * w, y);
-                if (w == 2 && Sh::PARTS > 1) hand_over(1);
+              };
+#pragma unroll 1
+              for (int w = KT / 32 - 1; w > 0; w -= 2) {
+                tm_load(ahead, s_at + 32 * (w - 1));
+                weigh(x, w);
+                tm_wait();
+                ready(ahead);
+                if (w > 1) tm_load(x, s_at + 32 * (w - 2));
+                weigh(ahead, w - 1);
+                tm_wait();
+                ready(x);
+                if (w > 1) hand_over(1);
               }
             } else {
             uint32_t x[64];
