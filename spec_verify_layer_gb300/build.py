@@ -11,7 +11,7 @@ SOURCES = [os.path.join(HERE, "csrc", f) for f in ("moe_verify.cu", "moe_prefill
                                                   "moe_tree_attn.cu", "moe_logprob.cu", "moe_cache8.cu", "moe_cache8_attn.cu",
                                                   "moe_verify_drafts.cu", "moe_host.cpp")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("moe_internal.h", "moe_common.cuh", "moe_round_ops.cuh", "moe_vocab.cuh",
-                                                  "moe_tree_attn.cuh")] + [
+                                                  "moe_attn_parts.cuh", "moe_few_rows.cuh", "moe_tree_attn.cuh")] + [
     os.path.join(ROOT, "include", "moe_verify.h")]
 OUT = os.path.join(HERE, "libmoeverify.so")
 

@@ -51,6 +51,21 @@ int choose(const moe_tree_attention8_args& a, Plan p, int sms, cudaStream_t st) 
     p.head_first = a.cache.head_stride < a.cache.slot_stride;
     if (!encode(&maps.k, a.cache.k, a, p.box, p.head_first) || !encode(&maps.v, a.cache.v, a, p.box, p.head_first)) p.box = 0;
   }
+  // Few query rows a head: products of codes in registers.  (64 requests of one row and 8 heads a key, up to
+  // 8,192 keys: FEW_A us against FEW_B.)
+  const int rows = a.max_tree * p.group, nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 && a.head_dim < 256 ? 4 : 0;
+  if (nt) {
+    const auto few = [&](auto d, auto n) { return launch<A, FMT, decltype(d)::value, false, decltype(n)::value>(a, p, sms, st); };
+    using I = std::integral_constant<int, 64>;
+    using J = std::integral_constant<int, 128>;
+    using K = std::integral_constant<int, 256>;
+    std::integral_constant<int, 1> one;
+    std::integral_constant<int, 2> two;
+    std::integral_constant<int, 4> four;
+    if (a.head_dim == 64) return nt == 1 ? few(I{}, one) : nt == 2 ? few(I{}, two) : few(I{}, four);
+    if (a.head_dim == 128) return nt == 1 ? few(J{}, one) : nt == 2 ? few(J{}, two) : few(J{}, four);
+    return nt == 1 ? few(K{}, one) : few(K{}, two);
+  }
   switch (a.head_dim) {
     case 64: return coarse ? launch<A, FMT, 64, true>(a, p, sms, st, maps) : launch<A, FMT, 64, false>(a, p, sms, st, maps);
     case 128: return coarse ? launch<A, FMT, 128, true>(a, p, sms, st, maps) : launch<A, FMT, 128, false>(a, p, sms, st, maps);
