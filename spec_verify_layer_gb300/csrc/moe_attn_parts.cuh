@@ -2,8 +2,6 @@
 // the list of work and its shares, the plan, codes of a cache in 8 bits.
 #pragma once
 
-#include <cuda.h>
-
 #include <atomic>
 #include <type_traits>
 
@@ -16,7 +14,8 @@ inline std::atomic<unsigned long long> g_attention_wait_ns{2000000000ull};
 namespace {
 
 constexpr int kTree = 64;
-constexpr int kSoftmaxThreads = 256, kProducers = 3, kConverters = 3;  // (of keys, and as many of values)
+constexpr int kThreads = 384;  // 8 softmax warps, 3 producer warps, 1 issuing warp: 168 registers a thread
+constexpr int kSoftmaxThreads = 256, kProducers = 3;
 constexpr int kMaxBlocks = 160;         // workspace sizing; the launch takes min(SM count, this)
 constexpr int kMaxSlots = 10;
 // Weights are 2^(score - maximum + kBias), and a maximum may lag 2^kRescale behind.  fp16 has few
@@ -43,9 +42,6 @@ constexpr bool kQ8 = std::is_same_v<A, moe_tree_attention8_args>;
 
 template <typename A, int D>
 struct Shape {
-  // 8 softmax warps, 1 issuing warp, and 3 producer warps (168 registers a thread) or, of codes, 1 loader
-  // and 6 converters (128 registers)
-  static constexpr int kThreads = kQ8<A> ? 512 : 384;
   static constexpr int KT = kKeyTile<D>;
   static constexpr int NS = D == 256 ? 1 : 2;          // streams (tensor memory holds 512 columns)
   static constexpr int PARTS = KT / 64;                // the weights are handed over 64 keys at a time
@@ -56,14 +52,15 @@ struct Shape {
   static constexpr int CC = kQ8<A> ? D / 16 : D / 8;   // and of a cached row
   static constexpr int RPI = 32 / CC;                  // rows that a warp copies with one instruction
   static constexpr int STEPS = (KT / RPI + kProducers - 1) / kProducers;  // instructions of a producer for a tile
-  // Codes: stages of raw codes, a tile's keys or values each; scale of the key, logarithm and reciprocal of
-  // the value's scale, of each key of kRing tiles (a tile's are written when its slot of keys is free, up
-  // to half the slots ahead of the softmax); a factor a query row; and, of two tiles, pages and raw
-  // scales as they were looked up.
+  // Codes: scale of the key, logarithm and reciprocal of the value's scale, of each key of kRing tiles (a
+  // tile's are written when its slot of keys is free, up to half the slots ahead of the softmax); a
+  // factor a query row; page and scales of the rows that a producer's lane looks up, twice; codes on
+  // their way, a stage for a tile's keys or values.
+  static constexpr int LOOKS = (STEPS * RPI + 31) / 32;  // rows of a producer that a lane looks up
   static constexpr int kRing = D == 64 ? 8 : 4;
   static constexpr int kRaw = KT * D, kRawStages = 3;
-  static constexpr int kPages = 2 * KT;
-  static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kPages + 2 * 2 * KT) * 4 + kRawStages * kRaw : 0;
+  static constexpr int kLooked = kProducers * 2 * 4 * LOOKS * 32;
+  static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kLooked) * 4 + kRawStages * kRaw : 0;
   // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
   // there is one stream); the weights, in 16 bits, go over the second half of their scores.
   __host__ __device__ static constexpr int s_col(int buf) { return NS == 2 ? 256 * buf : 64 * buf; }
@@ -83,8 +80,6 @@ struct Plan {  // host-computed, the same for every block
   float c;     // |scale| * log2(e); codes: 1 (scores are made powers of two key by key)
   float score; // codes: scale * log2(e), times what a code's fp16 number has to be multiplied with
   int block_shift;  // codes: log2 of the tokens of a block
-  int head_first;   // the tensor maps' order
-  int box;          // rows that a box of the tensor map has, 8 .. the tile's keys; 0: no boxes
   float4* part;      // [blocks][2: as Control::split][D / 4][part_rows]: a warp's rows side by side
   float2* part_ml;   // [blocks][2][part_rows]: maximum, sum
   unsigned* arrive;  // [blocks]
@@ -99,11 +94,9 @@ struct Split {  // a head that is split over blocks: its request's rows, its fir
 struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
-  unsigned long long raw_full[3], raw_empty[3], known[2];  // codes
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  unsigned gone[8][4];                // codes, per tile: rows whose values are zeros
-  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes: a bit a row)
-  int red[16], redn[16];
+  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows
+  int red[kThreads / 32], redn[kThreads / 32];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;
   int start_b, gangs, groups, gang, member;
@@ -149,11 +142,11 @@ __device__ __forceinline__ bool bar_wait(unsigned long long* b, uint32_t parity,
   if (bar_try(smem_u32(b), parity)) return true;
   return bar_wait_slow(smem_u32(b), parity, ct, status);
 }
-// The last wait, for products or copies in flight: they end by themselves, whatever other waits of the block
+// The last wait, for products in flight: they end by themselves, whatever other waits of the block
 // gave up, and until they have the block may neither free tensor memory nor leave.
-__device__ __forceinline__ void bar_drain(unsigned long long* b, uint32_t parity, unsigned* status) {
+__device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned* status) {
   const long long t0 = clock64();
-  while (!bar_try(smem_u32(b), parity)) {
+  while (!bar_try(smem_u32(b), 0)) {
     if (clock64() - t0 > (long long)kWaitNs * kCyclesPerNs) {
       atomicOr(status, MOE_DEV_TIMEOUT);
       return;
@@ -246,13 +239,6 @@ __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tm_store2(uint32_t addr, float x, float y) {

@@ -61,7 +61,7 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
 
 // A block's share of the list, unit after unit; all kFewWarps warps.
 template <typename A, int FMT, int D, int NT>
-__device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct, unsigned char* smem, Walk<A, D>& wk, unsigned& flags) {
+__device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct, unsigned char* smem, Walk<A, D>& wk, int member, unsigned& flags) {
   using F = FewShape<D, NT>;
   constexpr int KT = kKeyTile<D>, KS = F::KS, MT = KS / 16, CC = D / 16, STEPS = D / 16, OT = D / 16, RPI = 32 / CC, COPIES = KS / RPI;
   constexpr uint32_t kNone = 0xffffffffu;
@@ -85,7 +85,7 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
   const uint32_t page_units = (uint32_t)(a.cache.page_stride >> 4), slot_units = (uint32_t)(a.cache.slot_stride >> 4);
 
   for (int seq = 0; wk.more(); wk.next(a)) {
-    const int rows = wk.q.n * G;
+    const int m0 = member * F::ROWS, rows = min(F::ROWS, wk.q.n * G - m0);  // of the request's query rows
     if (rows <= 0 || wk.t0 == wk.t1) continue;
     const int len = wk.q.ctx + wk.q.n, k0 = wk.t0 * KT, k1 = min(len, wk.t1 * KT);
     const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
@@ -144,7 +144,7 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
     // The queries as the products take them, fp16 whatever their type: each row times the power of two
     // that brings its largest element to 2^14 .. 2^15, which the row's factor takes back.  An n-tile a warp.
     if (warp < NT) {
-      const int mi = min(warp * 8 + g, rows - 1), n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi;
+      const int mi = m0 + min(warp * 8 + g, rows - 1), n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi;
       const bool there = warp * 8 + g < rows, bf = a.dtype == MOE_BF16;
       const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (long long)(wk.q.s + n) * a.q_stride + (wk.h * G + mi - n * G) * D + t * 16;
       uint4 x[D / 64][2];
@@ -289,7 +289,7 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int mi = min(nt * 8 + 2 * t + e, rows - 1), n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi;
+                const int mi = m0 + min(nt * 8 + 2 * t + e, rows - 1), n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi;
                 const bool seen = there && (node < 0 || (a.tree_mask ? (__ldg(a.tree_mask + wk.q.s + n) >> (node & 63) & 1) != 0 : node <= n));
                 if (!seen) s[mt][nt][2 * h + e] = -INFINITY;
               }
@@ -405,15 +405,15 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
     const long long slot = (long long)blockIdx.x * 2 + part;
 #pragma unroll 1
     for (int i = tid; i < rows * (D / 4); i += kFewWarps * 32) {
-      const int mi = i / (D / 4), c4 = i % (D / 4), n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = wk.h * G + mi - n * G;
+      const int r = i / (D / 4), c4 = i % (D / 4), mi = m0 + r, n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = wk.h * G + mi - n * G;
       float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, ml[w * F::ROWS + mi].x);
+      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, ml[w * F::ROWS + r].x);
 #pragma unroll
       for (int w = 0; w < kFewWarps; ++w) {
-        const float2 v = ml[w * F::ROWS + mi];
+        const float2 v = ml[w * F::ROWS + r];
         const float f = v.x == -INFINITY ? 1.f : exp2_fast(v.x - top);  // nothing seen: zeros, or NaN that has to stay
-        const float4 y = *reinterpret_cast<const float4*>(sums + (w * F::ROWS + mi) * F::kPitch + c4 * 4);
+        const float4 y = *reinterpret_cast<const float4*>(sums + (w * F::ROWS + r) * F::kPitch + c4 * 4);
         total = fmaf(v.y, f, total);
         x[0] = fmaf(y.x, f, x[0]);
         x[1] = fmaf(y.y, f, x[1]);
@@ -442,13 +442,13 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
         if (c4 == 0 && a.lse)
           a.lse[(long long)(wk.q.s + n) * a.q_heads + head] = total == 0.f ? -INFINITY : (top - kBias<MOE_F16> + log2f(total)) * 0.6931471805599453f;
       } else {
-        __stcg(p.part + (slot * (D / 4) + c4) * p.part_rows + mi, make_float4(x[0], x[1], x[2], x[3]));
-        if (c4 == 0) __stcg(p.part_ml + slot * p.part_rows + mi, make_float2(top, total));
+        __stcg(p.part + (slot * (D / 4) + c4) * p.part_rows + r, make_float4(x[0], x[1], x[2], x[3]));
+        if (c4 == 0) __stcg(p.part_ml + slot * p.part_rows + r, make_float2(top, total));
       }
     }
     __syncthreads();
     if (!whole && tid == 0)  // releases what the block wrote before the barrier
-      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.arrive + ct.split[part].first) : "memory");
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.arrive + ct.split[part].first * ct.groups + member) : "memory");
     ++seq;
   }
 }

@@ -65,299 +65,27 @@
 namespace moe {
 namespace {
 
-// Codes come into a ring of raw stages, a tile's keys and values in turn; one warp asks for them, six turn
-// them into fp16.
-struct Maps {
-  CUtensorMap k, v;  // [page][head][slot][D], bytes; slot and head in the order of their strides
-};
-struct NoMaps {};
-template <typename A>
-using MapsOf = std::conditional_t<kQ8<A>, Maps, NoMaps>;
-
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int y, int z, int page, unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(0), "r"(y), "r"(z), "r"(page), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void bar_expect(unsigned long long* b, int bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bar_copies(unsigned long long* b) {  // an arrival when this thread's copies so far are there
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-// The loader: looks up pages (a tile ahead) and scales, asks for a tile's keys while the tile before is
-// worked on and for its values when a stage is free, and writes down what the softmax and the
-// converters have to know of the tile.  Where a page is a multiple of 8 rows (p.box) the rows of a
-// page come as boxes of a tensor map, otherwise by 16-byte copies.  All that it looks up are asynchronous
-// copies too: a register that waits for memory holds up every exchange and barrier behind it.
-template <typename A, int FMT, int D, bool COARSE>
-__device__ __forceinline__ void load_codes(const A& a, const Plan& p, const Maps& maps, Control& ct, unsigned char* sm_raw, float* sm_scale,
-                                           unsigned char* sm_looked, Walk<A, D>& wk, int member, unsigned& flags) {
-  using Sh = Shape<A, D>;
-  constexpr int KT = Sh::KT, WORDS = KT / 32, CC = Sh::CC;
-  const int lane = threadIdx.x & 31;
-  const uint32_t raw0 = smem_u32(sm_raw), looked0 = smem_u32(sm_looked);
-  volatile int* const pages = reinterpret_cast<volatile int*>(sm_looked);
-  volatile float* const raw_scale = reinterpret_cast<volatile float*>(sm_looked + Sh::kPages * 4);  // [2: tiles][keys, values][KT]
-  int tile_seq = 0, stage = 0, asked = 0;
-  uint32_t ph = 1;  // stages start empty
-  bool ok = true;
-  const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
-  for (; ok && wk.more(); wk.next(a)) {
-    if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
-    const int len = wk.q.ctx + wk.q.n;
-    const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-    const long long scale_at = wk.h * a.cache.scale_head_stride;
-    if (!(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {        // who shares this head: read when the unit ends
-      const int at = ct.w1 - wk.left - wk.p0 + kUnit;  // the place of the head's first tile
-      const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
-      if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
-    }
-    // pages are looked up of runs of 8 rows, a lane each, or (without boxes) of the rows lane, lane + 32 ...
-    const auto look = [&](int t) {
-#pragma unroll
-      for (int j = 0; j < WORDS; ++j) {
-        if (j > 0 && p.box) break;
-        const int r = p.box ? lane * 8 : j * 32 + lane, pos = t * KT + r;
-        const bool there = r < KT && pos < len;
-        copy4(looked0 + (((t & 1) * WORDS + j) * 32 + lane) * 4, table + (there ? column(pos) : 0), there);
-      }
-    };
-    const auto page_of = [&](int t, int r) { return pages[((t & 1) * WORDS * 32) + (p.box ? r >> 3 : r)]; };
-    int box_page = 0, box_row = 0;  // of this lane's box
-    const auto ask = [&](int t, bool values) {  // the next stage: keys or values of tile t, whose pages are there
-      ok = __all_sync(0xffffffffu, bar_wait(&ct.raw_empty[stage], ph, ct, a.dev_status));
-      if (!ok) return;
-      unsigned long long* const full = &ct.raw_full[stage];
-      const uint32_t dst = raw0 + stage * Sh::kRaw;
-      if (p.box) {
-        // (what lies past the end or has no page is asked for at a page that is not there: zeros)
-        if (lane == 0) bar_expect(full, Sh::kRaw);
-        __syncwarp();
-        if (lane * 8 < KT && lane * 8 % p.box == 0)
-          copy_box(dst + lane * 8 * D, values ? &maps.v : &maps.k, p.head_first ? wk.h : box_row, p.head_first ? box_row : wk.h, box_page, full);
-      } else {
-        const uint8_t* const base = static_cast<const uint8_t*>(values ? a.cache.v : a.cache.k) + wk.h * a.cache.head_stride + lane % CC * 16;
-#pragma unroll 2
-        for (int r = lane / CC; r < KT; r += 32 / CC) {
-          const int pos = t * KT + r, page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
-          const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
-          copy16(dst + r * D + lane % CC * 16, base + (good ? page * a.cache.page_stride + in_page * a.cache.slot_stride : 0), good);
-        }
-        bar_copies(full);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      ++asked;
-      if (++stage == Sh::kRawStages) {
-        stage = 0;
-        ph ^= 1;
-      }
-    };
-    // Scales stand for runs of the block's tokens, 16 at most: keys' first, then values'.
-    const int run_log = min(p.block_shift, 4), runs = KT >> run_log;
-    const auto ask_tile = [&](int t, int tile) {  // tile t of the head, the block's tile-th
-#pragma unroll 1
-      for (int i = lane; i < 2 * runs; i += 32) {
-        const int r = (i < runs ? i : i - runs) << run_log, pos = t * KT + r;
-        const int page = page_of(t, r), in_page = pos - column(pos) * a.cache.page_size;
-        const bool good = pos < len && page >= 0 && page < a.cache.n_pages;
-        const long long sc = good ? page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at : 0;
-        copy4(looked0 + (Sh::kPages + (tile & 1) * 2 * KT + i) * 4, (i < runs ? a.cache.k_scale : a.cache.v_scale) + sc, good);
-      }
-      if (p.box) {
-        const int pos = t * KT + lane * 8, page = lane * 8 < KT ? page_of(t, lane * 8) : -1;
-        box_page = pos < len && page >= 0 && page < a.cache.n_pages ? page : a.cache.n_pages;
-        box_row = pos - column(pos) * a.cache.page_size;
-      }
-      if (t + 1 < wk.t1) look(t + 1);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      ask(t, false);
-      if (ok) ask(t, true);
-    };
-    // scales as the softmax takes them, and the rows whose values are zeros: without a page, past the end,
-    // or of a scale that counts as 0
-    const auto write_down = [&](int t) {
-      const volatile float* const rs = raw_scale + (tile_seq & 1) * 2 * KT;
-      float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
-      const int left = len - t * KT;  // rows up to the end
-      unsigned missing = 0, gone = 0;  // of the word that this lane writes
-      if (p.box && run_log >= 3) {
-        // by runs of 8 rows, a bit each, which are spread to a byte
-        const int r = lane * 8;
-        const bool here = r < KT, there = here && r < left;
-        const int page = here ? page_of(t, r) : 0;
-        const bool good = there && page >= 0 && page < a.cache.n_pages;
-        unsigned seen = 0;  // (reported where the scales are written)
-        const float vs = good ? value_scale(rs[runs + (r >> run_log)], seen) : 0.f;
-        const auto spread = [&](unsigned m) {
-          m = m >> (4 * lane & 31) & 15;
-          return ((m | m << 7 | m << 14 | m << 21) & 0x01010101u) * 0xffu;
-        };
-        missing = spread(__ballot_sync(0xffffffffu, there && !good));
-        gone = spread(__ballot_sync(0xffffffffu, here && vs == 0.f));
-      } else {
-#pragma unroll 1
-        for (int j = 0; j < WORDS; ++j) {
-          const int r = j * 32 + lane, page = page_of(t, r);
-          const bool there = r < left, good = there && page >= 0 && page < a.cache.n_pages;
-          unsigned seen = 0;
-          const float vs = good ? value_scale(rs[runs + (r >> run_log)], seen) : 0.f;
-          const unsigned m = __ballot_sync(0xffffffffu, there && !good), g = __ballot_sync(0xffffffffu, vs == 0.f);
-          missing = lane == j ? m : missing;
-          gone = lane == j ? g : gone;
-        }
-      }
-      if (lane < WORDS) {
-        const int n = left - 32 * lane;  // (of a run that the end cuts)
-        if (n < 32) gone |= n <= 0 ? 0xffffffffu : ~0u << n;
-        ct.hole[tile_seq & 7][lane] = missing;
-        ct.gone[tile_seq & 7][lane] = gone;
-        if (missing) flags |= MOE_DEV_INDEX;
-      }
-#pragma unroll 1
-      for (int r = COARSE ? lane * 16 : lane; r < KT; r += COARSE ? KT : 32) {
-        const float ks = scale_of(rs[r >> run_log], flags), vs = value_scale(rs[runs + (r >> run_log)], flags);
-        float log, inv;  // (off by 2^-22 or so, in the weights' sum and in their products alike)
-        asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(vs));
-        sc[r] = ks;
-        sc[KT + r] = vs == 0.f ? 0.f : log;  // values of scale 0 are zeros at scale 1
-        sc[2 * KT + r] = vs == 0.f ? 1.f : inv;
-      }
-    };
-    look(wk.t0);
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncwarp();
-    ask_tile(wk.t0, tile_seq);
-    for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
-      asm volatile("cp.async.wait_group 2;" ::: "memory");  // all but the codes: this tile's scales and the next one's pages
-      __syncwarp();
-      write_down(t);
-      __syncwarp();
-      if (lane == 0) bar_arrive(&ct.known[tile_seq & 1]);
-      if (t + 1 < wk.t1) ask_tile(t + 1, tile_seq + 1);
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  // a wait that gave up: boxes in flight end by themselves, and the block does not leave before
-  for (int i = 1; !ok && i <= Sh::kRawStages && i <= asked; ++i)
-    bar_drain(&ct.raw_full[(asked - i) % Sh::kRawStages], (asked - i) / Sh::kRawStages & 1, a.dev_status);
-}
-
-// The converters, three for keys and three for values: each turns a third of their rows into fp16, 16
-// codes a lane and step, in the 128-byte swizzle that the tensor cores read.
-template <typename A, int FMT, int D>
-__device__ __forceinline__ void convert_codes(const A& a, const Plan& p, Control& ct, unsigned char* sm_kv, unsigned char* sm_raw,
-                                              Walk<A, D>& wk, bool values, int cw, int member) {
-  using Sh = Shape<A, D>;
-  constexpr int KT = Sh::KT, CC = Sh::CC, RPI = Sh::RPI, WORDS = KT / 32, STEPS = (KT / RPI + kConverters - 1) / kConverters;
-  constexpr uint32_t kBlk = KT * 128;
-  const int lane = threadIdx.x & 31, chunk = lane % CC, sub = lane / CC;
-  const uint32_t kv0 = smem_u32(sm_kv);
-  // lanes whose block of 64 elements is an odd one write their second eight first, so that the eight lanes
-  // of a store meet eight different banks of the swizzle
-  const int odd = CC > 4 ? chunk >> 2 & 1 : 0;
-  int slot = values, tile_seq = 0, stage = values;  // keys and values take turns in both rings
-  uint32_t phase = 1, ph = 0;                       // slots start empty
-  bool ok = true;
-  const auto wait = [&](unsigned long long* b, uint32_t parity) {
-    ok = __all_sync(0xffffffffu, bar_wait(b, parity, ct, a.dev_status));
-    return ok;
-  };
-  for (int seq = 0; ok && wk.more(); wk.next(a)) {
-    if (wk.q.n * p.group <= member * Sh::MG || wk.t0 == wk.t1) continue;
-#pragma unroll 1
-    for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
-      if (!wait(&ct.known[tile_seq & 1], tile_seq >> 1 & 1)) break;
-      if (!wait(&ct.raw_full[stage], ph)) break;
-      unsigned char* const src = sm_raw + stage * Sh::kRaw + cw * 512 + lane * 16;
-      if (values) {
-        // Values that are not there are zeros, and so are, in drafted rows, codes that are NaN: those are
-        // noted, and added at the end to the rows that see them.
-        unsigned gone = 0;
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) gone |= *(volatile unsigned*)&ct.gone[tile_seq & 7][w];
-        const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
-        if (gone || (FMT == MOE_E4M3 && node0 < KT)) {
-#pragma unroll 1
-          for (int k = 0; k < STEPS; ++k) {
-            const int r = (k * kConverters + cw) * RPI + sub;
-            if (r >= KT) break;
-            uint4* const v = reinterpret_cast<uint4*>(src + k * kConverters * 512);
-            if (ct.gone[tile_seq & 7][r >> 5] >> (r & 31) & 1) {
-              *v = make_uint4(0, 0, 0, 0);
-            } else if (FMT == MOE_E4M3 && r >= node0) {
-              const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
-              if (n.x | n.y | n.z | n.w) {
-                *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-                atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
-              }
-            }
-          }
-          __syncwarp();
-        }
-      }
-      uint4 x[STEPS];  // (all loads ahead of the stores)
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k)
-        if ((k + 1) * kConverters <= KT / RPI || k * kConverters + cw < KT / RPI)
-          x[k] = *reinterpret_cast<const uint4*>(src + k * kConverters * 512);
-      if (!wait(&ct.empty[slot], phase)) break;
-      const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        const int g = k * kConverters + cw, r = g * RPI + sub;
-        if ((k + 1) * kConverters <= KT / RPI || g < KT / RPI) {
-          const uint32_t to = dst + r * 128 + (((2 * (chunk & 3) + odd) ^ (r & 7)) << 4);
-          const uint4 lo = codes_to_half<FMT>(odd ? x[k].z : x[k].x, odd ? x[k].w : x[k].y);
-          const uint4 hi = codes_to_half<FMT>(odd ? x[k].x : x[k].z, odd ? x[k].y : x[k].w);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
-        }
-      }
-      fence_async();  // what the lanes wrote, before the tensor cores read it
-      __syncwarp();
-      if (lane == 0) {
-        bar_arrive(&ct.full[slot]);
-        bar_arrive(&ct.raw_empty[stage]);
-      }
-      stage += 2;
-      if (stage >= Sh::kRawStages) {
-        stage -= Sh::kRawStages;
-        ph ^= 1;
-      }
-      slot += 2;
-      if (slot >= p.nslot) {
-        slot -= p.nslot;
-        phase ^= 1;
-      }
-    }
-    ++seq;
-  }
-}
-
 // ---- the kernel -------------------------------------------------------------------------
 
 // FMT: the type of q, cache and out (16-bit cache), or of the codes.  COARSE: a scale stands for 16 keys or
-// more.  NT: codes, up to 8 NT query rows a head, without tensor memory; 0: with.
+// more.  NT: codes, groups of 8 NT query rows, without tensor memory; 0: with.
 template <typename A, int FMT, int D, bool COARSE, int NT>
-__global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThreads, 1)
-    k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p, const __grid_constant__ MapsOf<A> maps) {
+__global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : kThreads, 1)
+    k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p) {
   using Sh = Shape<A, D>;
   constexpr bool Q8 = kQ8<A>;
   constexpr int DT = Q8 ? MOE_F16 : FMT;  // of the products
-  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kThreads = NT > 0 ? kFewWarps * 32 : Sh::kThreads;
+  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kBlock = NT > 0 ? kFewWarps * 32 : kThreads;
+  constexpr int MG = NT > 0 ? 8 * NT : Sh::MG;  // query rows of a group
   constexpr uint32_t kBlk = KT * 128;  // bytes of a 64-element block of a key or value tile
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sm_q = smem;
   unsigned char* sm_kv = smem + (size_t)p.nq * Sh::kQ;
-  unsigned char* const sm_raw = sm_kv + (size_t)p.nslot * Sh::kSlot;
-  Control& ct = *reinterpret_cast<Control*>(NT > 0 ? smem + FewShape<D, NT>::kBytes : sm_raw + (Q8 ? Sh::kRawStages * Sh::kRaw : 0));
+  Control& ct = *reinterpret_cast<Control*>(NT > 0 ? smem + FewShape<D, NT>::kBytes : sm_kv + (size_t)p.nslot * Sh::kSlot);
   float* const sm_scale = reinterpret_cast<float*>(&ct + 1);  // [kRing][3][KT]
   float* const sm_row = sm_scale + Sh::kRing * 3 * KT;        // [256]
-  unsigned char* const sm_looked = reinterpret_cast<unsigned char*>(sm_row + 256);
+  unsigned char* const sm_looked = reinterpret_cast<unsigned char*>(sm_row + 256), *const sm_raw = sm_looked + Sh::kLooked * 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.group;
   const auto result2 = [&](float x, float y) {
@@ -382,7 +110,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == 11) {
     if (lane < p.nslot) {
-      bar_init(&ct.full[lane], Q8 ? kConverters : 33 * kProducers);  // a warp's copies, and what its first lane wrote
+      bar_init(&ct.full[lane], Q8 ? kProducers : 33 * kProducers);  // a warp's copies, and what its first lane wrote
       bar_init(&ct.empty[lane], 1);
     }
     if (lane < 4) bar_init(&ct.p_full[lane], 4);
@@ -393,13 +121,6 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
     if (lane == 0) {
       bar_init(&ct.q_ready, kSoftmaxThreads / 32);
       bar_init(&ct.drain, 1);
-      if constexpr (Q8) {
-        for (int i = 0; i < Sh::kRawStages; ++i) {
-          bar_init(&ct.raw_full[i], p.box ? 1 : 32);
-          bar_init(&ct.raw_empty[i], kConverters);
-        }
-        for (int i = 0; i < 2; ++i) bar_init(&ct.known[i], 1);
-      }
       ct.abort = 0;
       ct.wait_cycles = p.wait_cycles;
       ct.split[0].parts = ct.split[1].parts = 0;
@@ -425,7 +146,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
     __syncthreads();
     lo = total + incl - mine;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < kBlock / 32; ++i) {
       const int x = ct.red[i];
       if (i < warp) lo += x;
       total += x;
@@ -433,13 +154,13 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
     }
   };
   scan(0, first);
-  for (int b0 = kThreads; b0 < a.n_req; b0 += kThreads) {
+  for (int b0 = kBlock; b0 < a.n_req; b0 += kBlock) {
     Req q{0, 0, 0, 0};
     if (b0 + tid < a.n_req) q = request<D>(a, b0 + tid);
     scan(b0, q);
   }
   {
-    const int groups = max(1, (maxn * G + Sh::MG - 1) / Sh::MG);
+    const int groups = max(1, (maxn * G + MG - 1) / MG);
     const int gangs = min(total, max(1, (int)gridDim.x / groups));
     const int gang = (int)blockIdx.x / groups;
     const bool works = gang < gangs && groups <= (int)gridDim.x;
@@ -453,9 +174,9 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
       ct.gang = gang;
       ct.member = (int)blockIdx.x - gang * groups;
     }
-    if (works && a.n_req > kThreads) {  // the sums again, up to that request
+    if (works && a.n_req > kBlock) {  // the sums again, up to that request
       total = 0;
-      for (int b0 = 0; b0 < a.n_req && total <= w0; b0 += kThreads) {
+      for (int b0 = 0; b0 < a.n_req && total <= w0; b0 += kBlock) {
         __syncthreads();
         Req q{0, 0, 0, 0};
         if (b0 + tid < a.n_req) q = request<D>(a, b0 + tid);
@@ -483,7 +204,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
 #pragma unroll 1
     for (int which = 0; ok && which < 2; ++which) {
       const Split sp = ct.split[which];
-      const int m0 = member * Sh::MG, rows = min(Sh::MG, sp.n * G - m0);
+      const int m0 = member * MG, rows = min(MG, sp.n * G - m0);
       if (sp.parts == 0 || rows <= 0) continue;
       unsigned* arrive = p.arrive + sp.first * ct.groups + member;
       if (tid == 0) {
@@ -588,12 +309,227 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
   };
 
   if constexpr (NT > 0) {
-    few_rows<A, FMT, D, NT>(a, p, ct, smem, wk, flags);
+    few_rows<A, FMT, D, NT>(a, p, ct, smem, wk, member, flags);
     join_splits(true);
-  } else if (Q8 ? warp >= 8 && warp != 10 : warp == 8 || warp == 9 || warp == 11) {
+  } else if (warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
-      if (warp == 8) load_codes<A, FMT, D, COARSE>(a, p, maps, ct, sm_raw, sm_scale, sm_looked, wk, member, flags);
-      else convert_codes<A, FMT, D>(a, p, ct, sm_kv, sm_raw, wk, warp >= 13, warp == 9 ? 0 : (warp - 10) % 3, member);
+    // ---------------- producers of codes.  A warp's rows of a tile are dealt out as below, 16 codes
+    // a lane and step: they are copied into a ring of stages (keys and values of a tile in turn),
+    // read back by the lane that copied them, and written as fp16 into the tile's slot.  All that
+    // comes from memory comes by asynchronous copies, table entries and scales too: a register that
+    // waits for memory holds up every exchange and barrier behind it (they share few counters),
+    // 263 us against 438 with the codes in registers for 64 requests of one row over up to 8,192 keys
+    // with these in better and in worse order.
+    // Eight lanes side by side take four chunks each of two rows: their stores meet eight different
+    // banks of the swizzle.
+    constexpr int kBlocks = CC / 4;  // 64-element blocks of a row
+    const int pw = warp == 11 ? 2 : warp - 8, chunk = (lane & 3) | ((lane >> 3) & (kBlocks - 1)) << 2;
+    const int sub = (lane >> 2 & 1) | (lane / (8 * kBlocks)) << 1;
+    constexpr int LOOKS = Sh::LOOKS;
+    const auto row_of = [&](int j) {  // the j-th row that this lane looks up; KT and more: none
+      const int mine = 32 * j + lane;
+      return (mine / RPI * kProducers + pw) * RPI + mine % RPI;
+    };
+    constexpr uint32_t kNone = 0xffffffffu;
+    const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw) + lane * 16, looked0 = smem_u32(sm_looked);
+    const uint32_t page_units = (uint32_t)(a.cache.page_stride >> 4), slot_units = (uint32_t)(a.cache.slot_stride >> 4);
+    int slot = 0, tile_seq = 0, ask_stage = 0, put_stage = 0;
+    uint32_t phase = 1;  // the slots start empty
+    bool ok = true;
+    for (int seq = 0; ok && wk.more(); wk.next(a)) {
+      if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
+      const int len = wk.q.ctx + wk.q.n;
+      const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
+      const uint32_t head_units = (uint32_t)(wk.h * a.cache.head_stride >> 4);
+      const long long scale_at = wk.h * a.cache.scale_head_stride;
+      if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
+        const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
+        const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
+        if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
+      }
+      unsigned hole[2], next_hole[2] = {0, 0};
+      uint32_t at[LOOKS];  // in units of 16 bytes
+      // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
+      // scale.  COARSE: lanes 0 .. KT/8 - 1 look up the scale of keys, then of values, of a run of 16 keys
+      // each: its page (3) and scale (1).
+      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 4 + what) * LOOKS + j) * 32 + lane; };
+      const auto column = [&](int pos) { return (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift); };
+      const auto look_at = [&](int t, int r, int what, int j) {
+        const int pos = t * KT + r;
+        const bool there = r < KT && pos < len;
+        copy4(looked0 + looked(t, what, j) * 4, table + (there ? column(pos) : 0), there);
+      };
+      const int run = lane < KT / 8 ? (lane & (KT / 16 - 1)) * 16 : KT;
+      const auto look = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
+        if constexpr (COARSE) look_at(t, run, 3, 0);
+      };
+      const auto read = [&](int t, int what, int j) { return *reinterpret_cast<volatile int*>(sm_looked + looked(t, what, j) * 4); };
+      const auto scale_place = [&](int page, int in_page) {
+        return page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
+      };
+      const auto ask = [&](const void* base) {  // the tile that `at` is of, into the next stage
+        uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k)
+          from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
+        const uint32_t dst = raw0 + ask_stage * Sh::kRaw + pw * 512;
+        const uint4* const src = static_cast<const uint4*>(base) + chunk;
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k) {
+          const int g = k * kProducers + pw;
+          const bool there = from[k] != kNone;
+          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI)
+            copy16(dst + k * kProducers * 512, src + (there ? from[k] : 0), there);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++ask_stage == Sh::kRawStages) ask_stage = 0;
+      };
+      // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
+      const auto ask_keys = [&](int t) {
+        int page[LOOKS];
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) page[j] = read(t, 0, j);
+        if constexpr (COARSE) {
+          const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, run_page = read(t, 3, 0);
+          const bool good = run < KT && pos < len && run_page >= 0 && run_page < a.cache.n_pages;
+          copy4(looked0 + looked(t, 1, 0) * 4, (lane < KT / 16 ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(run_page, in_page) : 0), good);
+        }
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size;
+          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
+          // (below 2^32, so the product may be taken in 32 bits)
+          at[j] = good ? (uint32_t)page[j] * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
+          if constexpr (!COARSE) {
+            const long long sc = good ? scale_place(page[j], in_page) : 0;
+            copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
+            copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
+          }
+          next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
+        }
+        if (t + 1 < wk.t1) look(t + 1);
+        ask(a.cache.k);
+      };
+      const auto put = [&](int slot) {  // the next stage's codes into a slot
+        const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
+        const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+        uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k)
+          if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
+            x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
+#pragma unroll
+        for (int k = 0; k < Sh::STEPS; ++k) {
+          const int g = k * kProducers + pw, r = g * RPI + sub;
+          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
+            const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
+            const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+          }
+        }
+        if (++put_stage == Sh::kRawStages) put_stage = 0;
+      };
+      // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
+      // are noted, and added at the end to the rows that see them.
+      const auto clean = [&](const unsigned (&zero)[2], int node0) {
+        unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+#pragma unroll 1
+        for (int k = 0; k < Sh::STEPS; ++k) {
+          const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r >> 4 : k * RPI + sub;
+          if (r >= KT) break;
+          uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
+          if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
+          if (FMT == MOE_E4M3 && r >= node0) {
+            const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
+            if (n.x | n.y | n.z | n.w) {
+              *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+              atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
+            }
+          }
+        }
+      };
+      // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum
+      // and in their products alike); values of scale 0 are zeros at scale 1
+      const auto put_scale = [&](float* sc, float s, bool of_value) {
+        float log, inv;
+        asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(s));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        if (of_value) {
+          sc[KT] = s == 0.f ? 0.f : log;
+          sc[2 * KT] = s == 0.f ? 1.f : inv;
+        } else {
+          sc[0] = s;
+        }
+      };
+      const auto filled = [&](int slot) {  // what the lanes wrote, before the tensor cores read it
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&ct.full[slot]);
+      };
+      look(wk.t0);
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+      ask_keys(wk.t0);
+      ask(a.cache.v);
+      for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
+        const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
+        const bool more = t + 1 < wk.t1;
+        // keys, scales, and the next tile's pages are there; its values are on their way
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        hole[0] = next_hole[0];
+        hole[1] = next_hole[1];
+        float key[LOOKS], value[LOOKS];
+#pragma unroll
+        for (int j = 0; j < LOOKS; ++j) {
+          if (j == 0 || !COARSE) key[j] = __int_as_float(read(t, 1, j));
+          if (!COARSE) value[j] = __int_as_float(read(t, 2, j));
+        }
+        if (more) ask_keys(t + 1);
+        ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
+        if (!ok) break;
+        unsigned zero[2] = {0, 0};
+        float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
+        if constexpr (COARSE) {
+          const bool of_value = lane >= KT / 16;
+          const float s = of_value ? value_scale(key[0], flags) : scale_of(key[0], flags);
+          zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> (KT / 16);
+          if (run < KT) put_scale(sc + run, s, of_value);
+        } else {
+#pragma unroll
+          for (int j = 0; j < LOOKS; ++j) {
+            const int r = row_of(j);
+            const float ks = scale_of(key[j], flags), vs = value_scale(value[j], flags);
+            zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);
+            if (r < KT) {
+              put_scale(sc + r, ks, false);
+              put_scale(sc + r, vs, true);
+            }
+          }
+        }
+        if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
+        if (lane == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
+        put(slot);
+        filled(slot);
+        if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+        ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status));
+        if (!ok) break;
+        const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+        if ((zero[0] | zero[1]) || (FMT == MOE_E4M3 && node0 < KT)) clean(zero, node0);
+        if (more) ask(a.cache.v);  // (into the keys' stage)
+        put(v_slot);
+        filled(v_slot);
+        slot += 2;
+        if (slot >= p.nslot) {
+          slot -= p.nslot;
+          phase ^= 1;
+        }
+      }
+      ++seq;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
     // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
     // g = k * kProducers + its number
@@ -834,7 +770,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
         }
       }
       commit(&ct.drain);  // nothing runs on when the block ends, also where a wait gave up
-      bar_drain(&ct.drain, 0, a.dev_status);
+      bar_drain(&ct.drain, a.dev_status);
       __syncwarp();
     }
   } else {
@@ -874,7 +810,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
           for (int o = CPR / 2; o >= 1; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
           const bool bf = a.dtype == MOE_BF16;
           const int k = min(126, 14 - (bf ? (int)(most >> 7) - 127 : (int)(most >> 10) - 15));
-          const float by = __uint_as_float((uint32_t)(k + 127) << 23 | (p.score < 0.f ? 0x80000000u : 0u));
+          const float by = __uint_as_float((uint32_t)(k + 127) << 23);
           uint32_t y[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -882,7 +818,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
             y[j] = pack2<MOE_F16>(v.x * by, v.y * by);
           }
           *reinterpret_cast<uint4*>(smem + (q_at(i) - q0)) = make_uint4(y[0], y[1], y[2], y[3]);
-          if (i % CPR == 0) sm_row[i / CPR] = fabsf(p.score) * __uint_as_float((uint32_t)(127 - k) << 23);
+          if (i % CPR == 0) sm_row[i / CPR] = p.score * __uint_as_float((uint32_t)(127 - k) << 23);
         } else
         copy16(q_at(i), static_cast<const uint16_t*>(a.q) + (long long)(wk.q.s + n) * a.q_stride + (wk.h * G + g) * D + i % CPR * 8,
                i < rows * CPR);
@@ -951,9 +887,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
               if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
               const int v = len - base - 32 * w;  // positions of the word
               bits = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
-              if (Q8) {
-                bits &= ~hole[w];
-              } else if (holes) {
+              if (holes) {
 #pragma unroll 1
                 for (int j = 0; j < 32; ++j) {
                   const int r = 32 * w + j, g = r / RPI, q = g / kProducers * RPI + r % RPI;
@@ -969,135 +903,13 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
             // handed over, the tile is gone through again.  The halves are a rolled loop and the
             // mask a branch inside: this code is fetched anew by every launch, and its length
             // shows in the short ones.
-            if constexpr (Q8) {
-              // Codes: scores become powers of two with the value's scale in them, s * key's scale *
-              // row's factor + log2(value's scale) (the factor is not negative).  First their maximum, 64 at a
-              // time, then weights, 32 at a time and the last keys first: that needs fewer registers than
-              // the way below, so that there is room for converters.
-              const float* const scales = sm_scale + ((tile_seq + ti) & (Sh::kRing - 1)) * 3 * KT;
-              const uint32_t s_at = lanes + Sh::s_col(buf);
-              float top = -INFINITY;
-              uint32_t x[32], ahead[32];
-              const auto most_of = [&](uint32_t (&x)[32], int w) {
-                if (!all) {
-                  const unsigned bits = seen(w);
-#pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (!(bits >> j & 1)) x[j] = 0xff800000u;
-                }
-                const float* const sc = scales + 32 * w;
-#pragma unroll
-                for (int j = 0; j < 32; j += COARSE ? 16 : 4) {
-                  if constexpr (COARSE) {
-                    float most = __uint_as_float(x[j]);
-#pragma unroll
-                    for (int i = 1; i < 16; ++i) most = fmaxf(most, __uint_as_float(x[j + i]));
-                    // (a factor of 0 would make NaN of what is not seen)
-                    if (most > -INFINITY) top = fmaxf(top, fmaf(most, sc[j] * row_factor, sc[KT + j]));
-                  } else {
-                    const float4 f = *reinterpret_cast<const float4*>(sc + j), v = *reinterpret_cast<const float4*>(sc + KT + j);
-                    const float f_of[4] = {f.x, f.y, f.z, f.w}, v_of[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const float s = __uint_as_float(x[j + i]);
-                      if (s > -INFINITY) top = fmaxf(top, fmaf(s, f_of[i] * row_factor, v_of[i]));
-                    }
-                  }
-                }
-              };
-              // (the next 32 on their way while these are gone through)
-              tm_read(x, s_at);
-#pragma unroll 1
-              for (int w = 0; w < KT / 32; w += 2) {
-                tm_load(ahead, s_at + 32 * (w + 1));
-                most_of(x, w);
-                tm_wait();
-                ready(ahead);
-                tm_load(x, s_at + 32 * (w + 2 < KT / 32 ? w + 2 : KT / 32 - 1));  // (the last: for the weights)
-                most_of(ahead, w + 1);
-                tm_wait();
-                ready(x);
-              }
-              if (m == -INFINITY) m = top;  // every weight so far was 0
-              const bool far = mr < rows && top - m > kRescale<DT>;
-              if (__any_sync(0xffffffffu, far)) {
-                // row by row: what the rows beside it do leaves a row's bits as they are
-                const float f = far ? exp2_fast(m - top) : 1.f;
-                if (ti > ti0) {  // O holds something
-                  if (!last_product()) break;
-                  uint32_t y[32];
-#pragma unroll 1
-                  for (int w = 0; w < D / 32; ++w) {
-                    tm_read(y, lanes + Sh::o_col(o) + 32 * w);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                    tm_store32(lanes + Sh::o_col(o) + 32 * w, y);
-                  }
-                  tm_wait_store();
-                }
-                l *= f;
-                if (far) m = top;
-              }
-              const float shift = m == -INFINITY ? 0.f : m - kBias<DT>;
-              const auto weigh = [&](uint32_t (&x)[32], int w) {
-                uint32_t y[16];
-                const unsigned bits = all ? 0xffffffffu : seen(w);
-                const float* const sc = scales + 32 * w;
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 32; j += COARSE ? 16 : 4) {
-                  Pair part[2] = {0, 0};
-                  float4 f4, v4;
-                  float inv = 0.f;
-                  if constexpr (COARSE) {
-                    const float f = sc[j] * row_factor, v = sc[KT + j] - shift;
-                    f4 = make_float4(f, f, f, f);
-                    v4 = make_float4(v, v, v, v);
-                    inv = sc[2 * KT + j];
-                  } else {
-                    f4 = *reinterpret_cast<const float4*>(sc + j);
-                    v4 = *reinterpret_cast<const float4*>(sc + KT + j);
-                    f4 = make_float4(f4.x * row_factor, f4.y * row_factor, f4.z * row_factor, f4.w * row_factor);
-                    v4 = make_float4(v4.x - shift, v4.y - shift, v4.z - shift, v4.w - shift);
-                  }
-#pragma unroll
-                  for (int i = j; i < j + (COARSE ? 16 : 4); i += 2) {
-                    const bool second = !COARSE && (i & 2);
-                    float2 z = split(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), second ? pair(f4.z, f4.w) : pair(f4.x, f4.y),
-                                          second ? pair(v4.z, v4.w) : pair(v4.x, v4.y)));
-                    if (!all) {
-                      if (!(bits >> i & 1)) z.x = -INFINITY;
-                      if (!(bits >> (i + 1) & 1)) z.y = -INFINITY;
-                    }
-                    const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
-                    y[i / 2] = pack2<DT>(e0, e1);
-                    if constexpr (COARSE) {
-                      part[i / 2 & 1] = add2(part[i / 2 & 1], pair(e0, e1));
-                    } else {
-                      const float2 iv = *reinterpret_cast<const float2*>(sc + 2 * KT + i);
-                      part[i / 2 & 1] = mul2(pair(e0, e1), pair(iv));
-                    }
-                  }
-                  const float2 both = split(add2(part[0], part[1]));
-                  sum = COARSE ? fmaf(both.x + both.y, inv, sum) : sum + (both.x + both.y);
-                }
-                l += sum;
-                tm_store16(lanes + Sh::p_col(buf) + 16 * w, y);
-              };
-#pragma unroll 1
-              for (int w = KT / 32 - 1; w > 0; w -= 2) {
-                tm_load(ahead, s_at + 32 * (w - 1));
-                weigh(x, w);
-                tm_wait();
-                ready(ahead);
-                if (w > 1) tm_load(x, s_at + 32 * (w - 2));
-                weigh(ahead, w - 1);
-                tm_wait();
-                ready(x);
-                if (w > 1) hand_over(1);
-              }
-            } else {
             uint32_t x[64];
+            const float4* const scales = reinterpret_cast<const float4*>(sm_scale + ((tile_seq + ti) & (Sh::kRing - 1)) * 3 * KT);
+            const auto scaled = [](uint32_t* x, Pair factor, Pair more) {
+              const float2 y = split(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), factor, more));
+              x[0] = __float_as_uint(y.x);
+              x[1] = __float_as_uint(y.y);
+            };
             const auto fetch = [&](int half) {
               const uint32_t at = lanes + Sh::s_col(buf) + 64 * half;
               tm_load(x, at);
@@ -1105,6 +917,24 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
               tm_wait();
               ready(x);
               ready(x + 32);
+              if constexpr (Q8) {
+                // to powers of two with the value's scale in them: s * key's scale * row's factor +
+                // log2(value's scale)
+#pragma unroll
+                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {
+                  const float4* const ks = scales + (64 * half + j) / 4;
+                  if constexpr (COARSE) {
+                    const float f = ks->x * row_factor, lv = ks[KT / 4].x;
+                    const Pair f2 = pair(f, f), lv2 = pair(lv, lv);
+#pragma unroll
+                    for (int i = j; i < j + 16; i += 2) scaled(x + i, f2, lv2);
+                  } else {
+                    const float4 s = *ks, lv = ks[KT / 4];
+                    scaled(x + j, pair(s.x * row_factor, s.y * row_factor), pair(lv.x, lv.y));
+                    scaled(x + j + 2, pair(s.z * row_factor, s.w * row_factor), pair(lv.z, lv.w));
+                  }
+                }
+              }
               if (!all) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
@@ -1156,6 +986,29 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
               }
               const float shift = m == -INFINITY ? 0.f : fmaf(m, c, -kBias<DT>);
               const Pair shift2 = pair(-shift, -shift);
+              if constexpr (Q8) {
+#pragma unroll
+                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {  // the sum is of the weights without the values' scales
+                  const float4* const iv = scales + 2 * (KT / 4) + (64 * half + j) / 4;
+                  const auto weights = [&](int i, Pair inv, Pair& sum) {
+                    const float2 z = split(add2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), shift2));
+                    const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                    sum = COARSE ? add2(sum, pair(e0, e1)) : fma2(pair(e0, e1), inv, sum);
+                    y[i / 2] = pack2<DT>(e0, e1);
+                  };
+                  if constexpr (COARSE) {
+                    Pair part[2] = {0, 0};
+#pragma unroll
+                    for (int i = j; i < j + 16; i += 2) weights(i, 0, part[i / 2 & 1]);
+                    const float inv = iv->x;
+                    sums[0] = fma2(add2(part[0], part[1]), pair(inv, inv), sums[0]);
+                  } else {
+                    const float4 v = *iv;
+                    weights(j, pair(v.x, v.y), sums[0]);
+                    weights(j + 2, pair(v.z, v.w), sums[1]);
+                  }
+                }
+              } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float2 z = split(fma2(pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, shift2));
@@ -1163,12 +1016,12 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
                 sums[j & 1] = add2(sums[j & 1], pair(e0, e1));
                 y[j] = pack2<DT>(e0, e1);
               }
+              }
             }
             if (!ok) break;
             tm_store32(lanes + Sh::p_col(buf), y);
             const float2 sum = split(add2(sums[0], sums[1]));
             l += sum.x + sum.y;
-            }
           } else if (KT == 128) {
             hand_over(1);
           }
@@ -1295,7 +1148,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : Shape<A, D>::kThread
   __syncwarp();
   if (NT == 0 && warp == 10) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   // requests that are left out: their rows, where they are rows at all, get nothing seen
-  for (int b = (int)blockIdx.x * kThreads + tid; b < a.n_req; b += (int)gridDim.x * kThreads) {
+  for (int b = (int)blockIdx.x * kBlock + tid; b < a.n_req; b += (int)gridDim.x * kBlock) {
     const Req q = request<D>(a, b);
     if (q.n == 0 || q.tiles) continue;
     flags |= MOE_DEV_LENGTH;
@@ -1363,7 +1216,7 @@ Workspace layout(const A& a) {
 }
 
 template <typename A, int FMT, int D, bool COARSE = true, int NT = 0>
-int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps = {}) {
+int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   using Sh = Shape<A, D>;
   constexpr int kSmem = 227 * 1024;
   const int need = a.max_tree * p.group;
@@ -1371,7 +1224,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps =
   p.nslot = (kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - p.nq * Sh::kQ) / Sh::kSlot;
   if (p.nslot > kMaxSlots) p.nslot = kMaxSlots;
   static_assert(kMaxSlots / 2 + 1 <= 8, "holes");
-  if (kQ8<A> && p.nslot > 2 * Sh::kRing - 3) p.nslot = 2 * Sh::kRing - 3;
+  if (kQ8<A> && p.nslot > 2 * Sh::kRing - 2) p.nslot = 2 * Sh::kRing - 2;
   static_assert((kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - Sh::NS * Sh::kQ) / Sh::kSlot >= (kQ8<A> ? 3 : 4), "ring");
   static thread_local int ready = -1;  // device whose shared-memory limit this thread has set
   int dev = 0;
@@ -1383,7 +1236,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps =
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < kMaxBlocks ? sms : kMaxBlocks);
-  cfg.blockDim = dim3(NT > 0 ? kFewWarps * 32 : Sh::kThreads);
+  cfg.blockDim = dim3(NT > 0 ? kFewWarps * 32 : kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1391,7 +1244,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st, const MapsOf<A>& maps =
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, COARSE, NT>, a, p, maps));
+  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, COARSE, NT>, a, p));
 }
 
 // Checks, workspace and what the host computes, alike for both caches.
