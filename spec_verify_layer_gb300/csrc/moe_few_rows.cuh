@@ -8,8 +8,8 @@
 // V as rows; both of a product's operands then have the query rows as their 8 columns.  A lane's
 // 16 bytes of a key are pairs along the product's depth as they lie (any order of elements does, if the
 // queries have the same); values are paired key by key with a byte permutation; P comes out of S by an
-// 8 x 8 transpose.  Eight warps take steps of 32 keys in turn, each with a ring of stages and a softmax of its
-// own, and are joined when the share of the head ends.
+// 8 x 8 transpose.  Eight or twelve warps take steps of 32 keys in turn, each with a ring of stages and a softmax
+// of its own, and are joined when the share of the head ends.
 #pragma once
 
 #include "moe_attn_parts.cuh"
@@ -17,20 +17,23 @@
 namespace moe {
 namespace {
 
-constexpr int kFewWarps = 8, kFewStages = 3;
-
 template <int D, int NT>
 struct FewShape {
+  // Twelve warps (and two stages each, if three are too large) where a warp's sums leave the registers for it, else eight and three.
+  static constexpr int W = D / 16 * NT <= 8 ? 12 : 8, STAGES = W == 12 && D > 64 ? 2 : 3;
   static constexpr int KS = D == 256 ? 16 : 32;  // keys of a step
   static constexpr int kStage = 2 * KS * D;      // codes of keys and values
-  static constexpr int kRing = kFewWarps * kFewStages * kStage;
+  static constexpr int kRing = W * STAGES * kStage;
   static constexpr int ROWS = 8 * NT, kPitch = D + 4;
-  static constexpr int kScales = kFewWarps * kFewStages * 2 * KS * 4;  // of keys and values
-  static constexpr int kPages = kFewWarps * 4 * KS * 4, kHoles = kFewWarps * 4 * 4;
-  static constexpr int kQuery = NT * (D / 16) * 32 * 8, kRowBytes = ROWS * 4, kMl = kFewWarps * ROWS * 8;
+  static constexpr int kScales = W * STAGES * 2 * KS * 4;  // of keys and values
+  static constexpr int kPages = W * 4 * KS * 4, kHoles = W * 4 * 4;
+  static constexpr int kQuery = NT * (D / 16) * 32 * 8, kRowBytes = ROWS * 4, kMl = W * ROWS * 8;
   static constexpr int kBytes = kRing + kScales + kPages + kHoles + kQuery + kRowBytes + kMl;
-  static_assert(kFewWarps * ROWS * kPitch * 4 <= kRing, "the ring holds the warps' sums");
+  static_assert(W * ROWS * kPitch * 4 <= kRing, "the ring holds the warps' sums");
 };
+
+template <int D, int NT>
+constexpr int kFewThreads = FewShape<D, NT == 0 ? 1 : NT>::W * 32;
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -59,15 +62,16 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// A block's share of the list, unit after unit; all kFewWarps warps.
+// A block's share of the list, unit after unit; all W warps.
 template <typename A, int FMT, int D, int NT>
 __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct, unsigned char* smem, Walk<A, D>& wk, int member, unsigned& flags) {
   using F = FewShape<D, NT>;
+  constexpr int W = F::W, STAGES = F::STAGES;
   constexpr int KT = kKeyTile<D>, KS = F::KS, MT = KS / 16, CC = D / 16, STEPS = D / 16, OT = D / 16, RPI = 32 / CC, COPIES = KS / RPI;
   constexpr uint32_t kNone = 0xffffffffu;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3, G = p.group;
-  unsigned char* const ring = smem + warp * kFewStages * F::kStage;
-  float* const scales = reinterpret_cast<float*>(smem + F::kRing) + warp * kFewStages * 2 * KS;  // [stage][keys, values][KS]
+  unsigned char* const ring = smem + warp * STAGES * F::kStage;
+  float* const scales = reinterpret_cast<float*>(smem + F::kRing) + warp * STAGES * 2 * KS;  // [stage][keys, values][KS]
   volatile int* const pages = reinterpret_cast<int*>(smem + F::kRing + F::kScales) + warp * 4 * KS;
   volatile unsigned* const holes = reinterpret_cast<unsigned*>(smem + F::kRing + F::kScales + F::kPages) + warp * 4;
   uint2* const query = reinterpret_cast<uint2*>(smem + F::kRing + F::kScales + F::kPages + F::kHoles);  // [NT][STEPS][32]
@@ -98,10 +102,10 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
         ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
       }
     }
-    const int steps = (k1 - k0 + KS - 1) / KS, mine = steps > warp ? (steps - warp + kFewWarps - 1) / kFewWarps : 0;
+    const int steps = (k1 - k0 + KS - 1) / KS, mine = steps > warp ? (steps - warp + W - 1) / W : 0;
     const uint32_t head_units = (uint32_t)(wk.h * a.cache.head_stride >> 4);
     const long long scale_at = wk.h * a.cache.scale_head_stride;
-    const auto key0 = [&](int j) { return k0 + (warp + j * kFewWarps) * KS; };
+    const auto key0 = [&](int j) { return k0 + (warp + j * W) * KS; };
     const auto look = [&](int j) {  // the pages of this warp's step j
       const int pos = key0(j) + lane;
       const bool there = j < mine && lane < KS && pos < k1;
@@ -203,7 +207,7 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
     for (int j = 0; j < mine; ++j) {
       asm volatile("cp.async.wait_group 1;" ::: "memory");  // this step; the next is on its way
       __syncwarp();
-      ask(j + 2, stage == 0 ? kFewStages - 1 : stage - 1);  // into the stage before, which is done with
+      if (STAGES == 3) ask(j + 2, stage == 0 ? STAGES - 1 : stage - 1);  // into the stage before, which is done with
       const unsigned char* const keys = ring + stage * F::kStage;
       unsigned char* const values = ring + stage * F::kStage + KS * D;
       const float* const sc = scales + stage * 2 * KS;
@@ -376,7 +380,11 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
             }
         }
       }
-      if (++stage == kFewStages) stage = 0;
+      if (STAGES == 2) {
+        __syncwarp();
+        ask(j + 2, stage);
+      }
+      if (++stage == STAGES) stage = 0;
     }
 
     // ---- the warps' parts together
@@ -404,13 +412,13 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
     const int part = wk.t0 == 0;
     const long long slot = (long long)blockIdx.x * 2 + part;
 #pragma unroll 1
-    for (int i = tid; i < rows * (D / 4); i += kFewWarps * 32) {
+    for (int i = tid; i < rows * (D / 4); i += W * 32) {
       const int r = i / (D / 4), c4 = i % (D / 4), mi = m0 + r, n = p.group_mul ? (int)__umulhi((unsigned)mi, p.group_mul) : mi, head = wk.h * G + mi - n * G;
       float top = -INFINITY, total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, ml[w * F::ROWS + r].x);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * F::ROWS + r].x);
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float2 v = ml[w * F::ROWS + r];
         const float f = v.x == -INFINITY ? 1.f : exp2_fast(v.x - top);  // nothing seen: zeros, or NaN that has to stay
         const float4 y = *reinterpret_cast<const float4*>(sums + (w * F::ROWS + r) * F::kPitch + c4 * 4);

@@ -70,19 +70,19 @@ namespace {
 // FMT: the type of q, cache and out (16-bit cache), or of the codes.  COARSE: a scale stands for 16 keys or
 // more.  NT: codes, groups of 8 NT query rows, without tensor memory; 0: with.
 template <typename A, int FMT, int D, bool COARSE, int NT>
-__global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : kThreads, 1)
+__global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
     k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p) {
   using Sh = Shape<A, D>;
   constexpr bool Q8 = kQ8<A>;
   constexpr int DT = Q8 ? MOE_F16 : FMT;  // of the products
-  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kBlock = NT > 0 ? kFewWarps * 32 : kThreads;
+  constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kBlock = NT > 0 ? kFewThreads<D, NT> : kThreads;
   constexpr int MG = NT > 0 ? 8 * NT : Sh::MG;  // query rows of a group
   constexpr uint32_t kBlk = KT * 128;  // bytes of a 64-element block of a key or value tile
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sm_q = smem;
   unsigned char* sm_kv = smem + (size_t)p.nq * Sh::kQ;
-  Control& ct = *reinterpret_cast<Control*>(NT > 0 ? smem + FewShape<D, NT>::kBytes : sm_kv + (size_t)p.nslot * Sh::kSlot);
+  Control& ct = *reinterpret_cast<Control*>(NT > 0 ? smem + FewShape<D, NT == 0 ? 1 : NT>::kBytes : sm_kv + (size_t)p.nslot * Sh::kSlot);
   float* const sm_scale = reinterpret_cast<float*>(&ct + 1);  // [kRing][3][KT]
   float* const sm_row = sm_scale + Sh::kRing * 3 * KT;        // [256]
   unsigned char* const sm_looked = reinterpret_cast<unsigned char*>(sm_row + 256), *const sm_raw = sm_looked + Sh::kLooked * 4;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewWarps * 32 : kThreads, 1)
 
   if constexpr (NT > 0) {
     few_rows<A, FMT, D, NT>(a, p, ct, smem, wk, member, flags);
-    join_splits(true);
+    if (warp < kSoftmaxThreads / 32) join_splits(true);
   } else if (warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
     // ---------------- producers of codes.  A warp's rows of a tile are dealt out as below, 16 codes
@@ -1236,7 +1236,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return launch_status(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms < kMaxBlocks ? sms : kMaxBlocks);
-  cfg.blockDim = dim3(NT > 0 ? kFewWarps * 32 : kThreads);
+  cfg.blockDim = dim3(NT > 0 ? kFewThreads<D, NT> : kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
