@@ -17,7 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRows = 16;  // of a thread block
+constexpr int kRows = 64;  // of a thread block, at most
 
 struct Request {
   int s, n, ctx;  // first row, rows, context; n < 0: not a request that can be worked on
@@ -33,6 +33,9 @@ __device__ __forceinline__ Request request(const moe_cache8_args& a, int b) {
   q.n = ok ? e - q.s : -1;
   return q;
 }
+
+// The request of a row: the last that begins at or before it.
+__device__ __forceinline__ int request_of(const moe_cache8_args& a, int row) { return last_not_above(a.row_start, a.n_req, row); }
 
 __device__ __forceinline__ unsigned bad_requests(const moe_cache8_args& a) {
   unsigned flags = 0;
@@ -72,14 +75,22 @@ struct Row8 {
   }
 };
 
-// The values of four codes (a product by a power of two where the code's exponent is put into
-// that of a 32-bit number).
+// The values of four codes.
 __device__ __forceinline__ void decode4(uint32_t w, bool i8, float* x) {
+  if (i8) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = (int8_t)(w >> (8 * j));
-    x[j] = i8 ? (float)c : __uint_as_float(((uint32_t)c & 0x80000000u) | ((uint32_t)(c & 0x7f) << 20)) * 1.329227995784916e36f;  // 2^120
+    for (int j = 0; j < 4; ++j) x[j] = (float)(int8_t)(w >> (8 * j));
+    return;
   }
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  const float2 a = unpack2<MOE_F16>(lo), b = unpack2<MOE_F16>(hi);
+  x[0] = a.x;
+  x[1] = a.y;
+  x[2] = b.x;
+  x[3] = b.y;
 }
 
 __device__ __forceinline__ uint32_t encode4(const float* x, float inv, bool i8) {
@@ -107,40 +118,41 @@ __device__ __forceinline__ int scale_exponent(float most, bool i8) {
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ moe_cache8_args a, PageDivide pd, int lanes) {
+__global__ void __launch_bounds__(kThreads, 3) k_append(const __grid_constant__ moe_cache8_args a, PageDivide pd, int lanes, int rows) {
   constexpr int CPR = D / 8;  // chunks of eight elements of a row
+  constexpr int kHold = DT == MOE_F32 ? 4 : 8;
   struct Begin {              // a block of tokens that begins among these rows
     long long codes, scales;  // of its first slot, and of its scale, head 0
     int row, held, rows;      // first row, slots before it, rows
   };
   __shared__ Begin begin[kRows];
   __shared__ int count;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.cache.block_size;
+  const int tid = threadIdx.x, lane = tid & 31, B = a.cache.block_size;
   const bool i8 = a.cache.format == MOE_I8;
-  unsigned flags = bad_requests(a);
+  unsigned flags = blockIdx.y == 0 ? bad_requests(a) : 0;
   if (tid == 0) count = 0;
   __syncthreads();
-  for (int i = warp; i < kRows; i += kWarps) {
-    const int r = blockIdx.x * kRows + i;
-    if (r >= a.n_rows) break;
-    const int b = last_not_above_warp(a.row_start, a.n_req, r);
+  const int r = blockIdx.x * rows + tid;  // a thread a row
+  if (tid < rows && r < a.n_rows) {
+    const int b = request_of(a, r);
     const Request q = request(a, b);
     const int pos = q.ctx + r - q.s, in_block = pos & (B - 1);
-    if (r < q.s || r - q.s >= q.n || (r > q.s && in_block)) continue;
-    const int col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
-    const int page = __ldg(a.block_table + (long long)b * a.table_width + col);
-    if (page < 0 || page >= a.cache.n_pages) {
-      flags |= MOE_DEV_INDEX;
-      continue;
+    if (r >= q.s && r - q.s < q.n && (r == q.s || !in_block)) {
+      const int col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
+      const int page = __ldg(a.block_table + (long long)b * a.table_width + col);
+      if (page < 0 || page >= a.cache.n_pages) {
+        flags |= MOE_DEV_INDEX;
+      } else {
+        const int slot = pos - in_block - col * a.cache.page_size;
+        begin[atomicAdd(&count, 1)] = {page * a.cache.page_stride + slot * a.cache.slot_stride,
+                                       page * a.cache.scale_page_stride + slot / B * a.cache.scale_block_stride,
+                                       r, in_block, min(B - in_block, q.n - (r - q.s))};
+      }
     }
-    const int slot = pos - in_block - col * a.cache.page_size;
-    if (lane == 0)
-      begin[atomicAdd(&count, 1)] = {page * a.cache.page_stride + slot * a.cache.slot_stride,
-                                     page * a.cache.scale_page_stride + slot / B * a.cache.scale_block_stride,
-                                     r, in_block, min(B - in_block, q.n - (r - q.s))};
   }
   __syncthreads();
-  const int heads = a.kv_heads, tasks = count * 2 * heads, group = tid / lanes, groups = kThreads / lanes, at = tid & (lanes - 1);
+  const int heads = a.kv_heads, tasks = count * 2 * heads, at = tid & (lanes - 1);
+  const int group = blockIdx.y * (kThreads / lanes) + tid / lanes, groups = gridDim.y * (kThreads / lanes);
   const unsigned members = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (lane & ~(lanes - 1));
   for (int t = group; t < tasks; t += groups) {
     const int head = t % heads, kv = t / heads & 1;
@@ -169,8 +181,22 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ moe
       for (int j = 0; j < 8; ++j) v[j] *= old;
       look(v);
     }
+    // the first kHold of a lane's chunks stay in registers, what is more is read again
+    Row8<DT> kept[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int c = at + i * lanes;
+      if (c < g.rows * CPR) kept[i].load(x, x0 + c / CPR * x_stride + c % CPR * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (at + i * lanes < g.rows * CPR) {
+        float v[8];
+        kept[i].floats(v);
+        look(v);
+      }
 #pragma unroll 4
-    for (int c = at; c < g.rows * CPR; c += lanes) {
+    for (int c = at + kHold * lanes; c < g.rows * CPR; c += lanes) {
       Row8<DT> y;
       y.load(x, x0 + c / CPR * x_stride + c % CPR * 8);
       float v[8];
@@ -192,14 +218,20 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ moe
         for (int j = 0; j < 8; ++j) v[j] *= old;
         *p = make_uint2(encode4(v, inv, i8), encode4(v + 4, inv, i8));
       }
-#pragma unroll 4
-    for (int c = at; c < g.rows * CPR; c += lanes) {
-      Row8<DT> y;
-      y.load(x, x0 + c / CPR * x_stride + c % CPR * 8);
+    const auto put = [&](const Row8<DT>& y, int c) {
       float v[8];
       y.floats(v);
-      *reinterpret_cast<uint2*>(codes + (g.held + c / CPR) * a.cache.slot_stride + c % CPR * 8) =
-          make_uint2(encode4(v, inv, i8), encode4(v + 4, inv, i8));
+      __stcs(reinterpret_cast<uint2*>(codes + (g.held + c / CPR) * a.cache.slot_stride + c % CPR * 8),
+             make_uint2(encode4(v, inv, i8), encode4(v + 4, inv, i8)));
+    };
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (at + i * lanes < g.rows * CPR) put(kept[i], at + i * lanes);
+#pragma unroll 4
+    for (int c = at + kHold * lanes; c < g.rows * CPR; c += lanes) {
+      Row8<DT> y;
+      y.load(x, x0 + c / CPR * x_stride + c % CPR * 8);
+      put(y, c);
     }
     if (at == 0) *scale = now;
   }
@@ -207,15 +239,15 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ moe
 }
 
 template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ moe_cache8_args a, PageDivide pd) {
+__global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ moe_cache8_args a, PageDivide pd, int rows_most) {
   constexpr int CPR = D / 16;
   __shared__ long long from[kRows], scales[kRows];  // -1: not a row of a request, -2: nothing cached
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool i8 = a.cache.format == MOE_I8;
   unsigned flags = bad_requests(a);
-  const int r0 = blockIdx.x * kRows, rows = min(kRows, a.n_rows - r0);
-  for (int i = warp; i < rows; i += kWarps) {
-    const int r = r0 + i, b = last_not_above_warp(a.row_start, a.n_req, r);
+  const int r0 = blockIdx.x * rows_most, rows = min(rows_most, a.n_rows - r0);
+  if (tid < rows) {  // a thread a row
+    const int r = r0 + tid, b = request_of(a, r);
     const Request q = request(a, b);
     long long at = -1, scale = 0;
     if (r >= q.s && r - q.s < q.n) {
@@ -229,42 +261,56 @@ __global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ moe_c
         scale = page * a.cache.scale_page_stride + slot / a.cache.block_size * a.cache.scale_block_stride;
       }
     }
-    if (lane == 0) {
-      from[i] = at;
-      scales[i] = scale;
-    }
+    from[tid] = at;
+    scales[tid] = scale;
   }
   __syncthreads();
   const int per_row = 2 * a.kv_heads * CPR;
-#pragma unroll 2
-  for (int t = tid; t < rows * per_row; t += kThreads) {
-    const int i = t / per_row, h2 = t % per_row / CPR, c = t % CPR, kv = h2 >= a.kv_heads, head = h2 - (kv ? a.kv_heads : 0);
-    if (from[i] == -1) continue;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    float s = 0.f;
-    if (from[i] >= 0) {
-      w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? a.cache.v : a.cache.k) + from[i] +
-                                          head * a.cache.head_stride + c * 16);
-      s = scale_of((kv ? a.cache.v_scale : a.cache.k_scale)[scales[i] + head * a.cache.scale_head_stride], flags);
-    }
-    const long long to = (long long)(r0 + i) * (kv ? a.v_stride : a.k_stride) + head * D + c * 16;
-    float x[16];
-    decode4(w.x, i8, x);
-    decode4(w.y, i8, x + 4);
-    decode4(w.z, i8, x + 8);
-    decode4(w.w, i8, x + 12);
+  for (int t = lane; t < per_row; t += 32) {
+    const int h2 = t / CPR, c = t % CPR, kv = h2 >= a.kv_heads, head = h2 - (kv ? a.kv_heads : 0);
+    const uint8_t* const codes = static_cast<const uint8_t*>(kv ? a.cache.v : a.cache.k) + head * a.cache.head_stride + c * 16;
+    const float* const scale = (kv ? a.cache.v_scale : a.cache.k_scale) + head * a.cache.scale_head_stride;
+    const long long stride = kv ? a.v_stride : a.k_stride, to0 = (long long)r0 * stride + head * D + c * 16;
+    constexpr int kAhead = 4;  // rows on their way
+    for (int i0 = warp; i0 < rows; i0 += kWarps * kAhead) {
+      uint4 w[kAhead];
+      float s[kAhead];
+      bool there[kAhead];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] *= s;
-    if constexpr (DT == MOE_F32) {
-      float4* out = reinterpret_cast<float4*>(static_cast<float*>(kv ? a.v : a.k) + to);
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u * kWarps;
+        there[u] = i < rows && from[i] != -1;
+        w[u] = make_uint4(0, 0, 0, 0);
+        s[u] = 0.f;
+        if (there[u] && from[i] >= 0) {
+          w[u] = __ldcs(reinterpret_cast<const uint4*>(codes + from[i]));
+          s[u] = __ldg(scale + scales[i]);
+        }
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) out[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-    } else {
-      uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? a.v : a.k) + to);
+      for (int u = 0; u < kAhead; ++u) {
+        if (!there[u]) continue;
+        const float f = scale_of(s[u], flags);
+        const long long to = to0 + (i0 + u * kWarps) * stride;
+        float x[16];
+        decode4(w[u].x, i8, x);
+        decode4(w[u].y, i8, x + 4);
+        decode4(w[u].z, i8, x + 8);
+        decode4(w[u].w, i8, x + 12);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        out[j] = make_uint4(pack2<DT>(x[8 * j], x[8 * j + 1]), pack2<DT>(x[8 * j + 2], x[8 * j + 3]),
-                            pack2<DT>(x[8 * j + 4], x[8 * j + 5]), pack2<DT>(x[8 * j + 6], x[8 * j + 7]));
+        for (int j = 0; j < 16; ++j) x[j] *= f;
+        if constexpr (DT == MOE_F32) {
+          float4* out = reinterpret_cast<float4*>(static_cast<float*>(kv ? a.v : a.k) + to);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) __stcs(out + j, make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]));
+        } else {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? a.v : a.k) + to);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            __stcs(out + j, make_uint4(pack2<DT>(x[8 * j], x[8 * j + 1]), pack2<DT>(x[8 * j + 2], x[8 * j + 3]),
+                                       pack2<DT>(x[8 * j + 4], x[8 * j + 5]), pack2<DT>(x[8 * j + 6], x[8 * j + 7])));
+        }
+      }
     }
   }
   if (flags) atomicOr(a.dev_status, flags);
@@ -286,17 +332,34 @@ int check(const moe_cache8_args* p) {
   return MOE_OK;
 }
 
+// Rows of a thread block: as many as leave blocks for every SM, 16 at least.
+int block_rows(int n_rows) {
+  int rows = kRows;
+  while (rows > 16 && n_rows / rows < 600) rows /= 2;
+  return rows;
+}
+
 template <int DT>
 cudaError_t append(const moe_cache8_args& a, cudaStream_t st) {
   // lanes of a task: no more than it has chunks of eight elements
   const int chunks = a.cache.block_size * a.head_dim / 8, lanes = chunks >= 32 ? 32 : chunks;
   const auto fn = a.head_dim == 64 ? k_append<DT, 64> : a.head_dim == 128 ? k_append<DT, 128> : k_append<DT, 256>;
-  return launch_kernel(fn, (a.n_rows + kRows - 1) / kRows, kThreads, 0, st, a, page_divide(a.cache.page_size), lanes);
+  // few rows: their tasks over several thread blocks
+  const int rows = block_rows(a.n_rows);
+  const unsigned across = (a.n_rows + rows - 1) / rows;
+  unsigned down = 1;
+  while (across * down < 600 && down * kThreads / lanes < 2u * a.kv_heads) down *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(across, down);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, fn, a, page_divide(a.cache.page_size), lanes, rows);
 }
 template <int DT>
 cudaError_t read(const moe_cache8_args& a, cudaStream_t st) {
   const auto fn = a.head_dim == 64 ? k_read<DT, 64> : a.head_dim == 128 ? k_read<DT, 128> : k_read<DT, 256>;
-  return launch_kernel(fn, (a.n_rows + kRows - 1) / kRows, kThreads, 0, st, a, page_divide(a.cache.page_size));
+  const int rows = block_rows(a.n_rows);
+  return launch_kernel(fn, (a.n_rows + rows - 1) / rows, kThreads, 0, st, a, page_divide(a.cache.page_size), rows);
 }
 
 }  // namespace

@@ -1,15 +1,18 @@
-// Which drafted tokens stand and which token follows (moe_verify_drafts), two launches.
+// Which drafted tokens stand and which token follows (moe_verify_drafts), three launches, each of
+// which starts while the one before it ends.
 //
 // k_sums: one pass over the logits of the rows that drafts hang on (greedy: of all rows); a block
 // takes a slice of a row, a thread running maximum m and sum s = sum 2^((x - m) c), c = log2(e) / T
 // (greedy: the largest logit's key).  Rows without drafts behind them need no sums and are
 // left out.
 //
-// k_draw: a request's blocks each join its rows' sums and walk down its drafts (a few dozen numbers, in
-// 64 bits; cheaper done in each block than handed from one to the others), then scan a slice of the
-// row where the walk ended for the largest rest(x) / noise(x): an exponential race, so the
-// draw needs one pass, no prefix sums, and no order between slices.  The request's block that
-// ends last joins the slices, by (ratio, lower id), so it does not matter which one that is.
+// k_walk: a block a request joins its rows' sums and walks down its drafts, a few dozen numbers, in 64
+// bits.  (Done by each of the last launch's blocks for itself: 70 us of the 90 that 64 chains took.)
+//
+// k_draw: a request's blocks each scan a slice of the row where the walk ended for the largest
+// rest(x) / noise(x): an exponential race, so the draw needs one pass, no prefix sums, and no
+// order between slices.  The request's block that ends last joins the slices, by (ratio, lower id), so
+// it does not matter which one that is.
 //
 // The exponent (x - m) c is taken with c in two parts (c >= hi, lo > 0, so that -infinity stays
 // what it is): with c rounded to 32 bits probabilities far from the maximum would be off by
@@ -24,13 +27,20 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTree = 64;
 constexpr int kVecs = 4;         // vectors a thread has on their way
 constexpr int kMaxSlices = 32;
-constexpr int kBlocks = 608;     // four of an SM: rows and requests are cut into slices up to there
-constexpr int kSliceMin = 2048;  // entries of a slice at least
+constexpr int kBlocks = 2400;    // rows and requests are cut into slices up to about so many blocks
+constexpr int kSliceMin = 4096;  // entries of a slice at least
 constexpr int kCounters = (int)(kCounterBytes / sizeof(unsigned));
 
 struct Drawn {  // a slice's candidates: of the rest, and of p for where nothing of the rest is left
   float m, best, best_p;
   int id, id_p, bad;
+};
+
+struct End {  // of a request's walk, in the workspace
+  double S;
+  float m;
+  int last, child, n_out, inner;  // last < 0: nothing to draw
+  int out[kTree];                 // tokens that were rejected behind the last row
 };
 
 struct Plan {
@@ -41,6 +51,7 @@ struct Plan {
   float2* sums;    // [rows][row_slices]: m, s
   Key* keys;       // greedy: [rows][row_slices]
   Drawn* drawn;    // [requests][draw_slices]
+  End* end;        // [requests]
   unsigned* left;  // [requests]
 };
 
@@ -75,6 +86,7 @@ __global__ void __launch_bounds__(kThreads) k_sums(const __grid_constant__ moe_v
   __shared__ Key k_of[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / p.row_slices, slice = blockIdx.x - row * p.row_slices;
+  asm volatile("griddepcontrol.launch_dependents;");  // k_walk's blocks may take their places; they wait for this launch's end
   {
     // every warp finds the row's request and looks for its children
     const int b = last_not_above_warp(a.row_start, a.n_req, row);
@@ -173,11 +185,7 @@ __global__ void __launch_bounds__(kThreads) k_sums(const __grid_constant__ moe_v
 struct Walk {  // of one request, in shared memory
   double prob[kTree], S[kTree], border[kTree];
   float m[kTree], u[kTree];
-  int parent[kTree], token[kTree], best[kTree], inner[kTree];
-  bool again[kTree];
-  int order[kTree];
-  int out[kTree], n_out;  // tokens that were rejected behind the last row
-  int last, stands, child;
+  int parent[kTree], token[kTree], best[kTree], inner[kTree], order[kTree];
 };
 
 // N consecutive entries of a row from `first` on, in 32 bits; `other` outside [0, n).
@@ -213,12 +221,32 @@ __device__ __forceinline__ void entries(const void* row, int dt, int first, int 
   for (int j = 0; j < N; ++j) x[j] = first + j >= 0 && first + j < n ? element(row, dt, first + j) : other;
 }
 
-// One warp goes down the drafts of rows [s, s + n).
+// A block a request: joins its rows' sums, a warp a row, and goes down its drafts.
 template <int DT>
-__device__ __forceinline__ unsigned walk_down(const moe_verify_args& a, const Plan& p, Walk& w, int s, int n, bool greedy) {
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads) k_walk(const __grid_constant__ moe_verify_args a, const __grid_constant__ Plan p) {
+  __shared__ Walk w;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  const bool greedy = isinf(a.inv_temperature);
+  const int s = __ldg(a.row_start + b), e = __ldg(a.row_start + b + 1);
   unsigned flags = 0;
-  for (int i = lane; i < n; i += 32) {
+  if (b == 0 && tid == 0 && s != 0) flags |= MOE_DEV_LENGTH;
+  const bool ok = s >= 0 && e >= s && e <= a.n_rows && e - s <= kTree;
+  const int n = ok ? e - s : 0;
+  if (n == 0) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (the workspace may be in use)
+    if (tid == 0) {
+      if (!ok) flags |= MOE_DEV_LENGTH;
+      a.accepted[b] = 0;
+      a.next_token[b] = -1;
+      if (!greedy) p.end[b].last = -1;
+      if (flags) atomicOr(a.dev_status, flags);
+    }
+    return;
+  }
+  // what does not wait for the sums
+  if (tid < n) {
+    const int i = tid;
     int up = i - 1, token = i ? __ldg(a.tokens + s + i) : -1;
     if (a.parents && i) {
       up = __ldg(a.parents + s + i);
@@ -236,137 +264,137 @@ __device__ __forceinline__ unsigned walk_down(const moe_verify_args& a, const Pl
     w.u[i] = greedy || !i ? 0.f : __ldg(a.uniform + s + i);
     w.inner[i] = 0;
   }
-  __syncwarp();
-  for (int i = lane; i < n; i += 32)
-    if (w.parent[i] >= 0) w.inner[w.parent[i]] = 1;
-  __syncwarp();
-  for (int i = lane; i < n; i += 32) {
-    w.best[i] = -1;
-    w.m[i] = -INFINITY;
-    w.S[i] = 0.;
-    if (greedy) {
-      const Key* key = p.keys + (long long)(s + i) * p.row_slices;
-      Key top = 0;
-      for (int j = 0; j < p.row_slices; ++j) top = max_key(top, key[j]);
-      w.best[i] = top == 0 ? -1 : top == ~0ull ? -2 : key_id(top);
-    } else if (w.inner[i]) {
-      const float2* part = p.sums + (long long)(s + i) * p.row_slices;
-      float m = -INFINITY;
-#pragma unroll 4
-      for (int j = 0; j < p.row_slices; ++j) m = fmaxf(m, part[j].x);
-      double S = 0.;
-#pragma unroll 4
-      for (int j = 0; j < p.row_slices; ++j) {
-        const float2 v = part[j];
-        S += v.x == -INFINITY ? (double)v.y : (double)v.y * factor(v.x, m, p);
-      }
-      w.m[i] = m;
-      w.S[i] = S;
+  __syncthreads();
+  if (tid < n && w.parent[tid] >= 0) w.inner[w.parent[tid]] = 1;
+  float x = 0.f, q = 0.f;
+  bool tried = false, again = false;
+  if (tid < n) {
+    const int up = w.parent[tid], token = w.token[tid];
+    tried = up >= 0 && token >= 0;
+    if (tried && !greedy) {
+      x = logit_at<DT>(static_cast<const char*>(a.logits), (long long)(s + up) * a.stride + token);
+      if (a.draft_probs) q = element(a.draft_probs, a.draft_dtype, (long long)(s + tid) * a.draft_stride + token);
+      else
+        for (int j = 0; j < tid; ++j) again |= w.parent[j] == up && w.token[j] == token;
     }
   }
-  __syncwarp();
-  for (int i = lane; i < n; i += 32) {
-    const int up = w.parent[i], token = w.token[i];
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");  // k_draw's blocks may take their places; they wait for this launch's end
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = warp; i < n; i += kWarps) {
+    if (greedy) {
+      Key top = lane < p.row_slices ? p.keys[(long long)(s + i) * p.row_slices + lane] : 0;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) top = max_key(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) w.best[i] = top == 0 ? -1 : top == ~0ull ? -2 : key_id(top);
+    } else if (w.inner[i]) {
+      const float2 part = lane < p.row_slices ? p.sums[(long long)(s + i) * p.row_slices + lane] : make_float2(-INFINITY, 0.f);
+      float m = part.x;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      double S = part.x == -INFINITY ? (double)part.y : (double)part.y * factor(part.x, m, p);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+      if (lane == 0) {
+        w.m[i] = m;
+        w.S[i] = S;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < n) {
     double prob = 0., border = 1.;
-    bool again = false;
-    if (up >= 0 && token >= 0) {
+    if (tried) {
+      const int up = w.parent[tid];
       if (greedy) {
-        prob = w.best[up] == token ? 1. : 0.;
+        prob = w.best[up] == w.token[tid] ? 1. : 0.;
         border = 0.;
       } else {
-        const float x = logit_at<DT>(static_cast<const char*>(a.logits), (long long)(s + up) * a.stride + token);
-        const double S = w.S[up];
-        if (S != 0.) prob = exp(((double)x - (double)w.m[up]) * p.inv_t) / S;
-        if (a.draft_probs) {
-          border = (double)w.u[i] * (double)element(a.draft_probs, a.draft_dtype, (long long)(s + i) * a.draft_stride + token);
-        } else {
-          for (int j = 0; j < i; ++j) again |= w.parent[j] == up && w.token[j] == token;
+        if (w.S[up] != 0. && !again) prob = exp(((double)x - (double)w.m[up]) * p.inv_t) / w.S[up];
+        border = (double)w.u[tid] * (double)q;
+      }
+    }
+    w.prob[tid] = prob;
+    w.border[tid] = border;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // the walk itself, by all lanes alike
+    int last = 0, stands = 0;
+    double rest = 1.;
+    const bool chain = greedy || a.draft_probs;
+    for (int i = 1; i < n; ++i) {
+      if (w.parent[i] != last) continue;
+      const double prob = w.prob[i], border = chain ? w.border[i] : (double)w.u[i] * rest;
+      if (prob > 0. && border < prob) {
+        last = i;
+        rest = 1.;
+        ++stands;
+        if (lane == 0) w.order[stands] = i;
+      } else {
+        rest -= prob;
+      }
+    }
+    if (lane == 0) w.order[0] = 0;
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) a.path[s + i] = i <= stands ? w.order[i] : -1;
+    if (lane == 0) {
+      a.accepted[b] = stands;
+      if (greedy) {
+        a.next_token[b] = max(w.best[last], -1);
+        if (w.best[last] == -2) flags |= MOE_DEV_VALUE;
+      } else {
+        End& end = p.end[b];
+        const bool inner = w.inner[last] != 0, none = inner && !(w.S[last] > 0.);  // nothing to draw from
+        end.last = none ? -1 : last;
+        end.inner = inner;
+        end.S = inner ? w.S[last] : 0.;
+        end.m = inner ? w.m[last] : 0.f;
+        int child = -1, n_out = 0;
+        for (int i = last + 1; i < n; ++i)
+          if (w.parent[i] == last && w.token[i] >= 0) {
+            child = i;
+            end.out[n_out++] = w.token[i];
+          }
+        end.child = child;
+        end.n_out = n_out;
+        if (none) {
+          a.next_token[b] = -1;
+          if (w.S[last] != 0.) flags |= MOE_DEV_VALUE;
         }
       }
     }
-    w.prob[i] = again ? 0. : prob;
-    w.border[i] = border;
   }
-  __syncwarp();
-  // the walk itself, by all lanes alike
-  int last = 0, stands = 0;
-  double rest = 1.;
-  const bool chain = greedy || a.draft_probs;
-  for (int i = 1; i < n; ++i) {
-    if (w.parent[i] != last) continue;
-    const double prob = w.prob[i], border = chain ? w.border[i] : (double)w.u[i] * rest;
-    if (prob > 0. && border < prob) {
-      last = i;
-      rest = 1.;
-      ++stands;
-      if (lane == 0) w.order[stands] = i;
-    } else {
-      rest -= prob;
-    }
-  }
-  if (lane == 0) {
-    w.order[0] = 0;
-    w.last = last;
-    w.stands = stands;
-    w.child = -1;
-    w.n_out = 0;
-    for (int i = last + 1; i < n; ++i)
-      if (w.parent[i] == last && w.token[i] >= 0) {
-        w.child = i;
-        w.out[w.n_out++] = w.token[i];
-      }
-  }
-  return flags;
+  if (flags) atomicOr(a.dev_status, flags);
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_verify_args a, const __grid_constant__ Plan p) {
   constexpr int N = Vec<DT>::N;
-  __shared__ Walk w;
   __shared__ Drawn all[kWarps];
-  __shared__ int ends;
+  __shared__ int out[kTree], ends;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.draw_slices, slice = blockIdx.x - b * p.draw_slices;
-  const bool greedy = isinf(a.inv_temperature);
-  const int s = __ldg(a.row_start + b), e = __ldg(a.row_start + b + 1), n = e - s;
-  if (b == 0 && slice == 0 && tid == 0 && s != 0) atomicOr(a.dev_status, MOE_DEV_LENGTH);
-  if (s < 0 || e < s || e > a.n_rows || n > kTree || n == 0) {
-    if (slice == 0 && tid == 0) {
-      a.accepted[b] = 0;
-      a.next_token[b] = -1;
-      if (n != 0 || s < 0 || e > a.n_rows) atomicOr(a.dev_status, MOE_DEV_LENGTH);
-    }
-    return;
-  }
-  if (warp == 0) {
-    const unsigned flags = walk_down<DT>(a, p, w, s, n, greedy);
-    if (flags && slice == 0) atomicOr(a.dev_status, flags);
-  }
+  const int s = __ldg(a.row_start + b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const End* const end = p.end + b;
+  const int last = __ldcg(&end->last), child = __ldcg(&end->child), rejected = __ldcg(&end->n_out);
+  const bool inner = __ldcg(&end->inner) != 0;
+  const double S = __ldcg(&end->S);
+  const float m = __ldcg(&end->m);
+  if (last < 0) return;
+  if (tid < rejected) out[tid] = __ldcg(&end->out[tid]);
   __syncthreads();
-  const int last = w.last;
-  if (slice == 0) {
-    for (int i = tid; i < n; i += kThreads) a.path[s + i] = i <= w.stands ? w.order[i] : -1;
-    if (tid == 0) a.accepted[b] = w.stands;
-  }
-  const bool inner = w.inner[last] != 0;
-  const double S = w.S[last];
-  if (greedy || (inner && !(S > 0.))) {  // known already, or nothing to draw from
-    if (slice == 0 && tid == 0) {
-      a.next_token[b] = greedy ? max(w.best[last], -1) : -1;
-      if (greedy ? w.best[last] == -2 : S != 0.) atomicOr(a.dev_status, MOE_DEV_VALUE);
-    }
-    return;
-  }
 
   const Row<DT> r(a, s + last);
   const float* noise = a.noise + b * a.noise_stride;
-  const int child = w.child, n_out = a.draft_probs ? 0 : w.n_out;
+  const int n_out = a.draft_probs ? 0 : rejected;
   const char* q = a.draft_probs && child >= 0
                       ? static_cast<const char*>(a.draft_probs) + (long long)(s + child) * a.draft_stride * (a.draft_dtype == MOE_F32 ? 4 : 2)
                       : nullptr;
   const bool residual = q || n_out > 0;
   const float inv_S = inner ? (float)(1. / S) : 1.f;
-  Drawn d{inner ? w.m[last] : -INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
+  Drawn d{inner ? m : -INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
   const int v0 = slice * p.draw_vecs, v1 = min(v0 + p.draw_vecs, r.vecs);
 #pragma unroll 1
   for (int v = v0 + tid; v < v1; v += 2 * kThreads) {
@@ -410,10 +438,10 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
           if (residual && ratio > d.best) {  // (the rest is no more than p)
             const float rest = q ? mass - fmaxf(from[j][i + h], 0.f) : mass;
             const float left = noisy > 0.f && rest > 0.f ? __fdividef(rest, noisy) : 0.f;
-            bool out = false;
+            bool gone = false;
             if (left > d.best) {
-              for (int k = 0; k < n_out; ++k) out |= w.out[k] == id + h;
-              if (!out) {
+              for (int k = 0; k < n_out; ++k) gone |= out[k] == id + h;
+              if (!gone) {
                 d.best = left;
                 d.id = id + h;
               }
@@ -511,7 +539,7 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Workspace {
   int row_slices, draw_slices;
-  size_t sums, drawn, total;
+  size_t sums, drawn, end, total;
 };
 Workspace layout(const moe_verify_args& a) {
   Workspace w{};
@@ -519,8 +547,24 @@ Workspace layout(const moe_verify_args& a) {
   w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab) : 1;
   w.sums = kCounterBytes;
   w.drawn = w.sums + up256((size_t)a.n_rows * w.row_slices * sizeof(Key));
-  w.total = w.drawn + up256((size_t)a.n_req * w.draw_slices * sizeof(Drawn));
+  w.end = w.drawn + up256((size_t)a.n_req * w.draw_slices * sizeof(Drawn));
+  w.total = w.end + up256((size_t)a.n_req * sizeof(End));
   return w;
+}
+
+// A launch whose blocks may start while the one before it ends.
+template <typename F>
+cudaError_t after(F fn, unsigned grid, bool overlap, cudaStream_t st, const moe_verify_args& a, const Plan& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, a, p);
 }
 
 template <int DT>
@@ -530,7 +574,9 @@ cudaError_t launch(const moe_verify_args& a, const Plan& p, bool greedy, cudaStr
     const cudaError_t e = launch_kernel(fn, (unsigned)a.n_rows * p.row_slices, kThreads, 0, st, a, p);
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(k_draw<DT>, (unsigned)a.n_req * p.draw_slices, kThreads, 0, st, a, p);
+  const cudaError_t e = after(k_walk<DT>, (unsigned)a.n_req, a.n_rows > 0, st, a, p);
+  if (e != cudaSuccess || greedy || a.n_rows == 0) return e;
+  return after(k_draw<DT>, (unsigned)a.n_req * p.draw_slices, true, st, a, p);
 }
 
 }  // namespace
@@ -569,6 +615,7 @@ extern "C" int moe_verify_drafts(const moe_verify_args* args, void* ws, size_t w
   p.sums = reinterpret_cast<float2*>(base + w.sums);
   p.keys = reinterpret_cast<Key*>(base + w.sums);
   p.drawn = reinterpret_cast<Drawn*>(base + w.drawn);
+  p.end = reinterpret_cast<End*>(base + w.end);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launch_status(a.dtype == MOE_BF16  ? launch<MOE_BF16>(a, p, greedy, st)
                        : a.dtype == MOE_F16 ? launch<MOE_F16>(a, p, greedy, st)
