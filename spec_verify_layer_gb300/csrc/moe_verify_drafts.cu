@@ -27,14 +27,23 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTree = 64;
 constexpr int kVecs = 4;         // vectors a thread has on their way
 constexpr int kMaxSlices = 32;
-constexpr int kBlocks = 2400;    // rows and requests are cut into slices up to about so many blocks
-constexpr int kSliceMin = 4096;  // entries of a slice at least
+// Rows (of sums, most blocks of which have none to take) and requests (of draws) are cut into slices up to
+// about so many blocks, of so many entries at least.
+constexpr int kSumBlocks = 1500, kDrawBlocks = 456, kSliceMin = 2048;
 constexpr int kCounters = (int)(kCounterBytes / sizeof(unsigned));
 
-struct Drawn {  // a slice's candidates: of the rest, and of p for where nothing of the rest is left
-  float m, best, best_p;
-  int id, id_p, bad;
+// Ratios and ids of candidates as keys: the larger ratio, of equal ones the lower id; 0: none.
+struct Drawn {  // a slice's: of the rest, and of p for where nothing of the rest is left
+  Key best, best_p;
+  float m;  // that the ratios are taken from
+  int bad;
 };
+__device__ __forceinline__ Key ratio_key(float ratio, int id) { return ratio > 0.f ? (Key)__float_as_uint(ratio) << 32 | (uint32_t)~id : 0; }
+__device__ __forceinline__ Key warp_max(Key k) {
+  const unsigned hi = (unsigned)(k >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+  return (Key)top << 32 | __reduce_max_sync(0xffffffffu, hi == top ? (unsigned)k : 0u);
+}
+__device__ __forceinline__ float warp_max(float x) { return key_value(__reduce_max_sync(0xffffffffu, order_key(x))); }
 
 struct End {  // of a request's walk, in the workspace
   double S;
@@ -319,18 +328,24 @@ __global__ void __launch_bounds__(kThreads) k_walk(const __grid_constant__ moe_v
   }
   __syncthreads();
   if (warp == 0) {
-    // the walk itself, by all lanes alike
+    // the walk itself, by all lanes alike: the children of `last` one after the other
+    const int up0 = lane < n ? w.parent[lane] : -1, up1 = lane + 32 < n ? w.parent[lane + 32] : -1;
+    const auto children = [&](int i) {
+      return (unsigned long long)__ballot_sync(0xffffffffu, up0 == i) | (unsigned long long)__ballot_sync(0xffffffffu, up1 == i) << 32;
+    };
     int last = 0, stands = 0;
     double rest = 1.;
     const bool chain = greedy || a.draft_probs;
-    for (int i = 1; i < n; ++i) {
-      if (w.parent[i] != last) continue;
+    for (unsigned long long left = children(0); left;) {
+      const int i = __ffsll((long long)left) - 1;
+      left &= left - 1;
       const double prob = w.prob[i], border = chain ? w.border[i] : (double)w.u[i] * rest;
       if (prob > 0. && border < prob) {
         last = i;
         rest = 1.;
         ++stands;
         if (lane == 0) w.order[stands] = i;
+        left = children(i);
       } else {
         rest -= prob;
       }
@@ -338,26 +353,27 @@ __global__ void __launch_bounds__(kThreads) k_walk(const __grid_constant__ moe_v
     if (lane == 0) w.order[0] = 0;
     __syncwarp();
     for (int i = lane; i < n; i += 32) a.path[s + i] = i <= stands ? w.order[i] : -1;
-    if (lane == 0) {
-      a.accepted[b] = stands;
-      if (greedy) {
+    if (lane == 0) a.accepted[b] = stands;
+    if (greedy) {
+      if (lane == 0) {
         a.next_token[b] = max(w.best[last], -1);
         if (w.best[last] == -2) flags |= MOE_DEV_VALUE;
-      } else {
-        End& end = p.end[b];
-        const bool inner = w.inner[last] != 0, none = inner && !(w.S[last] > 0.);  // nothing to draw from
+      }
+    } else {
+      End& end = p.end[b];
+      const bool inner = w.inner[last] != 0, none = inner && !(w.S[last] > 0.);  // nothing to draw from
+      // its children with tokens, all of them rejected
+      const bool r0 = up0 == last && lane < n && w.token[lane] >= 0, r1 = up1 == last && lane + 32 < n && w.token[lane + 32] >= 0;
+      const unsigned m0 = __ballot_sync(0xffffffffu, r0), m1 = __ballot_sync(0xffffffffu, r1), before = (1u << lane) - 1;
+      if (r0) end.out[__popc(m0 & before)] = w.token[lane];
+      if (r1) end.out[__popc(m0) + __popc(m1 & before)] = w.token[lane + 32];
+      if (lane == 0) {
         end.last = none ? -1 : last;
         end.inner = inner;
         end.S = inner ? w.S[last] : 0.;
         end.m = inner ? w.m[last] : 0.f;
-        int child = -1, n_out = 0;
-        for (int i = last + 1; i < n; ++i)
-          if (w.parent[i] == last && w.token[i] >= 0) {
-            child = i;
-            end.out[n_out++] = w.token[i];
-          }
-        end.child = child;
-        end.n_out = n_out;
+        end.child = m1 ? 63 - __clz(m1) : m0 ? 31 - __clz(m0) : -1;
+        end.n_out = __popc(m0) + __popc(m1);
         if (none) {
           a.next_token[b] = -1;
           if (w.S[last] != 0.) flags |= MOE_DEV_VALUE;
@@ -394,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
                       : nullptr;
   const bool residual = q || n_out > 0;
   const float inv_S = inner ? (float)(1. / S) : 1.f;
-  Drawn d{inner ? m : -INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
+  struct { float m, best, best_p; int id, id_p, bad; } d = {inner ? m : -INFINITY, 0.f, 0.f, 0, 0, 0};
   const int v0 = slice * p.draw_vecs, v1 = min(v0 + p.draw_vecs, r.vecs);
 #pragma unroll 1
   for (int v = v0 + tid; v < v1; v += 2 * kThreads) {
@@ -450,59 +466,41 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
         }
       }
   }
-  // joined: the larger ratio, of equal ones the lower id.  (Where the maxima differ, no rest is asked for.)
-  const auto join = [&](const Drawn& o) {
-    const float to = fmaxf(d.m, o.m);
-    if (o.best > d.best || (o.best == d.best && o.id < d.id)) {
-      d.best = o.best;
-      d.id = o.id;
-    }
-    const float mine = d.m < to && d.m > -INFINITY ? d.best_p * factor(d.m, to, p) : d.best_p;
-    const float other = o.m < to && o.m > -INFINITY ? o.best_p * factor(o.m, to, p) : o.best_p;
-    d.best_p = fmaxf(mine, other);
-    if (other > mine || (other == mine && o.id_p < d.id_p)) d.id_p = o.id_p;
-    d.m = to;
-    d.bad |= o.bad;
-  };
-  const auto warp_join = [&]() {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      Drawn x;
-      x.m = __shfl_xor_sync(0xffffffffu, d.m, o);
-      x.best = __shfl_xor_sync(0xffffffffu, d.best, o);
-      x.best_p = __shfl_xor_sync(0xffffffffu, d.best_p, o);
-      x.id = __shfl_xor_sync(0xffffffffu, d.id, o);
-      x.id_p = __shfl_xor_sync(0xffffffffu, d.id_p, o);
-      x.bad = __shfl_xor_sync(0xffffffffu, d.bad, o);
-      join(x);
-    }
-  };
-  warp_join();
-  if (lane == 0) all[warp] = d;
+  // The block's, taken from its largest maximum.  (A NaN is in `bad` already.)
+  const auto scaled = [&](float from, float to) { return from < to && from > -INFINITY ? factor(from, to, p) : 1.f; };
+  const float warp_top = warp_max(d.m);
+  const Key best = warp_max(ratio_key(d.best, d.id)), best_p = warp_max(ratio_key(d.best_p * scaled(d.m, warp_top), d.id_p));
+  const int bad = __any_sync(0xffffffffu, d.bad);
+  if (lane == 0) all[warp] = {best, best_p, warp_top, bad};
   __syncthreads();
   if (warp != 0) return;
-  d = lane < kWarps ? all[lane] : Drawn{-INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
-  warp_join();
+  const auto joined = [&](const Drawn& x) {  // over the warp's lanes
+    const float top = warp_max(x.m);
+    return Drawn{warp_max(x.best), warp_max(ratio_key(__uint_as_float((unsigned)(x.best_p >> 32)) * scaled(x.m, top), key_id(x.best_p))),
+                 top, __any_sync(0xffffffffu, x.bad)};
+  };
+  const Drawn none{0, 0, -INFINITY, 0};
+  Drawn own = joined(lane < kWarps ? all[lane] : none);
   if (p.draw_slices > 1) {
     if (lane == 0) {
-      p.drawn[blockIdx.x] = d;
+      p.drawn[blockIdx.x] = own;
       unsigned before;
       asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.left + b) : "memory");
       ends = before == (unsigned)p.draw_slices - 1;
     }
     __syncwarp();
     if (!ends) return;
-    d = Drawn{-INFINITY, 0.f, 0.f, 0x7fffffff, 0x7fffffff, 0};
+    Drawn part = none;
     if (lane < p.draw_slices) {
       const Drawn* o = p.drawn + (long long)b * p.draw_slices + lane;
-      d = Drawn{__ldcg(&o->m), __ldcg(&o->best), __ldcg(&o->best_p), __ldcg(&o->id), __ldcg(&o->id_p), __ldcg(&o->bad)};
+      part = Drawn{__ldcg(&o->best), __ldcg(&o->best_p), __ldcg(&o->m), __ldcg(&o->bad)};
     }
-    warp_join();
+    own = joined(part);
     if (lane == 0) p.left[b] = 0;  // ready for the next call
   }
   if (lane == 0) {
-    a.next_token[b] = d.bad ? -1 : d.best > 0.f ? d.id : d.best_p > 0.f ? d.id_p : -1;
-    if (d.bad) atomicOr(a.dev_status, MOE_DEV_VALUE);
+    a.next_token[b] = own.bad ? -1 : own.best ? key_id(own.best) : own.best_p ? key_id(own.best_p) : -1;
+    if (own.bad) atomicOr(a.dev_status, MOE_DEV_VALUE);
   }
 }
 
@@ -530,9 +528,9 @@ int check(const moe_verify_args* args) {
   return MOE_OK;
 }
 
-int slices_for(int64_t rows, int vocab) {
+int slices_for(int64_t rows, int vocab, int blocks) {
   int n = 1;
-  while (n < kMaxSlices && rows * n < kBlocks && vocab / (2 * n) >= kSliceMin) n *= 2;
+  while (n < kMaxSlices && rows * n < blocks && vocab / (2 * n) >= kSliceMin) n *= 2;
   return n;
 }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -543,8 +541,8 @@ struct Workspace {
 };
 Workspace layout(const moe_verify_args& a) {
   Workspace w{};
-  w.row_slices = slices_for(a.n_rows, a.vocab);
-  w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab) : 1;
+  w.row_slices = slices_for(a.n_rows, a.vocab, kSumBlocks);
+  w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab, kDrawBlocks) : 1;
   w.sums = kCounterBytes;
   w.drawn = w.sums + up256((size_t)a.n_rows * w.row_slices * sizeof(Key));
   w.end = w.drawn + up256((size_t)a.n_req * w.draw_slices * sizeof(Drawn));
