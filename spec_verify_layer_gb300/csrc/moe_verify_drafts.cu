@@ -412,12 +412,18 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
   const float inv_S = inner ? (float)(1. / S) : 1.f;
   struct { float m, best, best_p; int id, id_p, bad; } d = {inner ? m : -INFINITY, 0.f, 0.f, 0, 0, 0};
   const int v0 = slice * p.draw_vecs, v1 = min(v0 + p.draw_vecs, r.vecs);
+  // Ratios are compared as products with the warp's best so far; only where one of its lanes has a
+  // larger one, which is some ln(entries) times, they are divided and looked at one by one.  (With a best
+  // of each lane's own that was nearly every time: 41 us for 64 chains.)
+  constexpr int VECS = N == 8 ? 1 : 2;
+  float least = 0.f, least_p = 0.f;
 #pragma unroll 1
-  for (int v = v0 + tid; v < v1; v += 2 * kThreads) {
-    Vec<DT> x[2];
-    float race[2][N], from[2][N];
+  for (int vw = v0 + warp * 32; vw < v1; vw += VECS * kThreads) {
+    const int v = vw + lane;
+    Vec<DT> x[VECS];
+    float race[VECS][N], from[VECS][N];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < VECS; ++j) {
       const int at = v + j * kThreads, first = at < v1 ? at * N - r.lead : a.vocab;
       x[j] = load_vec<DT>(r.base, first, a.vocab);
       entries<N>(noise, MOE_F32, first, a.vocab, 0.f, race[j]);
@@ -425,43 +431,83 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
     }
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < VECS; ++j)
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float f = x[j].at(i);
         d.bad |= !(f < INFINITY);
         top = fmaxf(top, f);
       }
-    if (top > d.m) {
-      if (d.m > -INFINITY) d.best_p *= factor(d.m, top, p);
-      d.m = top;
+    if (!inner) {  // the maximum is not known: the warp's so far
+      top = warp_max(top);
+      if (top > d.m) {
+        if (d.m > -INFINITY) {
+          const float f = factor(d.m, top, p);
+          d.best_p *= f;
+          least_p *= f;
+        }
+        d.m = top;
+      }
     }
     const float shift = d.m == -INFINITY ? 0.f : d.m;
+    float mass[VECS][N];
+    bool larger = false;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < VECS; ++j)
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         const float2 u = exponent(make_float2(x[j].at(i), x[j].at(i + 1)), shift, p);
-        const int id = (v + j * kThreads) * N - r.lead + i;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mass = exp2_fast(h ? u.y : u.x) * inv_S, noisy = race[j][i + h];
-          const float ratio = noisy > 0.f ? __fdividef(mass, noisy) : 0.f;
+          const float y = exp2_fast(h ? u.y : u.x) * inv_S;
+          mass[j][i + h] = y;
+          larger |= y > least_p * race[j][i + h];
+          if (residual) larger |= (q ? y - fmaxf(from[j][i + h], 0.f) : y) > least * race[j][i + h];
+        }
+      }
+    if (!__any_sync(0xffffffffu, larger)) continue;
+    // A bound that the largest of these reach, from reciprocals that may be off by 2^-22; then those above it.
+    float most = 0.f, most_p = 0.f;
+    int most_id = -1;
+#pragma unroll
+    for (int j = 0; j < VECS; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float noisy = race[j][i], y = mass[j][i];
+        float inv;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(noisy));
+        inv = noisy > 0.f ? fminf(inv, 3e38f) : 0.f;  // (of the smallest numbers it is infinite)
+        most_p = fmaxf(most_p, y * inv);
+        const float left = (q ? y - fmaxf(from[j][i], 0.f) : y) * inv;
+        if (left > most) {
+          most = left;
+          most_id = (v + j * kThreads) * N - r.lead + i;
+        }
+      }
+    for (int k = 0; k < n_out; ++k)
+      if (out[k] == most_id) most = 0.f;
+    least_p = fmaxf(least_p, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_p))) * 0.99999f);
+    least = fmaxf(least, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most))) * 0.99999f);
+#pragma unroll
+    for (int j = 0; j < VECS; ++j)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int id = (v + j * kThreads) * N - r.lead + i;
+        const float noisy = race[j][i], y = mass[j][i], rest = q ? y - fmaxf(from[j][i], 0.f) : y;
+        if (y > least_p * noisy && noisy > 0.f) {
+          const float ratio = y / noisy;
           if (ratio > d.best_p) {
             d.best_p = ratio;
-            d.id_p = id + h;
+            d.id_p = id;
           }
-          if (residual && ratio > d.best) {  // (the rest is no more than p)
-            const float rest = q ? mass - fmaxf(from[j][i + h], 0.f) : mass;
-            const float left = noisy > 0.f && rest > 0.f ? __fdividef(rest, noisy) : 0.f;
-            bool gone = false;
-            if (left > d.best) {
-              for (int k = 0; k < n_out; ++k) gone |= out[k] == id + h;
-              if (!gone) {
-                d.best = left;
-                d.id = id + h;
-              }
-            }
+        }
+        if (residual && rest > least * noisy && noisy > 0.f && rest > 0.f) {
+          const float ratio = rest / noisy;
+          bool gone = !(ratio > d.best);
+          for (int k = 0; k < n_out; ++k) gone |= out[k] == id;
+          if (!gone) {
+            d.best = ratio;
+            d.id = id;
           }
         }
       }
