@@ -496,13 +496,12 @@ int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_
  * 16, not negative), its scale at the float page * scale_page_stride + (slot /
  * block_size) * scale_block_stride + head * scale_head_stride (not negative).  block_size: a
  * power of two, 1..128, that divides page_size; 1 is a scale a token.
- *   format MOE_E4M3: 1 sign, 4 exponent (bias 7) and 3 mantissa bits; all codes are numbers
- *   here, 0x7f and 0xff, which the calls never write, +-480.  MOE_I8: two's complement; the
- *   calls write -127..127.
+ *   format MOE_E4M3: 1 sign, 4 exponent (bias 7) and 3 mantissa bits, 0x7f and 0xff NaN (the
+ *   calls never write those).  MOE_I8: two's complement; the calls write -127..127.
  * A scale is 0 or a finite positive normal number; any other counts as 0 and raises
- * MOE_DEV_VALUE where a position that a call reads goes by it.  So no cached bits are
- * infinite or NaN.  moe_cache8_append writes powers of two; a program's own calibrated
- * scales may be any.  Pages are numbered as in moe_kv_cache. */
+ * MOE_DEV_VALUE where a position that a call reads goes by it.  moe_cache8_append writes
+ * powers of two; a program's own calibrated scales may be any.  Pages are numbered as in
+ * moe_kv_cache. */
 typedef struct moe_kv_cache8 {
   void* k;
   void* v;
@@ -525,8 +524,8 @@ typedef struct moe_kv_cache8 {
  *   is rounded again from its values where the scale has changed.  With MOE_E4M3 that is
  *   exact but for codes that fall below the smallest normal one; with MOE_I8 a value
  *   that was rounded again is off by less than one step of its present scale (rounded once:
- *   half a step).  Infinities become the largest code with their sign, NaN 0, and both raise
- *   MOE_DEV_VALUE.  The last block of a context is written as a whole, so it must not be shared
+ *   half a step).  Infinities become the largest code with their sign, NaN 0 (rows and what
+ *   is held alike), and both raise MOE_DEV_VALUE.  The last block of a context is written as a whole, so it must not be shared
  *   with another request (a shared prefix ends with a block); no two rows of a call may
  *   fall into one slot.
  *   read: k, v = code * scale, rounded once to dtype.
@@ -555,10 +554,13 @@ int moe_cache8_read(const moe_cache8_args* args, void* stream);
  * raised bits and workspace rules, with keys and values code * scale (a scale that is not
  * one counts as 0 and raises MOE_DEV_VALUE).  dtype is that of q and out.  Inside, codes are
  * 16-bit numbers (exactly), queries 16-bit numbers with a power of two for each row and
- * head (exactly, but for elements below 2^-38 of its largest), the softmax weights, with the
- * values' scale in them, are rounded to fp16 for the product with the codes (what is lost
- * are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  The span of
- * either cache is below 2^36 - 2048 bytes here.
+ * head (exactly, but for elements below 2^-38 of its largest), and the softmax weights, with
+ * the values' scale in them, are rounded to fp16 for the product with the codes (what is
+ * lost are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  Scales of
+ * values are taken between 2^-48 and 2^48: smaller ones count as 0 (their values are below
+ * 1.6e-12), and so do larger ones, which raise MOE_DEV_VALUE.  The span of either cache is
+ * below 2^36 - 2048 bytes here.
+ * Positions that are not seen have no influence, whatever codes and scales are cached there.
  * Waits go by moe_set_attention_wait_limit_ns. */
 typedef struct moe_tree_attention8_args {
   const void* q;

@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
   constexpr int N = Vec<DT>::N;
   __shared__ Drawn all[kWarps];
   __shared__ int out[kTree], ends;
+  __shared__ unsigned bound[2];  // what the block's warps have reached, of the rest and of p (a known maximum)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.draw_slices, slice = blockIdx.x - b * p.draw_slices;
   const int s = __ldg(a.row_start + b);
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
   const double S = __ldcg(&end->S);
   const float m = __ldcg(&end->m);
   if (last < 0) return;
+  if (tid < 2) bound[tid] = 0;
   if (tid < rejected) out[tid] = __ldcg(&end->out[tid]);
   __syncthreads();
 
@@ -412,8 +414,8 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
   const float inv_S = inner ? (float)(1. / S) : 1.f;
   struct { float m, best, best_p; int id, id_p, bad; } d = {inner ? m : -INFINITY, 0.f, 0.f, 0, 0, 0};
   const int v0 = slice * p.draw_vecs, v1 = min(v0 + p.draw_vecs, r.vecs);
-  // Ratios are compared as products with the warp's best so far; only where one of its lanes has a
-  // larger one, which is some ln(entries) times, they are divided and looked at one by one.  (With a best
+  // Ratios are compared as products with the best so far; only where one of a warp's lanes has a larger
+  // one, which is some ln(entries) times, they are divided and looked at one by one.  (With a best
   // of each lane's own that was nearly every time: 41 us for 64 chains.)
   constexpr int VECS = N == 8 ? 1 : 2;
   float least = 0.f, least_p = 0.f;
@@ -448,6 +450,10 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
         }
         d.m = top;
       }
+    }
+    if (inner) {
+      least = fmaxf(least, __uint_as_float(*(volatile unsigned*)&bound[0]));
+      least_p = fmaxf(least_p, __uint_as_float(*(volatile unsigned*)&bound[1]));
     }
     const float shift = d.m == -INFINITY ? 0.f : d.m;
     float mass[VECS][N];
@@ -488,6 +494,10 @@ __global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_v
       if (out[k] == most_id) most = 0.f;
     least_p = fmaxf(least_p, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most_p))) * 0.99999f);
     least = fmaxf(least, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most))) * 0.99999f);
+    if (inner && lane == 0) {
+      atomicMax(&bound[0], __float_as_uint(least));
+      atomicMax(&bound[1], __float_as_uint(least_p));
+    }
 #pragma unroll
     for (int j = 0; j < VECS; ++j)
 #pragma unroll
