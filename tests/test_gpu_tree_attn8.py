@@ -117,7 +117,8 @@ def test_what_lies_past_the_end_has_no_influence(n):
 @pytest.mark.parametrize("block", [4, 16])
 def test_pages_that_are_none(n, block):
     case = Tree8Case(8, [100], [n], hq=4, hkv=2, d=64, page=16, block=block, fmt="e4m3")
-    case.raw("v")[case.n_pages - 1] = 0x7f
+    unused = sorted(set(range(case.n_pages)) - set(case.table[0].tolist()))
+    case.raw("v")[unused] = 0x7f  # (NaN, in pages of nobody)
     case.table[0, 2] = -1
     case.table[0, 4] = case.n_pages
     hidden = torch.zeros(100 + n, dtype=torch.bool, device=DEV)

@@ -222,7 +222,7 @@ def test_equal_largest_logits_and_ratios_go_to_the_lowest_id():
 
 
 def test_draws_follow_the_target():
-    """20,000 requests of one token and one draft: what comes first is distributed as the target says, within five
+    """10,000 requests of one token and one draft: what comes first is distributed as the target says, within five
     standard deviations."""
     n, vocab = 10000, 8
     rng = np.random.default_rng(10)
@@ -291,9 +291,6 @@ def test_bad_tokens_parents_and_lengths():
     case = VerifyCase(15, [3, 65, 2], 700)
     got, status = case.run()
     assert status == mv.MOE_DEV_LENGTH and got[0][1] == 0 and got[2][1] == -1 and (got[1][3:68] == -9).all()
-    case.counts = [3, 0, 2]
-    want = case.plain
-    case.start = np.array([0, 3, 3, 5])  # (as the checks below see them)
     case = VerifyCase(16, [3, 4, 2], 700)
     for start in ([0, 9, 4, 9], [0, -3, 7, 9], [2**31 - 1, 0, 5, 9], [5, 3, 2, 2**31 - 1], [0, 3, 7, 10]):
         outs, flags = case.outputs(), word()
