@@ -370,6 +370,9 @@ __device__ __forceinline__ uint4 codes_to_half(uint32_t a, uint32_t b) {
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
+// Values whose scale counts as 0 are zeros of the smallest scale, so that their weights, which count in the
+// sum, stay below those of any other.
+constexpr float kNoValueLog = -48.f, kNoValueInverse = 281474976710656.f;
 // A value's scale: 2^-48 .. 2^48.  The weights' sum is taken from the weights with the scales in them, so
 // these may not lie further apart than 32-bit exponents reach; smaller ones count as 0 (their
 // values are below 1.6e-12), larger ones too and are reported.

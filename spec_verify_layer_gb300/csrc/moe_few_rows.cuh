@@ -280,8 +280,8 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
           float log;
           asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
           asm("rcp.approx.f32 %0, %1;" : "=f"(inv[mt][h]) : "f"(vs));
-          no_value[mt][h] = vs == 0.f;  // such values are zeros, at scale 1
-          if (vs == 0.f) log = 0.f, inv[mt][h] = 1.f;
+          no_value[mt][h] = vs == 0.f;  // such values are zeros
+          if (vs == 0.f) log = kNoValueLog, inv[mt][h] = kNoValueInverse;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -452,14 +452,14 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
         }
       };
       // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum
-      // and in their products alike); values of scale 0 are zeros at scale 1
+      // and in their products alike); values of scale 0 are zeros
       const auto put_scale = [&](float* sc, float s, bool of_value) {
         float log, inv;
         asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(s));
         asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
         if (of_value) {
-          sc[KT] = s == 0.f ? 0.f : log;
-          sc[2 * KT] = s == 0.f ? 1.f : inv;
+          sc[KT] = s == 0.f ? kNoValueLog : log;
+          sc[2 * KT] = s == 0.f ? kNoValueInverse : inv;
         } else {
           sc[0] = s;
         }
