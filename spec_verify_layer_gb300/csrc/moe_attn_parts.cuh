@@ -59,7 +59,7 @@ struct Shape {
   static constexpr int LOOKS = (STEPS * RPI + 31) / 32;  // rows of a producer that a lane looks up
   static constexpr int kRing = D == 64 ? 8 : 4;
   static constexpr int kRaw = KT * D, kRawStages = 3;
-  static constexpr int kLooked = kProducers * 2 * 4 * LOOKS * 32;
+  static constexpr int kLooked = kProducers * 2 * 3 * LOOKS * 32;
   static constexpr int kScales = kQ8<A> ? (kRing * 3 * KT + 256 + kLooked) * 4 + kRawStages * kRaw : 0;
   // Columns of tensor memory.  Scores: a buffer for each stream (or two that take turns where
   // there is one stream); the weights, in 16 bits, go over the second half of their scores.
@@ -95,7 +95,7 @@ struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows
+  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes, COARSE: a bit a run of 16)
   int red[kThreads / 32], redn[kThreads / 32];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;

@@ -350,10 +350,10 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
       unsigned hole[2], next_hole[2] = {0, 0};
       uint32_t at[LOOKS];  // in units of 16 bytes
       // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
-      // scale.  COARSE: lanes 0 .. KT/8 - 1 look up the scale of keys, then of values, of a run of 16 keys
-      // each: its page (3) and scale (1).
-      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 4 + what) * LOOKS + j) * 32 + lane; };
-      const auto column = [&](int pos) { return (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift); };
+      // scale.  COARSE: lanes 0 .. KT/8 - 1 look up runs of 16 keys, once for keys and once for values: page
+      // (0) and scale (1).
+      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 3 + what) * LOOKS + j) * 32 + lane; };
+      const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
       const auto look_at = [&](int t, int r, int what, int j) {
         const int pos = t * KT + r;
         const bool there = r < KT && pos < len;
@@ -361,19 +361,30 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
       };
       const int run = lane < KT / 8 ? (lane & (KT / 16 - 1)) * 16 : KT;
       const auto look = [&](int t) {
+        if constexpr (COARSE) {
+          look_at(t, run, 0, 0);
+        } else {
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
-        if constexpr (COARSE) look_at(t, run, 3, 0);
+          for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
+        }
       };
       const auto read = [&](int t, int what, int j) { return *reinterpret_cast<volatile int*>(sm_looked + looked(t, what, j) * 4); };
       const auto scale_place = [&](int page, int in_page) {
         return page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
       };
-      const auto ask = [&](const void* base) {  // the tile that `at` is of, into the next stage
+      int left = 0;  // rows up to the end, of the tile that `at` is of
+      const auto ask = [&](const void* base) {  // that tile, into the next stage
         uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
 #pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k)
-          from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
+        for (int k = 0; k < Sh::STEPS; ++k) {
+          const int r = (k * kProducers + pw) * RPI + sub;
+          if constexpr (COARSE) {
+            from[k] = __shfl_sync(0xffffffffu, at[0], r >> 4 & 7);
+            from[k] = from[k] == kNone || r >= left ? kNone : from[k] + (r & 15) * slot_units;
+          } else {
+            from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
+          }
+        }
         const uint32_t dst = raw0 + ask_stage * Sh::kRaw + pw * 512;
         const uint4* const src = static_cast<const uint4*>(base) + chunk;
 #pragma unroll
@@ -388,26 +399,25 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
       };
       // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
       const auto ask_keys = [&](int t) {
-        int page[LOOKS];
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) page[j] = read(t, 0, j);
+        left = len - t * KT;
+        // (places below 2^32, so the products may be taken in 32 bits)
         if constexpr (COARSE) {
-          const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, run_page = read(t, 3, 0);
-          const bool good = run < KT && pos < len && run_page >= 0 && run_page < a.cache.n_pages;
-          copy4(looked0 + looked(t, 1, 0) * 4, (lane < KT / 16 ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(run_page, in_page) : 0), good);
-        }
+          const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, 0);
+          const bool there = run < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
+          at[0] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
+          copy4(looked0 + looked(t, 1, 0) * 4, (lane < KT / 16 ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(page, in_page) : 0), good);
+          next_hole[0] = __ballot_sync(0xffffffffu, lane < KT / 16 && there && !good);  // a bit a run
+        } else {
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size;
-          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
-          // (below 2^32, so the product may be taken in 32 bits)
-          at[j] = good ? (uint32_t)page[j] * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
-          if constexpr (!COARSE) {
-            const long long sc = good ? scale_place(page[j], in_page) : 0;
+          for (int j = 0; j < LOOKS; ++j) {
+            const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, j);
+            const bool there = r < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
+            at[j] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
+            const long long sc = good ? scale_place(page, in_page) : 0;
             copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
             copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
+            next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
           }
-          next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
         }
         if (t + 1 < wk.t1) look(t + 1);
         ask(a.cache.k);
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
           }
         }
         if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
-        if (lane == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
+        if (lane == 0 && (!COARSE || pw == 0)) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
         put(slot);
         filled(slot);
         if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -887,7 +897,9 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
               if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
               const int v = len - base - 32 * w;  // positions of the word
               bits = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
-              if (holes) {
+              if (Q8 && COARSE) {  // a bit a run of 16 rows
+                bits &= ~((hole[0] >> (2 * w) & 1 ? 0xffffu : 0u) | (hole[0] >> (2 * w) & 2 ? 0xffff0000u : 0u));
+              } else if (holes) {
 #pragma unroll 1
                 for (int j = 0; j < 32; ++j) {
                   const int r = 32 * w + j, g = r / RPI, q = g / kProducers * RPI + r % RPI;
