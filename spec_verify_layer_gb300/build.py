@@ -9,9 +9,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("moe_verify.cu", "moe_prefill.cu", "moe_round_map.cu", "moe_qk_rope.cu",
                                                   "moe_tree_attn.cu", "moe_logprob.cu", "moe_cache8.cu", "moe_cache8_attn.cu",
+                                                  "moe_cache8_attn_i8.cu",
                                                   "moe_verify_drafts.cu", "moe_host.cpp")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("moe_internal.h", "moe_common.cuh", "moe_round_ops.cuh", "moe_vocab.cuh",
-                                                  "moe_attn_parts.cuh", "moe_few_rows.cuh", "moe_tree_attn.cuh")] + [
+                                                  "moe_attn_parts.cuh", "moe_few_rows.cuh", "moe_tree_attn.cuh", "moe_cache8_attn.cuh")] + [
     os.path.join(ROOT, "include", "moe_verify.h")]
 OUT = os.path.join(HERE, "libmoeverify.so")
 

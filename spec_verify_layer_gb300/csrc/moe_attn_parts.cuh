@@ -95,7 +95,7 @@ struct Control {
   unsigned long long full[kMaxSlots], empty[kMaxSlots];
   unsigned long long s_full[2], p_full[4], o_done[2], q_ready, drain;  // p_full: [buffer][part]
   unsigned long long bad[8];          // per unit: tree rows with values that are not finite
-  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes, COARSE: a bit a run of 16)
+  __align__(16) unsigned hole[8][8];  // per tile: rows without a page, two words for each producer's rows (codes: a bit a run)
   int red[kThreads / 32], redn[kThreads / 32];
   // the block's share of the list: places [w0, w1) of total, from start_off of request start_b on
   int total, w0, w1, start_off;

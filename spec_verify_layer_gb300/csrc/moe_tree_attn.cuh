@@ -67,13 +67,14 @@ namespace {
 
 // ---- the kernel -------------------------------------------------------------------------
 
-// FMT: the type of q, cache and out (16-bit cache), or of the codes.  COARSE: a scale stands for 16 keys or
-// more.  NT: codes, groups of 8 NT query rows, without tensor memory; 0: with.
-template <typename A, int FMT, int D, bool COARSE, int NT>
+// FMT: the type of q, cache and out (16-bit cache), or of the codes.  RUN: keys that one scale stands for,
+// 16 (also more) or 8; 0: fewer.  NT: codes, groups of 8 NT query rows, without tensor memory; 0: with.
+template <typename A, int FMT, int D, int RUN, int NT>
 __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
     k_tree_attn(const __grid_constant__ A a, const __grid_constant__ Plan p) {
   using Sh = Shape<A, D>;
-  constexpr bool Q8 = kQ8<A>;
+  constexpr bool Q8 = kQ8<A>, COARSE = RUN > 0;
+  constexpr int LOOK = COARSE ? RUN : 16, RUNS = kKeyTile<D> / LOOK;  // COARSE: rows that are looked up together, and how many such
   constexpr int DT = Q8 ? MOE_F16 : FMT;  // of the products
   constexpr int KT = Sh::KT, NS = Sh::NS, CPR = Sh::CPR, CC = Sh::CC, RPI = Sh::RPI, kBlock = NT > 0 ? kFewThreads<D, NT> : kThreads;
   constexpr int MG = NT > 0 ? 8 * NT : Sh::MG;  // query rows of a group
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
       unsigned hole[2], next_hole[2] = {0, 0};
       uint32_t at[LOOKS];  // in units of 16 bytes
       // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
-      // scale.  COARSE: lanes 0 .. KT/8 - 1 look up runs of 16 keys, once for keys and once for values: page
+      // scale.  COARSE: lanes 0 .. 2 RUNS - 1 look up runs of RUN keys, once for keys and once for values: page
       // (0) and scale (1).
       const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 3 + what) * LOOKS + j) * 32 + lane; };
       const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
         const bool there = r < KT && pos < len;
         copy4(looked0 + looked(t, what, j) * 4, table + (there ? column(pos) : 0), there);
       };
-      const int run = lane < KT / 8 ? (lane & (KT / 16 - 1)) * 16 : KT;
+      const int run = lane < 2 * RUNS ? (lane & (RUNS - 1)) * LOOK : KT;
       const auto look = [&](int t) {
         if constexpr (COARSE) {
           look_at(t, run, 0, 0);
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
         for (int k = 0; k < Sh::STEPS; ++k) {
           const int r = (k * kProducers + pw) * RPI + sub;
           if constexpr (COARSE) {
-            from[k] = __shfl_sync(0xffffffffu, at[0], r >> 4 & 7);
-            from[k] = from[k] == kNone || r >= left ? kNone : from[k] + (r & 15) * slot_units;
+            from[k] = __shfl_sync(0xffffffffu, at[0], r / LOOK & (RUNS - 1));
+            from[k] = from[k] == kNone || r >= left ? kNone : from[k] + (r & (LOOK - 1)) * slot_units;
           } else {
             from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
           }
@@ -405,8 +406,8 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
           const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, 0);
           const bool there = run < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
           at[0] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
-          copy4(looked0 + looked(t, 1, 0) * 4, (lane < KT / 16 ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(page, in_page) : 0), good);
-          next_hole[0] = __ballot_sync(0xffffffffu, lane < KT / 16 && there && !good);  // a bit a run
+          copy4(looked0 + looked(t, 1, 0) * 4, (lane < RUNS ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(page, in_page) : 0), good);
+          next_hole[0] = __ballot_sync(0xffffffffu, lane < RUNS && there && !good);  // a bit a run
         } else {
 #pragma unroll
           for (int j = 0; j < LOOKS; ++j) {
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
         unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
 #pragma unroll 1
         for (int k = 0; k < Sh::STEPS; ++k) {
-          const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r >> 4 : k * RPI + sub;
+          const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r / LOOK : k * RPI + sub;
           if (r >= KT) break;
           uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
           if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
@@ -502,9 +503,9 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
         unsigned zero[2] = {0, 0};
         float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
         if constexpr (COARSE) {
-          const bool of_value = lane >= KT / 16;
+          const bool of_value = lane >= RUNS;
           const float s = of_value ? value_scale(key[0], flags) : scale_of(key[0], flags);
-          zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> (KT / 16);
+          zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> RUNS;
           if (run < KT) put_scale(sc + run, s, of_value);
         } else {
 #pragma unroll
@@ -897,8 +898,10 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
               if (k < 32) bits |= (unsigned)(k > 0 ? tree << k : k > -64 ? tree >> -k : 0ull);
               const int v = len - base - 32 * w;  // positions of the word
               bits = v >= 32 ? bits : v > 0 ? bits & ((1u << v) - 1) : 0u;
-              if (Q8 && COARSE) {  // a bit a run of 16 rows
-                bits &= ~((hole[0] >> (2 * w) & 1 ? 0xffffu : 0u) | (hole[0] >> (2 * w) & 2 ? 0xffff0000u : 0u));
+              if (Q8 && COARSE) {  // a bit a run
+#pragma unroll
+                for (int j = 0; j < 32; j += LOOK)
+                  if (hole[0] >> ((32 * w + j) / LOOK) & 1) bits &= ~(((1u << LOOK) - 1) << j);
               } else if (holes) {
 #pragma unroll 1
                 for (int j = 0; j < 32; ++j) {
@@ -933,13 +936,13 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
                 // to powers of two with the value's scale in them: s * key's scale * row's factor +
                 // log2(value's scale)
 #pragma unroll
-                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {
+                for (int j = 0; j < 64; j += COARSE ? LOOK : 4) {
                   const float4* const ks = scales + (64 * half + j) / 4;
                   if constexpr (COARSE) {
                     const float f = ks->x * row_factor, lv = ks[KT / 4].x;
                     const Pair f2 = pair(f, f), lv2 = pair(lv, lv);
 #pragma unroll
-                    for (int i = j; i < j + 16; i += 2) scaled(x + i, f2, lv2);
+                    for (int i = j; i < j + LOOK; i += 2) scaled(x + i, f2, lv2);
                   } else {
                     const float4 s = *ks, lv = ks[KT / 4];
                     scaled(x + j, pair(s.x * row_factor, s.y * row_factor), pair(lv.x, lv.y));
@@ -1000,7 +1003,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
               const Pair shift2 = pair(-shift, -shift);
               if constexpr (Q8) {
 #pragma unroll
-                for (int j = 0; j < 64; j += COARSE ? 16 : 4) {  // the sum is of the weights without the values' scales
+                for (int j = 0; j < 64; j += COARSE ? LOOK : 4) {  // the sum is of the weights without the values' scales
                   const float4* const iv = scales + 2 * (KT / 4) + (64 * half + j) / 4;
                   const auto weights = [&](int i, Pair inv, Pair& sum) {
                     const float2 z = split(add2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), shift2));
@@ -1011,7 +1014,7 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
                   if constexpr (COARSE) {
                     Pair part[2] = {0, 0};
 #pragma unroll
-                    for (int i = j; i < j + 16; i += 2) weights(i, 0, part[i / 2 & 1]);
+                    for (int i = j; i < j + LOOK; i += 2) weights(i, 0, part[i / 2 & 1]);
                     const float inv = iv->x;
                     sums[0] = fma2(add2(part[0], part[1]), pair(inv, inv), sums[0]);
                   } else {
@@ -1227,7 +1230,7 @@ Workspace layout(const A& a) {
   return w;
 }
 
-template <typename A, int FMT, int D, bool COARSE = true, int NT = 0>
+template <typename A, int FMT, int D, int RUN = 16, int NT = 0>
 int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   using Sh = Shape<A, D>;
   constexpr int kSmem = 227 * 1024;
@@ -1242,7 +1245,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && ready != dev) {
-    e = cudaFuncSetAttribute(k_tree_attn<A, FMT, D, COARSE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(k_tree_attn<A, FMT, D, RUN, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess) ready = dev;
   }
   if (e != cudaSuccess) return launch_status(e);
@@ -1256,7 +1259,7 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, COARSE, NT>, a, p));
+  return launch_status(cudaLaunchKernelEx(&cfg, k_tree_attn<A, FMT, D, RUN, NT>, a, p));
 }
 
 // Checks, workspace and what the host computes, alike for both caches.
