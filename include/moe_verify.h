@@ -297,8 +297,8 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const u
  * the paged cache (moe_qk_rope_cache), the attention of the drafted rows over that cache
  * (moe_tree_attention), the log probabilities of the drafted tokens under the logits
  * (moe_token_logprobs), and which of them stand (moe_verify_drafts).  The cache may be in 8
- * bits (moe_cache8_append, moe_cache8_read, moe_tree_attention8).  The pages leave these steps to the surrounding engine; their
- * definitions here are this library's own.
+ * bits (moe_cache8_append, moe_cache8_read, moe_tree_attention8).  The pages leave these steps
+ * to the surrounding engine; their definitions here are this library's own.
  *
  * Conventions, besides those at the top of this file:
  *   - No handle.  A call runs on the current device and takes one descriptor struct that
@@ -525,9 +525,9 @@ typedef struct moe_kv_cache8 {
  *   exact but for codes that fall below the smallest normal one; with MOE_I8 a value
  *   that was rounded again is off by less than one step of its present scale (rounded once:
  *   half a step).  Infinities become the largest code with their sign, NaN 0 (rows and what
- *   is held alike), and both raise MOE_DEV_VALUE.  The last block of a context is written as a whole, so it must not be shared
- *   with another request (a shared prefix ends with a block); no two rows of a call may
- *   fall into one slot.
+ *   is held alike), and both raise MOE_DEV_VALUE.  The last block of a context is written as a
+ *   whole, so it must not be shared with another request (a shared prefix ends with a block);
+ *   no two rows of a call may fall into one slot.
  *   read: k, v = code * scale, rounded once to dtype.
  *   k, v [n_rows][kv_heads][D] of MOE_BF16, MOE_F16 or MOE_F32, the strides from row to row in
  *   elements (multiples of 8); they must not lie in the cache.  Rows that belong to no request
@@ -659,8 +659,8 @@ int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, 
  *   elements; draft_probs [n_rows][vocab] of draft_dtype, draft_stride; uniform [n_rows] and
  *   noise [n_req][vocab] (noise_stride) fp32; any alignment of their element types.  n_req
  *   1..16384, n_rows 0..2^20, vocab 1..2^24, inv_temperature > 0.
- * ws: moe_verify_drafts_workspace_bytes (it goes by n_req and n_rows; 0 for arguments that the
- * call would refuse), 16-byte aligned, set to zero once before its first use; every call
+ * ws: moe_verify_drafts_workspace_bytes (it goes by n_req, n_rows and vocab; 0 for arguments
+ * that the call would refuse), 16-byte aligned, set to zero once before its first use; every call
  * leaves it ready for the next, whatever its shape. */
 typedef struct moe_verify_args {
   const void* logits;

@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kThreads) k_walk(const __grid_constant__ moe_v
       Key top = lane < p.row_slices ? p.keys[(long long)(s + i) * p.row_slices + lane] : 0;
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) top = max_key(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) w.best[i] = top == 0 ? -1 : top == ~0ull ? -2 : key_id(top);
+      // (requests that overlap, of which one may have no sums, must not bring tokens that are none)
+      if (lane == 0) w.best[i] = top == ~0ull ? -2 : top == 0 || (unsigned)key_id(top) >= (unsigned)a.vocab ? -1 : key_id(top);
     } else if (w.inner[i]) {
       const float2 part = lane < p.row_slices ? p.sums[(long long)(s + i) * p.row_slices + lane] : make_float2(-INFINITY, 0.f);
       float m = part.x;

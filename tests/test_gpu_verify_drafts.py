@@ -355,3 +355,20 @@ def test_a_replayed_graph_follows_contents_on_another_stream(mode):
         for a, b in zip(outs, case.plain()):
             np.testing.assert_array_equal(a.cpu().numpy(), b)
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("mode", ["greedy", "lookup", "drawn"])
+def test_lengths_that_descend_bring_no_token_outside_the_vocabulary(mode):
+    big = VerifyCase(60, [8, 8, 8], 4000, mode=mode)
+    args = big.args(big.outputs(), word())
+    ws = torch.zeros(mv.moe_verify_drafts_workspace_bytes(args), dtype=torch.uint8, device=DEV)
+    mv.moe_verify_drafts(args, at(ws), ws.numel(), stream())  # leaves sums and tokens of its own behind
+    c = VerifyCase(61, [10, 4, 6], 100, mode=mode)
+    c.start = np.array([0, 10, 5, 20])  # the third request's rows are partly the first's
+    outs, status = c.outputs(), word()
+    mv.moe_verify_drafts(c.args(outs, status), at(ws), ws.numel(), stream())
+    accepted, path, follow = (t.cpu().numpy() for t in outs)
+    assert int(status.item()) & mv.MOE_DEV_LENGTH
+    assert accepted[1] == 0 and follow[1] == -1
+    assert np.all((accepted >= 0) & (accepted < 15)) and np.all((follow >= -1) & (follow < 100))
+    assert np.all((path >= -1) & (path < 15))
