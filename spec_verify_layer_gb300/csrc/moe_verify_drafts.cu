@@ -14,6 +14,12 @@
 // order between slices.  The request's block that ends last joins the slices, by (ratio, lower id), so
 // it does not matter which one that is.
 //
+// Five rows of 32,003 in fp32 (one request) 15.7 us: latency of three launches in a chain, each of which waits for
+// the one before.  64 chains of up to 8 rows of 131,072 in bf16, with draft probabilities (101 MB), 52.2 us:
+// sums 17 (5.9 TB/s), walk 8.5, draws 33 in profiles of each alone; the draws are bound by what an
+// entry costs (logit, noise and draft probability each unpacked, compared in products).  24 trees of
+// 8 to 48 rows of 129,283 in fp32 (183 MB), 87.6 us: sums 50, walk 12.5, draws 22.
+//
 // The exponent (x - m) c is taken with c in two parts (c >= hi, lo > 0, so that -infinity stays
 // what it is): with c rounded to 32 bits probabilities far from the maximum would be off by
 // some 1e-6, and a decision lies that near its border far more often than by the 1e-7 of the
@@ -27,9 +33,13 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTree = 64;
 constexpr int kVecs = 4;         // vectors a thread has on their way
 constexpr int kMaxSlices = 32;
-// Rows (of sums, most blocks of which have none to take) and requests (of draws) are cut into slices up to
-// about so many blocks, of so many entries at least.
-constexpr int kSumBlocks = 1500, kDrawBlocks = 456, kSliceMin = 2048;
+// Rows (of sums, most blocks of which have none to take) are cut into slices up to about so many blocks, requests
+// (of draws) while the blocks stay within the 608 that run at once (64 chains, 512 blocks, 52.7 us with the 456
+// of three blocks an SM and 45.5 with 608; 24 trees 84 with 768 blocks and 80.6 with 384); slices have so
+// many entries at least.
+// Long slices (in bytes) of rows are cut once more, since the last of them to begin end alone: 24 trees of
+// fp32 rows 88.4 us without, 84.0 so; 64 chains of bf16 rows, whose slices would be 16 KB then, 52.5 and 55.9.
+constexpr int kSumBlocks = 1500, kDrawBlocks = 304, kSliceMin = 2048, kLongSlice = 48 << 10;
 constexpr int kCounters = (int)(kCounterBytes / sizeof(unsigned));
 
 // Ratios and ids of candidates as keys: the larger ratio, of equal ones the lower id; 0: none.
@@ -386,7 +396,7 @@ __global__ void __launch_bounds__(kThreads) k_walk(const __grid_constant__ moe_v
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) k_draw(const __grid_constant__ moe_verify_args a, const __grid_constant__ Plan p) {
+__global__ void __launch_bounds__(kThreads, 4) k_draw(const __grid_constant__ moe_verify_args a, const __grid_constant__ Plan p) {
   constexpr int N = Vec<DT>::N;
   __shared__ Drawn all[kWarps];
   __shared__ int out[kTree], ends;
@@ -585,9 +595,11 @@ int check(const moe_verify_args* args) {
   return MOE_OK;
 }
 
-int slices_for(int64_t rows, int vocab, int blocks) {
+int slices_for(int64_t rows, int vocab, int size, int blocks) {
   int n = 1;
-  while (n < kMaxSlices && rows * n < blocks && vocab / (2 * n) >= kSliceMin) n *= 2;
+  while (n < kMaxSlices && vocab / (2 * n) >= kSliceMin &&
+         (rows * n < blocks || (rows * n < 2 * blocks && (int64_t)vocab / (2 * n) * size >= kLongSlice)))
+    n *= 2;
   return n;
 }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -598,8 +610,8 @@ struct Workspace {
 };
 Workspace layout(const moe_verify_args& a) {
   Workspace w{};
-  w.row_slices = slices_for(a.n_rows, a.vocab, kSumBlocks);
-  w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab, kDrawBlocks) : 1;
+  w.row_slices = slices_for(a.n_rows, a.vocab, a.dtype == MOE_F32 ? 4 : 2, kSumBlocks);
+  w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab, 0, kDrawBlocks) : 1;
   w.sums = kCounterBytes;
   w.drawn = w.sums + up256((size_t)a.n_rows * w.row_slices * sizeof(Key));
   w.end = w.drawn + up256((size_t)a.n_req * w.draw_slices * sizeof(Drawn));
