@@ -15,15 +15,15 @@
 // the prompts below, 89.1 -> 69.6 with int8, whose rounding is one addition, all with three thread
 // blocks an SM).
 //   One token 6.2 us: latency (lengths, page, rows, one after the other).  200 requests of up to 9 rows,
-// 8 heads of 64, 18.7 us: the same, and groups that look for the blocks of ragged rows.  Prompts of
-// 20,011 to 32,768 rows, 4 heads of 128 (243 MB), 63.8 us, 3.8 TB/s, 56 % of measured: a group holds
+// 8 heads of 64, 17.8 us: the same, and groups that look for the blocks of ragged rows.  Prompts of
+// 20,011 to 32,768 rows, 4 heads of 128 (243 MB), 63.5 us, 3.8 TB/s, 56 % of measured: a group holds
 // one task's 4 KB at a time and waits for it before it stores, and two thread blocks an SM hold as many
 // tasks as registers allow.  Three with the spills that they bring 69.0 us, four with half as many
 // elements kept and the rest read again 81.8; fp32 rows 76 (88 with half of them kept).
 //
 // Read.  A thread takes 16 codes of four rows at a time; a row's request, page and scale's place are looked
 // up once a thread block.  1,500 rows, 4 heads of 128, 6.6 us: latency.  Five contexts of 1,001 to 65,536 rows, 8
-// heads of 64 (511 MB), 98.3 us, 5.2 TB/s, 76 % of measured, two thirds of it written; 122 with a look-up a warp.
+// heads of 64 (511 MB), 98.0 us, 5.2 TB/s, 76 % of measured, two thirds of it written; 122 with a look-up a warp.
 #include "moe_round_ops.cuh"
 
 namespace moe {

@@ -1,15 +1,25 @@
-// Attention over codes for few query rows a key/value head (moe_cache8_attn.cu): up to 8 NT of them.
+// Attention over codes for few query rows a key/value head (moe_tree_attention8): up to 8 NT of them.
 //
-// Here the memory is the bound (with one row of 8 heads a tile of 128 keys of 128 elements takes 1,420
-// cycles of an SM's share of it), and turning codes into fp16 through shared memory for the tensor
-// memory path costs more than that: some 4,200 warp instructions a tile, 180 to 240 us for 64 requests
-// of one row over up to 8,192 keys in several forms.  So codes go straight into the registers of
-// mma.sync, 1,500 instructions a tile: S^T = K Q^T with keys as rows, O^T += V^T P^T with elements of
-// V as rows; both of a product's operands then have the query rows as their 8 columns.  A lane's
-// 16 bytes of a key are pairs along the product's depth as they lie (any order of elements does, if the
-// queries have the same); values are paired key by key with a byte permutation; P comes out of S by an
-// 8 x 8 transpose.  Eight or twelve warps take steps of 32 keys in turn, each with a ring of stages and a softmax
-// of its own, and are joined when the share of the head ends.
+// Mathematics, as in moe_tree_attn.cuh: scores times the key's scale, weights with the value's scale in
+// them, their sum from weight / scale; running maximum and sum a warp, joined when a head's share ends.
+//
+// Here the memory is the bound (with one row of 8 heads a tile of 128 keys of 128 elements takes
+// 1,420 cycles of an SM's share of it), and turning codes into fp16 through shared memory for the
+// tensor memory path costs more than that: some 4,200 warp instructions a tile, 176 to 240 us for 64
+// requests of one row over up to 8,192 keys in several forms.  So codes go straight into the registers
+// of mma.sync, 1,500 instructions a tile: S^T = K Q^T with keys as rows, O^T += V^T P^T with elements
+// of V as rows; both of a product's operands then have the query rows as their 8 columns.  A lane's
+// 16 bytes of a key are pairs along the product's depth as they lie (any order of elements does, if
+// the queries have the same); values are paired key by key with a byte permutation; P comes out of S
+// by an 8 x 8 transpose.  Eight or twelve warps take steps of 32 keys in turn, each with a ring of
+// stages and a softmax of its own, so that no barrier stands between a warp's loads and its products.
+//
+// 64 requests of one row over 4,096 to 8,192 keys, 32/4 heads of 128 (403 MB): 82.7 us, 4.9 TB/s, 71 %
+// of the 59 us that the bytes take; 88 with eight warps.  Bound: instructions issued and the latency of
+// a warp's own chain (copy, scores, weights, products), 12 warps being all that registers allow.
+// One row over up to 1,000 keys 12.3 us: latency, as for the 16-bit cache.  Six groups of 8 rows for
+// heads of 64 (33 ragged requests of up to 48 query rows) 108 us against 89 through tensor memory: sums of
+// that many rows leave registers for steps of 16 keys only.
 #pragma once
 
 #include "moe_attn_parts.cuh"
@@ -19,7 +29,8 @@ namespace {
 
 template <int D, int NT>
 struct FewShape {
-  // Twelve warps (and two stages each, if three are too large) where a warp's sums leave the registers for it, else eight and three.
+  // Twelve warps (and two stages each, if three are too large) where a warp's sums leave the registers
+  // for it, else eight and three.
   static constexpr int W = D / 16 * NT <= 8 ? 12 : 8, STAGES = W == 12 && D > 64 ? 2 : 3;
   static constexpr int KS = D == 256 ? 16 : 32;  // keys of a step
   static constexpr int kStage = 2 * KS * D;      // codes of keys and values

@@ -54,6 +54,22 @@
 // chain) or at all that a stream waits for in one go (267 against 260); the first half's
 // weights handed over in the middle of the second half's exponentials (263 against 256).
 //
+// A cache of 8 bits (moe_tree_attention8, more than 32 query rows a key/value head): the same kernel, with
+// producers that turn codes into fp16 on their way, which is exact, and fp16 products.  A key's scale
+// multiplies its scores.  A value's scale goes into the weights: with t = log2(e) s + log2(v_scale) the
+// weight 2^t is the softmax weight times the scale, what the codes have to be multiplied with; the
+// sum of the softmax weights is taken from the same numbers times 1 / v_scale.  So values need no
+// multiplication, and the running maximum is that of the weights as the product sees them, whose
+// fp16 places it has to keep (a scale far above the others is then no loss).
+// Full trees of the above sizes 396 us (16-bit cache 260): stages of raw codes leave room for three slots
+// of fp16 in place of five, so products wait for tiles (clocks of a producer for the keys and values of a
+// tile: copies asked for 1,390 cycles, scales 460, codes into fp16 1,160, before look-ups by runs) as
+// well as for the softmax, which has three more numbers to read a key.  33 ragged requests of up to 24
+// rows, 16/8 heads of 64, 89 us (55.8), bound by the same producers; 121 with the scales of blocks of
+// 8 tokens taken key by key.  Tried and slower: raw codes by the tensor memory accelerator (422; 183
+// against 176 for one row), a loader and six converters in sixteen warps (438 to 539: the softmax
+// spills at 128 registers).
+//
 // What is not seen gets the weight 0, but 0 times a cached NaN would still be NaN in the
 // product: slots past the last position are zero-filled, and the values of drafted rows
 // are looked over on their way: what is not finite becomes 0 in the slot and is added at
@@ -314,362 +330,363 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
     if (warp < kSoftmaxThreads / 32) join_splits(true);
   } else if (warp == 8 || warp == 9 || warp == 11) {
     if constexpr (Q8) {
-    // ---------------- producers of codes.  A warp's rows of a tile are dealt out as below, 16 codes
-    // a lane and step: they are copied into a ring of stages (keys and values of a tile in turn),
-    // read back by the lane that copied them, and written as fp16 into the tile's slot.  All that
-    // comes from memory comes by asynchronous copies, table entries and scales too: a register that
-    // waits for memory holds up every exchange and barrier behind it (they share few counters),
-    // 263 us against 438 with the codes in registers for 64 requests of one row over up to 8,192 keys
-    // with these in better and in worse order.
-    // Eight lanes side by side take four chunks each of two rows: their stores meet eight different
-    // banks of the swizzle.
-    constexpr int kBlocks = CC / 4;  // 64-element blocks of a row
-    const int pw = warp == 11 ? 2 : warp - 8, chunk = (lane & 3) | ((lane >> 3) & (kBlocks - 1)) << 2;
-    const int sub = (lane >> 2 & 1) | (lane / (8 * kBlocks)) << 1;
-    constexpr int LOOKS = Sh::LOOKS;
-    const auto row_of = [&](int j) {  // the j-th row that this lane looks up; KT and more: none
-      const int mine = 32 * j + lane;
-      return (mine / RPI * kProducers + pw) * RPI + mine % RPI;
-    };
-    constexpr uint32_t kNone = 0xffffffffu;
-    const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw) + lane * 16, looked0 = smem_u32(sm_looked);
-    const uint32_t page_units = (uint32_t)(a.cache.page_stride >> 4), slot_units = (uint32_t)(a.cache.slot_stride >> 4);
-    int slot = 0, tile_seq = 0, ask_stage = 0, put_stage = 0;
-    uint32_t phase = 1;  // the slots start empty
-    bool ok = true;
-    for (int seq = 0; ok && wk.more(); wk.next(a)) {
-      if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
-      const int len = wk.q.ctx + wk.q.n;
-      const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-      const uint32_t head_units = (uint32_t)(wk.h * a.cache.head_stride >> 4);
-      const long long scale_at = wk.h * a.cache.scale_head_stride;
-      if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
-        const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
-        const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
-        if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
-      }
-      unsigned hole[2], next_hole[2] = {0, 0};
-      uint32_t at[LOOKS];  // in units of 16 bytes
-      // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
-      // scale.  COARSE: lanes 0 .. 2 RUNS - 1 look up runs of RUN keys, once for keys and once for values: page
-      // (0) and scale (1).
-      const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 3 + what) * LOOKS + j) * 32 + lane; };
-      const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
-      const auto look_at = [&](int t, int r, int what, int j) {
-        const int pos = t * KT + r;
-        const bool there = r < KT && pos < len;
-        copy4(looked0 + looked(t, what, j) * 4, table + (there ? column(pos) : 0), there);
+      // ---------------- producers of codes.  A warp's rows of a tile are dealt out as below, 16 codes
+      // a lane and step: they are copied into a ring of stages (keys and values of a tile in turn),
+      // read back by the lane that copied them, and written as fp16 into the tile's slot.  All that
+      // comes from memory comes by asynchronous copies, table entries and scales too: a register that
+      // waits for memory holds up every exchange and barrier behind it (they share few counters).
+      // 64 requests of one row over up to 8,192 keys, when they still took this path: 438 us with the
+      // codes in registers, 263 with all exchanges ahead of the loads, 213 through the ring, 176 with a
+      // look-up a run of 16 keys.
+      // Eight lanes side by side take four chunks each of two rows: their stores meet eight different
+      // banks of the swizzle.
+      constexpr int kBlocks = CC / 4;  // 64-element blocks of a row
+      const int pw = warp == 11 ? 2 : warp - 8, chunk = (lane & 3) | ((lane >> 3) & (kBlocks - 1)) << 2;
+      const int sub = (lane >> 2 & 1) | (lane / (8 * kBlocks)) << 1;
+      constexpr int LOOKS = Sh::LOOKS;
+      const auto row_of = [&](int j) {  // the j-th row that this lane looks up; KT and more: none
+        const int mine = 32 * j + lane;
+        return (mine / RPI * kProducers + pw) * RPI + mine % RPI;
       };
-      const int run = lane < 2 * RUNS ? (lane & (RUNS - 1)) * LOOK : KT;
-      const auto look = [&](int t) {
-        if constexpr (COARSE) {
-          look_at(t, run, 0, 0);
-        } else {
-#pragma unroll
-          for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
+      constexpr uint32_t kNone = 0xffffffffu;
+      const uint32_t kv0 = smem_u32(sm_kv), raw0 = smem_u32(sm_raw) + lane * 16, looked0 = smem_u32(sm_looked);
+      const uint32_t page_units = (uint32_t)(a.cache.page_stride >> 4), slot_units = (uint32_t)(a.cache.slot_stride >> 4);
+      int slot = 0, tile_seq = 0, ask_stage = 0, put_stage = 0;
+      uint32_t phase = 1;  // the slots start empty
+      bool ok = true;
+      for (int seq = 0; ok && wk.more(); wk.next(a)) {
+        if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
+        const int len = wk.q.ctx + wk.q.n;
+        const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
+        const uint32_t head_units = (uint32_t)(wk.h * a.cache.head_stride >> 4);
+        const long long scale_at = wk.h * a.cache.scale_head_stride;
+        if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
+          const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
+          const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
+          if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
         }
-      };
-      const auto read = [&](int t, int what, int j) { return *reinterpret_cast<volatile int*>(sm_looked + looked(t, what, j) * 4); };
-      const auto scale_place = [&](int page, int in_page) {
-        return page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
-      };
-      int left = 0;  // rows up to the end, of the tile that `at` is of
-      const auto ask = [&](const void* base) {  // that tile, into the next stage
-        uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int r = (k * kProducers + pw) * RPI + sub;
+        unsigned hole[2], next_hole[2] = {0, 0};
+        uint32_t at[LOOKS];  // in units of 16 bytes
+        // Of the j-th row that this lane looks up, of odd and even tiles: page (0), key's (1) and value's (2)
+        // scale.  COARSE: lanes 0 .. 2 RUNS - 1 look up runs of RUN keys, once for keys and once for values: page
+        // (0) and scale (1).
+        const auto looked = [&](int t, int what, int j) { return (((pw * 2 + (t & 1)) * 3 + what) * LOOKS + j) * 32 + lane; };
+        const auto column = [&](int pos) { return (int)(__umulhi((unsigned)pos << 1, p.page_mul) >> (p.page_shift - 31)); };
+        const auto look_at = [&](int t, int r, int what, int j) {
+          const int pos = t * KT + r;
+          const bool there = r < KT && pos < len;
+          copy4(looked0 + looked(t, what, j) * 4, table + (there ? column(pos) : 0), there);
+        };
+        const int run = lane < 2 * RUNS ? (lane & (RUNS - 1)) * LOOK : KT;
+        const auto look = [&](int t) {
           if constexpr (COARSE) {
-            from[k] = __shfl_sync(0xffffffffu, at[0], r / LOOK & (RUNS - 1));
-            from[k] = from[k] == kNone || r >= left ? kNone : from[k] + (r & (LOOK - 1)) * slot_units;
+            look_at(t, run, 0, 0);
           } else {
-            from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
+#pragma unroll
+            for (int j = 0; j < LOOKS; ++j) look_at(t, row_of(j), 0, j);
           }
-        }
-        const uint32_t dst = raw0 + ask_stage * Sh::kRaw + pw * 512;
-        const uint4* const src = static_cast<const uint4*>(base) + chunk;
+        };
+        const auto read = [&](int t, int what, int j) { return *reinterpret_cast<volatile int*>(sm_looked + looked(t, what, j) * 4); };
+        const auto scale_place = [&](int page, int in_page) {
+          return page * a.cache.scale_page_stride + (in_page >> p.block_shift) * a.cache.scale_block_stride + scale_at;
+        };
+        int left = 0;  // rows up to the end, of the tile that `at` is of
+        const auto ask = [&](const void* base) {  // that tile, into the next stage
+          uint32_t from[Sh::STEPS];               // (all exchanges ahead of the copies)
 #pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int g = k * kProducers + pw;
-          const bool there = from[k] != kNone;
-          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI)
-            copy16(dst + k * kProducers * 512, src + (there ? from[k] : 0), there);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (++ask_stage == Sh::kRawStages) ask_stage = 0;
-      };
-      // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
-      const auto ask_keys = [&](int t) {
-        left = len - t * KT;
-        // (places below 2^32, so the products may be taken in 32 bits)
-        if constexpr (COARSE) {
-          const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, 0);
-          const bool there = run < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
-          at[0] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
-          copy4(looked0 + looked(t, 1, 0) * 4, (lane < RUNS ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(page, in_page) : 0), good);
-          next_hole[0] = __ballot_sync(0xffffffffu, lane < RUNS && there && !good);  // a bit a run
-        } else {
-#pragma unroll
-          for (int j = 0; j < LOOKS; ++j) {
-            const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, j);
-            const bool there = r < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
-            at[j] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
-            const long long sc = good ? scale_place(page, in_page) : 0;
-            copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
-            copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
-            next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
-          }
-        }
-        if (t + 1 < wk.t1) look(t + 1);
-        ask(a.cache.k);
-      };
-      const auto put = [&](int slot) {  // the next stage's codes into a slot
-        const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
-        const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
-        uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k)
-          if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
-            x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int g = k * kProducers + pw, r = g * RPI + sub;
-          if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
-            const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
-            const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
-          }
-        }
-        if (++put_stage == Sh::kRawStages) put_stage = 0;
-      };
-      // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
-      // are noted, and added at the end to the rows that see them.
-      const auto clean = [&](const unsigned (&zero)[2], int node0) {
-        unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
-#pragma unroll 1
-        for (int k = 0; k < Sh::STEPS; ++k) {
-          const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r / LOOK : k * RPI + sub;
-          if (r >= KT) break;
-          uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
-          if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
-          if (FMT == MOE_E4M3 && r >= node0) {
-            const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
-            if (n.x | n.y | n.z | n.w) {
-              *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-              atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
+          for (int k = 0; k < Sh::STEPS; ++k) {
+            const int r = (k * kProducers + pw) * RPI + sub;
+            if constexpr (COARSE) {
+              from[k] = __shfl_sync(0xffffffffu, at[0], r / LOOK & (RUNS - 1));
+              from[k] = from[k] == kNone || r >= left ? kNone : from[k] + (r & (LOOK - 1)) * slot_units;
+            } else {
+              from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
             }
           }
-        }
-      };
-      // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum
-      // and in their products alike); values of scale 0 are zeros
-      const auto put_scale = [&](float* sc, float s, bool of_value) {
-        float log, inv;
-        asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(s));
-        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
-        if (of_value) {
-          sc[KT] = s == 0.f ? kNoValueLog : log;
-          sc[2 * KT] = s == 0.f ? kNoValueInverse : inv;
-        } else {
-          sc[0] = s;
-        }
-      };
-      const auto filled = [&](int slot) {  // what the lanes wrote, before the tensor cores read it
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&ct.full[slot]);
-      };
-      look(wk.t0);
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-      ask_keys(wk.t0);
-      ask(a.cache.v);
-      for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
-        const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
-        const bool more = t + 1 < wk.t1;
-        // keys, scales, and the next tile's pages are there; its values are on their way
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        hole[0] = next_hole[0];
-        hole[1] = next_hole[1];
-        float key[LOOKS], value[LOOKS];
+          const uint32_t dst = raw0 + ask_stage * Sh::kRaw + pw * 512;
+          const uint4* const src = static_cast<const uint4*>(base) + chunk;
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          if (j == 0 || !COARSE) key[j] = __int_as_float(read(t, 1, j));
-          if (!COARSE) value[j] = __int_as_float(read(t, 2, j));
-        }
-        if (more) ask_keys(t + 1);
-        ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
-        if (!ok) break;
-        unsigned zero[2] = {0, 0};
-        float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
-        if constexpr (COARSE) {
-          const bool of_value = lane >= RUNS;
-          const float s = of_value ? value_scale(key[0], flags) : scale_of(key[0], flags);
-          zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> RUNS;
-          if (run < KT) put_scale(sc + run, s, of_value);
-        } else {
+          for (int k = 0; k < Sh::STEPS; ++k) {
+            const int g = k * kProducers + pw;
+            const bool there = from[k] != kNone;
+            if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI)
+              copy16(dst + k * kProducers * 512, src + (there ? from[k] : 0), there);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (++ask_stage == Sh::kRawStages) ask_stage = 0;
+        };
+        // tile t's rows from their pages (which are there), their scales, its keys, and the pages of the next
+        const auto ask_keys = [&](int t) {
+          left = len - t * KT;
+          // (places below 2^32, so the products may be taken in 32 bits)
+          if constexpr (COARSE) {
+            const int pos = t * KT + run, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, 0);
+            const bool there = run < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
+            at[0] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
+            copy4(looked0 + looked(t, 1, 0) * 4, (lane < RUNS ? a.cache.k_scale : a.cache.v_scale) + (good ? scale_place(page, in_page) : 0), good);
+            next_hole[0] = __ballot_sync(0xffffffffu, lane < RUNS && there && !good);  // a bit a run
+          } else {
 #pragma unroll
-          for (int j = 0; j < LOOKS; ++j) {
-            const int r = row_of(j);
-            const float ks = scale_of(key[j], flags), vs = value_scale(value[j], flags);
-            zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);
-            if (r < KT) {
-              put_scale(sc + r, ks, false);
-              put_scale(sc + r, vs, true);
+            for (int j = 0; j < LOOKS; ++j) {
+              const int r = row_of(j), pos = t * KT + r, in_page = pos - column(pos) * a.cache.page_size, page = read(t, 0, j);
+              const bool there = r < KT && pos < len, good = there && page >= 0 && page < a.cache.n_pages;
+              at[j] = good ? (uint32_t)page * page_units + (uint32_t)in_page * slot_units + head_units : kNone;
+              const long long sc = good ? scale_place(page, in_page) : 0;
+              copy4(looked0 + looked(t, 1, j) * 4, a.cache.k_scale + sc, good);
+              copy4(looked0 + looked(t, 2, j) * 4, a.cache.v_scale + sc, good);
+              next_hole[j] = __ballot_sync(0xffffffffu, there && !good);
             }
           }
-        }
-        if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
-        if (lane == 0 && (!COARSE || pw == 0)) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
-        put(slot);
-        filled(slot);
-        if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");
-        ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status));
-        if (!ok) break;
-        const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
-        if ((zero[0] | zero[1]) || (FMT == MOE_E4M3 && node0 < KT)) clean(zero, node0);
-        if (more) ask(a.cache.v);  // (into the keys' stage)
-        put(v_slot);
-        filled(v_slot);
-        slot += 2;
-        if (slot >= p.nslot) {
-          slot -= p.nslot;
-          phase ^= 1;
-        }
-      }
-      ++seq;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-    // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
-    // g = k * kProducers + its number
-    const int pw = warp == 11 ? 2 : warp - 8, chunk = lane % CC, sub = lane / CC;
-    constexpr int LOOKS = (Sh::STEPS * RPI + 31) / 32;  // rows of a warp that a lane looks up
-    constexpr uint32_t kNone = 0xffffffffu;
-    const uint32_t kv0 = smem_u32(sm_kv);
-    int slot = 0, tile_seq = 0;
-    uint32_t phase = 1;  // the slots start empty
-    bool ok = true;
-    for (int seq = 0; ok && wk.more(); wk.next(a)) {
-      if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
-      const int len = wk.q.ctx + wk.q.n;
-      const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
-      const long long head_at = wk.h * a.cache.head_stride;
-      if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
-        const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
-        const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
-        if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
-      }
-      // the table entries of this lane's rows, a tile ahead of their use
-      int page[LOOKS];
-      const auto look = [&](int t) {
+          if (t + 1 < wk.t1) look(t + 1);
+          ask(a.cache.k);
+        };
+        const auto put = [&](int slot) {  // the next stage's codes into a slot
+          const uint32_t dst = kv0 + slot * Sh::kSlot + (chunk >> 2) * kBlk;
+          const unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
+          uint4 x[Sh::STEPS];  // (all loads ahead of the stores)
 #pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int mine = 32 * j + lane, r = (mine / RPI * kProducers + pw) * RPI + mine % RPI, pos = t * KT + r;
-          page[j] = 0;
-          if (r < KT && pos < len) page[j] = __ldg(table + (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift));
-        }
-      };
-      look(wk.t0);
-      for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
-        uint32_t at[LOOKS];  // places in the cache in units of 16 bytes
-        unsigned hole[2] = {0, 0};
-#pragma unroll
-        for (int j = 0; j < LOOKS; ++j) {
-          const int mine = 32 * j + lane, r = (mine / RPI * kProducers + pw) * RPI + mine % RPI, pos = t * KT + r;
-          const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
-          const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
-          at[j] = good ? (uint32_t)((page[j] * a.cache.page_stride + (pos - col * a.cache.page_size) * a.cache.slot_stride +
-                                     head_at) >> 3)
-                       : kNone;
-          hole[j] = __ballot_sync(0xffffffffu, there && !good);
-        }
-        if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
-        if (t + 1 < wk.t1) look(t + 1);
-        // a row's place to the lanes that copy it; all of them ahead of the copies, which would
-        // otherwise each wait for their own exchange
-        uint32_t from[Sh::STEPS];
-#pragma unroll
-        for (int k = 0; k < Sh::STEPS; ++k)
-          from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
-        const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
-        ok = bar_wait(&ct.empty[slot], phase, ct, a.dev_status) &&
-             bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        {
-          const uint4* k_src = static_cast<const uint4*>(a.cache.k) + chunk;
-          const uint4* v_src = static_cast<const uint4*>(a.cache.v) + chunk;
-          const uint32_t k_dst = kv0 + slot * Sh::kSlot + (chunk >> 3) * kBlk;
-          const uint32_t v_dst = kv0 + v_slot * Sh::kSlot + (chunk >> 3) * kBlk;
+          for (int k = 0; k < Sh::STEPS; ++k)
+            if ((k + 1) * kProducers <= KT / RPI || k * kProducers + pw < KT / RPI)
+              x[k] = *reinterpret_cast<const uint4*>(src + k * kProducers * 512);
 #pragma unroll
           for (int k = 0; k < Sh::STEPS; ++k) {
             const int g = k * kProducers + pw, r = g * RPI + sub;
-            const uint32_t to = r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-            const bool there = from[k] != kNone;
-            const uint32_t off = there ? from[k] : 0;
             if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
-              copy16(k_dst + to, k_src + off, there);
-              copy16(v_dst + to, v_src + off, there);
+              const uint32_t to = dst + r * 128 + (((2 * (chunk & 3)) ^ (r & 7)) << 4);
+              const uint4 lo = codes_to_half<FMT>(x[k].x, x[k].y), hi = codes_to_half<FMT>(x[k].z, x[k].w);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
             }
           }
-        }
+          if (++put_stage == Sh::kRawStages) put_stage = 0;
+        };
+        // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
+        // are noted, and added at the end to the rows that see them.
+        const auto clean = [&](const unsigned (&zero)[2], int node0) {
+          unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
-          if (kv == 1 && node0 < KT) {
-            // drafted rows' values: what is not finite is noted and taken out (a thread
-            // looks over what it copied itself)
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            const int from = max(node0, 0), to = min(KT, node0 + wk.q.n);
-#pragma unroll 1
-            for (int k = max(0, (from / RPI - pw) / kProducers); k < Sh::STEPS; ++k) {
-              const int r = (k * kProducers + pw) * RPI + sub;
-              if (r - sub >= to) break;
-              if (r < from || r >= to) continue;
-              uint4* v = reinterpret_cast<uint4*>(sm_kv + (size_t)slot * Sh::kSlot + (chunk >> 3) * kBlk + r * 128 +
-                                                  (((chunk & 7) ^ (r & 7)) << 4));
-              const uint4 x = *v;
-              uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              constexpr uint32_t kExp = DT == MOE_BF16 ? 0x7f80u : 0x7c00u;
-              bool found = false;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if ((w[j] & kExp) == kExp) {
-                  w[j] &= 0xffff0000u;
-                  found = true;
-                }
-                if ((w[j] >> 16 & kExp) == kExp) {
-                  w[j] &= 0xffffu;
-                  found = true;
-                }
-              }
-              if (found) {
-                *v = make_uint4(w[0], w[1], w[2], w[3]);
-                atomicOr(&ct.bad[seq & 7], 1ull << (r - node0));
+          for (int k = 0; k < Sh::STEPS; ++k) {
+            const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r / LOOK : k * RPI + sub;
+            if (r >= KT) break;
+            uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
+            if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
+            if (FMT == MOE_E4M3 && r >= node0) {
+              const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
+              if (n.x | n.y | n.z | n.w) {
+                *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+                atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
               }
             }
-            __syncwarp();
-            fence_async();
-            bar_arrive(&ct.full[slot]);
+          }
+        };
+        // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum
+        // and in their products alike); values of scale 0 are zeros
+        const auto put_scale = [&](float* sc, float s, bool of_value) {
+          float log, inv;
+          asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(s));
+          asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+          if (of_value) {
+            sc[KT] = s == 0.f ? kNoValueLog : log;
+            sc[2 * KT] = s == 0.f ? kNoValueInverse : inv;
           } else {
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&ct.full[slot])) : "memory");
+            sc[0] = s;
           }
-          if (lane == 0) {
-            if (kv == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
-            bar_arrive(&ct.full[slot]);  // behind what this lane wrote
-          }
+        };
+        const auto filled = [&](int slot) {  // what the lanes wrote, before the tensor cores read it
+          fence_async();
           __syncwarp();
-          if (++slot == p.nslot) {
-            slot = 0;
+          if (lane == 0) bar_arrive(&ct.full[slot]);
+        };
+        look(wk.t0);
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        ask_keys(wk.t0);
+        ask(a.cache.v);
+        for (int t = wk.t0; t < wk.t1; ++t, ++tile_seq) {
+          const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
+          const bool more = t + 1 < wk.t1;
+          // keys, scales, and the next tile's pages are there; its values are on their way
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          hole[0] = next_hole[0];
+          hole[1] = next_hole[1];
+          float key[LOOKS], value[LOOKS];
+#pragma unroll
+          for (int j = 0; j < LOOKS; ++j) {
+            if (j == 0 || !COARSE) key[j] = __int_as_float(read(t, 1, j));
+            if (!COARSE) value[j] = __int_as_float(read(t, 2, j));
+          }
+          if (more) ask_keys(t + 1);
+          ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[slot], phase, ct, a.dev_status));
+          if (!ok) break;
+          unsigned zero[2] = {0, 0};
+          float* const sc = sm_scale + (tile_seq & (Sh::kRing - 1)) * 3 * KT;
+          if constexpr (COARSE) {
+            const bool of_value = lane >= RUNS;
+            const float s = of_value ? value_scale(key[0], flags) : scale_of(key[0], flags);
+            zero[0] = __ballot_sync(0xffffffffu, of_value && run < KT && t * KT + run < len && s == 0.f) >> RUNS;
+            if (run < KT) put_scale(sc + run, s, of_value);
+          } else {
+#pragma unroll
+            for (int j = 0; j < LOOKS; ++j) {
+              const int r = row_of(j);
+              const float ks = scale_of(key[j], flags), vs = value_scale(value[j], flags);
+              zero[j] = __ballot_sync(0xffffffffu, r < KT && t * KT + r < len && vs == 0.f);
+              if (r < KT) {
+                put_scale(sc + r, ks, false);
+                put_scale(sc + r, vs, true);
+              }
+            }
+          }
+          if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
+          if (lane == 0 && (!COARSE || pw == 0)) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
+          put(slot);
+          filled(slot);
+          if (more) asm volatile("cp.async.wait_group 1;" ::: "memory");
+          else asm volatile("cp.async.wait_group 0;" ::: "memory");
+          ok = __all_sync(0xffffffffu, bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status));
+          if (!ok) break;
+          const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+          if ((zero[0] | zero[1]) || (FMT == MOE_E4M3 && node0 < KT)) clean(zero, node0);
+          if (more) ask(a.cache.v);  // (into the keys' stage)
+          put(v_slot);
+          filled(v_slot);
+          slot += 2;
+          if (slot >= p.nslot) {
+            slot -= p.nslot;
             phase ^= 1;
           }
         }
+        ++seq;
       }
-      ++seq;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // ---------------- producers: step k of a warp copies the rows [g RPI, (g + 1) RPI) of a tile,
+      // g = k * kProducers + its number
+      const int pw = warp == 11 ? 2 : warp - 8, chunk = lane % CC, sub = lane / CC;
+      constexpr int LOOKS = (Sh::STEPS * RPI + 31) / 32;  // rows of a warp that a lane looks up
+      constexpr uint32_t kNone = 0xffffffffu;
+      const uint32_t kv0 = smem_u32(sm_kv);
+      int slot = 0, tile_seq = 0;
+      uint32_t phase = 1;  // the slots start empty
+      bool ok = true;
+      for (int seq = 0; ok && wk.more(); wk.next(a)) {
+        if (wk.q.n * G <= member * Sh::MG || wk.t0 == wk.t1) continue;
+        const int len = wk.q.ctx + wk.q.n;
+        const int32_t* table = a.block_table + (long long)wk.b * a.table_width;
+        const long long head_at = wk.h * a.cache.head_stride;
+        if (pw == 2 && !(wk.t0 == 0 && wk.t1 == wk.q.tiles)) {  // who shares this head: read when the unit ends
+          const int at = ct.w1 - wk.left - wk.p0 + kUnit;       // the place of the head's first tile
+          const int first = gang_of(ct.total, ct.gangs, at), last = gang_of(ct.total, ct.gangs, at + wk.q.tiles - 1);
+          if (lane == 0) ct.split[wk.t0 == 0] = {wk.q.s, wk.q.n, wk.h, first, last - first + 1};
+        }
+        // the table entries of this lane's rows, a tile ahead of their use
+        int page[LOOKS];
+        const auto look = [&](int t) {
+#pragma unroll
+          for (int j = 0; j < LOOKS; ++j) {
+            const int mine = 32 * j + lane, r = (mine / RPI * kProducers + pw) * RPI + mine % RPI, pos = t * KT + r;
+            page[j] = 0;
+            if (r < KT && pos < len) page[j] = __ldg(table + (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift));
+          }
+        };
+        look(wk.t0);
+        for (int t = wk.t0; ok && t < wk.t1; ++t, ++tile_seq) {
+          uint32_t at[LOOKS];  // places in the cache in units of 16 bytes
+          unsigned hole[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < LOOKS; ++j) {
+            const int mine = 32 * j + lane, r = (mine / RPI * kProducers + pw) * RPI + mine % RPI, pos = t * KT + r;
+            const bool there = r < KT && pos < len, good = there && page[j] >= 0 && page[j] < a.cache.n_pages;
+            const int col = (int)(((unsigned long long)(unsigned)pos * p.page_mul) >> p.page_shift);
+            at[j] = good ? (uint32_t)((page[j] * a.cache.page_stride + (pos - col * a.cache.page_size) * a.cache.slot_stride +
+                                       head_at) >> 3)
+                         : kNone;
+            hole[j] = __ballot_sync(0xffffffffu, there && !good);
+          }
+          if (hole[0] | hole[1]) flags |= MOE_DEV_INDEX;
+          if (t + 1 < wk.t1) look(t + 1);
+          // a row's place to the lanes that copy it; all of them ahead of the copies, which would
+          // otherwise each wait for their own exchange
+          uint32_t from[Sh::STEPS];
+#pragma unroll
+          for (int k = 0; k < Sh::STEPS; ++k)
+            from[k] = __shfl_sync(0xffffffffu, LOOKS > 1 && k * RPI >= 32 ? at[LOOKS - 1] : at[0], (k * RPI + sub) & 31);
+          const int v_slot = slot + 1 < p.nslot ? slot + 1 : 0;
+          ok = bar_wait(&ct.empty[slot], phase, ct, a.dev_status) &&
+               bar_wait(&ct.empty[v_slot], phase ^ (v_slot == 0), ct, a.dev_status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          {
+            const uint4* k_src = static_cast<const uint4*>(a.cache.k) + chunk;
+            const uint4* v_src = static_cast<const uint4*>(a.cache.v) + chunk;
+            const uint32_t k_dst = kv0 + slot * Sh::kSlot + (chunk >> 3) * kBlk;
+            const uint32_t v_dst = kv0 + v_slot * Sh::kSlot + (chunk >> 3) * kBlk;
+#pragma unroll
+            for (int k = 0; k < Sh::STEPS; ++k) {
+              const int g = k * kProducers + pw, r = g * RPI + sub;
+              const uint32_t to = r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+              const bool there = from[k] != kNone;
+              const uint32_t off = there ? from[k] : 0;
+              if ((k + 1) * kProducers <= KT / RPI || g < KT / RPI) {
+                copy16(k_dst + to, k_src + off, there);
+                copy16(v_dst + to, v_src + off, there);
+              }
+            }
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            const int node0 = wk.q.ctx - t * KT;  // the tile's row of the first drafted one
+            if (kv == 1 && node0 < KT) {
+              // drafted rows' values: what is not finite is noted and taken out (a thread
+              // looks over what it copied itself)
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              const int from = max(node0, 0), to = min(KT, node0 + wk.q.n);
+#pragma unroll 1
+              for (int k = max(0, (from / RPI - pw) / kProducers); k < Sh::STEPS; ++k) {
+                const int r = (k * kProducers + pw) * RPI + sub;
+                if (r - sub >= to) break;
+                if (r < from || r >= to) continue;
+                uint4* v = reinterpret_cast<uint4*>(sm_kv + (size_t)slot * Sh::kSlot + (chunk >> 3) * kBlk + r * 128 +
+                                                    (((chunk & 7) ^ (r & 7)) << 4));
+                const uint4 x = *v;
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                constexpr uint32_t kExp = DT == MOE_BF16 ? 0x7f80u : 0x7c00u;
+                bool found = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  if ((w[j] & kExp) == kExp) {
+                    w[j] &= 0xffff0000u;
+                    found = true;
+                  }
+                  if ((w[j] >> 16 & kExp) == kExp) {
+                    w[j] &= 0xffffu;
+                    found = true;
+                  }
+                }
+                if (found) {
+                  *v = make_uint4(w[0], w[1], w[2], w[3]);
+                  atomicOr(&ct.bad[seq & 7], 1ull << (r - node0));
+                }
+              }
+              __syncwarp();
+              fence_async();
+              bar_arrive(&ct.full[slot]);
+            } else {
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&ct.full[slot])) : "memory");
+            }
+            if (lane == 0) {
+              if (kv == 0) *reinterpret_cast<uint2*>(&ct.hole[tile_seq & 7][2 * pw]) = make_uint2(hole[0], hole[1]);
+              bar_arrive(&ct.full[slot]);  // behind what this lane wrote
+            }
+            __syncwarp();
+            if (++slot == p.nslot) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        ++seq;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp == 10) {
     // ---------------- issue of the products.  The warp goes through the loop as one and one lane

@@ -14,11 +14,11 @@
 // order between slices.  The request's block that ends last joins the slices, by (ratio, lower id), so
 // it does not matter which one that is.
 //
-// Five rows of 32,003 in fp32 (one request) 15.7 us: latency of three launches in a chain, each of which waits for
-// the one before.  64 chains of up to 8 rows of 131,072 in bf16, with draft probabilities (101 MB), 52.2 us:
-// sums 17 (5.9 TB/s), walk 8.5, draws 33 in profiles of each alone; the draws are bound by what an
-// entry costs (logit, noise and draft probability each unpacked, compared in products).  24 trees of
-// 8 to 48 rows of 129,283 in fp32 (183 MB), 87.6 us: sums 50, walk 12.5, draws 22.
+// Five rows of 32,003 in fp32 (one request) 16.4 us: latency of three launches in a chain, each of which
+// waits for the one before.  64 chains of up to 8 rows of 131,072 in bf16, with draft probabilities (101
+// MB), 45.5 us: by themselves sums 18, walk 10, draws 24, the draws bound by what an entry costs (logit,
+// noise and draft probability each unpacked, compared in products).  24 trees of 8 to 48 rows of 129,283
+// in fp32, 80.8 us: sums 47 (224 MB, 4.7 TB/s), walk 14, draws 18.
 //
 // The exponent (x - m) c is taken with c in two parts (c >= hi, lo > 0, so that -infinity stays
 // what it is): with c rounded to 32 bits probabilities far from the maximum would be off by
