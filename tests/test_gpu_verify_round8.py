@@ -3,6 +3,7 @@ softmax attention in 64 bits over them, the verdicts against the definition, the
 import importlib.util
 import math
 import os
+from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
 import pytest
@@ -93,3 +94,106 @@ def run(ex, fmt, inv, prompts):
 
 def test_example_runs():
     example().main()
+
+
+def test_two_threads_on_streams_of_their_own():
+    ex = example()
+    rng = np.random.default_rng(5)
+    prompts = [[rng.integers(0, ex.VOCAB, n).tolist() * 2 for n in sizes] for sizes in ((40, 9), (3, 60))]
+
+    def one(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            layer = ex.Layer8(requests=2)
+            try:
+                texts, ctx, seen = ex.decode(layer, prompts[i], rounds=8, inv_temperature=0.5, seed=i)
+                out = [texts, ctx, int(layer.status.item())], [s["attended"].clone() for s in seen[1:]], layer.read(ctx)
+                torch.cuda.current_stream().synchronize()
+                return out
+            finally:
+                layer.close()
+
+    alone = [one(0), one(1)]
+    with ThreadPoolExecutor(2) as pool:
+        both = list(pool.map(one, (0, 1)))
+    for a, b in zip(alone, both):
+        assert a[0] == b[0] and a[0][2] == 0
+        assert all(torch.equal(x, y) for x, y in zip(a[1], b[1])) and all(torch.equal(x, y) for x, y in zip(a[2], b[2]))
+
+
+def test_a_captured_round():
+    """Append, attention and verification in one graph, replayed with other rows, lengths and pages: the same bits as call by call."""
+    ex = example()
+    layers = [ex.Layer8(requests=2) for _ in range(2)]
+    try:
+        gen = torch.Generator(device=DEV).manual_seed(3)
+        for layer in layers:
+            prompt = layer.map_rows([0, 0], [49, 6])
+            layer.cache_rows8(layer.embed[torch.arange(49 + 6, device=DEV)], prompt, [0, 0])
+        # what a round reads, in places that stay
+        counts = [3, 2]
+        n, heads, d = sum(counts), ex.KV_HEADS, ex.HEAD_DIM
+        q = torch.empty((n, ex.Q_HEADS, d), dtype=torch.bfloat16, device=DEV)
+        k, v = (torch.empty((n, heads, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        logits = torch.empty((n, ex.VOCAB), dtype=torch.bfloat16, device=DEV)
+        tokens, u = torch.empty(n, dtype=torch.int32, device=DEV), torch.empty(n, device=DEV)
+        noise = torch.empty((2, ex.VOCAB), device=DEV)
+        ctx, start = (torch.empty(m, dtype=torch.int32, device=DEV) for m in (2, 3))
+
+        def calls(layer, keep):
+            a8 = layer.rows_args(k, v, start, ctx, n)
+            out = torch.empty_like(q)
+            att = mv.make_tree_attention8_args(
+                n_req=2, n_rows=n, max_tree=4, q_heads=ex.Q_HEADS, kv_heads=heads, head_dim=d, dtype=mv.MOE_BF16, q=q.data_ptr(),
+                q_stride=q.stride(0), out=out.data_ptr(), out_stride=out.stride(0), row_start=start.data_ptr(), ctx_len=ctx.data_ptr(),
+                block_table=layer.table.data_ptr(), table_width=layer.width, cache=layer.cache8(), scale=d ** -0.5,
+                dev_status=layer.status.data_ptr())
+            acc, follow = (torch.empty(2, dtype=torch.int32, device=DEV) for _ in range(2))
+            path = torch.empty(n, dtype=torch.int32, device=DEV)
+            ver = mv.make_verify_args(
+                n_req=2, n_rows=n, vocab=ex.VOCAB, dtype=mv.MOE_BF16, logits=logits.data_ptr(), stride=logits.stride(0),
+                row_start=start.data_ptr(), tokens=tokens.data_ptr(), uniform=u.data_ptr(), noise=noise.data_ptr(),
+                noise_stride=noise.stride(0), inv_temperature=1.0, accepted=acc.data_ptr(), path=path.data_ptr(),
+                next_token=follow.data_ptr(), dev_status=layer.status.data_ptr())
+            ws = [torch.zeros(b, dtype=torch.uint8, device=DEV)
+                  for b in (mv.moe_tree_attention8_workspace_bytes(att), mv.moe_verify_drafts_workspace_bytes(ver))]
+            keep += [a8, att, ver, ws, out, acc, path, follow]
+
+            def run():
+                st = torch.cuda.current_stream().cuda_stream
+                mv.moe_cache8_append(a8, st)
+                mv.moe_tree_attention8(att, ws[0].data_ptr(), ws[0].numel(), st)
+                mv.moe_verify_drafts(ver, ws[1].data_ptr(), ws[1].numel(), st)
+            return run, (out, acc, path, follow)
+
+        def fill(at, shape):
+            for x in (q, k, v, logits):
+                x.copy_(torch.randn(x.shape, generator=gen, device=DEV))
+            u.copy_(torch.rand(n, generator=gen, device=DEV))
+            noise.exponential_(generator=gen)
+            tokens.copy_(torch.randint(0, ex.VOCAB, (n,), generator=gen, device=DEV, dtype=torch.int32))
+            ctx.copy_(torch.tensor(at, dtype=torch.int32))
+            start.copy_(torch.tensor(np.concatenate([[0], np.cumsum(shape)]), dtype=torch.int32))
+            for layer in layers:
+                layer.map_rows(at, shape)
+
+        keep = []
+        eager, eager_out = calls(layers[0], keep)
+        inner, graph_out = calls(layers[1], keep)
+        fill([49, 6], [3, 2])
+        eager()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            inner()
+        for step, (at, shape) in enumerate((([49, 6], [3, 2]), ([51, 8], [1, 4]), ([52, 9], [4, 0]), ([56, 9], [2, 3]))):
+            if step:
+                fill(at, shape)
+                eager()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(eager_out, graph_out)), step
+            assert all(torch.equal(x, y) for x, y in zip(layers[0].codes + layers[0].scales, layers[1].codes + layers[1].scales)), step
+        assert all(int(layer.status.item()) == 0 for layer in layers)
+    finally:
+        for layer in layers:
+            layer.close()
