@@ -68,7 +68,7 @@
 // rows, 16/8 heads of 64, 89 us (55.8), bound by the same producers; 121 with the scales of blocks of
 // 8 tokens taken key by key.  Tried and slower: raw codes by the tensor memory accelerator (422; 183
 // against 176 for one row), a loader and six converters in sixteen warps (438 to 539: the softmax
-// spills at 128 registers).
+// spills at 128 registers), a fourth producer (479; ragged batch 113: it spills at 152 too).
 //
 // What is not seen gets the weight 0, but 0 times a cached NaN would still be NaN in the
 // product: slots past the last position are zero-filled, and the values of drafted rows
