@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const __grid_constant__ 
     }
     const int e = scale_exponent(most, i8);
     const float now = __uint_as_float((uint32_t)(e + 127) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    if (now != old)
+    const auto carry = [&]() {  // what is held, under the new scale
+#pragma unroll 1
       for (int c = at; c < g.held * CPR; c += lanes) {
         uint2* p = reinterpret_cast<uint2*>(codes + c / CPR * a.cache.slot_stride + c % CPR * 8);
         const uint2 w = *p;
@@ -272,15 +273,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const __grid_constant__ 
         for (int j = 0; j < 8; ++j) v[j] *= old;
         *p = make_uint2(encode4<true>(v, inv, i8), encode4<true>(v + 4, inv, i8));
       }
+    };
     const auto place = [&](int c) { return reinterpret_cast<uint2*>(codes + (g.held + c / CPR) * a.cache.slot_stride + c % CPR * 8); };
     float v[8];
     if (odd) {
+      carry();  // under a scale that stays, too: a NaN code becomes 0
 #pragma unroll 1
       for (int c = at; c < g.rows * CPR; c += lanes) {
         again(c).floats(v);
         __stcs(place(c), make_uint2(encode4<true>(v, inv, i8), encode4<true>(v + 4, inv, i8)));
       }
     } else {
+      if (now != old) carry();
 #pragma unroll
       for (int i = 0; i < kHold; ++i)
         if (at + i * lanes < g.rows * CPR) {

@@ -252,3 +252,22 @@ def test_a_cache_whose_offsets_pass_32_bits():
     mv.moe_cache8_read(case.rows_args(out[:, :1], out[:, 1:], status), stream())
     assert int(status.item()) == 0
     assert torch.equal(out[:, 0].double(), case.values("k", 0, np.arange(16, 36))[:, 0])
+
+
+@pytest.mark.parametrize("moves", [False, True])
+@pytest.mark.parametrize("d,block", [(64, 4), (64, 16), (256, 64)])
+def test_held_nan_codes_become_zero_whether_the_scale_moves_or_not(d, block, moves):
+    case = Cache8(16, [block + block // 2 + 1, 0], [1, 2], hkv=2, d=d, page=64, block=block, fmt="e4m3")
+    p, o = (int(x) for x in case.where(0, np.array([block])))  # the first held position of the block
+    for name in ("k", "v"):
+        codes = case.raw(name)
+        getattr(case, name + "_scale")[p, o // block] = 0.25
+        codes[p, o, :, 0] = 0x7e  # the largest code: the scale stays where the rows are small
+        codes[p, o + 1, 0, 3], codes[p, o + 1, 1, d - 1] = 0x7f, 0xff
+    rows = {m: x * (1000 if moves else 0.01) for m, x in rows_of(case).items()}
+    want = case.appended(rows)
+    assert append(case, rows) == mv.MOE_DEV_VALUE
+    case.same(want)
+    held = case.raw("v")[p, o:o + block // 2 + 2].cpu().numpy()
+    assert not np.isnan(code_values("e4m3")[held]).any()
+    assert (float(case.v_scale[p, o // block, 0]) == 0.25) != moves
