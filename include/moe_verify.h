@@ -558,8 +558,8 @@ int moe_cache8_read(const moe_cache8_args* args, void* stream);
  * the values' scale in them, are rounded to fp16 for the product with the codes (what is
  * lost are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  Scales of
  * values are taken between 2^-48 and 2^48: smaller ones count as 0 (their values are below
- * 1.6e-12), and so do larger ones, which raise MOE_DEV_VALUE.  The span of either cache is
- * below 2^36 - 2048 bytes here.
+ * 1.6e-12), and so do larger ones, which raise MOE_DEV_VALUE.  A code that is NaN is NaN under any
+ * scale, 0 too, for the rows that see it.  The span of either cache is below 2^36 - 2048 bytes here.
  * Positions that are not seen have no influence, whatever codes and scales are cached there.
  * Waits go by moe_set_attention_wait_limit_ns. */
 typedef struct moe_tree_attention8_args {

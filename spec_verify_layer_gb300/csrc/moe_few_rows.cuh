@@ -291,7 +291,7 @@ __device__ __forceinline__ void few_rows(const A& a, const Plan& p, Control& ct,
           float log;
           asm("lg2.approx.f32 %0, %1;" : "=f"(log) : "f"(vs));
           asm("rcp.approx.f32 %0, %1;" : "=f"(inv[mt][h]) : "f"(vs));
-          no_value[mt][h] = vs == 0.f;  // such values are zeros
+          no_value[mt][h] = vs == 0.f;  // such values are zeros (and NaN, where a code is: 0 times it)
           if (vs == 0.f) log = kNoValueLog, inv[mt][h] = kNoValueInverse;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)

@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
           }
           if (++put_stage == Sh::kRawStages) put_stage = 0;
         };
-        // Values whose scale counts as 0 are zeros, and so are, in drafted rows, codes that are NaN: those
-        // are noted, and added at the end to the rows that see them.
+        // Values whose scale counts as 0 are zeros, but for codes that are NaN: 0 times them is NaN.  In drafted rows
+        // these are zeros too: they are noted, and added at the end to the rows that see them.
         const auto clean = [&](const unsigned (&zero)[2], int node0) {
           unsigned char* const src = sm_raw + put_stage * Sh::kRaw + pw * 512 + lane * 16;
 #pragma unroll 1
@@ -469,14 +469,14 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
             const int r = (k * kProducers + pw) * RPI + sub, mine = COARSE ? r / LOOK : k * RPI + sub;
             if (r >= KT) break;
             uint4* const v = reinterpret_cast<uint4*>(src + k * kProducers * 512);
-            if (zero[mine >> 5] >> (mine & 31) & 1) *v = make_uint4(0, 0, 0, 0);
-            if (FMT == MOE_E4M3 && r >= node0) {
-              const uint4 x = *v, n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
-              if (n.x | n.y | n.z | n.w) {
-                *v = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
-                atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
-              }
-            }
+            const bool none = zero[mine >> 5] >> (mine & 31) & 1, node = r >= node0;
+            if (!none && !(FMT == MOE_E4M3 && node)) continue;
+            const uint4 x = *v, n = FMT == MOE_E4M3 ? make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w))
+                                                    : make_uint4(0, 0, 0, 0);
+            const uint4 keep = make_uint4((none ? 0 : ~n.x) | (node ? 0 : n.x), (none ? 0 : ~n.y) | (node ? 0 : n.y),
+                                          (none ? 0 : ~n.z) | (node ? 0 : n.z), (none ? 0 : ~n.w) | (node ? 0 : n.w));
+            *v = make_uint4(x.x & keep.x, x.y & keep.y, x.z & keep.z, x.w & keep.w);
+            if (node && (n.x | n.y | n.z | n.w)) atomicOr(&ct.bad[seq & 7], 1ull << ((r - node0) & 63));
           }
         };
         // the scale of a key, or logarithm and reciprocal of a value's (off by 2^-22 or so, in the weights' sum

@@ -295,3 +295,31 @@ def test_long_flat_tails_beside_a_strong_key():
         p, o = case.where(0, np.array([5]))
         case.raw("k")[p, o, :, 0] = torch.tensor(12.0, device=DEV).to(torch.float8_e4m3fn).view(torch.uint8)
         good(case)
+
+
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("block", [4, 8, 16])
+@pytest.mark.parametrize("value,raised", [(0.0, 0), (2.0**-60, 0), (float("nan"), mv.MOE_DEV_VALUE), (2.0**60, mv.MOE_DEV_VALUE)])
+def test_nan_codes_under_scales_that_count_as_zero(n, block, value, raised):
+    """A NaN code is NaN whatever its scale (0 times it, too), in both kernels: for every row in the context, in drafted
+    rows for those that see them; other elements are as they are without it."""
+    case = Tree8Case(20, [90], [n], hq=4, hkv=2, d=64, page=16, block=block, fmt="e4m3")
+    pages = [int(case.table[0, c]) for c in (1, 5)]  # positions 16..31, and 80..95 with drafted rows
+    for page in pages:
+        case.v_scale[page] = value
+    clean, clean_lse, status = case.run()
+    assert status == raised and torch.isfinite(clean).all()
+    p, o = case.where(0, np.array([90 + 1]))  # a drafted row
+    case.raw("v")[p, o, :, 3:9] = 0xff
+    out, lse, status = case.run()
+    hit = case.seen(0)[:, 91].cpu()
+    assert status == raised and hit.any() and torch.equal(lse, clean_lse)
+    assert torch.isnan(out[hit][:, :, 3:9]).all() and torch.equal(out[~hit], clean[~hit])
+    assert torch.equal(out[hit][:, :, 9:], clean[hit][:, :, 9:]) and torch.equal(out[hit][:, :, :3], clean[hit][:, :, :3])
+    p, o = case.where(0, np.array([20]))  # of the context
+    case.raw("v")[p, o, 1, 40:42] = 0x7f
+    more, lse, status = case.run()
+    assert status == raised and torch.equal(lse, clean_lse)
+    assert torch.isnan(more[:, 2:, 40:42]).all()
+    more[:, 2:, 40:42] = out[:, 2:, 40:42]
+    assert torch.equal(torch.nan_to_num(more, nan=99.0), torch.nan_to_num(out, nan=99.0))
