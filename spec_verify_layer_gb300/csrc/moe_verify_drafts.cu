@@ -24,6 +24,8 @@
 // what it is): with c rounded to 32 bits probabilities far from the maximum would be off by
 // some 1e-6, and a decision lies that near its border far more often than by the 1e-7 of the
 // rounded sums.
+#include <algorithm>
+
 #include "moe_vocab.cuh"
 
 namespace moe {
@@ -595,12 +597,22 @@ int check(const moe_verify_args* args) {
   return MOE_OK;
 }
 
-int slices_for(int64_t rows, int vocab, int size, int blocks) {
+// The most that slices_for may give for rows of this vocabulary.
+int most_slices(int vocab) {
   int n = 1;
-  while (n < kMaxSlices && vocab / (2 * n) >= kSliceMin &&
-         (rows * n < blocks || (rows * n < 2 * blocks && (int64_t)vocab / (2 * n) * size >= kLongSlice)))
-    n *= 2;
+  while (n < kMaxSlices && vocab / (2 * n) >= kSliceMin) n *= 2;
   return n;
+}
+int slices_for(int64_t rows, int vocab, int size, int blocks) {
+  const int most = most_slices(vocab);
+  int n = 1;
+  while (n < most && (rows * n < blocks || (rows * n < 2 * blocks && (int64_t)vocab / (2 * n) * size >= kLongSlice))) n *= 2;
+  return n;
+}
+// A bound on rows * slices_for(...), whatever the size of an element, that does not fall as rows or vocab grow: rows
+// are cut once more while there are fewer than 2 * blocks slices, so there are fewer than 4 * blocks then.
+size_t places_for(int64_t rows, int vocab, int blocks) {
+  return (size_t)std::min(rows * most_slices(vocab), std::max(rows, (int64_t)4 * blocks));
 }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -608,13 +620,14 @@ struct Workspace {
   int row_slices, draw_slices;
   size_t sums, drawn, end, total;
 };
+// Sized by n_req, n_rows and vocab alone, so that what serves a program's largest round serves its others.
 Workspace layout(const moe_verify_args& a) {
   Workspace w{};
   w.row_slices = slices_for(a.n_rows, a.vocab, a.dtype == MOE_F32 ? 4 : 2, kSumBlocks);
   w.draw_slices = a.n_req <= kCounters ? slices_for(a.n_req, a.vocab, 0, kDrawBlocks) : 1;
   w.sums = kCounterBytes;
-  w.drawn = w.sums + up256((size_t)a.n_rows * w.row_slices * sizeof(Key));
-  w.end = w.drawn + up256((size_t)a.n_req * w.draw_slices * sizeof(Drawn));
+  w.drawn = w.sums + up256(places_for(a.n_rows, a.vocab, kSumBlocks) * sizeof(Key));
+  w.end = w.drawn + up256(places_for(a.n_req, a.vocab, kDrawBlocks) * sizeof(Drawn));
   w.total = w.end + up256((size_t)a.n_req * sizeof(End));
   return w;
 }

@@ -117,3 +117,25 @@ def test_nothing_is_refused_as_null():
     for fn, rest in (("moe_cache8_append", (None,)), ("moe_cache8_read", (None,)), ("moe_tree_attention8", (P, 1 << 30, None)),
                      ("moe_verify_drafts", (P, 1 << 30, None))):
         refused(fn, None, mv.MOE_EINVAL, *rest)
+
+
+def test_verify_workspace_does_not_fall_as_sizes_grow():
+    """Sized once for a program's largest round it serves every smaller one, of any type of logits and drafts."""
+    def size(**kw):
+        return mv.moe_verify_drafts_workspace_bytes(verify_args(**kw))
+
+    vocabs = [1, 1000, 4095, 4096, 8191, 8192, 16384, 32000, 32003, 65536, 129283, 131072, 262144, 1 << 24]
+    rows = [0, 1, 2, 46, 47, 93, 94, 187, 188, 375, 661, 749, 750, 1499, 1500, 2999, 3000, 5999, 6001, 1 << 20]
+    reqs = [1, 2, 9, 10, 18, 19, 24, 37, 38, 64, 75, 76, 151, 152, 303, 304, 320, 321, 700, 16384]
+    kinds = [(mv.MOE_F32, 1.0), (mv.MOE_BF16, 1.0), (mv.MOE_F16, math.inf)]
+    for req in (1, 24, 64, 320, 700):
+        table = [[size(n_req=req, n_rows=r, vocab=v) for v in vocabs] for r in rows]
+        for r, line in zip(rows, table):
+            assert line == sorted(line), (req, r)
+            for v, s in zip(vocabs, line):
+                assert all(size(n_req=req, n_rows=r, vocab=v, dtype=t, inv_temperature=inv) == s for t, inv in kinds)
+        for column in zip(*table):
+            assert list(column) == sorted(column)
+    for v in vocabs:
+        column = [size(n_req=n, n_rows=661, vocab=v) for n in reqs]
+        assert column == sorted(column), v
