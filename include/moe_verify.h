@@ -517,16 +517,22 @@ typedef struct moe_kv_cache8 {
  * where rows are appended, anywhere (0 for a whole prefix) where they are read.
  *   append: per block of tokens that rows fall into, and per head, of keys and of values, let
  *   a be the largest magnitude, finite ones only, of the block's new rows and of what it holds
- *   from before (the positions of the block that are below ctx_len[b]; what lies behind
- *   them, as of drafts that were rejected, has no influence).  The block's scale becomes 2^e
+ *   from before (the positions of the block that are below ctx_len[b]; codes behind them, as
+ *   of drafts that were rejected, are not looked at).  The block's scale becomes 2^e
  *   with the least e >= -126 for which a <= Q * 2^e, Q = 448 (MOE_E4M3) or 127 (MOE_I8).
  *   Rows are rounded to the nearest code (ties to even) of x / 2^e; what the block holds
- *   is rounded again from its values where the scale has changed.  With MOE_E4M3 that is
- *   exact but for codes that fall below the smallest normal one; with MOE_I8 a value
- *   that was rounded again is off by less than one step of its present scale (rounded once:
- *   half a step).  Infinities become the largest code with their sign, NaN 0 (rows and what
- *   is held alike), and both raise MOE_DEV_VALUE.  The last block of a context is written as a
- *   whole, so it must not be shared with another request (a shared prefix ends with a block);
+ *   is rounded again from its values where the scale has changed.  So a value carries the
+ *   rounding of every scale that its block has had since it was written, also of one that came
+ *   with rows that were rejected since: a scale that falls again does not bring back what was
+ *   lost under it.  Let S be the largest of them.  With MOE_I8 a value is off by less than S, one
+ *   step (rounded once: half a step); with MOE_E4M3 by less than 2^-9 S, one step of its smallest
+ *   codes, beside the first rounding (2^-4 of it), and not at all further while its code is a
+ *   normal one.  A held scale that is no power of two adds a rounding of its own when it is
+ *   replaced.  Where rows that may be rejected are far larger than the context, blocks of one
+ *   token keep them apart from it.
+ *   Infinities become the largest code with their sign, NaN 0 (rows and what is held alike), and
+ *   both raise MOE_DEV_VALUE.  The last block of a context is written as a whole, so it must not
+ *   be shared with another request (a shared prefix ends with a block);
  *   no two rows of a call may fall into one slot.
  *   read: k, v = code * scale, rounded once to dtype.
  *   k, v [n_rows][kv_heads][D] of MOE_BF16, MOE_F16 or MOE_F32, the strides from row to row in

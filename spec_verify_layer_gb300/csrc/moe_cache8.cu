@@ -4,8 +4,9 @@
 // Append.  A task is one block of tokens of one head, of keys or of values: its largest magnitude a, the
 // least power of two with a <= Q 2^e, the codes of x / 2^e.  With powers of two x / 2^e is exact, so a
 // row is rounded once, and for e4m3, which has the same relative precision at every scale, they cost
-// one binade of range and no precision; what a block holds from before is carried to another scale
-// without a further rounding (int8: with half a step of its own).  The rows of a block lie next to each
+// one binade of range and no precision; what a block holds from before is carried to a larger scale
+// with half a step of its own there (e4m3: only where its code falls below the smallest normal one), and
+// to a smaller one exactly.  The rows of a block lie next to each
 // other in the call, so a thread block takes up to 64 consecutive rows, a thread looks up the page of each,
 // and it works through the blocks that begin among them; a group of 8, 16 or 32 lanes takes a task, in
 // 16-byte loads.  A lane keeps what it has read for the maximum in registers (64 elements; more is read

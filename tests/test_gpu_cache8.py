@@ -271,3 +271,58 @@ def test_held_nan_codes_become_zero_whether_the_scale_moves_or_not(d, block, mov
     held = case.raw("v")[p, o:o + block // 2 + 2].cpu().numpy()
     assert not np.isnan(code_values("e4m3")[held]).any()
     assert (float(case.v_scale[p, o // block, 0]) == 0.25) != moves
+
+
+def appended_in_turn(fmt, block, steps, seed):
+    """Appends of which some rows are rejected: (rows brought, rows that stay, their size) a step.  Returns the case, the rows
+    that stayed in 64 bits, and for each the largest scale that its block had from then on."""
+    total = sum(keep for _, keep, _ in steps) + max(n for n, _, _ in steps)
+    case = Cache8(seed, [0], [total], hkv=2, d=64, page=64, block=block, fmt=fmt)
+    ctx, kept, largest = 0, np.zeros((total, 2, 64)), np.zeros((total, 2))
+    for i, (n, keep, size) in enumerate(steps):
+        case.ctx, case.counts, case.start = [ctx], [n], np.array([0, n])
+        rows = {m: x * size for m, x in rows_of(case, "f32", seed=i, spread=0.3).items()}
+        want = case.appended(rows)
+        assert append(case, rows) == 0
+        case.same(want)
+        kept[ctx:ctx + keep] = rows["v"][:keep].double().cpu().numpy()
+        p, o = case.where(0, np.arange(total))
+        scale = case.v_scale[p, o // block].double().cpu().numpy()
+        largest[ctx:ctx + keep] = 0
+        for at in range(ctx // block * block, ctx + keep):
+            largest[at] = np.maximum(largest[at], scale[at])
+        ctx += keep
+    return case, kept[:ctx], largest[:ctx]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("block", [1, 8, 64])
+def test_what_rejected_rows_leave_of_the_rows_before_them(fmt, block):
+    """A held value was rounded at every larger scale that its block has had, that of rows which were rejected since
+    included: off by less than one step of the largest (int8), or of its smallest codes beside the first rounding (e4m3)."""
+    rng = np.random.default_rng(block)
+    steps = []
+    for _ in range(40):
+        n = int(rng.integers(1, 7))
+        steps.append((n, int(rng.integers(1, n + 1)), float(2.0 ** rng.integers(-6, 8))))
+    case, kept, largest = appended_in_turn(fmt, block, steps, 17)
+    got = case.values("v", 0, np.arange(len(kept))).cpu().numpy()
+    bound = largest[..., None] if fmt == "i8" else np.abs(kept) * 2.0**-4 + largest[..., None] * 2.0**-9
+    assert (np.abs(got - kept) < bound).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+def test_a_large_row_that_was_rejected_leaves_its_rounding_unless_it_had_a_block_of_its_own(fmt):
+    """Rows of about 1, a row 2^12 times as large, rejected, a row of about 1: the scale is small again, and the first
+    rows are as the large scale left them; behind the end of a block they are as they were written."""
+    far = {}
+    for held in (5, 8):
+        case, kept, largest = appended_in_turn(fmt, 8, [(held, held, 1.0), (1, 0, 4096.0), (1, 1, 1.0)], 18)
+        got = case.values("v", 0, np.arange(held)).cpu().numpy()
+        p, o = case.where(0, np.arange(held))
+        step = case.v_scale[p, o // 8].double().cpu().numpy()[..., None] * (1 if fmt == "i8" else 2.0**-9)
+        off = np.abs(got - kept[:held]) - (0 if fmt == "i8" else np.abs(kept[:held]) * 2.0**-4)
+        far[held] = float((off / step).max())
+        large = largest[:held, :, None] * (1 if fmt == "i8" else 2.0**-9)
+        assert (off < large).all()
+    assert far[8] <= 0.5 and far[5] > 8
