@@ -559,8 +559,9 @@ int moe_cache8_read(const moe_cache8_args* args, void* stream);
 /* moe_tree_attention over a cache of 8 bits: the same rows, masks, lengths, outputs, limits,
  * raised bits and workspace rules, with keys and values code * scale (a scale that is not
  * one counts as 0 and raises MOE_DEV_VALUE).  dtype is that of q and out.  Inside, codes are
- * 16-bit numbers (exactly), queries 16-bit numbers with a power of two for each row and
- * head (exactly, but for elements below 2^-38 of its largest), and the softmax weights, with
+ * 16-bit numbers (exactly), queries fp16 numbers with a power of two for each row and
+ * head (exactly, but for elements below 2^-31, of fp16 queries 2^-28, of its largest, which
+ * are off by 2^-39 of that at most), and the softmax weights, with
  * the values' scale in them, are rounded to fp16 for the product with the codes (what is
  * lost are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  Scales of
  * values are taken between 2^-48 and 2^48: smaller ones count as 0 (their values are below

@@ -323,3 +323,26 @@ def test_nan_codes_under_scales_that_count_as_zero(n, block, value, raised):
     assert torch.isnan(more[:, 2:, 40:42]).all()
     more[:, 2:, 40:42] = out[:, 2:, 40:42]
     assert torch.equal(torch.nan_to_num(more, nan=99.0), torch.nan_to_num(out, nan=99.0))
+
+
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("dtype,largest,small,rounded", [("bf16", 1.0, 2.0**-31 * 1.9921875, False), ("bf16", 1.0, 2.0**-33 * 1.9921875, True),
+                                                         ("f16", 40000.0, 2.0**-13 * 1.9990234375, False),
+                                                         ("f16", 40000.0, 2.0**-14 * 1.9990234375, True)])
+def test_queries_with_elements_far_below_their_largest(n, dtype, largest, small, rounded):
+    """As fp16 numbers, with the largest at 2^14 or above: exact from 2^-31 (fp16 queries 2^-28) of the largest on, below
+    that off by 2^-25, so 2^-39 of the largest, at most.  Its key is 0, the score comes from the small ones alone."""
+    case = Tree8Case(22, [1], [n], hq=4, hkv=2, d=64, page=16, block=16, fmt="e4m3", dtype=dtype, mask="random", scale=2.0**30 / largest)
+    case.mask.zero_()  # the rows see the one context position: lse is its score
+    case.q.fill_(small)
+    case.q[:, :, 0] = largest
+    p, o = case.where(0, np.array([0]))
+    case.raw("k")[p, o] = 0x38  # 1
+    case.raw("k")[p, o, :, 0] = 0
+    case.k_scale.fill_(1.0)
+    score = 63 * float(case.q[0, 0, 1]) * case.scale
+    _, lse, status = case.run()
+    assert status == 0
+    off = (lse.double() - score).abs().max().item()
+    assert off <= 66 * 2**-24 * score + (63 * 2**-39 * largest * case.scale if rounded else 0) + 2**-22 * (score + 48) + 4e-6
+    assert off > 66 * 2**-24 * score + 2**-22 * (score + 48) + 4e-6 or not rounded
