@@ -51,6 +51,10 @@ __device__ __forceinline__ Request request(const moe_cache8_args& a, int b) {
 // The request of a row: the last that begins at or before it.
 __device__ __forceinline__ int request_of(const moe_cache8_args& a, int row) { return last_not_above(a.row_start, a.n_req, row); }
 
+// Is the row one of the request's?  (Of a request that can be worked on, first: the difference to a row_start of any
+// value may pass 32 bits and come round.)
+__device__ __forceinline__ bool holds(const Request& q, int row) { return q.n > 0 && row >= q.s && row - q.s < q.n; }
+
 __device__ __forceinline__ unsigned bad_requests(const moe_cache8_args& a) {
   unsigned flags = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(a.row_start) != 0) flags |= MOE_DEV_LENGTH;
@@ -176,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const __grid_constant__ 
   if (tid < rows && r < a.n_rows) {
     const int b = request_of(a, r);
     const Request q = request(a, b);
-    const int pos = q.ctx + r - q.s, in_block = pos & (B - 1);
-    if (r >= q.s && r - q.s < q.n && (r == q.s || !in_block)) {
+    const int pos = holds(q, r) ? q.ctx + (r - q.s) : -1, in_block = pos & (B - 1);
+    if (pos >= 0 && (r == q.s || !in_block)) {
       const int col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
       const int page = __ldg(a.block_table + (long long)b * a.table_width + col);
       if (page < 0 || page >= a.cache.n_pages) {
@@ -315,8 +319,8 @@ __global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ moe_c
     const int r = r0 + tid, b = request_of(a, r);
     const Request q = request(a, b);
     long long at = -1, scale = 0;
-    if (r >= q.s && r - q.s < q.n) {
-      const int pos = q.ctx + r - q.s, col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
+    if (holds(q, r)) {
+      const int pos = q.ctx + (r - q.s), col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
       const int page = __ldg(a.block_table + (long long)b * a.table_width + col), slot = pos - col * a.cache.page_size;
       if (page < 0 || page >= a.cache.n_pages) {
         flags |= MOE_DEV_INDEX;

@@ -326,3 +326,23 @@ def test_a_large_row_that_was_rejected_leaves_its_rounding_unless_it_had_a_block
         large = largest[:held, :, None] * (1 if fmt == "i8" else 2.0**-9)
         assert (off < large).all()
     assert far[8] <= 0.5 and far[5] > 8
+
+
+@pytest.mark.parametrize("first", [-2**31, -2**31 + 5, -2**31 + 40, -2**30, -1])
+def test_row_starts_as_far_below_zero_as_they_go(first):
+    """The request that begins there, and the one that ends there, are left out; the others are worked on as ever."""
+    ctx, n = [5, 9, 0, 40], [3, 4, 6, 2]
+    case = Cache8(24, ctx, n, hkv=2, d=64, page=16, block=8, fmt="e4m3")
+    rows = rows_of(case)
+    start = i32([0, first, 7, 13, 15])
+    want = case.appended(rows, only=[2, 3])
+    assert append(case, rows, start=start) == mv.MOE_DEV_LENGTH
+    case.same(want)
+    out = torch.full((15, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    status = word()
+    mv.moe_cache8_read(case.rows_args(out[:, :2], out[:, 2:], status, start=start), stream())
+    assert int(status.item()) == mv.MOE_DEV_LENGTH
+    for i, name in enumerate(("k", "v")):
+        want = torch.cat([case.values(name, b, np.arange(ctx[b], ctx[b] + n[b])) for b in (2, 3)])
+        assert torch.equal(out[7:, 2 * i:2 * i + 2], want.float().bfloat16())
+    assert (out[:7] == 7).all()
