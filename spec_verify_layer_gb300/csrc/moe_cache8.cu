@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const __grid_constant__ 
     long long codes, scales;  // of its first slot, and of its scale, head 0
     int row, held, rows;      // first row, slots before it, rows
   };
+  // In the order of rows within a warp.  Thread blocks beside each other deal out the same tasks, so they have to have
+  // them in the same order; they have 16 rows, the first warp's (with more there are enough blocks without).
   __shared__ Begin begin[kRows];
   __shared__ int count;
   const int tid = threadIdx.x, lane = tid & 31, B = a.cache.block_size;
@@ -176,23 +178,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_append(const __grid_constant__ 
   unsigned flags = blockIdx.y == 0 ? bad_requests(a) : 0;
   if (tid == 0) count = 0;
   __syncthreads();
-  const int r = blockIdx.x * rows + tid;  // a thread a row
-  if (tid < rows && r < a.n_rows) {
-    const int b = request_of(a, r);
-    const Request q = request(a, b);
-    const int pos = holds(q, r) ? q.ctx + (r - q.s) : -1, in_block = pos & (B - 1);
-    if (pos >= 0 && (r == q.s || !in_block)) {
-      const int col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
-      const int page = __ldg(a.block_table + (long long)b * a.table_width + col);
-      if (page < 0 || page >= a.cache.n_pages) {
-        flags |= MOE_DEV_INDEX;
-      } else {
-        const int slot = pos - in_block - col * a.cache.page_size;
-        begin[atomicAdd(&count, 1)] = {page * a.cache.page_stride + slot * a.cache.slot_stride,
-                                       page * a.cache.scale_page_stride + slot / B * a.cache.scale_block_stride,
-                                       r, in_block, min(B - in_block, q.n - (r - q.s))};
+  if (tid < kRows) {
+    const int r = blockIdx.x * rows + tid;  // a thread a row
+    Begin own;
+    bool begins = false;
+    if (tid < rows && r < a.n_rows) {
+      const int b = request_of(a, r);
+      const Request q = request(a, b);
+      const int pos = holds(q, r) ? q.ctx + (r - q.s) : -1, in_block = pos & (B - 1);
+      if (pos >= 0 && (r == q.s || !in_block)) {
+        const int col = (int)(((unsigned long long)(unsigned)pos * pd.mul) >> pd.shift);
+        const int page = __ldg(a.block_table + (long long)b * a.table_width + col);
+        if (page < 0 || page >= a.cache.n_pages) {
+          flags |= MOE_DEV_INDEX;
+        } else {
+          const int slot = pos - in_block - col * a.cache.page_size;
+          begins = true;
+          own = {page * a.cache.page_stride + slot * a.cache.slot_stride,
+                 page * a.cache.scale_page_stride + slot / B * a.cache.scale_block_stride,
+                 r, in_block, min(B - in_block, q.n - (r - q.s))};
+        }
       }
     }
+    const unsigned all = __ballot_sync(0xffffffffu, begins);
+    const int first = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(&count, __popc(all)) : 0, 0);
+    if (begins) begin[first + __popc(all & ((1u << lane) - 1))] = own;
   }
   __syncthreads();
   const int heads = a.kv_heads, tasks = count * 2 * heads, at = tid & (lanes - 1);
@@ -413,7 +423,7 @@ cudaError_t append(const moe_cache8_args& a, cudaStream_t st) {
   // lanes of a task: no more than it has chunks of eight elements
   const int chunks = a.cache.block_size * a.head_dim / 8, lanes = chunks >= 32 ? 32 : chunks;
   const auto fn = a.head_dim == 64 ? k_append<DT, 64> : a.head_dim == 128 ? k_append<DT, 128> : k_append<DT, 256>;
-  // few rows: their tasks over several thread blocks
+  // few rows (16 a block, see k_append): their tasks over several thread blocks
   const int rows = block_rows(a.n_rows);
   const unsigned across = (a.n_rows + rows - 1) / rows;
   unsigned down = 1;

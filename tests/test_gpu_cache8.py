@@ -346,3 +346,15 @@ def test_row_starts_as_far_below_zero_as_they_go(first):
         want = torch.cat([case.values(name, b, np.arange(ctx[b], ctx[b] + n[b])) for b in (2, 3)])
         assert torch.equal(out[7:, 2 * i:2 * i + 2], want.float().bfloat16())
     assert (out[:7] == 7).all()
+
+
+@pytest.mark.parametrize("hkv", [8, 32])
+def test_thread_blocks_beside_each_other_share_the_same_tasks(hkv):
+    """Few rows, many blocks that begin among them: each of the thread blocks that share them takes its part of one
+    order, every time."""
+    case = Cache8(19, [0, 3, 1], [16, 7, 9], hkv=hkv, d=256, page=4, block=1, fmt="i8")
+    for seed in range(10):
+        rows = rows_of(case, seed=seed)
+        want = case.appended(rows)
+        assert append(case, rows) == 0
+        case.same(want)
