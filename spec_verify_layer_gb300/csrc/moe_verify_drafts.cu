@@ -573,9 +573,19 @@ __global__ void __launch_bounds__(kThreads, 4) k_draw(const __grid_constant__ mo
   }
 }
 
+// The descriptor without what a greedy call does not read, which may be anything.
+moe_verify_args read_by(const moe_verify_args& args) {
+  moe_verify_args a = args;
+  if (std::isinf(a.inv_temperature)) {
+    a.draft_probs = nullptr;
+    a.uniform = a.noise = nullptr;
+  }
+  return a;
+}
+
 int check(const moe_verify_args* args) {
   if (!args) return MOE_EINVAL;
-  const moe_verify_args& a = *args;
+  const moe_verify_args a = read_by(*args);
   if (a.n_req < 1 || a.n_rows < 0 || a.vocab < 1 || !(a.inv_temperature > 0.f)) return MOE_EINVAL;
   const auto type_ok = [](int t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_F32; };
   if (!type_ok(a.dtype) || (a.draft_probs && !type_ok(a.draft_dtype))) return MOE_EINVAL;
@@ -671,12 +681,11 @@ extern "C" size_t moe_verify_drafts_workspace_bytes(const moe_verify_args* args)
 extern "C" int moe_verify_drafts(const moe_verify_args* args, void* ws, size_t ws_bytes, void* stream) {
   const int rc = check(args);
   if (rc != MOE_OK) return rc;
-  moe_verify_args a = *args;
+  const moe_verify_args a = read_by(*args);
   if (!ptr_ok(ws, 16)) return MOE_EINVAL;
   const Workspace w = layout(a);
   if (ws_bytes < w.total) return MOE_EWORKSPACE;
   const bool greedy = std::isinf(a.inv_temperature);
-  if (greedy) a.draft_probs = nullptr;
   char* base = static_cast<char*>(ws);
   Plan p{};
   const int N = a.dtype == MOE_F32 ? 4 : 8, vecs = (a.vocab + 2 * N - 2) / N;  // a row that begins off a vector's start has one more

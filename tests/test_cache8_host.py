@@ -139,3 +139,12 @@ def test_verify_workspace_does_not_fall_as_sizes_grow():
     for v in vocabs:
         column = [size(n_req=n, n_rows=661, vocab=v) for n in reqs]
         assert column == sorted(column), v
+
+
+def test_greedy_does_not_look_at_what_it_does_not_read():
+    """Random numbers and drafts' probabilities may be anything, also beside a tree."""
+    greedy = dict(inv_temperature=math.inf, parents=P, draft_probs=P + 1, draft_dtype=9, draft_stride=-4, uniform=P + 2, noise=P + 1,
+                  noise_stride=-1)
+    size = mv.moe_verify_drafts_workspace_bytes(verify_args(inv_temperature=math.inf, parents=P))
+    assert size > 0 and mv.moe_verify_drafts_workspace_bytes(verify_args(**greedy)) == size
+    refused("moe_verify_drafts", verify_args(**greedy), mv.MOE_EWORKSPACE, P, size - 1, None)

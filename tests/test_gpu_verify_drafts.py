@@ -372,3 +372,8 @@ def test_lengths_that_descend_bring_no_token_outside_the_vocabulary(mode):
     assert accepted[1] == 0 and follow[1] == -1
     assert np.all((accepted >= 0) & (accepted < 15)) and np.all((follow >= -1) & (follow < 100))
     assert np.all((path >= -1) & (path < 15))
+
+
+def test_greedy_trees_beside_draft_probabilities_that_are_not_read():
+    case = VerifyCase(24, [6, 3, 0, 4], 3001, mode="greedy", tree=True)
+    good(case, draft_probs=4096, draft_dtype=9, draft_stride=-4, noise_stride=-1)
