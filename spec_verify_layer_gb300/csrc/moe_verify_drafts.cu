@@ -698,7 +698,7 @@ extern "C" int moe_verify_drafts(const moe_verify_args* args, void* ws, size_t w
   if ((double)hi > c) hi = std::nextafter(hi, 0.f);
   const float lo = greedy || hi >= 3.0e38f ? 0.f : (float)(c - (double)hi);
   p.hi = hi;
-  p.lo = lo > 1e-30f ? lo : 1e-30f;
+  p.lo = lo > 0.f ? lo : 1.4e-45f;  // the smallest number: of no weight beside any c
   p.inv_t = (double)a.inv_temperature;
   p.left = reinterpret_cast<unsigned*>(base);
   p.sums = reinterpret_cast<float2*>(base + w.sums);

@@ -377,3 +377,13 @@ def test_lengths_that_descend_bring_no_token_outside_the_vocabulary(mode):
 def test_greedy_trees_beside_draft_probabilities_that_are_not_read():
     case = VerifyCase(24, [6, 3, 0, 4], 3001, mode="greedy", tree=True)
     good(case, draft_probs=4096, draft_dtype=9, draft_stride=-4, noise_stride=-1)
+
+
+@pytest.mark.parametrize("mode,tree", [("lookup", True), ("drawn", False)])
+@pytest.mark.parametrize("size", [1e30, 1e34, 1e37])
+def test_logits_and_temperatures_of_any_size(mode, tree, size):
+    """Large logits at as large a temperature: the probabilities are those of ordinary ones."""
+    case = VerifyCase(23, [9, 4, 1], 5003, mode=mode, tree=tree)
+    case.x = case.x * size
+    case.inv = float(np.float32(1 / size))
+    good(case)
