@@ -346,3 +346,16 @@ def test_queries_with_elements_far_below_their_largest(n, dtype, largest, small,
     off = (lse.double() - score).abs().max().item()
     assert off <= 66 * 2**-24 * score + (63 * 2**-39 * largest * case.scale if rounded else 0) + 2**-22 * (score + 48) + 4e-6
     assert off > 66 * 2**-24 * score + 2**-22 * (score + 48) + 4e-6 or not rounded
+
+
+@pytest.mark.parametrize("hq", [4, 32])
+def test_waits_that_give_up_are_reported(hq):
+    """Blocks that share a head end at different times, so with a bound of 1 ns some call's wait gives up."""
+    case = Tree8Case(23, [30000], [4], hq=hq, hkv=1, d=128, page=64, block=64, fmt="e4m3")
+    mv.moe_set_attention_wait_limit_ns(1)
+    try:
+        seen = [case.run()[2] for _ in range(10)]
+    finally:
+        mv.moe_set_attention_wait_limit_ns(0)
+    assert set(seen) <= {0, mv.MOE_DEV_TIMEOUT} and mv.MOE_DEV_TIMEOUT in seen
+    good(case)
