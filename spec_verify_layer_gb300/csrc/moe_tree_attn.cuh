@@ -1256,6 +1256,10 @@ int launch(const A& a, Plan p, int sms, cudaStream_t st) {
   p.nslot = (kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - p.nq * Sh::kQ) / Sh::kSlot;
   if (p.nslot > kMaxSlots) p.nslot = kMaxSlots;
   static_assert(kMaxSlots / 2 + 1 <= 8, "holes");
+  // Tile t's scales go where those of tile t - kRing were, whose softmax has to be over: its values have been multiplied.
+  // Keys and values take turns in the ring, tile t's are items 2 t and 2 t + 1.  A producer writes the scales when it has
+  // the slot of item 2 t, and so had that of 2 t - 1 before; the products that read items 2 t - nslot and 2 t - 1 - nslot
+  // are over then.  One of the two is of values, those of tile t - kRing or a later one with nslot <= 2 kRing - 2.
   if (kQ8<A> && p.nslot > 2 * Sh::kRing - 2) p.nslot = 2 * Sh::kRing - 2;
   static_assert((kSmem - 1024 - (int)sizeof(Control) - Sh::kScales - Sh::NS * Sh::kQ) / Sh::kSlot >= (kQ8<A> ? 3 : 4), "ring");
   static thread_local int ready = -1;  // device whose shared-memory limit this thread has set
