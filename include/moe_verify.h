@@ -652,6 +652,9 @@ int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, 
  *   path       [n_rows]  path[row_start[b] + i]: the i-th row that stands (path[row_start[b]]
  *                        is 0), as an index within the request; -1 behind the last
  *   next_token [n_req]   the token that follows
+ * The rows of a chain that stand lie in the cache as the next round needs them.  Those of a tree lie
+ * apart: before the next round they are cached once more behind the same context
+ * (moe_cache8_append with the same ctx_len, the rows gathered by path from the round's own).
  * A request without rows gets accepted 0 and next_token -1.  A draft of token -1 stands for
  * none and is not taken (its draft_probs are not read); other tokens outside the
  * vocabulary are not taken either and raise MOE_DEV_INDEX, as does a parent outside

@@ -10,8 +10,9 @@ import pytest
 import torch
 
 import spec_verify_layer_gb300 as mv
-from cache8_helpers import FORMATS, Tree8Case
+from cache8_helpers import FORMATS, Cache8, Tree8Case
 from round_ops_helpers import DEV
+from test_gpu_cache8 import append, rows_of
 from test_gpu_verify_drafts import VerifyCase
 
 pytestmark = pytest.mark.gpu
@@ -197,3 +198,43 @@ def test_a_captured_round():
     finally:
         for layer in layers:
             layer.close()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+def test_after_a_tree_the_rows_that_stand_are_appended_again(fmt):
+    """A tree's rows lie in the cache in their own order: those of its path, gathered from the round's rows, are appended
+    once more behind the same context, and the cache is as if the others had only left their scales' rounding."""
+    case = Cache8(25, [21, 8, 40], [7, 5, 1], hkv=2, d=64, page=16, block=8, fmt=fmt)
+    rows = rows_of(case)
+    want = case.appended(rows)
+    assert append(case, rows) == 0
+    case.same(want)
+    trees = VerifyCase(26, case.counts, 500, mode="greedy", tree=True)
+    best = trees.x.float().argmax(-1).cpu().numpy()
+    for b, n in enumerate(case.counts):  # every second row carries the token that its parent's logits say
+        for i in range(1, n):
+            r = int(trees.start[b]) + i
+            up = int(trees.parents[r])
+            trees.tokens[r] = best[trees.start[b] + up] if i % 2 == 0 and up >= 0 else -1
+    outs, flags = trees.run()
+    assert flags == 0
+    for got, expected in zip(outs, trees.plain()):
+        np.testing.assert_array_equal(got, expected)
+    accepted, path, _ = outs
+    assert accepted.max() > 0
+    stand = [trees.start[b] + path[trees.start[b]:trees.start[b] + accepted[b] + 1] for b in range(3)]
+    at = torch.from_numpy(np.concatenate(stand)).to(DEV)
+    assert (np.diff(stand[0]) > 1).any() or (np.diff(stand[1]) > 1).any()  # (something has to move)
+    case.counts = [len(s) for s in stand]
+    case.start = np.concatenate([[0], np.cumsum(case.counts)])
+    rows = {m: x[at] for m, x in rows.items()}
+    want = case.appended(rows)
+    assert append(case, rows) == 0
+    case.same(want)
+    for b, n in enumerate(case.counts):
+        r0, pos = int(case.start[b]), np.arange(case.ctx[b], case.ctx[b] + n)
+        p, o = case.where(b, pos)
+        for name in ("k", "v"):
+            x, scale = rows[name][r0:r0 + n].double(), getattr(case, name + "_scale")[p, o // 8].double()[..., None]
+            step = torch.maximum(x.abs() * 2**-4, scale * 2**-10) if fmt == "e4m3" else scale / 2
+            assert ((case.values(name, b, pos) - x).abs() <= step).all()
