@@ -561,9 +561,12 @@ int moe_cache8_read(const moe_cache8_args* args, void* stream);
  * one counts as 0 and raises MOE_DEV_VALUE).  dtype is that of q and out.  Inside, codes are
  * 16-bit numbers (exactly), queries fp16 numbers with a power of two for each row and
  * head (exactly, but for elements below 2^-31, of fp16 queries 2^-28, of its largest, which
- * are off by 2^-39 of that at most), and the softmax weights, with
- * the values' scale in them, are rounded to fp16 for the product with the codes (what is
- * lost are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  Scales of
+ * are off by 2^-39 of that at most, where that is 2^-112 or more), and the softmax weights,
+ * with the values' scale in them, are rounded to fp16 for the product with the codes (what is
+ * lost are weights times scale under 2^-32 of the largest); the rest is in 32 bits.  Among it is
+ * the product of a key's scale, |scale| and a power of two near a query row's largest element:
+ * where the three together (or |scale| alone) pass 2^127, scores are past 32 bits but for codes
+ * that cancel, and the row may be NaN where those would have given a number.  Scales of
  * values are taken between 2^-48 and 2^48: smaller ones count as 0 (their values are below
  * 1.6e-12), and so do larger ones, which raise MOE_DEV_VALUE.  A code that is NaN is NaN under any
  * scale, 0 too, for the rows that see it.  The span of either cache is below 2^36 - 2048 bytes here.

@@ -359,3 +359,18 @@ def test_waits_that_give_up_are_reported(hq):
         mv.moe_set_attention_wait_limit_ns(0)
     assert set(seen) <= {0, mv.MOE_DEV_TIMEOUT} and mv.MOE_DEV_TIMEOUT in seen
     good(case)
+
+
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("q,k,scale", [(2.0**100, 2.0**-100, 1 / 8), (2.0**-100, 2.0**100, 1 / 8), (2.0**60, 2.0**60, 2.0**-123),
+                                       (2.0**-40, 2.0**-60, 2.0**97), (2.0**20, 2.0**-120, 2.0**97)])
+def test_queries_and_scales_far_from_one_whose_scores_are_ordinary(n, q, k, scale):
+    case = Tree8Case(24, [150], [n], hq=4, hkv=2, d=64, page=16, block=16, fmt="e4m3", scale=scale)
+    case.q = (case.q.float() * q).to(case.dt)
+    case.k_scale.mul_(k)  # (at 2^-120 some are no normal numbers: they count as 0, which is said)
+    none = case.k_scale < 2.0**-126
+    p, _ = case.where(0, np.arange(150 + n))
+    out, lse, status = case.run()
+    assert status == (mv.MOE_DEV_VALUE if none[p].any() else 0)
+    case.k_scale[none] = 0
+    case.check(out, lse)
