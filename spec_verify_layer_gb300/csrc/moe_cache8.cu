@@ -15,16 +15,23 @@
 // that says that something is not finite are the rows looked at again one by one (78.6 -> 69.0 us for
 // the prompts below, 89.1 -> 69.6 with int8, whose rounding is one addition, all with three thread
 // blocks an SM).
-//   One token 6.2 us: latency (lengths, page, rows, one after the other).  200 requests of up to 9 rows,
-// 8 heads of 64, 17.8 us: the same, and groups that look for the blocks of ragged rows.  Prompts of
-// 20,011 to 32,768 rows, 4 heads of 128 (243 MB), 63.5 us, 3.8 TB/s, 56 % of measured: a group holds
-// one task's 4 KB at a time and waits for it before it stores, and two thread blocks an SM hold as many
-// tasks as registers allow.  Three with the spills that they bring 69.0 us, four with half as many
-// elements kept and the rest read again 81.8; fp32 rows 76 (88 with half of them kept).
+//   One token into a block of 16 that is half full 6.6 us: latency (lengths, page, row, one after the other).
+// 200 requests of up to 9 rows, 8 heads of 64, blocks of 8, 18.6 us: the same, and groups that look for the blocks
+// of ragged rows.  A begun block is walked by its one group, 8 bytes a lane and step, twice where the scale
+// moves: one token into a block that is full but for it takes, with blocks of 16, 64 and 128, 8.2, 14.3 and 22.3 us
+// with heads of 128, 9.1, 20.5 and 36.2 with heads of 256.
+//   Prompts of 20,011 to 32,768 rows, 4 heads of 128 (243 MB), blocks of 16, 63.5 to 65 us, 3.8 TB/s, 56 % of
+// measured: a group holds one task's 4 KB at a time and waits for it before it stores, and two thread blocks an SM
+// hold as many tasks as registers allow.  Three with the spills that they bring 69.0 us, four with half as many
+// elements kept and the rest read again 81.8; fp32 rows 76 (88 with half of them kept).  That size of a task is what
+// the registers just hold.  Larger ones are read twice: blocks of 32, 64 and 128 take 69.9, 77.0 and 94.1 us, heads of
+// 256 in blocks of 16 69.6.  Smaller ones leave less on its way: blocks of 8, 4, 2 and 1 take 99, 173, 254 and 244,
+// 8 heads of 64 in blocks of 16 106.
 //
 // Read.  A thread takes 16 codes of four rows at a time; a row's request, page and scale's place are looked
 // up once a thread block.  1,500 rows, 4 heads of 128, 6.6 us: latency.  Five contexts of 1,001 to 65,536 rows, 8
-// heads of 64 (511 MB), 98.0 us, 5.2 TB/s, 76 % of measured, two thirds of it written; 122 with a look-up a warp.
+// heads of 64 (511 MB), 98.0 us, 5.2 TB/s, 76 % of measured, two thirds of it written; 122 with a look-up a warp.  The same
+// rows as 2 heads of 256 in e4m3 to bf16 100 us, in int8 88, e4m3 to fp32 182 (4.7 TB/s); blocks of 1 and of 32 alike.
 #include "moe_round_ops.cuh"
 
 namespace moe {

@@ -10,8 +10,17 @@ int attention8_i8(const moe_tree_attention8_args* args, void* ws, size_t ws_byte
 namespace {
 
 // Query rows a key/value head up to which products of codes are taken in registers (moe_few_rows.cuh), and
-// above which through tensor memory.  16 requests over 4,096 to 8,192 keys, 32/4 heads of 128, us: 33
-// with 8 rows and 39 with 16, 56 against 59 with 32, 86 against 59 with 48, 150 against 67 with 128.
+// above which through tensor memory.  16 requests over 4,096 to 8,192 keys in blocks of 64, 8 query heads a
+// key/value head, us in registers / through tensor memory:
+//   query rows       8        16        24 and 32    48         64
+//   8 heads of 64    41 / 76  47 / 77   64 / 77      112 / 78   112 / 78    e4m3
+//                    43 / 80  48 / 82   65 / 82      113 / 84   114 / 84    int8
+//   4 heads of 128   33 / 57  39 / 57   55 / 58      86 / 59    86 / 59     e4m3
+//                    35 / 65  41 / 65   56 / 65      88 / 67    88 / 67     int8
+//   2 heads of 256   35 / 55  42 / 55   60 / 57      81 / 62    99 / 64     e4m3
+//                    36 / 63  41 / 64   61 / 64      84 / 69    104 / 70    int8
+// (Heads of 256 have 16 rows a group there, so 17 to 32 read the keys twice: 5 % slower than through tensor memory
+// with e4m3, 4 % faster with int8.)  The kernel goes by max_tree, not by the rows that a request brings.
 constexpr int kFewRows = 32;
 
 template <int FMT>

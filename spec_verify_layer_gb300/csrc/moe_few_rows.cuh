@@ -14,9 +14,11 @@
 // by an 8 x 8 transpose.  Eight or twelve warps take steps of 32 keys in turn, each with a ring of
 // stages and a softmax of its own, so that no barrier stands between a warp's loads and its products.
 //
-// 64 requests of one row over 4,096 to 8,192 keys, 32/4 heads of 128 (403 MB): 82.7 us, 4.9 TB/s, 71 %
-// of the 59 us that the bytes take; 88 with eight warps.  Bound: instructions issued and the latency of
-// a warp's own chain (copy, scores, weights, products), 12 warps being all that registers allow.
+// 64 requests of one row over 4,096 to 8,192 keys, 32/4 heads of 128 (403 MB): 82.5 us, 4.9 TB/s, 71 %
+// of measured (the bytes take 59 us); 88 with eight warps.  Bound: instructions issued and the latency of
+// a warp's own chain (copy, scores, weights, products), 12 warps being all that registers allow.  Page, scales,
+// logarithm and reciprocal are taken key by key, so blocks of 1, 4, 16 and 64 tokens take the same (83.7, 81.2, 81.0,
+// 82.5).  16/2 heads of 256 82.7, 64/8 heads of 64, twice as many keys of half the size, 135.
 // One row over up to 1,000 keys 12.3 us: latency, as for the 16-bit cache.  Six groups of 8 rows for
 // heads of 64 (33 ragged requests of up to 48 query rows) 108 us against 89 through tensor memory: sums of
 // that many rows leave registers for steps of 16 keys only.

@@ -61,12 +61,14 @@
 // sum of the softmax weights is taken from the same numbers times 1 / v_scale.  So values need no
 // multiplication, and the running maximum is that of the weights as the product sees them, whose
 // fp16 places it has to keep (a scale far above the others is then no loss).
-// Full trees of the above sizes 396 us (16-bit cache 260): stages of raw codes leave room for three slots
-// of fp16 in place of five, so products wait for tiles (clocks of a producer for the keys and values of a
-// tile: copies asked for 1,390 cycles, scales 460, codes into fp16 1,160, before look-ups by runs) as
-// well as for the softmax, which has three more numbers to read a key.  33 ragged requests of up to 24
-// rows, 16/8 heads of 64, 89 us (55.8), bound by the same producers; 121 with the scales of blocks of
-// 8 tokens taken key by key.  Tried and slower: raw codes by the tensor memory accelerator (422; 183
+// Full trees of the above sizes, blocks of 32, 396 to 400 us (16-bit cache 260), 446 with blocks of 8, 638
+// with blocks of 1 and 4, whose keys are looked up one by one; of 16/2 heads of 256 504 (322).  Stages of
+// raw codes leave room for three slots of fp16 in place of five, so products wait for tiles (clocks of a
+// producer for the keys and values of a tile: copies asked for 1,390 cycles, scales 460, codes into fp16
+// 1,160, before look-ups by runs) as well as for the softmax, which has three more numbers to read a key.
+// 33 ragged requests of up to 24 rows, 16/8 heads of 64, int8, blocks of 8, 89 us (55.8), bound by the same
+// producers; 121 with the scales of such blocks taken key by key, 117 with blocks of 1 and 4, 85 with blocks
+// of 16 (e4m3 some 5 us less each).  Tried and slower: raw codes by the tensor memory accelerator (422; 183
 // against 176 for one row), a loader and six converters in sixteen warps (438 to 539: the softmax
 // spills at 128 registers), a fourth producer (479; ragged batch 113: it spills at 152 too).
 //

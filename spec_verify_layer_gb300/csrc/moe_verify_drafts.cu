@@ -18,7 +18,11 @@
 // waits for the one before.  64 chains of up to 8 rows of 131,072 in bf16, with draft probabilities (101
 // MB), 45.5 us: by themselves sums 18, walk 10, draws 24, the draws bound by what an entry costs (logit,
 // noise and draft probability each unpacked, compared in products).  24 trees of 8 to 48 rows of 129,283
-// in fp32, 80.8 us: sums 47 (224 MB, 4.7 TB/s), walk 14, draws 18.
+// in fp32, 80.8 us: sums 47 (224 MB, 4.7 TB/s), walk 14, draws 18.  The draws wait for the walk before they read
+// anything, the noise too; where rows of noise and of logits begin apart (an odd vocabulary) its elements are loaded
+// one by one: the 64 chains over 131,071 entries 50 us.
+// Greedy, which reads every row and draws nothing: the five rows 8.7 us, 64 such chains 20.3 (68 MB, 3.4 TB/s),
+// in fp32 30.9 (4.4 TB/s), the 24 trees 69.2 (342 MB, 4.95 TB/s, 73 % of measured).
 //
 // The exponent (x - m) c is taken with c in two parts (c >= hi, lo > 0, so that -infinity stays
 // what it is): with c rounded to 32 bits probabilities far from the maximum would be off by
@@ -41,6 +45,9 @@ constexpr int kMaxSlices = 32;
 // many entries at least.
 // Long slices (in bytes) of rows are cut once more, since the last of them to begin end alone: 24 trees of
 // fp32 rows 88.4 us without, 84.0 so; 64 chains of bf16 rows, whose slices would be 16 KB then, 52.5 and 55.9.
+// Looked-up chains of 8, us as it is / never / always cut once more, in fp32: 96 rows of 262,144 49 / 49 / 48, 640 of
+// 131,072 94 / 90 / 94, 400 of 262,144 113 / 126 / 112, 760 of 200,000 160 / 183 / 160; in bf16: 200 of 262,144
+// 49 / 49 / 51, 400 of 262,144 73 / 74 / 73, 512 of 131,072 56 / 56 / 59.
 constexpr int kSumBlocks = 1500, kDrawBlocks = 304, kSliceMin = 2048, kLongSlice = 48 << 10;
 constexpr int kCounters = (int)(kCounterBytes / sizeof(unsigned));
 
