@@ -1186,11 +1186,12 @@ __global__ void __launch_bounds__(NT > 0 ? kFewThreads<D, NT> : kThreads, 1)
     const Req q = request<D>(a, b);
     if (q.n == 0 || q.tiles) continue;
     flags |= MOE_DEV_LENGTH;
-    for (int r = q.s; r < q.s + q.n; ++r) {
+    for (int i = 0; i < q.n; ++i) {  // (q.n -1: its start may be any number, and no row is its own)
+      const int r = q.s + i;
       uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (long long)r * a.out_stride);
-      for (int i = 0; i < a.q_heads * CPR; ++i) to[i] = make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < a.q_heads * CPR; ++c) to[c] = make_uint4(0, 0, 0, 0);
       if (a.lse)
-        for (int i = 0; i < a.q_heads; ++i) a.lse[(long long)r * a.q_heads + i] = -INFINITY;
+        for (int h = 0; h < a.q_heads; ++h) a.lse[(long long)r * a.q_heads + h] = -INFINITY;
     }
   }
   if (flags) atomicOr(a.dev_status, flags);

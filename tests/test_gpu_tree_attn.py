@@ -320,3 +320,13 @@ def test_small_weights_keep_their_bits(d):
     out, lse, status = case.run()
     assert status == 0
     case.check(out, lse, weight_step=2**-32)
+
+
+@pytest.mark.parametrize("first", [-2**31, -2**31 + 1, -2**31 + 5, -2**30, -1])
+def test_row_starts_as_far_below_zero_as_they_go(first):
+    """The request that begins there, and the one that ends there, are left out; no row is written for them."""
+    case = TreeCase(31, [40, 30, 20, 10], [3, 4, 2, 5], hq=8, hkv=2, d=64, page=16, dtype="bf16")
+    out, lse, status = case.run(start=i32([0, first, 7, 9, 14]))
+    assert status == mv.MOE_DEV_LENGTH
+    case.check(out, lse, only=[2, 3])
+    assert torch.isnan(out[:7]).all() and torch.isnan(lse[:7]).all()

@@ -374,3 +374,14 @@ def test_queries_and_scales_far_from_one_whose_scores_are_ordinary(n, q, k, scal
     assert status == (mv.MOE_DEV_VALUE if none[p].any() else 0)
     case.k_scale[none] = 0
     case.check(out, lse)
+
+
+@pytest.mark.parametrize("first", [-2**31, -2**31 + 1, -2**31 + 5, -2**30, -1])
+@pytest.mark.parametrize("hq", [4, 40])
+def test_row_starts_as_far_below_zero_as_they_go(hq, first):
+    """The request that begins there, and the one that ends there, are left out; no row is written for them."""
+    case = Tree8Case(25, [40, 30, 20, 10], [3, 4, 2, 5], hq=hq, hkv=2, d=64, page=16, block=16, fmt="e4m3", max_tree=5)
+    out, lse, status = case.run(start=i32([0, first, 7, 9, 14]))
+    assert status == mv.MOE_DEV_LENGTH
+    case.check(out, lse, only=[2, 3])
+    assert torch.isnan(out[:7]).all() and torch.isnan(lse[:7]).all()

@@ -387,3 +387,21 @@ def test_logits_and_temperatures_of_any_size(mode, tree, size):
     case.x = case.x * size
     case.inv = float(np.float32(1 / size))
     good(case)
+
+
+@pytest.mark.parametrize("first", [-2**31, -2**31 + 1, -2**31 + 5, -2**30, -1])
+@pytest.mark.parametrize("mode", ["greedy", "lookup", "drawn"])
+def test_row_starts_as_far_below_zero_as_they_go(mode, first):
+    """The request that begins there, and the one that ends there, get nothing; the others what they get without them."""
+    case = VerifyCase(27, [3, 4, 2, 5], 700, mode=mode)
+    want = case.plain()
+    outs, flags = case.outputs(), word()
+    args = case.args(outs, flags)
+    case.keep[0].copy_(i32([0, first, 7, 9, 14]))
+    ws = torch.zeros(mv.moe_verify_drafts_workspace_bytes(args), dtype=torch.uint8, device=DEV)
+    mv.moe_verify_drafts(args, at(ws), ws.numel(), stream())
+    accepted, path, follow = (t.cpu().numpy() for t in outs)
+    assert int(flags.item()) == mv.MOE_DEV_LENGTH
+    assert accepted[:2].tolist() == [0, 0] and follow[:2].tolist() == [-1, -1] and (path[:7] == -9).all()
+    for got, expected, rows in ((accepted, want[0], slice(2, 4)), (path, want[1], slice(7, 14)), (follow, want[2], slice(2, 4))):
+        np.testing.assert_array_equal(got[rows], expected[rows])
