@@ -317,6 +317,7 @@ int moe_decode_layer_noalloc(const moe_dims* dims, const moe_layer_w* w, const u
  *     under way at the same time, of other shapes and of either kind, if it is as large as
  *     the largest needs.
  *   - Outputs do not depend on the order in which thread blocks finish (bitwise).
+ *   - Outputs overlap neither inputs nor each other, except where a call says that they may.
  *   - Element types: MOE_BF16, MOE_F16, and MOE_F32 where a call says so.  Sums, softmax
  *     statistics and norms are held in 32 bits; results are rounded once.
  * ====================================================================================== */
@@ -500,8 +501,10 @@ int moe_tree_attention(const moe_tree_attention_args* args, void* ws, size_t ws_
  *   calls never write those).  MOE_I8: two's complement; the calls write -127..127.
  * A scale is 0 or a finite positive normal number; any other counts as 0 and raises
  * MOE_DEV_VALUE where a position that a call reads goes by it.  moe_cache8_append writes
- * powers of two; a program's own calibrated scales may be any.  Pages are numbered as in
- * moe_kv_cache. */
+ * powers of two; a program's own calibrated scales may be any.  Strides of scales may be 0, for one
+ * scale over pages, blocks or heads, where a cache is only read; moe_cache8_append wants codes and a
+ * scale for each block and head, of keys and of values, that no other shares (MOE_EINVAL for strides
+ * of 0 and for one array of scales for both).  Pages are numbered as in moe_kv_cache. */
 typedef struct moe_kv_cache8 {
   void* k;
   void* v;

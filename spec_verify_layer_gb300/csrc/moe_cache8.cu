@@ -418,6 +418,17 @@ int check(const moe_cache8_args* p) {
   return MOE_OK;
 }
 
+// May an append write this cache?  Each block of tokens and head has to have a scale and codes of its own; strides of 0,
+// as of a cache that is read under one scale for all, give several the same.
+bool own_places(const moe_cache8_args& a) {
+  const moe_kv_cache8& c = a.cache;
+  if (c.k_scale == c.v_scale) return false;
+  if (c.n_pages > 1 && (c.page_stride == 0 || c.scale_page_stride == 0)) return false;
+  if (c.page_size > 1 && c.slot_stride == 0) return false;
+  if (c.page_size > c.block_size && c.scale_block_stride == 0) return false;
+  return a.kv_heads == 1 || (c.head_stride != 0 && c.scale_head_stride != 0);
+}
+
 // Rows of a thread block: as many as leave blocks for every SM, 16 at least.
 int block_rows(int n_rows) {
   int rows = kRows;
@@ -455,7 +466,9 @@ using namespace moe;
 
 extern "C" int moe_cache8_append(const moe_cache8_args* args, void* stream) {
   const int rc = check(args);
-  if (rc != MOE_OK || args->n_rows == 0) return rc;
+  if (rc != MOE_OK) return rc;
+  if (!own_places(*args)) return MOE_EINVAL;
+  if (args->n_rows == 0) return MOE_OK;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return launch_status(args->dtype == MOE_BF16  ? append<MOE_BF16>(*args, st)
                        : args->dtype == MOE_F16 ? append<MOE_F16>(*args, st)

@@ -148,3 +148,16 @@ def test_greedy_does_not_look_at_what_it_does_not_read():
     size = mv.moe_verify_drafts_workspace_bytes(verify_args(inv_temperature=math.inf, parents=P))
     assert size > 0 and mv.moe_verify_drafts_workspace_bytes(verify_args(**greedy)) == size
     refused("moe_verify_drafts", verify_args(**greedy), mv.MOE_EWORKSPACE, P, size - 1, None)
+
+
+@pytest.mark.parametrize("kw", [dict(scale_page_stride=0), dict(scale_block_stride=0), dict(scale_head_stride=0), dict(page_stride=0),
+                                dict(slot_stride=0), dict(head_stride=0), dict(k_scale=P, v_scale=P)])
+def test_append_refuses_caches_whose_blocks_share_places(kw):
+    own = dict(k=P, v=2 * P, k_scale=3 * P, v_scale=4 * P)
+    refused("moe_cache8_append", rows_args(cache=cache8(**{**own, **kw}), n_rows=0), mv.MOE_EINVAL, None)
+    refused("moe_cache8_append", rows_args(cache=cache8(**own), n_rows=0), mv.MOE_OK, None)  # (no rows: nothing is touched)
+    refused("moe_cache8_read", rows_args(cache=cache8(**{**own, **kw}), n_rows=0), mv.MOE_OK, None)
+    # one of a kind needs no stride
+    alone = {**own, "n_pages": 1, "page_size": 8, "page_stride": 0, "scale_page_stride": 0, "scale_block_stride": 0, "head_stride": 0,
+             "scale_head_stride": 0}
+    refused("moe_cache8_append", rows_args(cache=cache8(**alone), kv_heads=1, n_rows=0), mv.MOE_OK, None)

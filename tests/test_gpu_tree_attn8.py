@@ -385,3 +385,20 @@ def test_row_starts_as_far_below_zero_as_they_go(hq, first):
     assert status == mv.MOE_DEV_LENGTH
     case.check(out, lse, only=[2, 3])
     assert torch.isnan(out[:7]).all() and torch.isnan(lse[:7]).all()
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_one_scale_for_all_by_strides_of_zero(n):
+    """A cache under one calibrated scale of keys and one of values: strides of 0, attended and read."""
+    case = Tree8Case(26, [150, 20], [n, 1], hq=4, hkv=2, d=64, page=16, block=16, fmt="i8")
+    for name, value in (("k", 0.011), ("v", 0.017)):
+        setattr(case, name + "_scale", torch.full((1, 1, 1), value, device=DEV).expand(case.n_pages, 1, 2))
+    assert case.cache().scale_page_stride == 0 and case.cache().scale_head_stride == 0
+    good(case)
+    out = torch.empty((n + 1, 4, 64), dtype=torch.float32, device=DEV)
+    status = word()
+    mv.moe_cache8_read(case.rows_args(out[:, :2], out[:, 2:], status), stream())
+    assert int(status.item()) == 0
+    for i, name in enumerate(("k", "v")):
+        want = torch.cat([case.values(name, b, np.arange(c, c + m)) for b, (c, m) in enumerate(zip(case.ctx, case.counts))])
+        assert torch.equal(out[:, 2 * i:2 * i + 2].double(), want)
