@@ -647,8 +647,8 @@ int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, 
  *   c's token was drawn from): c is taken if uniform[c] * q_c(x) < p_r(x), the rest after
  *   a rejection is max(p_r - q_c, 0);
  *   inv_temperature = +infinity (greedy): c is taken if x is the largest logit's token (of
- *   equal ones the lowest); the token that follows is that token; uniform, noise and
- *   draft_probs are not read and may be NULL.
+ *   equal ones the lowest; a row of -infinity alone has none); the token that follows is that
+ *   token; uniform, noise and draft_probs are not read and may be anything.
  * r goes on with the child that was taken; where none was, or there is none (the rest is
  * p_r then), the token that follows is the one with the largest rest(x) / noise[b][x], of
  * equal ones the lowest: a draw from rest if noise is exponentially distributed, entries

@@ -405,3 +405,14 @@ def test_row_starts_as_far_below_zero_as_they_go(mode, first):
     assert accepted[:2].tolist() == [0, 0] and follow[:2].tolist() == [-1, -1] and (path[:7] == -9).all()
     for got, expected, rows in ((accepted, want[0], slice(2, 4)), (path, want[1], slice(7, 14)), (follow, want[2], slice(2, 4))):
         np.testing.assert_array_equal(got[rows], expected[rows])
+
+
+def test_greedy_rows_in_which_nothing_can_occur():
+    """No token is the largest logit's, so no child stands, one of token 0 neither."""
+    case = VerifyCase(28, [3, 2], 50, mode="greedy")
+    case.x[0] = -math.inf
+    case.tokens[1] = 0
+    case.tokens[4] = int(case.x[3].argmax())
+    got, status = case.run()
+    assert status == 0 and got[0].tolist() == [0, 1] and got[1].tolist() == [0, -1, -1, 0, 1]
+    assert got[2].tolist() == [-1, int(case.x[4].argmax())]
