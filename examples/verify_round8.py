@@ -56,6 +56,8 @@ class Layer8(Layer):
         out = torch.empty((rows.count, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=self.device)
         # one page as long as the round: the rotation writes the rows' keys and values there
         staged = torch.empty((2, rows.count, KV_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=self.device)
+        if rows.count == 0:  # (a page has a slot at least)
+            return out, staged
         page = mv.make_kv_cache(staged[0].data_ptr(), staged[1].data_ptr(), n_pages=1, page_size=rows.count, page_stride=0,
                                 slot_stride=KV_HEADS * HEAD_DIM, head_stride=HEAD_DIM)
         slots = torch.arange(rows.count, dtype=torch.int32, device=self.device)

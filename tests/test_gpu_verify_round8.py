@@ -238,3 +238,14 @@ def test_after_a_tree_the_rows_that_stand_are_appended_again(fmt):
             x, scale = rows[name][r0:r0 + n].double(), getattr(case, name + "_scale")[p, o // 8].double()[..., None]
             step = torch.maximum(x.abs() * 2**-4, scale * 2**-10) if fmt == "e4m3" else scale / 2
             assert ((case.values(name, b, pos) - x).abs() <= step).all()
+
+
+def test_prompts_of_one_token():
+    """Nothing is cached before the first round."""
+    ex = example()
+    layer = ex.Layer8(requests=2)
+    try:
+        texts, ctx, _ = ex.decode(layer, [[5], [7]], rounds=3, inv_temperature=math.inf)
+        assert int(layer.status.item()) == 0 and [len(t) for t in texts] == [c + 1 for c in ctx] and min(ctx) >= 3
+    finally:
+        layer.close()
