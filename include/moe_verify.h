@@ -676,8 +676,8 @@ int moe_token_logprobs(const moe_logprob_args* args, void* ws, size_t ws_bytes, 
  *   noise [n_req][vocab] (noise_stride) fp32; any alignment of their element types.  n_req
  *   1..16384, n_rows 0..2^20, vocab 1..2^24, inv_temperature > 0.
  * ws: moe_verify_drafts_workspace_bytes (it goes by n_req, n_rows and vocab alone and does not
- * fall as they grow; 0 for arguments that the call would refuse), 16-byte aligned, set to zero once before its first use; every call
- * leaves it ready for the next, whatever its shape. */
+ * fall as they grow; 0 for arguments that the call would refuse), 16-byte aligned, set to zero
+ * once before its first use; every call leaves it ready for the next, whatever its shape. */
 typedef struct moe_verify_args {
   const void* logits;
   const void* draft_probs; /* or NULL */
